@@ -19,6 +19,52 @@ int hip_status(hipError_t e) {
     return KDA_EHIP;
 }
 
+bool lin_sizes_ok(int B, int H, int T, int dk, int dv, int N, int has_cu, int dtype) {
+    if (B <= 0 || H <= 0 || H > 65535 || T < 0 || !size_ok(dk) || !size_ok(dv)) return false;
+    if (dtype != KDA_F32 && dtype != KDA_BF16) return false;
+    if (has_cu && (B != 1 || N <= 0)) return false;
+    const int64_t n = has_cu ? N : B;
+    return n * H <= INT32_MAX && n * (T + 128LL) <= INT32_MAX;
+}
+
+// The checks that the linear-attention forward and backward share, and the
+// fields that they fill.
+int lin_args(kda::LinArgs* a, const void* q, const void* k, const void* v, const void* gate, const float* S0, int B,
+             int H, int T, int dk, int dv, const int32_t* cu_seqlens, int N, int dtype, int gate_kind, void* workspace,
+             void* stream) {
+    if (B <= 0 || H <= 0 || T < 0) return KDA_EINVAL;
+    const bool packed = cu_seqlens != nullptr;
+    if (packed ? (B != 1 || N <= 0) : (N != 0 && N != B)) return KDA_EINVAL;
+    if (!packed) N = B;
+    if (gate_kind != KDA_GATE_SCALAR && gate_kind != KDA_GATE_HEAD) return KDA_ENOTSUP;
+    if (!lin_sizes_ok(B, H, T, dk, dv, N, packed, dtype)) return KDA_ENOTSUP;
+    if (T > 0 && (!q || !k || !v || !gate)) return KDA_EINVAL;
+    const uintptr_t es = dtype == KDA_BF16 ? 2 : 4;
+    if (T > 0 && (!aligned(q) || !aligned(k) || !aligned(v) || !aligned(gate, gate_kind == KDA_GATE_HEAD ? 4 : es)))
+        return KDA_EALIGN;
+    if ((S0 && !aligned(S0, 4)) || (packed && !aligned(cu_seqlens, 4))) return KDA_EALIGN;
+    if (workspace && !aligned(workspace)) return KDA_EALIGN;
+    if (!workspace) return KDA_EINVAL;
+    *a = kda::LinArgs{};
+    a->q = q;
+    a->k = k;
+    a->v = v;
+    a->gate = gate;
+    a->S0 = S0;
+    a->B = B;
+    a->H = H;
+    a->T = T;
+    a->dk = dk;
+    a->dv = dv;
+    a->cu_seqlens = cu_seqlens;
+    a->N = N;
+    a->bf16 = dtype == KDA_BF16;
+    a->head_gate = gate_kind == KDA_GATE_HEAD;
+    a->workspace = workspace;
+    a->stream = reinterpret_cast<hipStream_t>(stream);
+    return KDA_OK;
+}
+
 }  // namespace
 
 namespace kda {
@@ -413,6 +459,74 @@ int kda_decode_step(const void* q, const void* k, const void* v, const void* gat
     kda::DecodeArgs a{q, k, v, gate, beta, S, o, N, H, dk, dv, dtype == KDA_BF16,
                       gate_kind == KDA_GATE_SCALAR, reinterpret_cast<hipStream_t>(stream)};
     return hip_status(kda::launch_decode(a));
+}
+
+size_t kda_linattn_fwd_workspace_bytes(int B, int H, int T, int dk, int dv, int N, int has_cu, int dtype) {
+    return lin_sizes_ok(B, H, T, dk, dv, N, has_cu, dtype)
+               ? kda::lin_workspace_bytes(B, H, T, dk, dv, has_cu != 0, N, dtype == KDA_BF16, false) : 0;
+}
+
+size_t kda_linattn_bwd_workspace_bytes(int B, int H, int T, int dk, int dv, int N, int has_cu, int dtype) {
+    return lin_sizes_ok(B, H, T, dk, dv, N, has_cu, dtype)
+               ? kda::lin_workspace_bytes(B, H, T, dk, dv, has_cu != 0, N, dtype == KDA_BF16, true) : 0;
+}
+
+int kda_linattn_fwd(const void* q, const void* k, const void* v, const void* gate, const float* S0, void* o,
+                    float* S_T, int B, int H, int T, int dk, int dv, const int32_t* cu_seqlens, int N, int dtype,
+                    int gate_kind, void* workspace, size_t workspace_bytes, void* stream) {
+    kda::LinArgs a{};
+    const int st = lin_args(&a, q, k, v, gate, S0, B, H, T, dk, dv, cu_seqlens, N, dtype, gate_kind, workspace, stream);
+    if (st != KDA_OK) return st;
+    if (T > 0 && !o) return KDA_EINVAL;
+    if ((T > 0 && !aligned(o)) || (S_T && !aligned(S_T, 4))) return KDA_EALIGN;
+    if (workspace_bytes < kda::lin_workspace_bytes(B, H, T, dk, dv, cu_seqlens != nullptr, a.N, a.bf16, false))
+        return KDA_EINVAL;
+    if (T == 0 && !S_T) return KDA_OK;
+    a.o = o;
+    a.S_T = S_T;
+    return hip_status(kda::launch_lin_fwd(a));
+}
+
+int kda_linattn_bwd(const void* q, const void* k, const void* v, const void* gate, const float* S0, const void* dO,
+                    const float* dS_T, void* grad_q, void* grad_k, void* grad_v, void* grad_gate, float* grad_S0,
+                    int B, int H, int T, int dk, int dv, const int32_t* cu_seqlens, int N, int dtype, int gate_kind,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+    kda::LinArgs a{};
+    const int st = lin_args(&a, q, k, v, gate, S0, B, H, T, dk, dv, cu_seqlens, N, dtype, gate_kind, workspace, stream);
+    if (st != KDA_OK) return st;
+    if (T > 0 && (!dO || !grad_q || !grad_k || !grad_v || (!grad_gate && !a.head_gate))) return KDA_EINVAL;
+    if (a.head_gate && grad_gate) return KDA_EINVAL;
+    const uintptr_t es = dtype == KDA_BF16 ? 2 : 4;
+    if (T > 0 && (!aligned(dO) || !aligned(grad_q) || !aligned(grad_k) || !aligned(grad_v) || !aligned(grad_gate, es)))
+        return KDA_EALIGN;
+    if ((dS_T && !aligned(dS_T, 4)) || (grad_S0 && !aligned(grad_S0, 4))) return KDA_EALIGN;
+    if (workspace_bytes < kda::lin_workspace_bytes(B, H, T, dk, dv, cu_seqlens != nullptr, a.N, a.bf16, true))
+        return KDA_EINVAL;
+    if (T == 0 && !grad_S0) return KDA_OK;
+    a.dO = dO;
+    a.dST = dS_T;
+    a.g_q = grad_q;
+    a.g_k = grad_k;
+    a.g_v = grad_v;
+    a.g_gate = grad_gate;
+    a.g_S0 = grad_S0;
+    return hip_status(kda::launch_lin_bwd(a));
+}
+
+int kda_linattn_decode_step(const void* q, const void* k, const void* v, const void* gate, float* S, void* o, int N,
+                            int H, int dk, int dv, int dtype, int gate_kind, void* stream) {
+    if (N <= 0 || H <= 0) return KDA_EINVAL;
+    if (!size_ok(dk) || !size_ok(dv) || (int64_t)N * H > INT32_MAX) return KDA_ENOTSUP;
+    if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ENOTSUP;
+    if (gate_kind != KDA_GATE_SCALAR && gate_kind != KDA_GATE_HEAD) return KDA_ENOTSUP;
+    if (!q || !k || !v || !gate || !S || !o) return KDA_EINVAL;
+    const uintptr_t es = dtype == KDA_BF16 ? 2 : 4;
+    if (!aligned(q, es) || !aligned(k, es) || !aligned(v, es) || !aligned(o, es) || !aligned(S) ||
+        !aligned(gate, gate_kind == KDA_GATE_HEAD ? 4 : es))
+        return KDA_EALIGN;
+    kda::LinDecodeArgs a{q, k, v, gate, S, o, N, H, dk, dv, dtype == KDA_BF16, gate_kind == KDA_GATE_HEAD,
+                         reinterpret_cast<hipStream_t>(stream)};
+    return hip_status(kda::launch_lin_decode(a));
 }
 
 }  // extern "C"

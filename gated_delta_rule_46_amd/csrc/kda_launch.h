@@ -65,6 +65,30 @@ struct GaugeArgs {
     hipStream_t stream;
 };
 
+// Linear attention with a decay per head; the gradient's fields are null in a
+// forward call and the other way round.
+struct LinArgs {
+    const void *q, *k, *v, *gate, *dO;
+    const float *S0, *dST;                  // initial state, adjoint of the final one, or null
+    void *o, *g_q, *g_k, *g_v, *g_gate;     // in the input type
+    float *S_T, *g_S0;                      // or null
+    int B, H, T, dk, dv;
+    const int32_t* cu_seqlens;              // device, N+1 entries, or null
+    int N;                                  // number of sequences (B when cu_seqlens is null)
+    bool bf16, head_gate;
+    void* workspace;
+    hipStream_t stream;
+};
+
+struct LinDecodeArgs {
+    const void *q, *k, *v, *gate;
+    float* S;
+    void* o;
+    int N, H, dk, dv;
+    bool bf16, head_gate;
+    hipStream_t stream;
+};
+
 // Bytes of intermediates one (chunk, head) pair occupies in the workspace.
 size_t chunk_block_bytes(int dk, int dv, int chunk, bool bf16);
 // Upper bound on the number of chunks over all sequences.
@@ -101,5 +125,10 @@ hipError_t launch_chunk_bwd(const BwdArgs& a);
 size_t cbwd_workspace_bytes(int B, int H, int T, int dk, int dv, bool varlen, int N);
 hipError_t launch_cbwd(const BwdArgs& a);
 hipError_t launch_chunk_fwd(const ChunkArgs& a);
+
+size_t lin_workspace_bytes(int B, int H, int T, int dk, int dv, bool packed, int N, bool bf16, bool grad);
+hipError_t launch_lin_fwd(const LinArgs& a);
+hipError_t launch_lin_bwd(const LinArgs& a);
+hipError_t launch_lin_decode(const LinDecodeArgs& a);
 
 }  // namespace kda

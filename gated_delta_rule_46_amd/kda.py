@@ -21,7 +21,7 @@ LIB_PATH = os.environ.get("KDA_LIB") or os.path.join(_HERE, "libkda.so")
 KDA_OK, KDA_EINVAL, KDA_ENOTSUP, KDA_EALIGN, KDA_EHIP, KDA_EWAIT, KDA_ESCRATCH = 0, -1, -2, -3, -4, -5, -6
 NOALLOC_SCRATCH_BYTES = 128 << 20
 KDA_F32, KDA_BF16 = 0, 1
-GATE_CHANNEL, GATE_SCALAR = 0, 1
+GATE_CHANNEL, GATE_SCALAR, GATE_HEAD = 0, 1, 2
 
 STAGE_PREP, STAGE_STATE, STAGE_ALL = 1, 2, 3
 
@@ -30,7 +30,8 @@ EXPORTS = ("kda_chunk_fwd", "kda_chunk_fwd_stage", "kda_chunk_fwd_workspace_byte
            "kda_chunk_fwd_gauge_workspace_bytes", "kda_decode_step", "kda_strerror", "kda_last_hip_error",
            "kda_version", "kda_chunk_fwd_status", "kda_chunk_fwd_noalloc", "kda_chunk_fwd_ew",
            "kda_decode_step_ew", "kda_chunk_bwd_cw", "kda_chunk_bwd_cw_workspace_bytes", "kda_chunk_bwd_ew",
-           "kda_chunk_bwd_ew_workspace_bytes")
+           "kda_chunk_bwd_ew_workspace_bytes", "kda_linattn_fwd", "kda_linattn_fwd_workspace_bytes", "kda_linattn_bwd",
+           "kda_linattn_bwd_workspace_bytes", "kda_linattn_decode_step")
 
 
 class KDAError(RuntimeError):
@@ -92,6 +93,16 @@ def load(path: str):
     lib.kda_chunk_fwd_ew.argtypes = [vp] * 9 + [i] * 6 + [vp, i, i, i, vp, sz, vp]
     lib.kda_decode_step_ew.restype = i
     lib.kda_decode_step_ew.argtypes = [vp] * 8 + [i] * 6 + [vp]
+    lib.kda_linattn_fwd.restype = i
+    lib.kda_linattn_fwd.argtypes = [vp] * 7 + [i] * 5 + [vp, i, i, i, vp, sz, vp]
+    lib.kda_linattn_fwd_workspace_bytes.restype = sz
+    lib.kda_linattn_fwd_workspace_bytes.argtypes = [i] * 8
+    lib.kda_linattn_bwd.restype = i
+    lib.kda_linattn_bwd.argtypes = [vp] * 12 + [i] * 5 + [vp, i, i, i, vp, sz, vp]
+    lib.kda_linattn_bwd_workspace_bytes.restype = sz
+    lib.kda_linattn_bwd_workspace_bytes.argtypes = [i] * 8
+    lib.kda_linattn_decode_step.restype = i
+    lib.kda_linattn_decode_step.argtypes = [vp] * 6 + [i] * 6 + [vp]
     lib.kda_chunk_fwd_noalloc.restype = i
     lib.kda_chunk_fwd_noalloc.argtypes = [vp] * 8 + [i] * 6 + [vp, i, i, i, vp]
     return lib
@@ -577,4 +588,164 @@ def decode_step_ew(q, k, v, gate, erase, write, S, out: Optional[torch.Tensor] =
                                    _ptr(out), N, H, dk, dv, dt, int(gate_kind), ctypes.c_void_p(st) if st else None)
     if rc != KDA_OK:
         raise KDAError(rc, "kda_decode_step_ew")
+    return out
+
+
+# ---------------------------------------------------------------- linear attention with a decay per head
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """The device of the inputs made current, and what the call allocates taken
+    from the pool of the stream that it runs on. Yields that stream's handle."""
+    if stream is None:
+        with torch.cuda.device(device):
+            st = torch.cuda.current_stream(device).cuda_stream
+            yield ctypes.c_void_p(st) if st else None
+    else:
+        with torch.cuda.device(device), torch.cuda.stream(stream):
+            yield ctypes.c_void_p(stream.cuda_stream) if stream.cuda_stream else None
+
+
+def _like(name, t, shape, dtype, device):
+    """Checks a tensor that a call writes: its shape, dtype, device and layout."""
+    if t.dtype != dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    _check_shape(name, t, shape)
+    _check_dev(name, t, device)
+
+
+def _scratch(workspace, need, device):
+    if workspace is None:
+        return torch.empty(max(need, 1), device=device, dtype=torch.uint8)
+    _check_dev("workspace", workspace, device)
+    if workspace.numel() * workspace.element_size() < need:
+        raise ValueError("workspace too small: %d < %d bytes" % (workspace.numel() * workspace.element_size(), need))
+    return workspace
+
+
+def _check_linattn(q, k, v, gate, cu_seqlens, lead):
+    """Shapes, dtypes and devices of a linear-attention call whose q has `lead`
+    leading dims before dk. Returns (sizes of those, dk, dv, gate kind)."""
+    if q.dim() != lead + 1:
+        raise ValueError("q must have %d dims, got %s" % (lead + 1, tuple(q.shape)))
+    dims, dk = tuple(q.shape[:-1]), q.shape[-1]
+    if v.dim() != lead + 1:
+        raise ValueError("v must have %d dims, got %s" % (lead + 1, tuple(v.shape)))
+    dv = v.shape[-1]
+    _check_shape("k", k, dims + (dk,))
+    _check_shape("v", v, dims + (dv,))
+    for name, t in (("k", k), ("v", v)):
+        if t.dtype != q.dtype:
+            raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, q.dtype))
+    if gate.dim() == 1:
+        kind, want = GATE_HEAD, torch.float32
+        _check_shape("gate", gate, dims[-1:])
+    else:
+        kind, want = GATE_SCALAR, q.dtype
+        _check_shape("gate", gate, dims)
+    if gate.dtype != want:
+        raise TypeError("gate has dtype %s, expected %s" % (gate.dtype, want))
+    if cu_seqlens is not None and dims[0] != 1:
+        raise ValueError("packed sequences (cu_seqlens) need B = 1, got %d" % dims[0])
+    for name, t in (("q", q), ("k", k), ("v", v), ("gate", gate)):
+        _check_dev(name, t, q.device)
+    return dims, dk, dv, kind
+
+
+def linattn_fwd_workspace_bytes(B: int, H: int, T: int, dk: int, dv: int, N: int = 0, varlen: bool = False,
+                                dtype: torch.dtype = torch.bfloat16) -> int:
+    code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    return int(_lib().kda_linattn_fwd_workspace_bytes(B, H, T, dk, dv, N, int(varlen), code))
+
+
+def linattn_bwd_workspace_bytes(B: int, H: int, T: int, dk: int, dv: int, N: int = 0, varlen: bool = False,
+                                dtype: torch.dtype = torch.bfloat16) -> int:
+    code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    return int(_lib().kda_linattn_bwd_workspace_bytes(B, H, T, dk, dv, N, int(varlen), code))
+
+
+def linattn_fwd(q, k, v, gate, S0=None, cu_seqlens=None, out: Optional[torch.Tensor] = None, state_out: bool = True,
+                S_T: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Linear attention with a decay per head, S_t = a_t S_{t-1} + k_t v_t^T,
+    o_t = S_t^T q_t (kda_linattn_fwd). q, k [B,T,H,dk]; v [B,T,H,dv]; gate
+    [B,T,H] in the same dtype, or [H] fp32 for a constant decay per head; S0
+    [N,H,dk,dv] fp32 or None; cu_seqlens int32 [N+1] on the device (B must be 1)
+    or None. Returns (o in the inputs' dtype, S_T fp32 or None)."""
+    (B, T, H), dk, dv, kind = _check_linattn(q, k, v, gate, cu_seqlens, 3)
+    device, dt = q.device, _dtype_code(q)
+    varlen, N = _check_varlen(cu_seqlens, B, device)
+    _check_state("S0", S0, N, H, dk, dv, device)
+    _check_state("S_T", S_T, N, H, dk, dv, device)
+    if out is not None:
+        _like("out", out, (B, T, H, dv), q.dtype, device)
+    need = linattn_fwd_workspace_bytes(B, H, T, dk, dv, N, varlen, q.dtype)
+    with _on(device, stream) as st:
+        if out is None:
+            out = torch.empty((B, T, H, dv), device=device, dtype=q.dtype)
+        if S_T is None and state_out:
+            S_T = torch.empty((N, H, dk, dv), device=device, dtype=torch.float32)
+        ws = _scratch(workspace, need, device)
+        rc = _lib().kda_linattn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(S0), _ptr(out), _ptr(S_T), B, H, T, dk,
+                                    dv, _ptr(cu_seqlens), N if varlen else 0, dt, kind, _ptr(ws),
+                                    ws.numel() * ws.element_size(), st)
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_linattn_fwd")
+    return out, S_T
+
+
+def linattn_bwd(q, k, v, gate, dO, S0=None, dS_T=None, cu_seqlens=None, want_dS0: bool = True,
+                out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradient of linattn_fwd for L = sum(o * dO) + sum(S_T * dS_T)
+    (kda_linattn_bwd). Inputs as for linattn_fwd; dO [B,T,H,dv] in their dtype;
+    dS_T fp32 [N,H,dk,dv] or None. Returns a dict of dq, dk, dv, dgate (inputs'
+    dtype and layouts; dgate None for a constant decay per head) and dS0 (fp32,
+    None when not wanted). ``out`` may supply that dict's tensors."""
+    (B, T, H), dk, dv, kind = _check_linattn(q, k, v, gate, cu_seqlens, 3)
+    device, dt = q.device, _dtype_code(q)
+    _like("dO", dO, (B, T, H, dv), q.dtype, device)
+    varlen, N = _check_varlen(cu_seqlens, B, device)
+    _check_state("S0", S0, N, H, dk, dv, device)
+    _check_state("dS_T", dS_T, N, H, dk, dv, device)
+    shapes = {"dq": (B, T, H, dk), "dk": (B, T, H, dk), "dv": (B, T, H, dv)}
+    if kind == GATE_SCALAR:
+        shapes["dgate"] = (B, T, H)
+    if out is not None:
+        for name, shape in shapes.items():
+            _like(name, out[name], shape, q.dtype, device)
+        if kind == GATE_HEAD and out.get("dgate") is not None:
+            raise ValueError("a constant decay per head has no dgate")
+        _check_state("dS0", out.get("dS0"), N, H, dk, dv, device)
+    need = linattn_bwd_workspace_bytes(B, H, T, dk, dv, N, varlen, q.dtype)
+    with _on(device, stream) as st:
+        if out is None:
+            out = {name: torch.empty(shape, device=device, dtype=q.dtype) for name, shape in shapes.items()}
+            out.setdefault("dgate", None)
+            out["dS0"] = torch.empty((N, H, dk, dv), device=device, dtype=torch.float32) if want_dS0 else None
+        ws = _scratch(workspace, need, device)
+        rc = _lib().kda_linattn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(S0), _ptr(dO), _ptr(dS_T),
+                                    _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out.get("dgate")),
+                                    _ptr(out.get("dS0")), B, H, T, dk, dv, _ptr(cu_seqlens), N if varlen else 0, dt,
+                                    kind, _ptr(ws), ws.numel() * ws.element_size(), st)
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_linattn_bwd")
+    return out
+
+
+def linattn_decode_step(q, k, v, gate, S, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One step of linear attention with a decay per head, S [N,H,dk,dv] fp32
+    updated in place (kda_linattn_decode_step). q, k [N,H,dk]; v [N,H,dv]; gate
+    [N,H] in the same dtype or [H] fp32. Returns o [N,H,dv] in that dtype."""
+    (N, H), dk, dv, kind = _check_linattn(q, k, v, gate, None, 2)
+    device, dt = q.device, _dtype_code(q)
+    _like("S", S, (N, H, dk, dv), torch.float32, device)
+    if out is not None:
+        _like("out", out, (N, H, dv), q.dtype, device)
+    with _on(device, stream) as st:
+        if out is None:
+            out = torch.empty((N, H, dv), device=device, dtype=q.dtype)
+        rc = _lib().kda_linattn_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(S), _ptr(out), N, H, dk, dv, dt,
+                                            kind, st)
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_linattn_decode_step")
     return out

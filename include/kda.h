@@ -65,6 +65,7 @@ extern "C" {
 /* gate_kind */
 #define KDA_GATE_CHANNEL 0 /* gate [.., dk]: one alpha per key channel (KDA, Complex KDA) */
 #define KDA_GATE_SCALAR 1  /* gate [..]: one alpha per token and head (GDN) */
+#define KDA_GATE_HEAD 2    /* gate [H] fp32: one constant alpha per head (kda_linattn_* only) */
 
 /*
  * Bytes of device workspace kda_chunk_fwd needs for these sizes (0 when the
@@ -329,6 +330,63 @@ int kda_chunk_fwd_gauge(const void* q, const void* k, const void* v, const void*
                         const float* S0, float* o, float* S_T, int B, int H, int T, int dk, int dv, int chunk,
                         const int32_t* cu_seqlens, int N, int dtype, int gate_kind, void* workspace,
                         size_t workspace_bytes, void* stream);
+
+/*
+ * Linear attention with a decay for each head: the recurrence without the
+ * delta term,
+ *   S_t = a_t S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t,
+ * for layers that sit beside the delta rule's in one model. Layouts of q, k,
+ * v, S0, S_T, cu_seqlens and N as for kda_chunk_fwd, so states and packed
+ * batches are shared. gate_kind: KDA_GATE_SCALAR (gate [B, T, H] in the input
+ * dtype) or KDA_GATE_HEAD (gate [H], fp32 whatever the dtype: decays near one
+ * have no bf16 neighbours). Any finite decay is allowed, zero and negative
+ * ones included; products of decays are formed directly. There is no query
+ * scaling.
+ *
+ * Unlike the delta rule's calls, o and the gradients have the input dtype
+ * (bf16 halves what the call writes); states are fp32. Rows of o at or behind
+ * cu_seqlens[N] are left as they are. A NaN or Inf at a token reaches every
+ * later output of its sequence, and may reach earlier ones of its block of 64
+ * tokens.
+ *
+ * q, k, v, o and the workspace must be 16-byte aligned, states to their
+ * element. H <= 65535 and B * (T + 128) (packed: N * (T + 128)) < 2^31;
+ * KDA_ENOTSUP otherwise. workspace: at least
+ * kda_linattn_fwd_workspace_bytes(...) bytes (segment states), required; no
+ * status word is kept in it. Returns KDA_OK or a negative status.
+ */
+size_t kda_linattn_fwd_workspace_bytes(int B, int H, int T, int dk, int dv, int N, int has_cu_seqlens, int dtype);
+int kda_linattn_fwd(const void* q, const void* k, const void* v, const void* gate, const float* S0, void* o,
+                    float* S_T, int B, int H, int T, int dk, int dv, const int32_t* cu_seqlens, int N, int dtype,
+                    int gate_kind, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of kda_linattn_fwd for L = sum_t <o_t, dO_t> + sum_seq <S_T, dS_T>.
+ * dO [B, T, H, dv] in the input dtype; dS_T [N, H, dk, dv] fp32 or NULL (zero).
+ * Outputs: grad_q, grad_k, grad_v and grad_gate in the input dtype and
+ * layouts, grad_S0 fp32 or NULL when not wanted. With KDA_GATE_HEAD the decay
+ * is a constant: grad_gate must be NULL (for a learned one, pass it
+ * per token and sum). grad_gate is the derivative with respect to the decay
+ * itself, an ordinary one at zero and negative decays. Nothing of a forward
+ * call is reused. dO and the gradients must be 16-byte aligned (grad_gate and
+ * states: their element). workspace: kda_linattn_bwd_workspace_bytes(...)
+ * bytes (segment states, and the state and adjoint of every block), required.
+ */
+size_t kda_linattn_bwd_workspace_bytes(int B, int H, int T, int dk, int dv, int N, int has_cu_seqlens, int dtype);
+int kda_linattn_bwd(const void* q, const void* k, const void* v, const void* gate, const float* S0, const void* dO,
+                    const float* dS_T, void* grad_q, void* grad_k, void* grad_v, void* grad_gate, float* grad_S0,
+                    int B, int H, int T, int dk, int dv, const int32_t* cu_seqlens, int N, int dtype, int gate_kind,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One step of the same recurrence for N sequences, S [N, H, dk, dv] fp32
+ * updated in place (16-byte aligned; every other pointer to its element).
+ * q, k [N, H, dk]; v, o [N, H, dv] in the input dtype; gate [N, H] in the
+ * input dtype (KDA_GATE_SCALAR) or [H] fp32 (KDA_GATE_HEAD). o must not alias
+ * S or the inputs.
+ */
+int kda_linattn_decode_step(const void* q, const void* k, const void* v, const void* gate, float* S, void* o, int N,
+                            int H, int dk, int dv, int dtype, int gate_kind, void* stream);
 
 /* Static text for a status code (never NULL). */
 const char* kda_strerror(int status);
