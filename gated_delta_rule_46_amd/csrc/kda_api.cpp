@@ -65,6 +65,54 @@ int lin_args(kda::LinArgs* a, const void* q, const void* k, const void* v, const
     return KDA_OK;
 }
 
+bool swa_counts_ok(int Hq, int Hkv, int window, int sinks, float scale) {
+    return Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && window >= 1 && sinks >= 0 && scale - scale == 0.f;
+}
+bool swa_heads_ok(int Hq, int Hkv, int d) {
+    return Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && Hq <= 65535 && (d == 32 || d == 64 || d == 128);
+}
+// slots of a cache
+bool swa_window_ok(int window, int sinks) { return window >= 1 && sinks >= 0 && (int64_t)window + sinks <= (1 << 30); }
+
+bool swa_sizes_ok(int B, int Hq, int Hkv, int T, int d, int window, int sinks, int N, int has_cu) {
+    if (B <= 0 || T < 0 || window < 1 || sinks < 0 || !swa_heads_ok(Hq, Hkv, d)) return false;
+    if (has_cu && (B != 1 || N <= 0)) return false;
+    const int64_t n = has_cu ? N : B, rows = has_cu ? T : n * T;
+    return n <= 65535 && n * (T + 128LL) <= INT32_MAX && (rows / 128 + n + 1) * Hq <= INT32_MAX;
+}
+
+// The checks that the window-attention calls over sequences share, and the
+// fields that they fill.
+int swa_args(kda::SwaArgs* a, const void* q, const void* k, const void* v, int B, int Hq, int Hkv, int T, int d,
+             int window, int sinks, float scale, const int32_t* cu_seqlens, int N, int dtype, void* stream) {
+    if (B <= 0 || T < 0 || !swa_counts_ok(Hq, Hkv, window, sinks, scale)) return KDA_EINVAL;
+    const bool packed = cu_seqlens != nullptr;
+    if (packed ? (B != 1 || N <= 0) : (N != 0 && N != B)) return KDA_EINVAL;
+    if (!packed) N = B;
+    if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ENOTSUP;
+    if (!swa_sizes_ok(B, Hq, Hkv, T, d, window, sinks, N, packed)) return KDA_ENOTSUP;
+    if (T > 0 && (!q || !k || !v)) return KDA_EINVAL;
+    if (T > 0 && (!aligned(q) || !aligned(k) || !aligned(v))) return KDA_EALIGN;
+    if (packed && !aligned(cu_seqlens, 4)) return KDA_EALIGN;
+    *a = kda::SwaArgs{};
+    a->q = q;
+    a->k = k;
+    a->v = v;
+    a->B = B;
+    a->T = T;
+    a->Hq = Hq;
+    a->Hkv = Hkv;
+    a->d = d;
+    a->window = window;
+    a->sinks = sinks;
+    a->scale = scale;
+    a->cu_seqlens = cu_seqlens;
+    a->N = N;
+    a->bf16 = dtype == KDA_BF16;
+    a->stream = reinterpret_cast<hipStream_t>(stream);
+    return KDA_OK;
+}
+
 }  // namespace
 
 namespace kda {
@@ -527,6 +575,81 @@ int kda_linattn_decode_step(const void* q, const void* k, const void* v, const v
     kda::LinDecodeArgs a{q, k, v, gate, S, o, N, H, dk, dv, dtype == KDA_BF16, gate_kind == KDA_GATE_HEAD,
                          reinterpret_cast<hipStream_t>(stream)};
     return hip_status(kda::launch_lin_decode(a));
+}
+
+size_t kda_swa_bwd_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int window, int sinks, int N, int has_cu) {
+    if (!swa_sizes_ok(B, Hq, Hkv, T, d, window, sinks, N, has_cu)) return 0;
+    return kda::swa_bwd_workspace_bytes(T, has_cu ? N : B, Hq, Hkv, d, window, sinks);
+}
+
+size_t kda_swa_decode_workspace_bytes(int N, int Hq, int Hkv, int d, int window, int sinks) {
+    if (N <= 0 || N > 65535 || !swa_heads_ok(Hq, Hkv, d) || !swa_window_ok(window, sinks)) return 0;
+    return kda::swa_decode_workspace_bytes(N, Hq, Hkv, d, window, sinks);
+}
+
+int kda_swa_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv, int T, int d,
+                int window, int sinks, float scale, const int32_t* cu_seqlens, int N, int dtype, void* stream) {
+    kda::SwaArgs a{};
+    const int st = swa_args(&a, q, k, v, B, Hq, Hkv, T, d, window, sinks, scale, cu_seqlens, N, dtype, stream);
+    if (st != KDA_OK) return st;
+    if (T == 0) return KDA_OK;
+    if (!o) return KDA_EINVAL;
+    if (!aligned(o) || (lse && !aligned(lse, 4))) return KDA_EALIGN;
+    a.out = o;
+    a.lse_out = lse;
+    return hip_status(kda::launch_swa_fwd(a));
+}
+
+int kda_swa_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                void* grad_q, void* grad_k, void* grad_v, int B, int Hq, int Hkv, int T, int d, int window, int sinks,
+                float scale, const int32_t* cu_seqlens, int N, int dtype, void* workspace, size_t workspace_bytes,
+                void* stream) {
+    kda::SwaArgs a{};
+    const int st = swa_args(&a, q, k, v, B, Hq, Hkv, T, d, window, sinks, scale, cu_seqlens, N, dtype, stream);
+    if (st != KDA_OK) return st;
+    if (T == 0) return KDA_OK;
+    if (!o || !lse || !dO || !grad_q || !grad_k || !grad_v || !workspace) return KDA_EINVAL;
+    if (!aligned(o) || !aligned(lse, 4) || !aligned(dO) || !aligned(grad_q) || !aligned(grad_k) || !aligned(grad_v) ||
+        !aligned(workspace))
+        return KDA_EALIGN;
+    if (workspace_bytes < kda::swa_bwd_workspace_bytes(T, a.N, Hq, Hkv, d, window, sinks)) return KDA_EINVAL;
+    a.o = o;
+    a.lse = lse;
+    a.dO = dO;
+    a.g_q = grad_q;
+    a.g_k = grad_k;
+    a.g_v = grad_v;
+    a.workspace = workspace;
+    return hip_status(kda::launch_swa_bwd(a));
+}
+
+int kda_swa_decode_step(const void* q, const void* k, const void* v, void* K_cache, void* V_cache, const int32_t* pos,
+                        void* o, int N, int Hq, int Hkv, int d, int window, int sinks, float scale, int dtype,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+    if (N <= 0 || !swa_counts_ok(Hq, Hkv, window, sinks, scale)) return KDA_EINVAL;
+    if (N > 65535 || !swa_heads_ok(Hq, Hkv, d) || !swa_window_ok(window, sinks)) return KDA_ENOTSUP;
+    if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ENOTSUP;
+    if (!q || !k || !v || !K_cache || !V_cache || !pos || !o || !workspace) return KDA_EINVAL;
+    if (!aligned(q) || !aligned(k) || !aligned(v) || !aligned(K_cache) || !aligned(V_cache) || !aligned(pos, 4) ||
+        !aligned(o) || !aligned(workspace))
+        return KDA_EALIGN;
+    if (workspace_bytes < kda::swa_decode_workspace_bytes(N, Hq, Hkv, d, window, sinks)) return KDA_EINVAL;
+    kda::SwaDecodeArgs a{q, k, v, K_cache, V_cache, o, pos, N, Hq, Hkv, d, window, sinks, scale, dtype == KDA_BF16,
+                         workspace, reinterpret_cast<hipStream_t>(stream)};
+    return hip_status(kda::launch_swa_decode(a));
+}
+
+int kda_swa_cache_fill(const void* k, const void* v, void* K_cache, void* V_cache, int B, int Hkv, int T, int d,
+                       int window, int sinks, const int32_t* cu_seqlens, int N, int dtype, void* stream) {
+    kda::SwaArgs a{};
+    const int st = swa_args(&a, k, k, v, B, Hkv, Hkv, T, d, window, sinks, 1.f, cu_seqlens, N, dtype, stream);
+    if (st != KDA_OK) return st;
+    if (a.N > 65535 || !swa_window_ok(window, sinks)) return KDA_ENOTSUP;
+    if (T == 0) return KDA_OK;
+    if (!K_cache || !V_cache) return KDA_EINVAL;
+    if (!aligned(K_cache) || !aligned(V_cache)) return KDA_EALIGN;
+    return hip_status(kda::launch_swa_cache_fill(kda::SwaFillArgs{k, v, K_cache, V_cache, T, a.N, Hkv, d, window, sinks,
+                                                                  cu_seqlens, a.bf16, a.stream}));
 }
 
 }  // extern "C"

@@ -89,6 +89,42 @@ struct LinDecodeArgs {
     hipStream_t stream;
 };
 
+// Window attention with sinks; the gradient's fields are null in a forward call
+// and the other way round.
+struct SwaArgs {
+    const void *q, *k, *v, *o, *dO;
+    const float* lse;
+    void *out, *g_q, *g_k, *g_v;
+    float* lse_out;                         // or null
+    int B, T, Hq, Hkv, d, window, sinks;
+    float scale;
+    const int32_t* cu_seqlens;              // device, N+1 entries, or null
+    int N;                                  // number of sequences (B when cu_seqlens is null)
+    bool bf16;
+    void* workspace;
+    hipStream_t stream;
+};
+
+struct SwaDecodeArgs {
+    const void *q, *k, *v;
+    void *Kc, *Vc, *o;
+    const int32_t* pos;
+    int N, Hq, Hkv, d, window, sinks;
+    float scale;
+    bool bf16;
+    void* workspace;
+    hipStream_t stream;
+};
+
+struct SwaFillArgs {
+    const void *k, *v;
+    void *Kc, *Vc;
+    int T, N, Hkv, d, window, sinks;
+    const int32_t* cu_seqlens;
+    bool bf16;
+    hipStream_t stream;
+};
+
 // Bytes of intermediates one (chunk, head) pair occupies in the workspace.
 size_t chunk_block_bytes(int dk, int dv, int chunk, bool bf16);
 // Upper bound on the number of chunks over all sequences.
@@ -130,5 +166,12 @@ size_t lin_workspace_bytes(int B, int H, int T, int dk, int dv, bool packed, int
 hipError_t launch_lin_fwd(const LinArgs& a);
 hipError_t launch_lin_bwd(const LinArgs& a);
 hipError_t launch_lin_decode(const LinDecodeArgs& a);
+
+size_t swa_bwd_workspace_bytes(int T, int N, int Hq, int Hkv, int d, int window, int sinks);
+size_t swa_decode_workspace_bytes(int N, int Hq, int Hkv, int d, int window, int sinks);
+hipError_t launch_swa_fwd(const SwaArgs& a);
+hipError_t launch_swa_bwd(const SwaArgs& a);
+hipError_t launch_swa_decode(const SwaDecodeArgs& a);
+hipError_t launch_swa_cache_fill(const SwaFillArgs& a);
 
 }  // namespace kda

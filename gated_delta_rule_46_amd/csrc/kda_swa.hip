@@ -1,0 +1,948 @@
+// Softmax attention over a sliding window with sinks: row i of a sequence sees
+// the keys j <= i with i - j < window, and the first `sinks` keys always.
+//
+//   s_ij = scale q_i . k_j,  p_ij = exp(s_ij - lse_i),  o_i = sum_j p_ij v_j
+//
+// Every product runs on 32x32 MFMA tiles, 16 deep (bf16; fp32: eight 32x32x2
+// steps): lane l = 32 h + n holds row (column) n of an operand at 8 of the 16
+// contracted places, and column n of the result at rows 8 (r / 4) + 4 h + r % 4.
+// Scores are formed transposed (keys down, queries across), so a lane owns one
+// query: its maximum and sum run over the lane's registers and one swap with
+// the other half, and the exponentials are the next product's operand as they
+// stand, with no pass through LDS (the contraction takes the keys in the order
+// in which the registers hold them).
+#include <algorithm>
+
+#include "kda_launch.h"
+#include "kda_tiles.h"
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+namespace kda {
+
+namespace {
+
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+struct SwaParams {
+    const void *q, *k, *v, *o, *dO;
+    const float* lse;
+    void *out, *dq, *dk, *dv;
+    float *lse_out, *delta;
+    float* part;            // gradients of sink blocks: [sequence][kv head][block][split][dk, dv][KB][D]
+    SeqMap map;
+    int Hq, Hkv, G;         // G = Hq / Hkv
+    int window, sinks;
+    float scale;
+    int blocks;             // blocks of rows over all sequences
+    int sink_blocks, splits, split_rows;   // gradient: key blocks with sinks, parts of their rows, rows in a part
+};
+
+__device__ __forceinline__ f32x16 mma32(const bf16x8& a, const bf16x8& b, const f32x16& c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma32(const f32x8& a, const f32x8& b, f32x16 c) {
+#pragma unroll
+    for (int m = 0; m < 8; ++m) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[m], b[m], c, 0, 0, 0);
+    return c;
+}
+__device__ __forceinline__ f32x16 zero16() {
+    f32x16 z;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) z[r] = 0.f;
+    return z;
+}
+
+// rows r0 + n, columns k0 + 8 h + (0..7)
+template <class T>
+__device__ __forceinline__ typename Frag<T>::V nat32(const T* t, int st, int r0, int k0, int n, int h) {
+    return frag_nat(t, st, r0 + n, k0, h);
+}
+// column c0 + n, rows r0 + 4 h + (0..3) and r0 + 8 + 4 h + (0..3)
+__device__ __forceinline__ bf16x8 tr32(const uint16_t* t, int st, int r0, int c0, int lane) {
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    const int i = lane & 15, b = (lane >> 4) & 1, h = lane >> 5;
+    const uint16_t* p = t + (r0 + 4 * h + (i >> 2)) * st + c0 + 16 * b + 4 * (i & 3);
+    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 8 * st));
+    const auto u = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_bit_cast(bf16x8, u);
+}
+__device__ __forceinline__ f32x8 tr32(const float* t, int st, int r0, int c0, int lane) {
+    const float* p = t + (r0 + 4 * (lane >> 5)) * st + c0 + (lane & 31);
+    f32x8 r;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        r[m] = p[m * st];
+        r[4 + m] = p[(8 + m) * st];
+    }
+    return r;
+}
+// half b of a result tile's rows as an operand (rows contracted)
+template <class T> __device__ __forceinline__ typename Frag<T>::V rows16(const f32x16& x, int b) {
+    f32x8 y;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) y[m] = x[8 * b + m];
+    return narrow<T>(y);
+}
+__device__ __forceinline__ int result_row(int r, int h) { return 8 * (r >> 2) + 4 * h + (r & 3); }
+
+// 8 consecutive elements of a row in global memory, or zeros
+template <class T> __device__ __forceinline__ typename Frag<T>::V load8(const T* p, bool in) {
+    constexpr int N = sizeof(T) / 2;
+    uint4 u[N];
+#pragma unroll
+    for (int m = 0; m < N; ++m) u[m] = in ? reinterpret_cast<const uint4*>(p)[m] : make_uint4(0u, 0u, 0u, 0u);
+    typename Frag<T>::V r;
+    __builtin_memcpy(&r, u, sizeof(r));
+    return r;
+}
+
+__device__ __forceinline__ float swap_max(float v) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float swap_sum(float v) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+__device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }   // 1 ulp, no range fix-up
+
+// keys (rows) per tile that a workgroup stages
+template <class T> constexpr int swa_tile() { return sizeof(T) == 2 ? 64 : 32; }
+
+// Whether rows [i0, i1] see none of the keys [j0, j1], or all of them.
+struct Seen { bool none, all; };
+__device__ __forceinline__ Seen seen(int i0, int i1, int j0, int j1, int window, int sinks) {
+    return Seen{j0 > i1 || (i0 - j1 >= window && j0 >= sinks), j1 <= i0 && (i1 - j0 < window || j1 < sinks)};
+}
+__device__ __forceinline__ bool sees(int i, int j, int window, int sinks) {
+    return j <= i && (i - j < window || j < sinks);
+}
+
+// The key tiles of rows [q0, q1]: first those with sinks, then the window's.
+struct KeyTiles {
+    int sink, first, count;
+    __device__ __forceinline__ KeyTiles(int q0, int q1, int tile, int window, int sinks) {
+        first = max(q0 - window + 1, 0) / tile;
+        sink = min((sinks + tile - 1) / tile, first);
+        count = sink + q1 / tile - first + 1;
+    }
+    __device__ __forceinline__ int operator[](int it) const { return it < sink ? it : first + it - sink; }
+};
+
+// workgroup number -> (block of rows, head): the heads of one block next to
+// each other on one XCD, which keeps the block's keys in its L2; late blocks,
+// which see more keys, first
+__device__ __forceinline__ void work_item(const SwaParams& p, int heads, int& blk, int& head) {
+    const int e = xcd_remap(blockIdx.x, p.blocks * heads);
+    blk = p.blocks - 1 - e / heads;
+    head = e % heads;
+}
+
+// ---------------------------------------------------------------- forward
+
+// NW waves of 32 queries each share the key tiles, staged twice over in LDS
+// (one barrier a tile).
+template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa_fwd_kernel(SwaParams p) {
+    constexpr int KT = swa_tile<T>(), NX = KT / 32, NT = 64 * NW, ST = tile_stride<T>(D), KD = D / 16, MD = D / 32;
+    using V8 = typename Frag<T>::V;
+    extern __shared__ __align__(16) unsigned char smem[];
+    lds_poison((uint32_t)(sizeof(T) * 4 * KT * ST));
+    T* const tiles = reinterpret_cast<T*>(smem);   // [2][k, v][KT][ST]
+
+    const int tid = threadIdx.x, lane = tid % WAVE, w = tid / WAVE, n = lane & 31, h2 = lane >> 5;
+    int blk, h;
+    work_item(p, p.Hq, blk, h);
+    SeqBlock b;
+    if (!seq_block(p.map, 32 * NW, blk, b)) return;
+    const int q0 = b.idx * 32 * NW, len = b.len;
+    const long ts = b.t0 - q0;
+    const int hk = h / p.G;
+    const int i0 = q0 + 32 * w, row = i0 + n;
+    const bool live = row < len;
+    const float c = p.scale * LOG2E;
+
+    V8 qf[KD];
+    {
+        const T* src = static_cast<const T*>(p.q) + ((size_t)(ts + (live ? row : 0)) * p.Hq + h) * D + 8 * h2;
+#pragma unroll
+        for (int ks = 0; ks < KD; ++ks) qf[ks] = load8<T>(src + 16 * ks, live);
+    }
+    const T* K = static_cast<const T*>(p.k) + ((size_t)ts * p.Hkv + hk) * D;
+    const T* V = static_cast<const T*>(p.v) + ((size_t)ts * p.Hkv + hk) * D;
+    const size_t rs = (size_t)p.Hkv * D;
+    const KeyTiles kt(q0, min(q0 + 32 * NW, len) - 1, KT, p.window, p.sinks);
+
+    Stage<T, D, KT, NT> sk, sv;
+    auto fetch = [&](int it) {
+        const int j0 = kt[it] * KT;
+        sk.load(K + (size_t)j0 * rs, rs, len - j0, tid);
+        sv.load(V + (size_t)j0 * rs, rs, len - j0, tid);
+    };
+    auto put = [&](int it) {
+        T* t = tiles + (it & 1) * 2 * KT * ST;
+        sk.store(t, tid);
+        sv.store(t + KT * ST, tid);
+    };
+    f32x16 O[MD];
+#pragma unroll
+    for (int m = 0; m < MD; ++m) O[m] = zero16();
+    float top = -INFINITY, sum = 0.f;   // sum: this lane's half of the keys
+
+    fetch(0);
+    put(0);
+    __syncthreads();
+    for (int it = 0; it < kt.count; ++it) {
+        if (it + 1 < kt.count) fetch(it + 1);
+        const T* tk = tiles + (it & 1) * 2 * KT * ST;
+        const T* tv = tk + KT * ST;
+        const int j0 = kt[it] * KT;
+        const Seen se = seen(i0, i0 + 31, j0, j0 + KT - 1, p.window, p.sinks);
+        if (!se.none && i0 < len) {
+            f32x16 s[NX];
+#pragma unroll
+            for (int x = 0; x < NX; ++x) s[x] = zero16();
+#pragma unroll
+            for (int ks = 0; ks < KD; ++ks)
+#pragma unroll
+                for (int x = 0; x < NX; ++x) s[x] = mma32(nat32<T>(tk, ST, 32 * x, 16 * ks, n, h2), qf[ks], s[x]);
+#pragma unroll
+            for (int x = 0; x < NX; ++x)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[x][r] *= c;
+            if (!se.all) {
+#pragma unroll
+                for (int x = 0; x < NX; ++x)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (!sees(row, j0 + 32 * x + result_row(r, h2), p.window, p.sinks)) s[x][r] = -INFINITY;
+            }
+            float mt = s[0][0];
+#pragma unroll
+            for (int x = 0; x < NX; ++x)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) mt = fmaxf(mt, s[x][r]);
+            mt = swap_max(mt);
+            if (__any(mt > top)) {
+                const float next = fmaxf(top, mt);
+                const float f = next == -INFINITY ? 1.f : fast_exp2(top - next);
+                top = next;
+                sum *= f;
+#pragma unroll
+                for (int m = 0; m < MD; ++m)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) O[m][r] *= f;
+            }
+            const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int x = 0; x < NX; ++x)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    s[x][r] = fast_exp2(s[x][r] - base);
+                    sum += s[x][r];
+                }
+#pragma unroll
+            for (int kb = 0; kb < KT / 16; ++kb) {
+                const V8 pf = rows16<T>(s[kb / 2], kb % 2);
+#pragma unroll
+                for (int m = 0; m < MD; ++m) O[m] = mma32(tr32(tv, ST, 16 * kb, 32 * m, lane), pf, O[m]);
+            }
+        }
+        if (it + 1 < kt.count) {
+            put(it + 1);
+            __syncthreads();
+        }
+    }
+    sum = swap_sum(sum);
+    // An Inf or NaN in v at a key that a tile holds but a row does not see has
+    // entered that row as 0 * v. Rows that are not finite are formed again, one
+    // key at a time, from the keys that they see.
+    float probe = 0.f;
+#pragma unroll
+    for (int m = 0; m < MD; ++m)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) probe += O[m][r] * 0.f;
+    if (__any(live && probe != 0.f)) {
+#pragma unroll
+        for (int m = 0; m < MD; ++m) O[m] = zero16();
+        const T* Q = static_cast<const T*>(p.q) + ((size_t)(ts + (live ? row : 0)) * p.Hq + h) * D;
+        for (int j = 0; j <= min(i0 + 31, len - 1); ++j) {
+            const bool in = live && sees(row, j, p.window, p.sinks);
+            if (!__any(in)) continue;
+            float dot = 0.f;
+            for (int x = 0; x < D; x += 8) {
+                const f32x8 y = widen(load8<T>(Q + x, true)) * widen(load8<T>(K + (size_t)j * rs + x, true));
+                dot += ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
+            }
+            const float e = fast_exp2(dot * c - top);
+            if (!in) continue;
+#pragma unroll
+            for (int m = 0; m < MD; ++m)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) O[m][r] += e * from_el(V[(size_t)j * rs + 32 * m + result_row(r, h2)]);
+        }
+    }
+    const float inv = 1.f / sum;
+    if (live) {
+        T* out = static_cast<T*>(p.out) + ((size_t)(ts + row) * p.Hq + h) * D + 4 * h2;
+#pragma unroll
+        for (int m = 0; m < MD; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                store4(out + 32 * m + 8 * r, f32x4{O[m][4 * r], O[m][4 * r + 1], O[m][4 * r + 2], O[m][4 * r + 3]} * inv);
+        if (p.lse_out && h2 == 0) p.lse_out[(size_t)(ts + row) * p.Hq + h] = (top + log2f(sum)) * LN2;
+    }
+}
+
+// ---------------------------------------------------------------- gradient with respect to q
+
+// As the forward, with dP^T = V dO^T and dS = P (dP - delta), delta_i = dO_i .
+// o_i (formed here and kept for the other gradients): dq^T = K^T dS^T.
+template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa_dq_kernel(SwaParams p) {
+    constexpr int KT = swa_tile<T>(), NT = 64 * NW, ST = tile_stride<T>(D), KD = D / 16, MD = D / 32;
+    using V8 = typename Frag<T>::V;
+    extern __shared__ __align__(16) unsigned char smem[];
+    lds_poison((uint32_t)(sizeof(T) * 4 * KT * ST));
+    T* const tiles = reinterpret_cast<T*>(smem);
+
+    const int tid = threadIdx.x, lane = tid % WAVE, w = tid / WAVE, n = lane & 31, h2 = lane >> 5;
+    int blk, h;
+    work_item(p, p.Hq, blk, h);
+    SeqBlock b;
+    if (!seq_block(p.map, 32 * NW, blk, b)) return;
+    const int q0 = b.idx * 32 * NW, len = b.len;
+    const long ts = b.t0 - q0;
+    const int hk = h / p.G;
+    const int i0 = q0 + 32 * w, row = i0 + n;
+    const bool live = row < len;
+    const float c = p.scale * LOG2E;
+
+    V8 qf[KD], gf[KD];
+    float delta = 0.f, lse2 = 0.f;
+    {
+        const size_t r0 = (size_t)(ts + (live ? row : 0)) * p.Hq + h;
+        const T* sq = static_cast<const T*>(p.q) + r0 * D + 8 * h2;
+        const T* sg = static_cast<const T*>(p.dO) + r0 * D + 8 * h2;
+        const T* so = static_cast<const T*>(p.o) + r0 * D + 8 * h2;
+#pragma unroll
+        for (int ks = 0; ks < KD; ++ks) {
+            qf[ks] = load8<T>(sq + 16 * ks, live);
+            gf[ks] = load8<T>(sg + 16 * ks, live);
+            const f32x8 x = widen(gf[ks]) * widen(load8<T>(so + 16 * ks, live));
+            delta += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+        }
+        delta = swap_sum(delta);
+        if (live) {
+            lse2 = p.lse[r0] * LOG2E;
+            if (h2 == 0) p.delta[r0] = delta;
+        }
+    }
+    const T* K = static_cast<const T*>(p.k) + ((size_t)ts * p.Hkv + hk) * D;
+    const T* V = static_cast<const T*>(p.v) + ((size_t)ts * p.Hkv + hk) * D;
+    const size_t rs = (size_t)p.Hkv * D;
+    const KeyTiles kt(q0, min(q0 + 32 * NW, len) - 1, KT, p.window, p.sinks);
+
+    Stage<T, D, KT, NT> sk, sv;
+    auto fetch = [&](int it) {
+        const int j0 = kt[it] * KT;
+        sk.load(K + (size_t)j0 * rs, rs, len - j0, tid);
+        sv.load(V + (size_t)j0 * rs, rs, len - j0, tid);
+    };
+    auto put = [&](int it) {
+        T* t = tiles + (it & 1) * 2 * KT * ST;
+        sk.store(t, tid);
+        sv.store(t + KT * ST, tid);
+    };
+    f32x16 A[MD];
+#pragma unroll
+    for (int m = 0; m < MD; ++m) A[m] = zero16();
+    fetch(0);
+    put(0);
+    __syncthreads();
+    for (int it = 0; it < kt.count; ++it) {
+        if (it + 1 < kt.count) fetch(it + 1);
+        const T* tk = tiles + (it & 1) * 2 * KT * ST;
+        const T* tv = tk + KT * ST;
+        if (i0 < len) {
+#pragma unroll
+            for (int x = 0; x < KT / 32; ++x) {
+                const int j0 = kt[it] * KT + 32 * x;
+                const Seen se = seen(i0, i0 + 31, j0, j0 + 31, p.window, p.sinks);
+                if (se.none) continue;
+                f32x16 s = zero16(), d = zero16();
+#pragma unroll
+                for (int ks = 0; ks < KD; ++ks) {
+                    s = mma32(nat32<T>(tk, ST, 32 * x, 16 * ks, n, h2), qf[ks], s);
+                    d = mma32(nat32<T>(tv, ST, 32 * x, 16 * ks, n, h2), gf[ks], d);
+                }
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const bool in = se.all || sees(row, j0 + result_row(r, h2), p.window, p.sinks);
+                    s[r] = in ? fast_exp2(s[r] * c - lse2) * (d[r] - delta) : 0.f;
+                }
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    const V8 df = rows16<T>(s, kb);
+#pragma unroll
+                    for (int m = 0; m < MD; ++m) A[m] = mma32(tr32(tk, ST, 32 * x + 16 * kb, 32 * m, lane), df, A[m]);
+                }
+            }
+        }
+        if (it + 1 < kt.count) {
+            put(it + 1);
+            __syncthreads();
+        }
+    }
+    if (live) {
+        T* out = static_cast<T*>(p.dq) + ((size_t)(ts + row) * p.Hq + h) * D + 4 * h2;
+#pragma unroll
+        for (int m = 0; m < MD; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                store4(out + 32 * m + 8 * r, f32x4{A[m][4 * r], A[m][4 * r + 1], A[m][4 * r + 2], A[m][4 * r + 3]} * p.scale);
+    }
+}
+
+// ---------------------------------------------------------------- gradients with respect to k and v
+
+// A workgroup owns KB keys of one kv head (32 a wave, k and v in registers)
+// and walks the rows that see them, over every query head of the group:
+// P [rows][keys] with a lane owning a key; dv^T += dO^T P, dk^T += Q^T dS.
+// The rows of a block with sinks reach to the end of the sequence: they are cut
+// into parts of their own workgroups, summed afterwards in a fixed order.
+template <class T> constexpr int swa_key_block() { return 128; }
+
+template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW, 1) swa_dkv_kernel(SwaParams p) {
+    constexpr int RT = swa_tile<T>(), NT = 64 * NW, KB = 32 * NW, ST = tile_stride<T>(D), KD = D / 16, MD = D / 32;
+    using V8 = typename Frag<T>::V;
+    extern __shared__ __align__(16) unsigned char smem[];
+    lds_poison((uint32_t)(sizeof(T) * 4 * RT * ST + 4 * 4 * RT));
+    T* const tiles = reinterpret_cast<T*>(smem);                                   // [2][q, dO][RT][ST]
+    float* const stats = reinterpret_cast<float*>(smem + sizeof(T) * 4 * RT * ST);   // [2][lse, delta][RT]
+
+    const int tid = threadIdx.x, lane = tid % WAVE, w = tid / WAVE, n = lane & 31, h2 = lane >> 5;
+    const int hk = blockIdx.y;
+    SeqBlock b;
+    int part = 0;
+    if ((int)blockIdx.x < p.blocks) {
+        if (!seq_block(p.map, KB, blockIdx.x, b)) return;
+    } else {   // parts 1.. of the blocks with sinks, of every sequence
+        const int e = blockIdx.x - p.blocks;
+        part = 1 + e % p.splits;
+        const int kb = (e / p.splits) % p.sink_blocks, s = e / p.splits / p.sink_blocks;
+        if (p.map.cu) {
+            const int c0 = seq_offset(p.map, s);
+            b.t0 = c0;
+            b.len = max(seq_offset(p.map, s + 1) - c0, 0);
+        } else {
+            b.t0 = (long)s * p.map.T;
+            b.len = p.map.T;
+        }
+        b.seq = s;
+        b.idx = kb;
+        b.t0 += (long)kb * KB;
+        b.n = min(KB, b.len - kb * KB);
+        if (b.n <= 0) return;
+    }
+    const int k0 = b.idx * KB, len = b.len;
+    const long ts = b.t0 - k0;
+    const bool cut = p.splits > 0 && b.idx < p.sink_blocks;
+    // rows of this workgroup: the window's, or the rest of the sequence in parts
+    const long reach = k0 < p.sinks && !cut ? (long)len : min((long)k0 + KB - 1 + p.window, (long)len);
+    int ra = k0, rb = (int)reach;
+    if (part > 0) {
+        const long a = reach + (long)(part - 1) * p.split_rows;
+        ra = (int)min(a, (long)len);
+        rb = part == p.splits ? len : (int)min(a + p.split_rows, (long)len);
+    }
+    const int key = k0 + 32 * w + n;
+    const bool live = key < len;
+    const float c = p.scale * LOG2E;
+
+    V8 kf[KD], vf[KD];
+    {
+        const size_t r0 = ((size_t)(ts + (live ? key : 0)) * p.Hkv + hk) * D + 8 * h2;
+#pragma unroll
+        for (int ks = 0; ks < KD; ++ks) {
+            kf[ks] = load8<T>(static_cast<const T*>(p.k) + r0 + 16 * ks, live);
+            vf[ks] = load8<T>(static_cast<const T*>(p.v) + r0 + 16 * ks, live);
+        }
+    }
+    f32x16 dK[MD], dV[MD];
+#pragma unroll
+    for (int m = 0; m < MD; ++m) dK[m] = dV[m] = zero16();
+
+    const int t0 = ra / RT, per = rb > ra ? (rb - 1) / RT - t0 + 1 : 0, count = per * p.G;
+    const size_t rs = (size_t)p.Hq * D;
+    Stage<T, D, RT, NT> sq, sg;
+    float stat = 0.f;
+    auto fetch = [&](int it) {
+        const int h = hk * p.G + it / per, r0 = (t0 + it % per) * RT;
+        const size_t at = (size_t)(ts + r0) * p.Hq + h;
+        sq.load(static_cast<const T*>(p.q) + at * D, rs, rb - r0, tid);
+        sg.load(static_cast<const T*>(p.dO) + at * D, rs, rb - r0, tid);
+        if (tid < 2 * RT) {
+            const int r = tid % RT;
+            const float* src = tid < RT ? p.lse : p.delta;
+            stat = r0 + r < rb ? src[at + (size_t)r * p.Hq] * (tid < RT ? LOG2E : 1.f) : 0.f;
+        }
+    };
+    auto put = [&](int it) {
+        T* t = tiles + (it & 1) * 2 * RT * ST;
+        sq.store(t, tid);
+        sg.store(t + RT * ST, tid);
+        if (tid < 2 * RT) stats[(it & 1) * 2 * RT + tid] = stat;
+    };
+    if (count) {
+        fetch(0);
+        put(0);
+        __syncthreads();
+    }
+    for (int it = 0; it < count; ++it) {
+        if (it + 1 < count) fetch(it + 1);
+        const T* tq = tiles + (it & 1) * 2 * RT * ST;
+        const T* tg = tq + RT * ST;
+        const float* sl = stats + (it & 1) * 2 * RT;
+        const float* sd = sl + RT;
+#pragma unroll
+        for (int x = 0; x < RT / 32; ++x) {
+            const int i0 = (t0 + it % per) * RT + 32 * x, j0 = k0 + 32 * w;
+            const Seen se = seen(i0, i0 + 31, j0, j0 + 31, p.window, p.sinks);
+            if (se.none || i0 + 31 < ra || i0 >= rb) continue;
+            const bool all = se.all && i0 >= ra;
+            f32x16 s = zero16(), d = zero16();
+#pragma unroll
+            for (int ks = 0; ks < KD; ++ks) {
+                s = mma32(nat32<T>(tq, ST, 32 * x, 16 * ks, n, h2), kf[ks], s);
+                d = mma32(nat32<T>(tg, ST, 32 * x, 16 * ks, n, h2), vf[ks], d);
+            }
+#pragma unroll
+            for (int r4 = 0; r4 < 4; ++r4) {
+                const f32x4 l4 = *reinterpret_cast<const f32x4*>(sl + 32 * x + 8 * r4 + 4 * h2);
+                const f32x4 d4 = *reinterpret_cast<const f32x4*>(sd + 32 * x + 8 * r4 + 4 * h2);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int r = 4 * r4 + m, i = i0 + 8 * r4 + 4 * h2 + m;
+                    const bool in = all || (i >= ra && sees(i, key, p.window, p.sinks));
+                    const float e = in ? fast_exp2(s[r] * c - l4[m]) : 0.f;
+                    d[r] = in ? e * (d[r] - d4[m]) : 0.f;
+                    s[r] = e;
+                }
+            }
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                const V8 pf = rows16<T>(s, kb), df = rows16<T>(d, kb);
+#pragma unroll
+                for (int m = 0; m < MD; ++m) {
+                    dV[m] = mma32(tr32(tg, ST, 32 * x + 16 * kb, 32 * m, lane), pf, dV[m]);
+                    dK[m] = mma32(tr32(tq, ST, 32 * x + 16 * kb, 32 * m, lane), df, dK[m]);
+                }
+            }
+        }
+        if (it + 1 < count) {
+            put(it + 1);
+            __syncthreads();
+        }
+    }
+    if (cut) {
+        float* dst = p.part + ((((size_t)b.seq * p.Hkv + hk) * p.sink_blocks + b.idx) * (1 + p.splits) + part) * (2 * KB * D) +
+                     (size_t)(32 * w + n) * D + 4 * h2;
+#pragma unroll
+        for (int m = 0; m < MD; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                *reinterpret_cast<f32x4*>(dst + 32 * m + 8 * r) =
+                    f32x4{dK[m][4 * r], dK[m][4 * r + 1], dK[m][4 * r + 2], dK[m][4 * r + 3]};
+                *reinterpret_cast<f32x4*>(dst + KB * D + 32 * m + 8 * r) =
+                    f32x4{dV[m][4 * r], dV[m][4 * r + 1], dV[m][4 * r + 2], dV[m][4 * r + 3]};
+            }
+    } else if (live) {
+        const size_t to = ((size_t)(ts + key) * p.Hkv + hk) * D + 4 * h2;
+#pragma unroll
+        for (int m = 0; m < MD; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                store4(static_cast<T*>(p.dk) + to + 32 * m + 8 * r,
+                       f32x4{dK[m][4 * r], dK[m][4 * r + 1], dK[m][4 * r + 2], dK[m][4 * r + 3]} * p.scale);
+                store4(static_cast<T*>(p.dv) + to + 32 * m + 8 * r,
+                       f32x4{dV[m][4 * r], dV[m][4 * r + 1], dV[m][4 * r + 2], dV[m][4 * r + 3]});
+            }
+    }
+}
+
+// the parts of the blocks with sinks, summed in order
+template <class T, int D> __global__ void __launch_bounds__(256) swa_sink_sum_kernel(SwaParams p) {
+    constexpr int KB = 128;
+    lds_poison(0);
+    const int kb = blockIdx.x % p.sink_blocks, hk = blockIdx.y, s = blockIdx.x / p.sink_blocks;
+    int len;
+    long ts;
+    if (p.map.cu) {
+        const int c0 = seq_offset(p.map, s);
+        ts = c0;
+        len = max(seq_offset(p.map, s + 1) - c0, 0);
+    } else {
+        ts = (long)s * p.map.T;
+        len = p.map.T;
+    }
+    const int e = 4 * (blockIdx.z * 256 + threadIdx.x);
+    const int key = kb * KB + e / D;
+    if (e >= KB * D || key >= len) return;
+    const float* src = p.part + (((size_t)s * p.Hkv + hk) * p.sink_blocks + kb) * (1 + p.splits) * (size_t)(2 * KB * D) + e;
+    f32x4 a = zero4(), c = zero4();
+    for (int m = 0; m <= p.splits; ++m) {
+        a += *reinterpret_cast<const f32x4*>(src + (size_t)m * (2 * KB * D));
+        c += *reinterpret_cast<const f32x4*>(src + (size_t)m * (2 * KB * D) + KB * D);
+    }
+    const size_t to = ((size_t)(ts + key) * p.Hkv + hk) * D + e % D;
+    store4(static_cast<T*>(p.dk) + to, a * p.scale);
+    store4(static_cast<T*>(p.dv) + to, c);
+}
+
+// ---------------------------------------------------------------- one token over a cache
+
+struct SwaDecodeParams {
+    const void *q, *k, *v;
+    void *Kc, *Vc, *o;
+    const int32_t* pos;
+    float *pm, *pl, *po;   // parts: running maximum (log2), sum, unnormalised o: [N * Hq][splits](, [D])
+    int N, Hq, Hkv, G, GC;   // GC: workgroups over a group's heads, 32 each
+    int window, sinks, slots, splits, per;   // per: slots of a part
+    float scale;
+};
+
+// One part of a cache for one kv head: each wave takes every NW-th tile of 32
+// slots through LDS of its own (no barrier), the group's query heads side by
+// side as the columns. The new token's row is read from k and v, and written to
+// its slot by the workgroup whose part holds it.
+template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa_decode_kernel(SwaDecodeParams p) {
+    constexpr int ST = tile_stride<T>(D), KD = D / 16, MD = D / 32, CPR = D * (int)sizeof(T) / 16, PER = 16 / (int)sizeof(T),
+                  RN = 32 * CPR / 64;
+    using V8 = typename Frag<T>::V;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const uint32_t lds = sizeof(T) * NW * 2 * 32 * ST;
+    lds_poison(lds);
+    const int tid = threadIdx.x, lane = tid % WAVE, w = tid / WAVE, n = lane & 31, h2 = lane >> 5;
+    T* const tk = reinterpret_cast<T*>(smem) + w * 2 * 32 * ST;
+    T* const tv = tk + 32 * ST;
+    const int part = blockIdx.x % p.splits, gc = blockIdx.x / p.splits, hk = blockIdx.y, seq = blockIdx.z;
+    const int g0 = 32 * gc, gn = min(32, p.G - g0);
+    const size_t head0 = (size_t)seq * p.Hq + hk * p.G + g0;
+    const int pos = p.pos[seq];
+    const int held = pos < 0 ? 0 : (int)min((long)pos + 1, (long)p.slots);
+    const int slot = pos < 0 ? -1 : pos < p.sinks ? pos : p.sinks + (pos - p.sinks) % p.window;
+    const int a = part * p.per, e = min(a + p.per, held);
+    const T* newk = static_cast<const T*>(p.k) + ((size_t)seq * p.Hkv + hk) * D;
+    const T* newv = static_cast<const T*>(p.v) + ((size_t)seq * p.Hkv + hk) * D;
+    T* Kc = static_cast<T*>(p.Kc) + ((size_t)seq * p.slots * p.Hkv + hk) * D;
+    T* Vc = static_cast<T*>(p.Vc) + ((size_t)seq * p.slots * p.Hkv + hk) * D;
+    const size_t rs = (size_t)p.Hkv * D;
+    if (gc == 0 && slot >= a && slot < e && tid < 2 * CPR) {
+        const bool isv = tid >= CPR;
+        const int x = (tid - (isv ? CPR : 0)) * PER;
+        *reinterpret_cast<uint4*>((isv ? Vc : Kc) + (size_t)slot * rs + x) =
+            *reinterpret_cast<const uint4*>((isv ? newv : newk) + x);
+    }
+    uint4 rk[RN], rv[RN];
+    auto fetch = [&](int j0) {
+#pragma unroll
+        for (int m = 0; m < RN; ++m) {
+            const int x = lane + 64 * m, j = j0 + x / CPR, col = x % CPR * PER;
+            rk[m] = rv[m] = make_uint4(0u, 0u, 0u, 0u);
+            if (j < e) {
+                rk[m] = *reinterpret_cast<const uint4*>((j == slot ? newk : Kc + (size_t)j * rs) + col);
+                rv[m] = *reinterpret_cast<const uint4*>((j == slot ? newv : Vc + (size_t)j * rs) + col);
+            }
+        }
+    };
+    V8 qf[KD];
+#pragma unroll
+    for (int ks = 0; ks < KD; ++ks)
+        qf[ks] = load8<T>(static_cast<const T*>(p.q) + (head0 + (n < gn ? n : 0)) * D + 16 * ks + 8 * h2, n < gn);
+    f32x16 O[MD];
+#pragma unroll
+    for (int m = 0; m < MD; ++m) O[m] = zero16();
+    float top = -INFINITY, sum = 0.f;
+    const float c = p.scale * LOG2E;
+    int j0 = a + 32 * w;
+    if (j0 < e) fetch(j0);
+    for (; j0 < e; j0 += 32 * NW) {
+        // the tile is this wave's own: its reads of the last one are done, its
+        // writes are in order before the reads below
+#pragma unroll
+        for (int m = 0; m < RN; ++m) {
+            const int x = lane + 64 * m;
+            *reinterpret_cast<uint4*>(tk + x / CPR * ST + x % CPR * PER) = rk[m];
+            *reinterpret_cast<uint4*>(tv + x / CPR * ST + x % CPR * PER) = rv[m];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (j0 + 32 * NW < e) fetch(j0 + 32 * NW);
+        f32x16 s = zero16();
+#pragma unroll
+        for (int ks = 0; ks < KD; ++ks) s = mma32(nat32<T>(tk, ST, 0, 16 * ks, n, h2), qf[ks], s);
+        float mt = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            s[r] = j0 + result_row(r, h2) < e ? s[r] * c : -INFINITY;
+            mt = fmaxf(mt, s[r]);
+        }
+        mt = swap_max(mt);
+        const float next = fmaxf(top, mt);
+        const float base = next == -INFINITY ? 0.f : next;
+        const float f = fast_exp2(top - base);
+        top = next;
+        sum *= f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            s[r] = fast_exp2(s[r] - base);
+            sum += s[r];
+        }
+#pragma unroll
+        for (int m = 0; m < MD; ++m)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) O[m][r] *= f;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            const V8 pf = rows16<T>(s, kb);
+#pragma unroll
+            for (int m = 0; m < MD; ++m) O[m] = mma32(tr32(tv, ST, 16 * kb, 32 * m, lane), pf, O[m]);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+    sum = swap_sum(sum);
+    // the waves' shares, joined through LDS: o in the tiles' place, [wave][head][D]
+    __shared__ float s_top[NW][32], s_sum[NW][32];
+    __syncthreads();
+    float* so = reinterpret_cast<float*>(smem);
+    if (h2 == 0) {
+        s_top[w][n] = top;
+        s_sum[w][n] = sum;
+    }
+    if (n < gn) {
+#pragma unroll
+        for (int m = 0; m < MD; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                *reinterpret_cast<f32x4*>(so + (size_t)(w * 32 + n) * D + 32 * m + 8 * r + 4 * h2) =
+                    f32x4{O[m][4 * r], O[m][4 * r + 1], O[m][4 * r + 2], O[m][4 * r + 3]};
+    }
+    __syncthreads();
+    for (int x = tid; x < gn * (D / 4); x += 64 * NW) {
+        const int g = x / (D / 4), d = x % (D / 4) * 4;
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int y = 0; y < NW; ++y) m = fmaxf(m, s_top[y][g]);
+        const float base = m == -INFINITY ? 0.f : m;
+        f32x4 acc = zero4();
+#pragma unroll
+        for (int y = 0; y < NW; ++y) {
+            const float f = fast_exp2(s_top[y][g] - base);
+            l += f * s_sum[y][g];
+            acc += *reinterpret_cast<const f32x4*>(so + (size_t)(y * 32 + g) * D + d) * f;
+        }
+        const size_t at = head0 + g;
+        if (p.splits == 1) {
+            store4(static_cast<T*>(p.o) + at * D + d, pos < 0 ? zero4() : acc * (1.f / l));
+        } else {
+            *reinterpret_cast<f32x4*>(p.po + (at * p.splits + part) * D + d) = acc;
+            if (d == 0) {
+                p.pm[at * p.splits + part] = m;
+                p.pl[at * p.splits + part] = l;
+            }
+        }
+    }
+}
+
+// joins the parts of one query head; four values a thread
+template <class T, int D> __global__ void __launch_bounds__(64) swa_join_kernel(SwaDecodeParams p) {
+    lds_poison(0);
+    const size_t at = (size_t)blockIdx.x * (64 / (D / 4)) + threadIdx.x / (D / 4);
+    if (at >= (size_t)p.N * p.Hq) return;
+    const int d = threadIdx.x % (D / 4) * 4;
+    float m = -INFINITY, l = 0.f;
+    for (int y = 0; y < p.splits; ++y) m = fmaxf(m, p.pm[at * p.splits + y]);
+    const float base = m == -INFINITY ? 0.f : m;
+    f32x4 acc = zero4();
+    for (int y = 0; y < p.splits; ++y) {
+        const float f = fast_exp2(p.pm[at * p.splits + y] - base);
+        l += f * p.pl[at * p.splits + y];
+        acc += *reinterpret_cast<const f32x4*>(p.po + (at * p.splits + y) * D + d) * f;
+    }
+    store4(static_cast<T*>(p.o) + at * D + d, p.pos[at / p.Hq] < 0 ? zero4() : acc * (1.f / l));
+}
+
+// ---------------------------------------------------------------- a prompt's keys into a cache
+
+// slot -> the newest position that belongs there; slots that no position of the
+// sequence belongs to stay as they are
+__global__ void __launch_bounds__(256) swa_fill_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
+                                                       uint4* __restrict__ Kc, uint4* __restrict__ Vc, SeqMap map,
+                                                       int window, int sinks, int slots, int row16) {
+    lds_poison(0);
+    const int seq = blockIdx.z, slot = blockIdx.x;
+    long t0;
+    int len;
+    if (map.cu) {
+        t0 = seq_offset(map, seq);
+        len = max(seq_offset(map, seq + 1) - (int)t0, 0);
+    } else {
+        t0 = (long)seq * map.T;
+        len = map.T;
+    }
+    int j = slot;
+    if (slot >= sinks) {
+        const int first = slot - sinks, most = len - 1 - sinks;   // offsets from the first position of the ring
+        if (most < first) return;
+        j = sinks + first + (most - first) / window * window;
+    }
+    if (j >= len) return;
+    const size_t from = (size_t)(t0 + j) * row16, to = ((size_t)seq * slots + slot) * row16;
+    for (int x = threadIdx.x; x < row16; x += 256) {
+        Kc[to + x] = k[from + x];
+        Vc[to + x] = v[from + x];
+    }
+}
+
+template <class K, class P> hipError_t launch(K kern, dim3 grid, int threads, size_t lds, hipStream_t st, const P& p) {
+    if (lds > 65536) {
+        const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(kern, grid, dim3(threads), lds, st, p);
+    return hipGetLastError();
+}
+
+size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+constexpr int KEY_BLOCK = 128;
+
+// Parts of the rows beyond the window that see a block with sinks. About as
+// many rows a part as the window gives a block, at most 64 parts in all blocks
+// of a sequence; none where the window covers everything anyway.
+void sink_parts(int T, int window, int sinks, int& blocks, int& splits, int& rows) {
+    blocks = splits = rows = 0;
+    if (sinks <= 0 || T <= window + KEY_BLOCK) return;
+    blocks = (int)((std::min((long)sinks, (long)T) + KEY_BLOCK - 1) / KEY_BLOCK);
+    rows = ((window + KEY_BLOCK) + 63) / 64 * 64;
+    const int most = 64 / blocks, want = (T - 1) / rows + 1;
+    splits = std::min(want, most);
+    if (splits == 0) {
+        blocks = 0;
+        return;
+    }
+    if (want > most) rows = ((T + splits - 1) / splits + 63) / 64 * 64;
+}
+
+SwaParams make_params(const SwaArgs& a, int rows) {
+    SwaParams p{};
+    p.q = a.q; p.k = a.k; p.v = a.v; p.o = a.o; p.dO = a.dO; p.lse = a.lse;
+    p.out = a.out; p.lse_out = a.lse_out;
+    p.dq = a.g_q; p.dk = a.g_k; p.dv = a.g_v;
+    p.map = SeqMap{a.cu_seqlens, a.T, a.N};
+    p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = a.Hq / a.Hkv;
+    p.window = std::min(a.window, a.T);
+    p.sinks = std::min(a.sinks, a.T);
+    p.scale = a.scale;
+    p.blocks = (int)seq_blocks_bound(a.T, a.N, rows, a.cu_seqlens != nullptr);
+    return p;
+}
+
+template <class T, int D> hipError_t forward(const SwaArgs& a) {
+    constexpr int NW = 4;
+    const SwaParams p = make_params(a, 32 * NW);
+    return launch(swa_fwd_kernel<T, D, NW>, dim3(p.blocks * p.Hq), 64 * NW,
+                  sizeof(T) * 4 * swa_tile<T>() * tile_stride<T>(D), a.stream, p);
+}
+
+template <class T, int D> hipError_t backward(const SwaArgs& a) {
+    constexpr int NW = 4;
+    SwaParams p = make_params(a, 32 * NW);
+    char* ws = static_cast<char*>(a.workspace);
+    p.delta = reinterpret_cast<float*>(ws);
+    p.part = reinterpret_cast<float*>(ws + al256((size_t)a.N * a.T * a.Hq * 4));
+    sink_parts(a.T, p.window, p.sinks, p.sink_blocks, p.splits, p.split_rows);
+    const size_t lds = sizeof(T) * 4 * swa_tile<T>() * tile_stride<T>(D);
+    hipError_t e = launch(swa_dq_kernel<T, D, NW>, dim3(p.blocks * p.Hq), 64 * NW, lds, a.stream, p);
+    if (e != hipSuccess) return e;
+    e = launch(swa_dkv_kernel<T, D, NW>, dim3(p.blocks + a.N * p.sink_blocks * p.splits, p.Hkv), 64 * NW,
+               lds + 16 * swa_tile<T>(), a.stream, p);
+    if (e != hipSuccess || p.splits == 0) return e;
+    return launch(swa_sink_sum_kernel<T, D>, dim3(a.N * p.sink_blocks, p.Hkv, (KEY_BLOCK * D / 4 + 255) / 256), 256, 0,
+                  a.stream, p);
+}
+
+// Parts of a cache: until two workgroups per CU, each of at least 128 slots.
+int decode_splits(int N, int Hkv, int gc, int slots) {
+    const long wgs = (long)N * Hkv * gc;
+    return (int)std::max(1L, std::min((512 + wgs - 1) / wgs, (long)(slots + 127) / 128));
+}
+
+template <class T, int D> hipError_t decode(const SwaDecodeArgs& a) {
+    constexpr int NW = 4;
+    SwaDecodeParams p{};
+    p.q = a.q; p.k = a.k; p.v = a.v; p.Kc = a.Kc; p.Vc = a.Vc; p.o = a.o; p.pos = a.pos;
+    p.N = a.N; p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = a.Hq / a.Hkv;
+    p.GC = (p.G + 31) / 32;
+    p.window = a.window; p.sinks = a.sinks; p.slots = a.window + a.sinks;
+    p.scale = a.scale;
+    p.splits = decode_splits(a.N, a.Hkv, p.GC, p.slots);
+    p.per = ((p.slots + p.splits - 1) / p.splits + 31) / 32 * 32;
+    const size_t heads = (size_t)a.N * a.Hq;
+    p.pm = static_cast<float*>(a.workspace);
+    p.pl = p.pm + heads * p.splits;
+    p.po = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + al256(heads * p.splits * 8));
+    const size_t tiles = sizeof(T) * NW * 2 * 32 * tile_stride<T>(D), join = sizeof(float) * NW * 32 * D;
+    hipError_t e = launch(swa_decode_kernel<T, D, NW>, dim3(p.splits * p.GC, p.Hkv, p.N), 64 * NW, std::max(tiles, join),
+                          a.stream, p);
+    if (e != hipSuccess || p.splits == 1) return e;
+    constexpr int HB = 64 / (D / 4);
+    return launch(swa_join_kernel<T, D>, dim3((unsigned)((heads + HB - 1) / HB)), 64, 0, a.stream, p);
+}
+
+#define KDA_SWA_DIM(d, D, ...)                                         \
+    [&] {                                                              \
+        switch (d) {                                                   \
+            case 32: { constexpr int D = 32; return __VA_ARGS__(); }   \
+            case 64: { constexpr int D = 64; return __VA_ARGS__(); }   \
+            default: { constexpr int D = 128; return __VA_ARGS__(); }  \
+        }                                                              \
+    }()
+
+}  // namespace
+
+size_t swa_bwd_workspace_bytes(int T, int N, int Hq, int Hkv, int d, int window, int sinks) {
+    int blocks, splits, rows;
+    sink_parts(T, std::min(window, T), std::min(sinks, T), blocks, splits, rows);
+    const size_t n = al256((size_t)N * T * Hq * 4) +
+                     (splits ? (size_t)N * Hkv * blocks * (1 + splits) * 2 * KEY_BLOCK * d * 4 : 0);
+    return n ? n : 256;
+}
+
+size_t swa_decode_workspace_bytes(int N, int Hq, int Hkv, int d, int window, int sinks) {
+    const size_t parts = (size_t)N * Hq * decode_splits(N, Hkv, (Hq / Hkv + 31) / 32, window + sinks);
+    return al256(parts * 8) + parts * d * 4;
+}
+
+hipError_t launch_swa_fwd(const SwaArgs& a) {
+    return KDA_SWA_DIM(a.d, D, [&] { return a.bf16 ? forward<uint16_t, D>(a) : forward<float, D>(a); });
+}
+hipError_t launch_swa_bwd(const SwaArgs& a) {
+    return KDA_SWA_DIM(a.d, D, [&] { return a.bf16 ? backward<uint16_t, D>(a) : backward<float, D>(a); });
+}
+hipError_t launch_swa_decode(const SwaDecodeArgs& a) {
+    return KDA_SWA_DIM(a.d, D, [&] { return a.bf16 ? decode<uint16_t, D>(a) : decode<float, D>(a); });
+}
+
+hipError_t launch_swa_cache_fill(const SwaFillArgs& a) {
+    const int row16 = (int)((size_t)a.Hkv * a.d * (a.bf16 ? 2 : 4) / 16), slots = a.window + a.sinks;
+    hipLaunchKernelGGL(swa_fill_kernel, dim3(slots, 1, a.N), dim3(256), 0, a.stream, (const uint4*)a.k,
+                       (const uint4*)a.v, (uint4*)a.Kc, (uint4*)a.Vc, SeqMap{a.cu_seqlens, a.T, a.N}, a.window, a.sinks,
+                       slots, row16);
+    return hipGetLastError();
+}
+
+}  // namespace kda

@@ -31,7 +31,8 @@ EXPORTS = ("kda_chunk_fwd", "kda_chunk_fwd_stage", "kda_chunk_fwd_workspace_byte
            "kda_version", "kda_chunk_fwd_status", "kda_chunk_fwd_noalloc", "kda_chunk_fwd_ew",
            "kda_decode_step_ew", "kda_chunk_bwd_cw", "kda_chunk_bwd_cw_workspace_bytes", "kda_chunk_bwd_ew",
            "kda_chunk_bwd_ew_workspace_bytes", "kda_linattn_fwd", "kda_linattn_fwd_workspace_bytes", "kda_linattn_bwd",
-           "kda_linattn_bwd_workspace_bytes", "kda_linattn_decode_step")
+           "kda_linattn_bwd_workspace_bytes", "kda_linattn_decode_step", "kda_swa_fwd", "kda_swa_bwd",
+           "kda_swa_bwd_workspace_bytes", "kda_swa_decode_step", "kda_swa_decode_workspace_bytes", "kda_swa_cache_fill")
 
 
 class KDAError(RuntimeError):
@@ -103,6 +104,19 @@ def load(path: str):
     lib.kda_linattn_bwd_workspace_bytes.argtypes = [i] * 8
     lib.kda_linattn_decode_step.restype = i
     lib.kda_linattn_decode_step.argtypes = [vp] * 6 + [i] * 6 + [vp]
+    f = ctypes.c_float
+    lib.kda_swa_fwd.restype = i
+    lib.kda_swa_fwd.argtypes = [vp] * 5 + [i] * 7 + [f, vp, i, i, vp]
+    lib.kda_swa_bwd.restype = i
+    lib.kda_swa_bwd.argtypes = [vp] * 9 + [i] * 7 + [f, vp, i, i, vp, sz, vp]
+    lib.kda_swa_bwd_workspace_bytes.restype = sz
+    lib.kda_swa_bwd_workspace_bytes.argtypes = [i] * 9
+    lib.kda_swa_decode_step.restype = i
+    lib.kda_swa_decode_step.argtypes = [vp] * 7 + [i] * 6 + [f, i, vp, sz, vp]
+    lib.kda_swa_decode_workspace_bytes.restype = sz
+    lib.kda_swa_decode_workspace_bytes.argtypes = [i] * 6
+    lib.kda_swa_cache_fill.restype = i
+    lib.kda_swa_cache_fill.argtypes = [vp] * 4 + [i] * 6 + [vp, i, i, vp]
     lib.kda_chunk_fwd_noalloc.restype = i
     lib.kda_chunk_fwd_noalloc.argtypes = [vp] * 8 + [i] * 6 + [vp, i, i, i, vp]
     return lib
@@ -747,5 +761,151 @@ def linattn_decode_step(q, k, v, gate, S, out: Optional[torch.Tensor] = None, st
         rc = _lib().kda_linattn_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(S), _ptr(out), N, H, dk, dv, dt,
                                             kind, st)
     if rc != KDA_OK:
-        raise KDAError(rc, "kda_linattn_decode_step")
+        raise KDAError(rc, "kda_linattn_decode_step", "kda_swa_fwd", "kda_swa_bwd",
+           "kda_swa_bwd_workspace_bytes", "kda_swa_decode_step", "kda_swa_decode_workspace_bytes", "kda_swa_cache_fill")
     return out
+
+
+# ---------------------------------------------------------------- window attention with sinks
+
+def _check_swa(q, k, v, cu_seqlens, window, sinks, lead):
+    """Shapes, dtypes and devices of a window-attention call whose q has `lead`
+    dims before the heads. Returns (those dims, Hq, Hkv, d)."""
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dim() != lead + 2:
+            raise ValueError("%s must have %d dims, got %s" % (name, lead + 2, tuple(t.shape)))
+    dims, Hq, d = tuple(q.shape[:lead]), q.shape[-2], q.shape[-1]
+    Hkv = k.shape[-2]
+    _check_shape("k", k, dims + (Hkv, d))
+    _check_shape("v", v, dims + (Hkv, d))
+    if Hkv == 0 or Hq % Hkv:
+        raise ValueError("q has %d heads, not a multiple of k's %d" % (Hq, Hkv))
+    for name, t in (("k", k), ("v", v)):
+        if t.dtype != q.dtype:
+            raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, q.dtype))
+    if window < 1 or sinks < 0:
+        raise ValueError("window must be at least 1 and sinks at least 0, got %d and %d" % (window, sinks))
+    if cu_seqlens is not None and dims[0] != 1:
+        raise ValueError("packed sequences (cu_seqlens) need B = 1, got %d" % dims[0])
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _check_dev(name, t, q.device)
+    return dims, Hq, Hkv, d
+
+
+def _int32(x: int) -> int:
+    """A window or a number of sinks as the C interface takes it; beyond 31 bits
+    it covers every sequence anyway."""
+    return min(int(x), 2 ** 31 - 1)
+
+
+def swa_fwd(q, k, v, window: int, sinks: int = 0, scale: Optional[float] = None, cu_seqlens=None,
+            out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, lse_out: bool = True,
+            stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Attention over a sliding window with sinks (kda_swa_fwd): row i sees keys
+    j <= i with i - j < window or j < sinks. q [B,T,Hq,d]; k, v [B,T,Hkv,d], Hq a
+    multiple of Hkv; scale defaults to d ** -0.5; cu_seqlens int32 [N+1] on the
+    device (B must be 1) or None. Returns (o in the inputs' dtype, lse fp32
+    [B,T,Hq] or None)."""
+    (B, T), Hq, Hkv, d = _check_swa(q, k, v, cu_seqlens, window, sinks, 2)
+    device, dt = q.device, _dtype_code(q)
+    varlen, N = _check_varlen(cu_seqlens, B, device)
+    if out is not None:
+        _like("out", out, (B, T, Hq, d), q.dtype, device)
+    if lse is not None:
+        _like("lse", lse, (B, T, Hq), torch.float32, device)
+    with _on(device, stream) as st:
+        if out is None:
+            out = torch.empty((B, T, Hq, d), device=device, dtype=q.dtype)
+        if lse is None and lse_out:
+            lse = torch.empty((B, T, Hq), device=device, dtype=torch.float32)
+        rc = _lib().kda_swa_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, Hkv, T, d, _int32(window),
+                                _int32(sinks), d ** -0.5 if scale is None else float(scale), _ptr(cu_seqlens),
+                                N if varlen else 0, dt, st)
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_swa_fwd")
+    return out, lse
+
+
+def swa_bwd_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, d: int, window: int, sinks: int = 0, N: int = 0,
+                            varlen: bool = False) -> int:
+    return int(_lib().kda_swa_bwd_workspace_bytes(B, Hq, Hkv, T, d, _int32(window), _int32(sinks), N, int(varlen)))
+
+
+def swa_bwd(q, k, v, o, lse, dO, window: int, sinks: int = 0, scale: Optional[float] = None, cu_seqlens=None,
+            out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradient of swa_fwd for L = sum(o * dO) (kda_swa_bwd); o and lse as swa_fwd
+    returned them, dO [B,T,Hq,d]. Returns a dict of dq, dk, dv in the inputs' dtype
+    and layouts. ``out`` may supply that dict's tensors."""
+    (B, T), Hq, Hkv, d = _check_swa(q, k, v, cu_seqlens, window, sinks, 2)
+    device, dt = q.device, _dtype_code(q)
+    _like("o", o, (B, T, Hq, d), q.dtype, device)
+    _like("dO", dO, (B, T, Hq, d), q.dtype, device)
+    _like("lse", lse, (B, T, Hq), torch.float32, device)
+    varlen, N = _check_varlen(cu_seqlens, B, device)
+    shapes = {"dq": (B, T, Hq, d), "dk": (B, T, Hkv, d), "dv": (B, T, Hkv, d)}
+    if out is not None:
+        for name, shape in shapes.items():
+            _like(name, out[name], shape, q.dtype, device)
+    need = swa_bwd_workspace_bytes(B, Hq, Hkv, T, d, window, sinks, N, varlen)
+    with _on(device, stream) as st:
+        if out is None:
+            out = {name: torch.empty(shape, device=device, dtype=q.dtype) for name, shape in shapes.items()}
+        ws = _scratch(workspace, need, device)
+        rc = _lib().kda_swa_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(out["dq"]),
+                                _ptr(out["dk"]), _ptr(out["dv"]), B, Hq, Hkv, T, d, _int32(window), _int32(sinks),
+                                d ** -0.5 if scale is None else float(scale), _ptr(cu_seqlens), N if varlen else 0, dt,
+                                _ptr(ws), ws.numel() * ws.element_size(), st)
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_swa_bwd")
+    return out
+
+
+def swa_decode_workspace_bytes(N: int, Hq: int, Hkv: int, d: int, window: int, sinks: int = 0) -> int:
+    return int(_lib().kda_swa_decode_workspace_bytes(N, Hq, Hkv, d, _int32(window), _int32(sinks)))
+
+
+def _check_cache(K_cache, V_cache, N, slots, Hkv, d, dtype, device):
+    for name, t in (("K_cache", K_cache), ("V_cache", V_cache)):
+        _like(name, t, (N, slots, Hkv, d), dtype, device)
+
+
+def swa_decode_step(q, k, v, K_cache, V_cache, pos, window: int, sinks: int = 0, scale: Optional[float] = None,
+                    out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """One token of window attention with sinks (kda_swa_decode_step). q [N,Hq,d];
+    k, v [N,Hkv,d], written to their slot of K_cache, V_cache
+    [N,sinks+window,Hkv,d]; pos int32 [N] on the device, the new token's position,
+    or negative for a sequence to leave out (o zero). Returns o [N,Hq,d]."""
+    (N,), Hq, Hkv, d = _check_swa(q, k, v, None, window, sinks, 1)
+    device, dt = q.device, _dtype_code(q)
+    _check_cache(K_cache, V_cache, N, window + sinks, Hkv, d, q.dtype, device)
+    _like("pos", pos, (N,), torch.int32, device)
+    if out is not None:
+        _like("out", out, (N, Hq, d), q.dtype, device)
+    need = swa_decode_workspace_bytes(N, Hq, Hkv, d, window, sinks)
+    with _on(device, stream) as st:
+        if out is None:
+            out = torch.empty((N, Hq, d), device=device, dtype=q.dtype)
+        ws = _scratch(workspace, need, device)
+        rc = _lib().kda_swa_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(K_cache), _ptr(V_cache), _ptr(pos), _ptr(out), N,
+                                        Hq, Hkv, d, _int32(window), _int32(sinks),
+                                        d ** -0.5 if scale is None else float(scale), dt, _ptr(ws),
+                                        ws.numel() * ws.element_size(), st)
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_swa_decode_step")
+    return out
+
+
+def swa_cache_fill(k, v, K_cache, V_cache, window: int, sinks: int = 0, cu_seqlens=None, stream=None) -> None:
+    """A prompt's k, v [B,T,Hkv,d] (or packed, with cu_seqlens) into the caches
+    [N,sinks+window,Hkv,d] that swa_decode_step continues from
+    (kda_swa_cache_fill); slots without a position are left as they are."""
+    (B, T), _, Hkv, d = _check_swa(k, k, v, cu_seqlens, window, sinks, 2)
+    device, dt = k.device, _dtype_code(k)
+    varlen, N = _check_varlen(cu_seqlens, B, device)
+    _check_cache(K_cache, V_cache, N, window + sinks, Hkv, d, k.dtype, device)
+    with _on(device, stream) as st:
+        rc = _lib().kda_swa_cache_fill(_ptr(k), _ptr(v), _ptr(K_cache), _ptr(V_cache), B, Hkv, T, d, _int32(window),
+                                       _int32(sinks), _ptr(cu_seqlens), N if varlen else 0, dt, st)
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_swa_cache_fill")

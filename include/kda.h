@@ -388,6 +388,71 @@ int kda_linattn_bwd(const void* q, const void* k, const void* v, const void* gat
 int kda_linattn_decode_step(const void* q, const void* k, const void* v, const void* gate, float* S, void* o, int N,
                             int H, int dk, int dv, int dtype, int gate_kind, void* stream);
 
+/*
+ * Softmax attention over a sliding window with sinks, for the local layers of
+ * models that mix them with the recurrences above. Row i of a sequence sees
+ * the keys j <= i with i - j < window, and the first `sinks` keys (j < sinks)
+ * always; window >= 1 counts the row itself, so that no row is empty. A window
+ * of at least the sequence's length is causal attention.
+ *   o_i = sum_j softmax_j(scale q_i . k_j) v_j,  lse_i = log sum_j exp(scale q_i . k_j)
+ *
+ * Layouts: q, o [B, T, Hq, d]; k, v [B, T, Hkv, d] in the input dtype, Hq a
+ * multiple of Hkv (query head h reads kv head h / (Hq / Hkv)); lse [B, T, Hq]
+ * fp32 or NULL; cu_seqlens and N as for kda_chunk_fwd, rows at or behind
+ * cu_seqlens[N] are left as they are. d in {32, 64, 128}; scale finite. o and
+ * the gradients have the input dtype. Sums and softmax statistics are fp32;
+ * bf16 inputs enter the second product with probabilities rounded to bf16.
+ *
+ * A NaN or Inf in k or v of a token that a row does not see does not reach
+ * that row in the forward and the decode step.
+ *
+ * Every pointer 16-byte aligned (lse, cu_seqlens: their element). At most
+ * 65,535 sequences and heads, N * (T + 128) < 2^31 (KDA_ENOTSUP otherwise).
+ * Needs no workspace. Returns KDA_OK or a negative status.
+ */
+int kda_swa_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv, int T, int d,
+                int window, int sinks, float scale, const int32_t* cu_seqlens, int N, int dtype, void* stream);
+
+/*
+ * Gradient of kda_swa_fwd for L = sum <o, dO>: o and lse as the forward left
+ * them, dO [B, T, Hq, d]. grad_q, grad_k, grad_v in the input dtype and
+ * layouts, those of a kv head summed over its query heads; sums run in a fixed
+ * order (repeated calls agree bit for bit). workspace:
+ * kda_swa_bwd_workspace_bytes(...) bytes, required.
+ */
+size_t kda_swa_bwd_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int window, int sinks, int N,
+                                   int has_cu_seqlens);
+int kda_swa_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                void* grad_q, void* grad_k, void* grad_v, int B, int Hq, int Hkv, int T, int d, int window, int sinks,
+                float scale, const int32_t* cu_seqlens, int N, int dtype, void* workspace, size_t workspace_bytes,
+                void* stream);
+
+/*
+ * One token for each of N sequences over caches of constant size: K_cache,
+ * V_cache [N, sinks + window, Hkv, d]. Position p of a sequence has slot p
+ * (p < sinks) or sinks + (p - sinks) % window. pos [N] int32 on the device is
+ * the position of the new token (the number of tokens before it); the call
+ * writes k, v [N, Hkv, d] to its slot and attends q [N, Hq, d] over the slots
+ * held so far, itself included. pos < 0 marks a sequence to leave out (a
+ * padded batch): its cache is not touched, its o [N, Hq, d] is zero. Slots
+ * that hold no token yet are never read. pos is not changed by the call.
+ * workspace: kda_swa_decode_workspace_bytes(...) bytes, required; calls that
+ * may overlap (two streams, two captured graphs) need one each.
+ */
+size_t kda_swa_decode_workspace_bytes(int N, int Hq, int Hkv, int d, int window, int sinks);
+int kda_swa_decode_step(const void* q, const void* k, const void* v, void* K_cache, void* V_cache, const int32_t* pos,
+                        void* o, int N, int Hq, int Hkv, int d, int window, int sinks, float scale, int dtype,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The caches that kda_swa_decode_step continues from after a prompt: k, v
+ * [B, T, Hkv, d] (or packed, as above) to the slots of their positions, the
+ * newest where several share one. Slots without a position are left as they
+ * are. The next token's pos is the sequence's length.
+ */
+int kda_swa_cache_fill(const void* k, const void* v, void* K_cache, void* V_cache, int B, int Hkv, int T, int d,
+                       int window, int sinks, const int32_t* cu_seqlens, int N, int dtype, void* stream);
+
 /* Static text for a status code (never NULL). */
 const char* kda_strerror(int status);
 

@@ -67,12 +67,16 @@ def visible(T, window, sinks, device):
 
 
 def swa(q, k, v, window, sinks, scale, seqs, dO=None):
-    """o, lse [B,T,Hq] and, with dO, the gradient dict of dq, dk, dv."""
+    """o, lse [B,T,Hq] and, with dO, the gradient dict of dq, dk, dv, and for each
+    the root of its terms' summed squares: p dO for dv, p (|dP| + |delta|) k (or
+    q), the terms whose difference they are, for dq and dk, where |dP| and |delta|
+    stand for the same root over the products dO v and dO o that they sum."""
     q, k, v = (x.double() for x in (q, k, v))
     group = q.shape[2] // k.shape[2]
     o = torch.zeros_like(q)
     lse = torch.zeros(q.shape[:3], dtype=torch.float64, device=q.device)
     g = {"dq": torch.zeros_like(q), "dk": torch.zeros_like(k), "dv": torch.zeros_like(v)}
+    size = {n: torch.zeros_like(t) for n, t in g.items()}
     for b, t0, t1 in seqs:
         seen = visible(t1 - t0, window, sinks, q.device)
         for h in range(q.shape[2]):
@@ -87,8 +91,16 @@ def swa(q, k, v, window, sinks, scale, seqs, dO=None):
             lse[b, t0:t1, h] = (m + tot.log())[:, 0]
             if dO is not None:
                 up = dO[b, t0:t1, h].double()
-                ds = p * (torch.mm(up, z.t().contiguous()) - (up * o[b, t0:t1, h]).sum(-1, keepdim=True)) * scale
+                dp, delta = torch.mm(up, z.t().contiguous()), (up * o[b, t0:t1, h]).sum(-1, keepdim=True)
+                ds = p * (dp - delta) * scale
+                parts = torch.mm(up.square(), z.square().t().contiguous()).sqrt()
+                parts = parts + (up * o[b, t0:t1, h]).square().sum(-1, keepdim=True).sqrt()
+                parts = (p * parts * scale).square()
+                size["dq"][b, t0:t1, h] = torch.mm(parts, y.square()).sqrt()
+                size["dk"][b, t0:t1, h // group] += torch.mm(parts.t().contiguous(), x.square())
+                size["dv"][b, t0:t1, h // group] += torch.mm(p.square().t().contiguous(), up.square())
                 g["dq"][b, t0:t1, h] = torch.mm(ds, y)
                 g["dk"][b, t0:t1, h // group] += torch.mm(ds.t().contiguous(), x)
                 g["dv"][b, t0:t1, h // group] += torch.mm(p.t().contiguous(), up)
-    return (o, lse) if dO is None else (o, lse, g)
+    size["dk"], size["dv"] = size["dk"].sqrt(), size["dv"].sqrt()
+    return (o, lse) if dO is None else (o, lse, g, size)
