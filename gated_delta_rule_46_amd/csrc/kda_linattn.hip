@@ -29,8 +29,9 @@
 // Precision. Products of inputs are exact in fp32. bf16 inputs: scores, states
 // and scaled rows enter the next product rounded to bf16, which moves o and the
 // gradients (bf16 themselves) by less than their own rounding; sums into the
-// final states S_T and dS_0, which are fp32, take the scaled rows as a pair of
-// bf16 numbers (16 mantissa bits). fp32 inputs: fp32 MFMA throughout.
+// final states S_T and dS_0, which are fp32, take the scaled rows as three bf16
+// numbers (24 mantissa bits: as exact as an fp32 sum). fp32 inputs: fp32 MFMA
+// throughout.
 #include "kda_launch.h"
 #include "kda_tiles.h"
 
@@ -136,11 +137,23 @@ __device__ __forceinline__ f32x4 tile_decays(const Decays<C>& s, int ti, int tj,
     return d * f;
 }
 
-template <class T> __device__ __forceinline__ float load_decay(const LinParams& p, long t, int h, bool in) {
-    if (!in) return 1.f;
-    return p.head_gate ? static_cast<const float*>(p.gate)[h]
-                       : ld_in(static_cast<const T*>(p.gate) + (size_t)t * p.H + h);
-}
+// A lane's decay as it lies in memory, and its value: apart, so that the load
+// can stay in flight over a block's work. Tokens past `n` have decay 1.
+template <class T> struct DecayLoad {
+    T raw = T(0);
+    float head = 1.f;
+    int n = 0;
+    __device__ __forceinline__ DecayLoad(const LinParams& p, int h) {
+        if (p.head_gate) head = static_cast<const float*>(p.gate)[h];
+    }
+    __device__ __forceinline__ void load(const LinParams& p, long t0, int h, int lane, int tokens) {
+        n = tokens;
+        if (!p.head_gate) raw = static_cast<const T*>(p.gate)[(size_t)(t0 + min(lane, n - 1)) * p.H + h];
+    }
+    __device__ __forceinline__ float value(const LinParams& p, int lane) const {
+        return lane >= n ? 1.f : p.head_gate ? head : from_el(raw);
+    }
+};
 
 // 8 factors at kpos(g, .) from position k0 of an LDS array
 __device__ __forceinline__ f32x8 factors(const float* s, int k0, int g) {
@@ -149,16 +162,26 @@ __device__ __forceinline__ f32x8 factors(const float* s, int k0, int g) {
     return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
+// x as a sum of PARTS operands of the input type, each the rounding of what the
+// ones before leave over
+template <class T, int PARTS> __device__ __forceinline__ void split(typename Frag<T>::V (&part)[PARTS], f32x8 x) {
+#pragma unroll
+    for (int e = 0; e < PARTS; ++e) {
+        part[e] = narrow<T>(x);
+        if (e + 1 < PARTS) x -= widen(part[e]);
+    }
+}
+
 // ---------------------------------------------------------------- state walk
 
 // One segment of one head in one direction: the state's transpose (rows dv,
 // columns dk) in accumulators, dk columns split over the waves.
 //   !STORE: from zero; writes the segment's contribution and its decay.
 //   STORE:  from the boundary state; writes the state before every block.
-template <class T, int DK, int DV, int NW, bool STORE, bool SPLIT>
+template <class T, int DK, int DV, int NW, bool STORE>
 __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
     constexpr int C = lin_block<T>(), NT = 64 * NW, NPW = DK / 16 / NW, MT = DV / 16;
-    constexpr int SX = tile_stride<T>(DV), SY = tile_stride<T>(DK);
+    constexpr int SX = tile_stride<T>(DV), SY = tile_stride<T>(DK), PARTS = sizeof(T) == 4 ? 1 : STORE ? 2 : 3;
     using V8 = typename Frag<T>::V;
     extern __shared__ __align__(16) unsigned char smem[];
     lds_poison((uint32_t)(sizeof(Decays<C>) + sizeof(T) * C * (SX + SY)));
@@ -190,14 +213,15 @@ __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
 
     Stage<T, DV, C, NT> stx;
     Stage<T, DK, C, NT> sty;
-    float a = 1.f, decay = 1.f;
+    DecayLoad<T> a(p, h);
+    float decay = 1.f;
     auto fetch = [&](int step) {
         const int c = rev ? nc - 1 - step : step;
         const long t = b.t0 + (long)c * C;
         const int n = min(C, b.n - c * C);
         stx.load(X + ((size_t)t * p.H + h) * DV, rx, n, tid);
         sty.load(Y + ((size_t)t * p.H + h) * DK, ry, n, tid);
-        if (w == 0) a = load_decay<T>(p, t + lane, h, lane < n);
+        if (w == 0) a.load(p, t, h, lane, n);
     };
     fetch(0);
     for (int step = 0; step < nc; ++step) {
@@ -214,7 +238,7 @@ __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
         if (step) __syncthreads();
         stx.store(sx, tid);
         sty.store(sy, tid);
-        if (w == 0) block_decays<C, false>(dec, a, lane);
+        if (w == 0) block_decays<C, false>(dec, a.value(p, lane), lane);
         __syncthreads();
         if (step + 1 < nc) fetch(step + 1);
         const float tot = dec.total;
@@ -227,22 +251,19 @@ __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
 #pragma unroll
         for (int ks = 0; ks < C / 32; ++ks) {
             const f32x8 fk = factors(f, 32 * ks, g);
-            V8 hi[NPW], lo[NPW];
+            V8 part[NPW][PARTS];
 #pragma unroll
-            for (int x = 0; x < NPW; ++x) {
-                const f32x8 y = widen(frag_tr(sy, SY, 32 * ks, 16 * (w * NPW + x), g, il)) * fk;
-                hi[x] = narrow<T>(y);
-                if constexpr (SPLIT && sizeof(T) == 2) lo[x] = narrow<T>(y - widen(hi[x]));
-            }
+            for (int x = 0; x < NPW; ++x)
+                split<T, PARTS>(part[x], widen(frag_tr(sy, SY, 32 * ks, 16 * (w * NPW + x), g, il)) * fk);
+            V8 xf[MT];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const V8 xf = frag_tr(sx, SX, 32 * ks, 16 * m, g, il);
+            for (int m = 0; m < MT; ++m) xf[m] = frag_tr(sx, SX, 32 * ks, 16 * m, g, il);
 #pragma unroll
-                for (int x = 0; x < NPW; ++x) {
-                    acc[x][m] = mma(xf, hi[x], acc[x][m]);
-                    if constexpr (SPLIT && sizeof(T) == 2) acc[x][m] = mma(xf, lo[x], acc[x][m]);
-                }
-            }
+            for (int e = 0; e < PARTS; ++e)   // no accumulator twice in a row
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int x = 0; x < NPW; ++x) acc[x][m] = mma(xf[m], part[x][e], acc[x][m]);
         }
     }
     if constexpr (!STORE) {
@@ -318,6 +339,7 @@ template <class T, int DK, int DV, int NW, bool WHOLE>
 __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
     constexpr int C = lin_block<T>(), NT = 64 * NW, NPW = DV / 16 / NW, MT = DK / 16, CT = C / 16;
     constexpr int KS = tile_cols<T>(DK) / 32, SK = tile_stride<T>(DK), SV = tile_stride<T>(DV), SP = tile_stride<T>(C);
+    constexpr int PARTS = sizeof(T) == 2 && WHOLE ? 3 : 1;
     using V8 = typename Frag<T>::V;
     extern __shared__ __align__(16) unsigned char smem[];
     lds_poison((uint32_t)(sizeof(Decays<C>) + sizeof(T) * C * (2 * SK + SV + SP)));
@@ -336,20 +358,9 @@ __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
     const size_t ends = ((size_t)b.seq * p.H + h) * (DK * DV);
     const size_t rk = (size_t)p.H * DK, rv = (size_t)p.H * DV;
 
-    f32x4 S[NPW][MT];
-    const float* init = WHOLE ? (p.S0 ? p.S0 + ends : nullptr)
-                              : p.seg[0] + ((size_t)blockIdx.x * p.H + h) * (DK * DV);
-#pragma unroll
-    for (int x = 0; x < NPW; ++x)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                S[x][m][r] = init ? init[(size_t)(16 * m + 4 * g + r) * DV + 16 * (w * NPW + x) + il] : 0.f;
-
     Stage<T, DK, C, NT> stq, stk;
     Stage<T, DV, C, NT> stv;
-    float a = 1.f;
+    DecayLoad<T> a(p, h);
     auto fetch = [&](int c) {
         const long t = b.t0 + (long)c * C;
         const int n = min(C, b.n - c * C);
@@ -357,9 +368,25 @@ __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
         stq.load(static_cast<const T*>(p.q) + r0 * DK, rk, n, tid);
         stk.load(static_cast<const T*>(p.k) + r0 * DK, rk, n, tid);
         stv.load(static_cast<const T*>(p.v) + r0 * DV, rv, n, tid);
-        if (w == 0) a = load_decay<T>(p, t + lane, h, lane < n);
+        if (w == 0) a.load(p, t, h, lane, n);
     };
     if (nc) fetch(0);
+    f32x4 S[NPW][MT];
+    const float* init = WHOLE ? (p.S0 ? p.S0 + ends : nullptr)
+                              : p.seg[0] + ((size_t)blockIdx.x * p.H + h) * (DK * DV);
+#pragma unroll
+    for (int x = 0; x < NPW; ++x)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) S[x][m] = zero4();
+    if (init) {
+#pragma unroll
+        for (int x = 0; x < NPW; ++x)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    S[x][m][r] = init[(size_t)(16 * m + 4 * g + r) * DV + 16 * (w * NPW + x) + il];
+    }
     zero_pad_cols<T, DK>(sq, C, tid, NT);
     zero_pad_cols<T, DK>(sk, C, tid, NT);
     for (int c = 0; c < nc; ++c) {
@@ -367,7 +394,7 @@ __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
         stq.store(sq, tid);
         stk.store(sk, tid);
         stv.store(sv, tid);
-        if (w == 0) block_decays<C, true>(dec, a, lane);
+        if (w == 0) block_decays<C, true>(dec, a.value(p, lane), lane);
         __syncthreads();
         if (c + 1 < nc) fetch(c + 1);
 
@@ -440,21 +467,16 @@ __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
 #pragma unroll
             for (int ks = 0; ks < C / 32; ++ks) {
                 const f32x8 fk = factors(dec.suf, 32 * ks, g);
-                V8 hi[NPW], lo[NPW];
+                V8 part[NPW][PARTS];
 #pragma unroll
-                for (int x = 0; x < NPW; ++x) {
-                    const f32x8 y = widen(vf[x][ks]) * fk;
-                    hi[x] = narrow<T>(y);
-                    if constexpr (WHOLE && sizeof(T) == 2) lo[x] = narrow<T>(y - widen(hi[x]));
-                }
+                for (int x = 0; x < NPW; ++x) split<T, PARTS>(part[x], widen(vf[x][ks]) * fk);
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     const V8 kf = frag_tr(sk, SK, 32 * ks, 16 * m, g, il);
 #pragma unroll
-                    for (int x = 0; x < NPW; ++x) {
-                        S[x][m] = mma(kf, hi[x], S[x][m]);
-                        if constexpr (WHOLE && sizeof(T) == 2) S[x][m] = mma(kf, lo[x], S[x][m]);
-                    }
+                    for (int x = 0; x < NPW; ++x)
+#pragma unroll
+                        for (int e = 0; e < PARTS; ++e) S[x][m] = mma(kf, part[x][e], S[x][m]);
                 }
             }
         }
@@ -528,7 +550,11 @@ __global__ void __launch_bounds__(4 * (DK > DV ? DK : DV)) lin_grad_kernel(LinPa
         cc.load(static_cast<const T*>(p.v) + r0 * DV, rv, n, tid);
         dd.load(static_cast<const T*>(p.dO) + r0 * DV, rv, n, tid);
         ee.load(static_cast<const T*>(p.blk[1]) + at, DV, DK, tid);
-        if (w == 0) block_decays<C, true>(s.dec, load_decay<T>(p, t0 + lane, h, lane < n), lane);
+        if (w == 0) {
+            DecayLoad<T> x(p, h);
+            x.load(p, t0, h, lane, n);
+            block_decays<C, true>(s.dec, x.value(p, lane), lane);
+        }
         a.store(s.q, tid);
         bb.store(s.k, tid);
         cc.store(s.v, tid);
@@ -823,10 +849,10 @@ template <class K> hipError_t launch(K kern, dim3 grid, int threads, size_t lds,
     return hipGetLastError();
 }
 
-template <class T, int DK, int DV, bool STORE, bool SPLIT>
+template <class T, int DK, int DV, bool STORE>
 hipError_t launch_state(const LinParams& p, int segs, int dirs, hipStream_t st) {
     constexpr int NW = DK / 16 < 4 ? DK / 16 : 4, C = lin_block<T>();
-    return launch(lin_state_kernel<T, DK, DV, NW, STORE, SPLIT>, dim3(segs, p.H, dirs), 64 * NW,
+    return launch(lin_state_kernel<T, DK, DV, NW, STORE>, dim3(segs, p.H, dirs), 64 * NW,
                   sizeof(Decays<C>) + sizeof(T) * C * (tile_stride<T>(DK) + tile_stride<T>(DV)), st, p);
 }
 
@@ -845,7 +871,7 @@ template <class T, int DK, int DV> hipError_t forward(LinParams p, const LinArgs
     }
     const int segs = (int)seq_blocks_bound(p.map.T, p.map.N, p.L, packed);
     hipError_t e = hipSuccess;
-    if (p.map.T > 0) e = launch_state<T, DK, DV, false, true>(p, segs, 1, a.stream);
+    if (p.map.T > 0) e = launch_state<T, DK, DV, false>(p, segs, 1, a.stream);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(lin_scan_kernel, dim3(p.map.N * p.H, (DK * DV / 4 + 255) / 256, 1), dim3(256), 0, a.stream, p, DK * DV);
     e = hipGetLastError();
@@ -857,12 +883,12 @@ template <class T, int DK, int DV> hipError_t backward(const LinParams& p, const
     const bool packed = p.map.cu != nullptr;
     const int segs = (int)seq_blocks_bound(p.map.T, p.map.N, p.L, packed);
     hipError_t e = hipSuccess;
-    if (p.map.T > 0) e = launch_state<T, DK, DV, false, true>(p, segs, 2, a.stream);
+    if (p.map.T > 0) e = launch_state<T, DK, DV, false>(p, segs, 2, a.stream);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(lin_scan_kernel, dim3(p.map.N * p.H, (DK * DV / 4 + 255) / 256, 2), dim3(256), 0, a.stream, p, DK * DV);
     e = hipGetLastError();
     if (e != hipSuccess || p.map.T == 0) return e;
-    e = launch_state<T, DK, DV, true, true>(p, segs, 2, a.stream);
+    e = launch_state<T, DK, DV, true>(p, segs, 2, a.stream);
     if (e != hipSuccess) return e;
     const dim3 grid(segs * (p.L / lin_block<T>()), p.H);
     constexpr int NT = 4 * (DK > DV ? DK : DV);

@@ -618,8 +618,7 @@ struct SwaDecodeParams {
 // side as the columns. The new token's row is read from k and v, and written to
 // its slot by the workgroup whose part holds it.
 template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa_decode_kernel(SwaDecodeParams p) {
-    constexpr int ST = tile_stride<T>(D), KD = D / 16, MD = D / 32, CPR = D * (int)sizeof(T) / 16, PER = 16 / (int)sizeof(T),
-                  RN = 32 * CPR / 64;
+    constexpr int ST = tile_stride<T>(D), KD = D / 16, MD = D / 32, CPR = D * (int)sizeof(T) / 16, PER = 16 / (int)sizeof(T);
     using V8 = typename Frag<T>::V;
     extern __shared__ __align__(16) unsigned char smem[];
     const uint32_t lds = sizeof(T) * NW * 2 * 32 * ST;
@@ -645,15 +644,18 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
         *reinterpret_cast<uint4*>((isv ? Vc : Kc) + (size_t)slot * rs + x) =
             *reinterpret_cast<const uint4*>((isv ? newv : newk) + x);
     }
-    uint4 rk[RN], rv[RN];
+    Stage<T, D, 32, 64> rk, rv;
     auto fetch = [&](int j0) {
+        rk.load(Kc + (size_t)j0 * rs, rs, e - j0, lane);
+        rv.load(Vc + (size_t)j0 * rs, rs, e - j0, lane);
+        if (slot >= j0 && slot < min(j0 + 32, e)) {   // the cache's row may not have it yet
 #pragma unroll
-        for (int m = 0; m < RN; ++m) {
-            const int x = lane + 64 * m, j = j0 + x / CPR, col = x % CPR * PER;
-            rk[m] = rv[m] = make_uint4(0u, 0u, 0u, 0u);
-            if (j < e) {
-                rk[m] = *reinterpret_cast<const uint4*>((j == slot ? newk : Kc + (size_t)j * rs) + col);
-                rv[m] = *reinterpret_cast<const uint4*>((j == slot ? newv : Vc + (size_t)j * rs) + col);
+            for (int m = 0; m < rk.N; ++m) {
+                const int x = lane + 64 * m, col = x % CPR * PER;
+                if (j0 + x / CPR == slot) {
+                    __builtin_memcpy(&rk.r[m], newk + col, 16);
+                    __builtin_memcpy(&rv.r[m], newv + col, 16);
+                }
             }
         }
     };
@@ -671,12 +673,8 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
     for (; j0 < e; j0 += 32 * NW) {
         // the tile is this wave's own: its reads of the last one are done, its
         // writes are in order before the reads below
-#pragma unroll
-        for (int m = 0; m < RN; ++m) {
-            const int x = lane + 64 * m;
-            *reinterpret_cast<uint4*>(tk + x / CPR * ST + x % CPR * PER) = rk[m];
-            *reinterpret_cast<uint4*>(tv + x / CPR * ST + x % CPR * PER) = rv[m];
-        }
+        rk.store(tk, lane);
+        rv.store(tv, lane);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         if (j0 + 32 * NW < e) fetch(j0 + 32 * NW);

@@ -108,24 +108,28 @@ __device__ __forceinline__ void store1(uint16_t* p, float x) {
 __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
 
 // A tile on its way from global memory to LDS through registers, 16 bytes a
-// thread and step: rows row0 + (0..R-1) of `stride` elements, rows past
-// `valid` read as zeros and touch no memory.
+// thread and step: rows row0 + (0..R-1) of `stride` elements. The loads go
+// through a buffer descriptor that ends behind row `valid` - 1, so that later
+// rows read as zeros and touch no memory, with no branch around a load.
 template <class T, int D, int R, int NT> struct Stage {
     static constexpr int PER = 16 / (int)sizeof(T), CPR = D / PER, TOT = R * CPR, N = (TOT + NT - 1) / NT;
-    uint4 r[N];
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    u32x4 r[N];
     __device__ __forceinline__ void load(const T* base, size_t stride, int valid, int tid) {
+        const uint32_t bytes = (uint32_t)stride * (uint32_t)sizeof(T);
+        const auto rsrc = make_rsrc(base, (uint32_t)min(max(valid, 0), R) * bytes);
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const int e = tid + n * NT, row = e / CPR, c = e % CPR;
-            r[n] = make_uint4(0u, 0u, 0u, 0u);
-            if (e < TOT && row < valid) r[n] = *reinterpret_cast<const uint4*>(base + (size_t)row * stride + c * PER);
+            const int e = tid + n * NT;
+            if (TOT % NT == 0 || e < TOT)
+                r[n] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, (uint32_t)(e / CPR) * bytes + (uint32_t)(e % CPR) * 16u, 0, 0);
         }
     }
     __device__ __forceinline__ void store(T* tile, int tid) const {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const int e = tid + n * NT;
-            if (e < TOT) *reinterpret_cast<uint4*>(tile + (e / CPR) * tile_stride<T>(D) + (e % CPR) * PER) = r[n];
+            if (TOT % NT == 0 || e < TOT) *reinterpret_cast<u32x4*>(tile + (e / CPR) * tile_stride<T>(D) + (e % CPR) * PER) = r[n];
         }
     }
 };

@@ -607,25 +607,41 @@ def decode_step_ew(q, k, v, gate, erase, write, S, out: Optional[torch.Tensor] =
 
 # ---------------------------------------------------------------- linear attention with a decay per head
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """The device of the inputs made current, and what the call allocates taken
-    from the pool of the stream that it runs on. Yields that stream's handle."""
-    if stream is None:
-        with torch.cuda.device(device):
-            st = torch.cuda.current_stream(device).cuda_stream
-            yield ctypes.c_void_p(st) if st else None
-    else:
+# torch.cuda.current_stream(device).cuda_stream without making a Stream object,
+# where this torch has it: one token's kernel is shorter than the difference
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _run(device, stream, call):
+    """call(stream handle) with the inputs' device current, and on a given stream
+    with that stream current too, so that what the call allocates comes from its
+    pool."""
+    if stream is not None:
         with torch.cuda.device(device), torch.cuda.stream(stream):
-            yield ctypes.c_void_p(stream.cuda_stream) if stream.cuda_stream else None
+            return call(stream.cuda_stream)
+    if torch.cuda.current_device() == device.index:
+        return call(_raw_stream(device.index))
+    with torch.cuda.device(device):
+        return call(_raw_stream(device.index))
+
+
+def _addr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _check_input(name, t, dtype, device):
+    if t.dtype != dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if not t.is_cuda or t.device != device or not t.is_contiguous():
+        _check_dev(name, t, device)
 
 
 def _like(name, t, shape, dtype, device):
-    """Checks a tensor that a call writes: its shape, dtype, device and layout."""
-    if t.dtype != dtype:
-        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    _check_shape(name, t, shape)
-    _check_dev(name, t, device)
+    """Checks a tensor that has to have this shape too."""
+    if t.shape != shape:
+        _check_shape(name, t, shape)
+    _check_input(name, t, dtype, device)
 
 
 def _scratch(workspace, need, device):
@@ -642,40 +658,32 @@ def _check_linattn(q, k, v, gate, cu_seqlens, lead):
     leading dims before dk. Returns (sizes of those, dk, dv, gate kind)."""
     if q.dim() != lead + 1:
         raise ValueError("q must have %d dims, got %s" % (lead + 1, tuple(q.shape)))
-    dims, dk = tuple(q.shape[:-1]), q.shape[-1]
     if v.dim() != lead + 1:
         raise ValueError("v must have %d dims, got %s" % (lead + 1, tuple(v.shape)))
-    dv = v.shape[-1]
-    _check_shape("k", k, dims + (dk,))
-    _check_shape("v", v, dims + (dv,))
-    for name, t in (("k", k), ("v", v)):
-        if t.dtype != q.dtype:
-            raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, q.dtype))
-    if gate.dim() == 1:
-        kind, want = GATE_HEAD, torch.float32
-        _check_shape("gate", gate, dims[-1:])
-    else:
-        kind, want = GATE_SCALAR, q.dtype
-        _check_shape("gate", gate, dims)
-    if gate.dtype != want:
-        raise TypeError("gate has dtype %s, expected %s" % (gate.dtype, want))
+    dims, dk, dv = q.shape[:-1], q.shape[-1], v.shape[-1]
     if cu_seqlens is not None and dims[0] != 1:
         raise ValueError("packed sequences (cu_seqlens) need B = 1, got %d" % dims[0])
-    for name, t in (("q", q), ("k", k), ("v", v), ("gate", gate)):
-        _check_dev(name, t, q.device)
-    return dims, dk, dv, kind
+    dtype, device = q.dtype, q.device
+    _check_input("q", q, dtype, device)
+    _like("k", k, q.shape, dtype, device)
+    _like("v", v, dims + (dv,), dtype, device)
+    if gate.dim() == 1:
+        _like("gate", gate, dims[-1:], torch.float32, device)
+        return dims, dk, dv, GATE_HEAD
+    _like("gate", gate, dims, dtype, device)
+    return dims, dk, dv, GATE_SCALAR
 
 
 def linattn_fwd_workspace_bytes(B: int, H: int, T: int, dk: int, dv: int, N: int = 0, varlen: bool = False,
                                 dtype: torch.dtype = torch.bfloat16) -> int:
     code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
-    return int(_lib().kda_linattn_fwd_workspace_bytes(B, H, T, dk, dv, N, int(varlen), code))
+    return _lib().kda_linattn_fwd_workspace_bytes(B, H, T, dk, dv, N, int(varlen), code)
 
 
 def linattn_bwd_workspace_bytes(B: int, H: int, T: int, dk: int, dv: int, N: int = 0, varlen: bool = False,
                                 dtype: torch.dtype = torch.bfloat16) -> int:
     code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
-    return int(_lib().kda_linattn_bwd_workspace_bytes(B, H, T, dk, dv, N, int(varlen), code))
+    return _lib().kda_linattn_bwd_workspace_bytes(B, H, T, dk, dv, N, int(varlen), code)
 
 
 def linattn_fwd(q, k, v, gate, S0=None, cu_seqlens=None, out: Optional[torch.Tensor] = None, state_out: bool = True,
@@ -694,18 +702,19 @@ def linattn_fwd(q, k, v, gate, S0=None, cu_seqlens=None, out: Optional[torch.Ten
     if out is not None:
         _like("out", out, (B, T, H, dv), q.dtype, device)
     need = linattn_fwd_workspace_bytes(B, H, T, dk, dv, N, varlen, q.dtype)
-    with _on(device, stream) as st:
-        if out is None:
-            out = torch.empty((B, T, H, dv), device=device, dtype=q.dtype)
-        if S_T is None and state_out:
-            S_T = torch.empty((N, H, dk, dv), device=device, dtype=torch.float32)
+
+    def call(st):
+        o = torch.empty((B, T, H, dv), device=device, dtype=q.dtype) if out is None else out
+        S = torch.empty((N, H, dk, dv), device=device, dtype=torch.float32) if S_T is None and state_out else S_T
         ws = _scratch(workspace, need, device)
-        rc = _lib().kda_linattn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(S0), _ptr(out), _ptr(S_T), B, H, T, dk,
-                                    dv, _ptr(cu_seqlens), N if varlen else 0, dt, kind, _ptr(ws),
-                                    ws.numel() * ws.element_size(), st)
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_linattn_fwd")
-    return out, S_T
+        rc = _lib().kda_linattn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(), _addr(S0), o.data_ptr(),
+                                    _addr(S), B, H, T, dk, dv, _addr(cu_seqlens), N if varlen else 0, dt, kind,
+                                    ws.data_ptr(), ws.numel() * ws.element_size(), st)
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_linattn_fwd")
+        return o, S
+
+    return _run(device, stream, call)
 
 
 def linattn_bwd(q, k, v, gate, dO, S0=None, dS_T=None, cu_seqlens=None, want_dS0: bool = True,
@@ -731,19 +740,23 @@ def linattn_bwd(q, k, v, gate, dO, S0=None, dS_T=None, cu_seqlens=None, want_dS0
             raise ValueError("a constant decay per head has no dgate")
         _check_state("dS0", out.get("dS0"), N, H, dk, dv, device)
     need = linattn_bwd_workspace_bytes(B, H, T, dk, dv, N, varlen, q.dtype)
-    with _on(device, stream) as st:
-        if out is None:
-            out = {name: torch.empty(shape, device=device, dtype=q.dtype) for name, shape in shapes.items()}
-            out.setdefault("dgate", None)
-            out["dS0"] = torch.empty((N, H, dk, dv), device=device, dtype=torch.float32) if want_dS0 else None
+
+    def call(st):
+        g = out
+        if g is None:
+            g = {name: torch.empty(shape, device=device, dtype=q.dtype) for name, shape in shapes.items()}
+            g.setdefault("dgate", None)
+            g["dS0"] = torch.empty((N, H, dk, dv), device=device, dtype=torch.float32) if want_dS0 else None
         ws = _scratch(workspace, need, device)
-        rc = _lib().kda_linattn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(S0), _ptr(dO), _ptr(dS_T),
-                                    _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out.get("dgate")),
-                                    _ptr(out.get("dS0")), B, H, T, dk, dv, _ptr(cu_seqlens), N if varlen else 0, dt,
-                                    kind, _ptr(ws), ws.numel() * ws.element_size(), st)
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_linattn_bwd")
-    return out
+        rc = _lib().kda_linattn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(), _addr(S0), dO.data_ptr(),
+                                    _addr(dS_T), g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(),
+                                    _addr(g.get("dgate")), _addr(g.get("dS0")), B, H, T, dk, dv, _addr(cu_seqlens),
+                                    N if varlen else 0, dt, kind, ws.data_ptr(), ws.numel() * ws.element_size(), st)
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_linattn_bwd")
+        return g
+
+    return _run(device, stream, call)
 
 
 def linattn_decode_step(q, k, v, gate, S, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -755,15 +768,16 @@ def linattn_decode_step(q, k, v, gate, S, out: Optional[torch.Tensor] = None, st
     _like("S", S, (N, H, dk, dv), torch.float32, device)
     if out is not None:
         _like("out", out, (N, H, dv), q.dtype, device)
-    with _on(device, stream) as st:
-        if out is None:
-            out = torch.empty((N, H, dv), device=device, dtype=q.dtype)
-        rc = _lib().kda_linattn_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(S), _ptr(out), N, H, dk, dv, dt,
-                                            kind, st)
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_linattn_decode_step", "kda_swa_fwd", "kda_swa_bwd",
-           "kda_swa_bwd_workspace_bytes", "kda_swa_decode_step", "kda_swa_decode_workspace_bytes", "kda_swa_cache_fill")
-    return out
+
+    def call(st):
+        o = torch.empty((N, H, dv), device=device, dtype=q.dtype) if out is None else out
+        rc = _lib().kda_linattn_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(), S.data_ptr(),
+                                            o.data_ptr(), N, H, dk, dv, dt, kind, st)
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_linattn_decode_step")
+        return o
+
+    return _run(device, stream, call)
 
 
 # ---------------------------------------------------------------- window attention with sinks
@@ -771,24 +785,19 @@ def linattn_decode_step(q, k, v, gate, S, out: Optional[torch.Tensor] = None, st
 def _check_swa(q, k, v, cu_seqlens, window, sinks, lead):
     """Shapes, dtypes and devices of a window-attention call whose q has `lead`
     dims before the heads. Returns (those dims, Hq, Hkv, d)."""
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dim() != lead + 2:
-            raise ValueError("%s must have %d dims, got %s" % (name, lead + 2, tuple(t.shape)))
-    dims, Hq, d = tuple(q.shape[:lead]), q.shape[-2], q.shape[-1]
-    Hkv = k.shape[-2]
-    _check_shape("k", k, dims + (Hkv, d))
-    _check_shape("v", v, dims + (Hkv, d))
+    if q.dim() != lead + 2 or k.dim() != lead + 2:
+        raise ValueError("q and k must have %d dims, got %s and %s" % (lead + 2, tuple(q.shape), tuple(k.shape)))
+    dims, Hq, Hkv, d = q.shape[:lead], q.shape[-2], k.shape[-2], q.shape[-1]
     if Hkv == 0 or Hq % Hkv:
         raise ValueError("q has %d heads, not a multiple of k's %d" % (Hq, Hkv))
-    for name, t in (("k", k), ("v", v)):
-        if t.dtype != q.dtype:
-            raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, q.dtype))
     if window < 1 or sinks < 0:
         raise ValueError("window must be at least 1 and sinks at least 0, got %d and %d" % (window, sinks))
     if cu_seqlens is not None and dims[0] != 1:
         raise ValueError("packed sequences (cu_seqlens) need B = 1, got %d" % dims[0])
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _check_dev(name, t, q.device)
+    dtype, device = q.dtype, q.device
+    _check_input("q", q, dtype, device)
+    _like("k", k, dims + (Hkv, d), dtype, device)
+    _like("v", v, dims + (Hkv, d), dtype, device)
     return dims, Hq, Hkv, d
 
 
@@ -813,22 +822,23 @@ def swa_fwd(q, k, v, window: int, sinks: int = 0, scale: Optional[float] = None,
         _like("out", out, (B, T, Hq, d), q.dtype, device)
     if lse is not None:
         _like("lse", lse, (B, T, Hq), torch.float32, device)
-    with _on(device, stream) as st:
-        if out is None:
-            out = torch.empty((B, T, Hq, d), device=device, dtype=q.dtype)
-        if lse is None and lse_out:
-            lse = torch.empty((B, T, Hq), device=device, dtype=torch.float32)
-        rc = _lib().kda_swa_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, Hkv, T, d, _int32(window),
-                                _int32(sinks), d ** -0.5 if scale is None else float(scale), _ptr(cu_seqlens),
-                                N if varlen else 0, dt, st)
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_swa_fwd")
-    return out, lse
+
+    def call(st):
+        o = torch.empty((B, T, Hq, d), device=device, dtype=q.dtype) if out is None else out
+        s = torch.empty((B, T, Hq), device=device, dtype=torch.float32) if lse is None and lse_out else lse
+        rc = _lib().kda_swa_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _addr(s), B, Hq, Hkv, T, d,
+                                _int32(window), _int32(sinks), d ** -0.5 if scale is None else float(scale),
+                                _addr(cu_seqlens), N if varlen else 0, dt, st)
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_swa_fwd")
+        return o, s
+
+    return _run(device, stream, call)
 
 
 def swa_bwd_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, d: int, window: int, sinks: int = 0, N: int = 0,
                             varlen: bool = False) -> int:
-    return int(_lib().kda_swa_bwd_workspace_bytes(B, Hq, Hkv, T, d, _int32(window), _int32(sinks), N, int(varlen)))
+    return _lib().kda_swa_bwd_workspace_bytes(B, Hq, Hkv, T, d, _int32(window), _int32(sinks), N, int(varlen))
 
 
 def swa_bwd(q, k, v, o, lse, dO, window: int, sinks: int = 0, scale: Optional[float] = None, cu_seqlens=None,
@@ -847,26 +857,26 @@ def swa_bwd(q, k, v, o, lse, dO, window: int, sinks: int = 0, scale: Optional[fl
         for name, shape in shapes.items():
             _like(name, out[name], shape, q.dtype, device)
     need = swa_bwd_workspace_bytes(B, Hq, Hkv, T, d, window, sinks, N, varlen)
-    with _on(device, stream) as st:
-        if out is None:
-            out = {name: torch.empty(shape, device=device, dtype=q.dtype) for name, shape in shapes.items()}
+
+    def call(st):
+        g = out
+        if g is None:
+            g = {name: torch.empty(shape, device=device, dtype=q.dtype) for name, shape in shapes.items()}
         ws = _scratch(workspace, need, device)
-        rc = _lib().kda_swa_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(out["dq"]),
-                                _ptr(out["dk"]), _ptr(out["dv"]), B, Hq, Hkv, T, d, _int32(window), _int32(sinks),
-                                d ** -0.5 if scale is None else float(scale), _ptr(cu_seqlens), N if varlen else 0, dt,
-                                _ptr(ws), ws.numel() * ws.element_size(), st)
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_swa_bwd")
-    return out
+        rc = _lib().kda_swa_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dO.data_ptr(),
+                                g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(), B, Hq, Hkv, T, d,
+                                _int32(window), _int32(sinks), d ** -0.5 if scale is None else float(scale),
+                                _addr(cu_seqlens), N if varlen else 0, dt, ws.data_ptr(),
+                                ws.numel() * ws.element_size(), st)
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_swa_bwd")
+        return g
+
+    return _run(device, stream, call)
 
 
 def swa_decode_workspace_bytes(N: int, Hq: int, Hkv: int, d: int, window: int, sinks: int = 0) -> int:
-    return int(_lib().kda_swa_decode_workspace_bytes(N, Hq, Hkv, d, _int32(window), _int32(sinks)))
-
-
-def _check_cache(K_cache, V_cache, N, slots, Hkv, d, dtype, device):
-    for name, t in (("K_cache", K_cache), ("V_cache", V_cache)):
-        _like(name, t, (N, slots, Hkv, d), dtype, device)
+    return _lib().kda_swa_decode_workspace_bytes(N, Hq, Hkv, d, _int32(window), _int32(sinks))
 
 
 def swa_decode_step(q, k, v, K_cache, V_cache, pos, window: int, sinks: int = 0, scale: Optional[float] = None,
@@ -878,22 +888,25 @@ def swa_decode_step(q, k, v, K_cache, V_cache, pos, window: int, sinks: int = 0,
     or negative for a sequence to leave out (o zero). Returns o [N,Hq,d]."""
     (N,), Hq, Hkv, d = _check_swa(q, k, v, None, window, sinks, 1)
     device, dt = q.device, _dtype_code(q)
-    _check_cache(K_cache, V_cache, N, window + sinks, Hkv, d, q.dtype, device)
+    _like("K_cache", K_cache, (N, sinks + window, Hkv, d), q.dtype, device)
+    _like("V_cache", V_cache, (N, sinks + window, Hkv, d), q.dtype, device)
     _like("pos", pos, (N,), torch.int32, device)
     if out is not None:
         _like("out", out, (N, Hq, d), q.dtype, device)
     need = swa_decode_workspace_bytes(N, Hq, Hkv, d, window, sinks)
-    with _on(device, stream) as st:
-        if out is None:
-            out = torch.empty((N, Hq, d), device=device, dtype=q.dtype)
+
+    def call(st):
+        o = torch.empty((N, Hq, d), device=device, dtype=q.dtype) if out is None else out
         ws = _scratch(workspace, need, device)
-        rc = _lib().kda_swa_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(K_cache), _ptr(V_cache), _ptr(pos), _ptr(out), N,
-                                        Hq, Hkv, d, _int32(window), _int32(sinks),
-                                        d ** -0.5 if scale is None else float(scale), dt, _ptr(ws),
+        rc = _lib().kda_swa_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(),
+                                        pos.data_ptr(), o.data_ptr(), N, Hq, Hkv, d, _int32(window), _int32(sinks),
+                                        d ** -0.5 if scale is None else float(scale), dt, ws.data_ptr(),
                                         ws.numel() * ws.element_size(), st)
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_swa_decode_step")
-    return out
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_swa_decode_step")
+        return o
+
+    return _run(device, stream, call)
 
 
 def swa_cache_fill(k, v, K_cache, V_cache, window: int, sinks: int = 0, cu_seqlens=None, stream=None) -> None:
@@ -903,9 +916,13 @@ def swa_cache_fill(k, v, K_cache, V_cache, window: int, sinks: int = 0, cu_seqle
     (B, T), _, Hkv, d = _check_swa(k, k, v, cu_seqlens, window, sinks, 2)
     device, dt = k.device, _dtype_code(k)
     varlen, N = _check_varlen(cu_seqlens, B, device)
-    _check_cache(K_cache, V_cache, N, window + sinks, Hkv, d, k.dtype, device)
-    with _on(device, stream) as st:
-        rc = _lib().kda_swa_cache_fill(_ptr(k), _ptr(v), _ptr(K_cache), _ptr(V_cache), B, Hkv, T, d, _int32(window),
-                                       _int32(sinks), _ptr(cu_seqlens), N if varlen else 0, dt, st)
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_swa_cache_fill")
+    _like("K_cache", K_cache, (N, sinks + window, Hkv, d), k.dtype, device)
+    _like("V_cache", V_cache, (N, sinks + window, Hkv, d), k.dtype, device)
+
+    def call(st):
+        rc = _lib().kda_swa_cache_fill(k.data_ptr(), v.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), B, Hkv, T, d,
+                                       _int32(window), _int32(sinks), _addr(cu_seqlens), N if varlen else 0, dt, st)
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_swa_cache_fill")
+
+    _run(device, stream, call)
