@@ -12,6 +12,7 @@
 // stand, with no pass through LDS (the contraction takes the keys in the order
 // in which the registers hold them).
 #include <algorithm>
+#include <type_traits>
 
 #include "kda_launch.h"
 #include "kda_tiles.h"
@@ -29,9 +30,10 @@ struct SwaParams {
     const float* lse;
     void *out, *dq, *dk, *dv;
     float *lse_out, *delta;
-    float* part;            // gradients of sink blocks: [sequence][kv head][block][split][dk, dv][KB][D]
+    float* part;            // gradients of sink blocks: [sequence][kv head][block][split][dv, dk][KB][D]
     SeqMap map;
     int Hq, Hkv, G;         // G = Hq / Hkv
+    int HW;                 // heads of a group that a workgroup takes together
     int window, sinks;
     float scale;
     int blocks;             // blocks of rows over all sequences
@@ -107,6 +109,17 @@ __device__ __forceinline__ float swap_sum(float v) {
     return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
+// largest of 16 values (IEEE maximum: takes a product's result as it is, where
+// fmaxf would first quiet every operand with an instruction of its own)
+__device__ __forceinline__ float tree_max(const f32x16& x) {
+    float m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m[i] = __builtin_elementwise_maximum(__builtin_elementwise_maximum(x[4 * i], x[4 * i + 1]),
+                                             __builtin_elementwise_maximum(x[4 * i + 2], x[4 * i + 3]));
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(m[0], m[1]), __builtin_elementwise_maximum(m[2], m[3]));
+}
+
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }   // 1 ulp, no range fix-up
 
 // keys (rows) per tile that a workgroup stages
@@ -120,6 +133,12 @@ __device__ __forceinline__ Seen seen(int i0, int i1, int j0, int j1, int window,
 __device__ __forceinline__ bool sees(int i, int j, int window, int sinks) {
     return j <= i && (i - j < window || j < sinks);
 }
+// The same for one lane and many keys at constant offsets from `j`.
+struct Mask {
+    int last, first, sink;   // offsets seen: first < c <= last, or c < sink and c <= last
+    __device__ __forceinline__ Mask(int i, int j, int window, int sinks) : last(i - j), first(i - j - window), sink(sinks - j) {}
+    __device__ __forceinline__ bool operator()(int c) const { return c <= last && (c > first || c < sink); }
+};
 
 // The key tiles of rows [q0, q1]: first those with sinks, then the window's.
 struct KeyTiles {
@@ -132,13 +151,21 @@ struct KeyTiles {
     __device__ __forceinline__ int operator[](int it) const { return it < sink ? it : first + it - sink; }
 };
 
-// workgroup number -> (block of rows, head): the heads of one block next to
-// each other on one XCD, which keeps the block's keys in its L2; late blocks,
+// A workgroup of NW waves takes HW heads of one group (the largest power of two
+// that divides both) for 32 NW / HW rows: heads side by side read the same key
+// tiles, and the fewer rows they have, the fewer tiles lie across a mask's edge.
+__host__ __device__ inline int heads_together(int G, int NW) {
+    int hw = NW;
+    while (G % hw) hw /= 2;
+    return hw;
+}
+// workgroup number -> (block of rows, first head): the heads of one block next
+// to each other on one XCD, which keeps the block's keys in its L2; late blocks,
 // which see more keys, first
-__device__ __forceinline__ void work_item(const SwaParams& p, int heads, int& blk, int& head) {
-    const int e = xcd_remap(blockIdx.x, p.blocks * heads);
+__device__ __forceinline__ void work_item(const SwaParams& p, int& blk, int& head) {
+    const int heads = p.Hq / p.HW, e = xcd_remap(blockIdx.x, p.blocks * heads);
     blk = p.blocks - 1 - e / heads;
-    head = e % heads;
+    head = e % heads * p.HW;
 }
 
 // ---------------------------------------------------------------- forward
@@ -154,26 +181,32 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
 
     const int tid = threadIdx.x, lane = tid % WAVE, w = tid / WAVE, n = lane & 31, h2 = lane >> 5;
     int blk, h;
-    work_item(p, p.Hq, blk, h);
+    work_item(p, blk, h);
+    const int rows = 32 * NW / p.HW;
     SeqBlock b;
-    if (!seq_block(p.map, 32 * NW, blk, b)) return;
-    const int q0 = b.idx * 32 * NW, len = b.len;
+    if (!seq_block(p.map, rows, blk, b)) return;
+    const int q0 = b.idx * rows, len = b.len;
     const long ts = b.t0 - q0;
     const int hk = h / p.G;
-    const int i0 = q0 + 32 * w, row = i0 + n;
+    h += w % p.HW;
+    const int i0 = q0 + w / p.HW * 32, row = i0 + n;
     const bool live = row < len;
-    const float c = p.scale * LOG2E;
+    // a negative scale goes into q, exactly, so that maxima scale as they stand
+    const float c = fabsf(p.scale) * LOG2E;
 
     V8 qf[KD];
     {
         const T* src = static_cast<const T*>(p.q) + ((size_t)(ts + (live ? row : 0)) * p.Hq + h) * D + 8 * h2;
 #pragma unroll
-        for (int ks = 0; ks < KD; ++ks) qf[ks] = load8<T>(src + 16 * ks, live);
+        for (int ks = 0; ks < KD; ++ks) {
+            qf[ks] = load8<T>(src + 16 * ks, live);
+            if (p.scale < 0.f) qf[ks] = -qf[ks];
+        }
     }
     const T* K = static_cast<const T*>(p.k) + ((size_t)ts * p.Hkv + hk) * D;
     const T* V = static_cast<const T*>(p.v) + ((size_t)ts * p.Hkv + hk) * D;
     const size_t rs = (size_t)p.Hkv * D;
-    const KeyTiles kt(q0, min(q0 + 32 * NW, len) - 1, KT, p.window, p.sinks);
+    const KeyTiles kt(q0, min(q0 + rows, len) - 1, KT, p.window, p.sinks);
 
     Stage<T, D, KT, NT> sk, sv;
     auto fetch = [&](int it) {
@@ -191,6 +224,75 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
     for (int m = 0; m < MD; ++m) O[m] = zero16();
     float top = -INFINITY, sum = 0.f;   // sum: this lane's half of the keys
 
+    auto tile = [&](const T* tk, const T* tv, int j0, auto masked) {
+        f32x16 s[NX];
+        V8 kf[NX][KD], vf[MD];
+#pragma unroll
+        for (int ks = 0; ks < KD; ++ks)
+#pragma unroll
+            for (int x = 0; x < NX; ++x) kf[x][ks] = nat32<T>(tk, ST, 32 * x, 16 * ks, n, h2);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int x = 0; x < NX; ++x) s[x] = zero16();
+#pragma unroll
+        for (int ks = 0; ks < KD; ++ks)
+#pragma unroll
+            for (int x = 0; x < NX; ++x) s[x] = mma32(kf[x][ks], qf[ks], s[x]);
+#pragma unroll
+        for (int m = 0; m < MD; ++m) vf[m] = tr32(tv, ST, 0, 32 * m, lane);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (masked.value) {
+            const Mask mask(row, j0 + 4 * h2, p.window, p.sinks);
+#pragma unroll
+            for (int x = 0; x < NX; ++x)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[x][r] = mask(32 * x + result_row(r, 0)) ? s[x][r] * c : -INFINITY;
+        }
+        const float f = masked.value ? 1.f : c;   // what is left to scale
+        float mt = tree_max(s[0]);
+#pragma unroll
+        for (int x = 1; x < NX; ++x) mt = __builtin_elementwise_maximum(mt, tree_max(s[x]));
+        mt = swap_max(mt * f);
+        // The subtracted maximum may lag behind by 2^8: sums stay far inside
+        // fp32, and most tiles leave o as it is.
+        if (__any(mt > top + 8.f || (top == -INFINITY && mt > top))) {
+            const float next = fmaxf(top, mt);
+            const float down = next == -INFINITY ? 1.f : fast_exp2(top - next);
+            top = next;
+            sum *= down;
+#pragma unroll
+            for (int m = 0; m < MD; ++m)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) O[m][r] *= down;
+        }
+        const float base = top == -INFINITY ? 0.f : top;
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < NX; ++x)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                s[x][r] = fast_exp2(fmaf(s[x][r], f, -base));
+                part[r & 3] += s[x][r];
+            }
+        sum += (part[0] + part[1]) + (part[2] + part[3]);
+#pragma unroll
+        for (int kb = 0; kb < KT / 16; ++kb) {
+            V8 next[MD];
+            if (kb + 1 < KT / 16) {
+#pragma unroll
+                for (int m = 0; m < MD; ++m) next[m] = tr32(tv, ST, 16 * (kb + 1), 32 * m, lane);
+            }
+            const V8 pf = rows16<T>(s[kb / 2], kb % 2);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int m = 0; m < MD; ++m) O[m] = mma32(vf[m], pf, O[m]);
+            if (kb + 1 < KT / 16) {
+#pragma unroll
+                for (int m = 0; m < MD; ++m) vf[m] = next[m];
+            }
+        }
+    };
+
     fetch(0);
     put(0);
     __syncthreads();
@@ -201,54 +303,7 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
         const int j0 = kt[it] * KT;
         const Seen se = seen(i0, i0 + 31, j0, j0 + KT - 1, p.window, p.sinks);
         if (!se.none && i0 < len) {
-            f32x16 s[NX];
-#pragma unroll
-            for (int x = 0; x < NX; ++x) s[x] = zero16();
-#pragma unroll
-            for (int ks = 0; ks < KD; ++ks)
-#pragma unroll
-                for (int x = 0; x < NX; ++x) s[x] = mma32(nat32<T>(tk, ST, 32 * x, 16 * ks, n, h2), qf[ks], s[x]);
-#pragma unroll
-            for (int x = 0; x < NX; ++x)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[x][r] *= c;
-            if (!se.all) {
-#pragma unroll
-                for (int x = 0; x < NX; ++x)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (!sees(row, j0 + 32 * x + result_row(r, h2), p.window, p.sinks)) s[x][r] = -INFINITY;
-            }
-            float mt = s[0][0];
-#pragma unroll
-            for (int x = 0; x < NX; ++x)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) mt = fmaxf(mt, s[x][r]);
-            mt = swap_max(mt);
-            if (__any(mt > top)) {
-                const float next = fmaxf(top, mt);
-                const float f = next == -INFINITY ? 1.f : fast_exp2(top - next);
-                top = next;
-                sum *= f;
-#pragma unroll
-                for (int m = 0; m < MD; ++m)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) O[m][r] *= f;
-            }
-            const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll
-            for (int x = 0; x < NX; ++x)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    s[x][r] = fast_exp2(s[x][r] - base);
-                    sum += s[x][r];
-                }
-#pragma unroll
-            for (int kb = 0; kb < KT / 16; ++kb) {
-                const V8 pf = rows16<T>(s[kb / 2], kb % 2);
-#pragma unroll
-                for (int m = 0; m < MD; ++m) O[m] = mma32(tr32(tv, ST, 16 * kb, 32 * m, lane), pf, O[m]);
-            }
+            if (se.all) tile(tk, tv, j0, std::false_type()); else tile(tk, tv, j0, std::true_type());
         }
         if (it + 1 < kt.count) {
             put(it + 1);
@@ -276,7 +331,7 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
                 const f32x8 y = widen(load8<T>(Q + x, true)) * widen(load8<T>(K + (size_t)j * rs + x, true));
                 dot += ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
             }
-            const float e = fast_exp2(dot * c - top);
+            const float e = fast_exp2(dot * (p.scale * LOG2E) - top);
             if (!in) continue;
 #pragma unroll
             for (int m = 0; m < MD; ++m)
@@ -309,13 +364,15 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
 
     const int tid = threadIdx.x, lane = tid % WAVE, w = tid / WAVE, n = lane & 31, h2 = lane >> 5;
     int blk, h;
-    work_item(p, p.Hq, blk, h);
+    work_item(p, blk, h);
+    const int rows = 32 * NW / p.HW;
     SeqBlock b;
-    if (!seq_block(p.map, 32 * NW, blk, b)) return;
-    const int q0 = b.idx * 32 * NW, len = b.len;
+    if (!seq_block(p.map, rows, blk, b)) return;
+    const int q0 = b.idx * rows, len = b.len;
     const long ts = b.t0 - q0;
     const int hk = h / p.G;
-    const int i0 = q0 + 32 * w, row = i0 + n;
+    h += w % p.HW;
+    const int i0 = q0 + w / p.HW * 32, row = i0 + n;
     const bool live = row < len;
     const float c = p.scale * LOG2E;
 
@@ -342,7 +399,7 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
     const T* K = static_cast<const T*>(p.k) + ((size_t)ts * p.Hkv + hk) * D;
     const T* V = static_cast<const T*>(p.v) + ((size_t)ts * p.Hkv + hk) * D;
     const size_t rs = (size_t)p.Hkv * D;
-    const KeyTiles kt(q0, min(q0 + 32 * NW, len) - 1, KT, p.window, p.sinks);
+    const KeyTiles kt(q0, min(q0 + rows, len) - 1, KT, p.window, p.sinks);
 
     Stage<T, D, KT, NT> sk, sv;
     auto fetch = [&](int it) {
@@ -358,6 +415,26 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
     f32x16 A[MD];
 #pragma unroll
     for (int m = 0; m < MD; ++m) A[m] = zero16();
+    auto tile = [&](const T* tk, const T* tv, int x, int j0, auto masked) {
+        f32x16 s = zero16(), d = zero16();
+#pragma unroll
+        for (int ks = 0; ks < KD; ++ks) {
+            s = mma32(nat32<T>(tk, ST, 32 * x, 16 * ks, n, h2), qf[ks], s);
+            d = mma32(nat32<T>(tv, ST, 32 * x, 16 * ks, n, h2), gf[ks], d);
+        }
+        const Mask mask(row, j0 + 4 * h2, p.window, p.sinks);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const float e = fast_exp2(fmaf(s[r], c, -lse2)) * (d[r] - delta);
+            s[r] = !masked.value || mask(result_row(r, 0)) ? e : 0.f;
+        }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            const V8 df = rows16<T>(s, kb);
+#pragma unroll
+            for (int m = 0; m < MD; ++m) A[m] = mma32(tr32(tk, ST, 32 * x + 16 * kb, 32 * m, lane), df, A[m]);
+        }
+    };
     fetch(0);
     put(0);
     __syncthreads();
@@ -371,23 +448,7 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
                 const int j0 = kt[it] * KT + 32 * x;
                 const Seen se = seen(i0, i0 + 31, j0, j0 + 31, p.window, p.sinks);
                 if (se.none) continue;
-                f32x16 s = zero16(), d = zero16();
-#pragma unroll
-                for (int ks = 0; ks < KD; ++ks) {
-                    s = mma32(nat32<T>(tk, ST, 32 * x, 16 * ks, n, h2), qf[ks], s);
-                    d = mma32(nat32<T>(tv, ST, 32 * x, 16 * ks, n, h2), gf[ks], d);
-                }
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const bool in = se.all || sees(row, j0 + result_row(r, h2), p.window, p.sinks);
-                    s[r] = in ? fast_exp2(s[r] * c - lse2) * (d[r] - delta) : 0.f;
-                }
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    const V8 df = rows16<T>(s, kb);
-#pragma unroll
-                    for (int m = 0; m < MD; ++m) A[m] = mma32(tr32(tk, ST, 32 * x + 16 * kb, 32 * m, lane), df, A[m]);
-                }
+                if (se.all) tile(tk, tv, x, j0, std::false_type()); else tile(tk, tv, x, j0, std::true_type());
             }
         }
         if (it + 1 < kt.count) {
@@ -407,22 +468,36 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
 
 // ---------------------------------------------------------------- gradients with respect to k and v
 
-// A workgroup owns KB keys of one kv head (32 a wave, k and v in registers)
-// and walks the rows that see them, over every query head of the group:
-// P [rows][keys] with a lane owning a key; dv^T += dO^T P, dk^T += Q^T dS.
+// A workgroup owns KEY_BLOCK keys of one kv head and walks the rows that see
+// them, over every query head of the group. P is formed as [rows][keys], a lane
+// owning a key: dv^T += dO^T P, dk^T += Q^T dS. Both sums and both operands of 32
+// keys would fill a SIMD's registers with one wave, so two waves share the work
+// of 32 keys and 32 rows of every tile: one holds k, forms P, hands it over
+// through LDS and sums dv; the other holds v, forms dP, and dS and dk from it. The
+// sums of a tile's two halves are joined at the end.
 // The rows of a block with sinks reach to the end of the sequence: they are cut
 // into parts of their own workgroups, summed afterwards in a fixed order.
-template <class T> constexpr int swa_key_block() { return 128; }
+constexpr int KEY_BLOCK = 64, GRAD_ROWS = 64;
 
-template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW, 1) swa_dkv_kernel(SwaParams p) {
-    constexpr int RT = swa_tile<T>(), NT = 64 * NW, KB = 32 * NW, ST = tile_stride<T>(D), KD = D / 16, MD = D / 32;
+template <class T, int D> constexpr size_t dkv_lds() {
+    const size_t tiles = sizeof(T) * 4 * GRAD_ROWS * tile_stride<T>(D) + 16 * GRAD_ROWS + 4 * 16 * 64 * 4;
+    const size_t join = KEY_BLOCK * 2 * D * 4;
+    return tiles > join ? tiles : join;
+}
+
+template <class T, int D> __global__ void __launch_bounds__(512, 2) swa_dkv_kernel(SwaParams p) {
+    constexpr int RT = GRAD_ROWS, NT = 512, KB = KEY_BLOCK, ST = tile_stride<T>(D), KD = D / 16, MD = D / 32;
     using V8 = typename Frag<T>::V;
     extern __shared__ __align__(16) unsigned char smem[];
-    lds_poison((uint32_t)(sizeof(T) * 4 * RT * ST + 4 * 4 * RT));
+    lds_poison((uint32_t)dkv_lds<T, D>());
     T* const tiles = reinterpret_cast<T*>(smem);                                   // [2][q, dO][RT][ST]
     float* const stats = reinterpret_cast<float*>(smem + sizeof(T) * 4 * RT * ST);   // [2][lse, delta][RT]
+    f32x4* const box = reinterpret_cast<f32x4*>(stats + 4 * RT);                     // [32 keys, 32 rows][4][lane]: P
 
-    const int tid = threadIdx.x, lane = tid % WAVE, w = tid / WAVE, n = lane & 31, h2 = lane >> 5;
+    const int tid = threadIdx.x, lane = tid % WAVE, n = lane & 31, h2 = lane >> 5;
+    // which 32 keys, which 32 rows of a tile, and which of the two tasks
+    const int w = tid / WAVE % 2, x = tid / WAVE / 2 % 2;
+    const bool grad = tid >= 256;
     const int hk = blockIdx.y;
     SeqBlock b;
     int part = 0;
@@ -461,39 +536,70 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW, 1) 
     const bool live = key < len;
     const float c = p.scale * LOG2E;
 
-    V8 kf[KD], vf[KD];
+    V8 own[KD];   // k or v of the lane's key
     {
-        const size_t r0 = ((size_t)(ts + (live ? key : 0)) * p.Hkv + hk) * D + 8 * h2;
+        const T* src = static_cast<const T*>(grad ? p.v : p.k) + ((size_t)(ts + (live ? key : 0)) * p.Hkv + hk) * D + 8 * h2;
 #pragma unroll
-        for (int ks = 0; ks < KD; ++ks) {
-            kf[ks] = load8<T>(static_cast<const T*>(p.k) + r0 + 16 * ks, live);
-            vf[ks] = load8<T>(static_cast<const T*>(p.v) + r0 + 16 * ks, live);
-        }
+        for (int ks = 0; ks < KD; ++ks) own[ks] = load8<T>(src + 16 * ks, live);
     }
-    f32x16 dK[MD], dV[MD];
+    f32x16 acc[MD];   // dv or dk
 #pragma unroll
-    for (int m = 0; m < MD; ++m) dK[m] = dV[m] = zero16();
+    for (int m = 0; m < MD; ++m) acc[m] = zero16();
 
     const int t0 = ra / RT, per = rb > ra ? (rb - 1) / RT - t0 + 1 : 0, count = per * p.G;
     const size_t rs = (size_t)p.Hq * D;
     Stage<T, D, RT, NT> sq, sg;
     float stat = 0.f;
+    int stat_rows = 0;
     auto fetch = [&](int it) {
         const int h = hk * p.G + it / per, r0 = (t0 + it % per) * RT;
         const size_t at = (size_t)(ts + r0) * p.Hq + h;
         sq.load(static_cast<const T*>(p.q) + at * D, rs, rb - r0, tid);
         sg.load(static_cast<const T*>(p.dO) + at * D, rs, rb - r0, tid);
-        if (tid < 2 * RT) {
-            const int r = tid % RT;
-            const float* src = tid < RT ? p.lse : p.delta;
-            stat = r0 + r < rb ? src[at + (size_t)r * p.Hq] * (tid < RT ? LOG2E : 1.f) : 0.f;
-        }
+        // taken as it lies: arithmetic here would wait for the tiles too
+        stat_rows = rb - r0;
+        if (tid < 2 * RT) stat = (tid < RT ? p.lse : p.delta)[at + (size_t)min(tid % RT, stat_rows - 1) * p.Hq];
     };
     auto put = [&](int it) {
         T* t = tiles + (it & 1) * 2 * RT * ST;
         sq.store(t, tid);
         sg.store(t + RT * ST, tid);
-        if (tid < 2 * RT) stats[(it & 1) * 2 * RT + tid] = stat;
+        if (tid < 2 * RT) stats[(it & 1) * 2 * RT + tid] =
+            tid % RT >= stat_rows ? 0.f : tid < RT ? stat * LOG2E : stat;
+    };
+    f32x4* const mine = box + (w + 2 * x) * (4 * WAVE) + lane;
+    const f32x16 none = zero16();
+    auto product = [&](const T* t) {   // rows of this half against the lane's key
+        f32x16 s = none;
+#pragma unroll
+        for (int ks = 0; ks < KD; ++ks) s = mma32(nat32<T>(t, ST, 32 * x, 16 * ks, n, h2), own[ks], s);
+        return s;
+    };
+    auto sum = [&](const T* t, const f32x16& s) {
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            const V8 f = rows16<T>(s, kb);
+#pragma unroll
+            for (int m = 0; m < MD; ++m) acc[m] = mma32(tr32(t, ST, 32 * x + 16 * kb, 32 * m, lane), f, acc[m]);
+        }
+    };
+    // P from the scores, and over to the other wave
+    auto weigh = [&](f32x16& s, const float* sl, int i0, auto masked) {
+        const Mask mask(i0 + 4 * h2, key, p.window, p.sinks);   // offsets count down from the first row
+        const int from = ra - i0 - 4 * h2;
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+            const f32x4 l4 = *reinterpret_cast<const f32x4*>(sl + 8 * r4 + 4 * h2);
+            f32x4 e;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int o = 8 * r4 + m;   // row - (i0 + 4 h2)
+                const bool in = !masked.value || (o >= from && -o <= mask.last && (-o > mask.first || key < p.sinks));
+                e[m] = in ? fast_exp2(fmaf(s[4 * r4 + m], c, -l4[m])) : 0.f;
+                s[4 * r4 + m] = e[m];
+            }
+            mine[r4 * WAVE] = e;
+        }
     };
     if (count) {
         fetch(0);
@@ -504,77 +610,65 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW, 1) 
         if (it + 1 < count) fetch(it + 1);
         const T* tq = tiles + (it & 1) * 2 * RT * ST;
         const T* tg = tq + RT * ST;
-        const float* sl = stats + (it & 1) * 2 * RT;
-        const float* sd = sl + RT;
-#pragma unroll
-        for (int x = 0; x < RT / 32; ++x) {
-            const int i0 = (t0 + it % per) * RT + 32 * x, j0 = k0 + 32 * w;
-            const Seen se = seen(i0, i0 + 31, j0, j0 + 31, p.window, p.sinks);
-            if (se.none || i0 + 31 < ra || i0 >= rb) continue;
-            const bool all = se.all && i0 >= ra;
-            f32x16 s = zero16(), d = zero16();
-#pragma unroll
-            for (int ks = 0; ks < KD; ++ks) {
-                s = mma32(nat32<T>(tq, ST, 32 * x, 16 * ks, n, h2), kf[ks], s);
-                d = mma32(nat32<T>(tg, ST, 32 * x, 16 * ks, n, h2), vf[ks], d);
+        const float* sl = stats + (it & 1) * 2 * RT + 32 * x;
+        const int i0 = (t0 + it % per) * RT + 32 * x, j0 = k0 + 32 * w;
+        const Seen se = seen(i0, i0 + 31, j0, j0 + 31, p.window, p.sinks);
+        const bool some = !se.none && i0 + 31 >= ra && i0 < rb;
+        f32x16 s = none;
+        if (some) {
+            s = product(grad ? tg : tq);
+            if (!grad) {
+                if (se.all && i0 >= ra) weigh(s, sl, i0, std::false_type()); else weigh(s, sl, i0, std::true_type());
             }
+        }
+        __syncthreads();
+        if (some) {
+            if (grad) {
 #pragma unroll
-            for (int r4 = 0; r4 < 4; ++r4) {
-                const f32x4 l4 = *reinterpret_cast<const f32x4*>(sl + 32 * x + 8 * r4 + 4 * h2);
-                const f32x4 d4 = *reinterpret_cast<const f32x4*>(sd + 32 * x + 8 * r4 + 4 * h2);
+                for (int r4 = 0; r4 < 4; ++r4) {
+                    const f32x4 d4 = *reinterpret_cast<const f32x4*>(sl + RT + 8 * r4 + 4 * h2);
+                    const f32x4 e = mine[r4 * WAVE];
+                    // where P is zero for a hidden row, dP may be anything
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int r = 4 * r4 + m, i = i0 + 8 * r4 + 4 * h2 + m;
-                    const bool in = all || (i >= ra && sees(i, key, p.window, p.sinks));
-                    const float e = in ? fast_exp2(s[r] * c - l4[m]) : 0.f;
-                    d[r] = in ? e * (d[r] - d4[m]) : 0.f;
-                    s[r] = e;
+                    for (int m = 0; m < 4; ++m) s[4 * r4 + m] = e[m] == 0.f ? 0.f : e[m] * (s[4 * r4 + m] - d4[m]);
                 }
             }
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                const V8 pf = rows16<T>(s, kb), df = rows16<T>(d, kb);
-#pragma unroll
-                for (int m = 0; m < MD; ++m) {
-                    dV[m] = mma32(tr32(tg, ST, 32 * x + 16 * kb, 32 * m, lane), pf, dV[m]);
-                    dK[m] = mma32(tr32(tq, ST, 32 * x + 16 * kb, 32 * m, lane), df, dK[m]);
-                }
-            }
+            sum(grad ? tq : tg, s);
         }
         if (it + 1 < count) {
             put(it + 1);
             __syncthreads();
         }
     }
-    if (cut) {
-        float* dst = p.part + ((((size_t)b.seq * p.Hkv + hk) * p.sink_blocks + b.idx) * (1 + p.splits) + part) * (2 * KB * D) +
-                     (size_t)(32 * w + n) * D + 4 * h2;
+    // the second half's sums to the first half's waves, four values a lane and step
+    __syncthreads();
+    f32x4* const so = reinterpret_cast<f32x4*>(smem) + (w + 2 * grad) * (MD * 4 * WAVE) + lane;
+    if (x) {
 #pragma unroll
         for (int m = 0; m < MD; ++m)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                *reinterpret_cast<f32x4*>(dst + 32 * m + 8 * r) =
-                    f32x4{dK[m][4 * r], dK[m][4 * r + 1], dK[m][4 * r + 2], dK[m][4 * r + 3]};
-                *reinterpret_cast<f32x4*>(dst + KB * D + 32 * m + 8 * r) =
-                    f32x4{dV[m][4 * r], dV[m][4 * r + 1], dV[m][4 * r + 2], dV[m][4 * r + 3]};
-            }
-    } else if (live) {
-        const size_t to = ((size_t)(ts + key) * p.Hkv + hk) * D + 4 * h2;
-#pragma unroll
-        for (int m = 0; m < MD; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                store4(static_cast<T*>(p.dk) + to + 32 * m + 8 * r,
-                       f32x4{dK[m][4 * r], dK[m][4 * r + 1], dK[m][4 * r + 2], dK[m][4 * r + 3]} * p.scale);
-                store4(static_cast<T*>(p.dv) + to + 32 * m + 8 * r,
-                       f32x4{dV[m][4 * r], dV[m][4 * r + 1], dV[m][4 * r + 2], dV[m][4 * r + 3]});
-            }
+            for (int r = 0; r < 4; ++r)
+                so[(4 * m + r) * WAVE] = f32x4{acc[m][4 * r], acc[m][4 * r + 1], acc[m][4 * r + 2], acc[m][4 * r + 3]};
     }
+    __syncthreads();
+    if (x) return;
+    float* const part_out = p.part + ((((size_t)b.seq * p.Hkv + hk) * p.sink_blocks + b.idx) * (1 + p.splits) + part) * (2 * KB * D) +
+                            (size_t)grad * (KB * D) + (size_t)(32 * w + n) * D + 4 * h2;
+    T* const out = static_cast<T*>(grad ? p.dk : p.dv) + ((size_t)(ts + key) * p.Hkv + hk) * D + 4 * h2;
+    const float f = grad ? p.scale : 1.f;
+#pragma unroll
+    for (int m = 0; m < MD; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const f32x4 y = f32x4{acc[m][4 * r], acc[m][4 * r + 1], acc[m][4 * r + 2], acc[m][4 * r + 3]} + so[(4 * m + r) * WAVE];
+            if (cut) *reinterpret_cast<f32x4*>(part_out + 32 * m + 8 * r) = y;
+            else if (live) store4(out + 32 * m + 8 * r, y * f);
+        }
 }
 
 // the parts of the blocks with sinks, summed in order
 template <class T, int D> __global__ void __launch_bounds__(256) swa_sink_sum_kernel(SwaParams p) {
-    constexpr int KB = 128;
+    constexpr int KB = KEY_BLOCK;
     lds_poison(0);
     const int kb = blockIdx.x % p.sink_blocks, hk = blockIdx.y, s = blockIdx.x / p.sink_blocks;
     int len;
@@ -597,8 +691,8 @@ template <class T, int D> __global__ void __launch_bounds__(256) swa_sink_sum_ke
         c += *reinterpret_cast<const f32x4*>(src + (size_t)m * (2 * KB * D) + KB * D);
     }
     const size_t to = ((size_t)(ts + key) * p.Hkv + hk) * D + e % D;
-    store4(static_cast<T*>(p.dk) + to, a * p.scale);
-    store4(static_cast<T*>(p.dv) + to, c);
+    store4(static_cast<T*>(p.dv) + to, a);
+    store4(static_cast<T*>(p.dk) + to, c * p.scale);
 }
 
 // ---------------------------------------------------------------- one token over a cache
@@ -816,8 +910,6 @@ template <class K, class P> hipError_t launch(K kern, dim3 grid, int threads, si
 
 size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-constexpr int KEY_BLOCK = 128;
-
 // Parts of the rows beyond the window that see a block with sinks. About as
 // many rows a part as the window gives a block, at most 64 parts in all blocks
 // of a sequence; none where the window covers everything anyway.
@@ -835,7 +927,7 @@ void sink_parts(int T, int window, int sinks, int& blocks, int& splits, int& row
     if (want > most) rows = ((T + splits - 1) / splits + 63) / 64 * 64;
 }
 
-SwaParams make_params(const SwaArgs& a, int rows) {
+SwaParams make_params(const SwaArgs& a, int NW) {
     SwaParams p{};
     p.q = a.q; p.k = a.k; p.v = a.v; p.o = a.o; p.dO = a.dO; p.lse = a.lse;
     p.out = a.out; p.lse_out = a.lse_out;
@@ -845,29 +937,30 @@ SwaParams make_params(const SwaArgs& a, int rows) {
     p.window = std::min(a.window, a.T);
     p.sinks = std::min(a.sinks, a.T);
     p.scale = a.scale;
-    p.blocks = (int)seq_blocks_bound(a.T, a.N, rows, a.cu_seqlens != nullptr);
+    p.HW = heads_together(p.G, NW);
+    p.blocks = (int)seq_blocks_bound(a.T, a.N, 32 * NW / p.HW, a.cu_seqlens != nullptr);
     return p;
 }
 
 template <class T, int D> hipError_t forward(const SwaArgs& a) {
     constexpr int NW = 4;
-    const SwaParams p = make_params(a, 32 * NW);
-    return launch(swa_fwd_kernel<T, D, NW>, dim3(p.blocks * p.Hq), 64 * NW,
+    const SwaParams p = make_params(a, NW);
+    return launch(swa_fwd_kernel<T, D, NW>, dim3(p.blocks * (p.Hq / p.HW)), 64 * NW,
                   sizeof(T) * 4 * swa_tile<T>() * tile_stride<T>(D), a.stream, p);
 }
 
 template <class T, int D> hipError_t backward(const SwaArgs& a) {
     constexpr int NW = 4;
-    SwaParams p = make_params(a, 32 * NW);
+    SwaParams p = make_params(a, NW);
     char* ws = static_cast<char*>(a.workspace);
     p.delta = reinterpret_cast<float*>(ws);
     p.part = reinterpret_cast<float*>(ws + al256((size_t)a.N * a.T * a.Hq * 4));
     sink_parts(a.T, p.window, p.sinks, p.sink_blocks, p.splits, p.split_rows);
     const size_t lds = sizeof(T) * 4 * swa_tile<T>() * tile_stride<T>(D);
-    hipError_t e = launch(swa_dq_kernel<T, D, NW>, dim3(p.blocks * p.Hq), 64 * NW, lds, a.stream, p);
+    hipError_t e = launch(swa_dq_kernel<T, D, NW>, dim3(p.blocks * (p.Hq / p.HW)), 64 * NW, lds, a.stream, p);
     if (e != hipSuccess) return e;
-    e = launch(swa_dkv_kernel<T, D, NW>, dim3(p.blocks + a.N * p.sink_blocks * p.splits, p.Hkv), 64 * NW,
-               lds + 16 * swa_tile<T>(), a.stream, p);
+    p.blocks = (int)seq_blocks_bound(a.T, a.N, KEY_BLOCK, a.cu_seqlens != nullptr);
+    e = launch(swa_dkv_kernel<T, D>, dim3(p.blocks + a.N * p.sink_blocks * p.splits, p.Hkv), 512, dkv_lds<T, D>(), a.stream, p);
     if (e != hipSuccess || p.splits == 0) return e;
     return launch(swa_sink_sum_kernel<T, D>, dim3(a.N * p.sink_blocks, p.Hkv, (KEY_BLOCK * D / 4 + 255) / 256), 256, 0,
                   a.stream, p);
