@@ -23,8 +23,9 @@
 //   dq_t = S_t dO_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,
 //   da_t = <S_{t-1}, G_t>,  dS_0 = a_1 G_1.
 // The same two launches give S at segment starts and G at segment ends (q, dO
-// in place of k, v, in reverse order); a walk stores both at every block, and
-// the last launch takes all blocks in parallel.
+// in place of k, v, in reverse order); the first keeps what it passes at every
+// block as well, so that the last one, block after block of a segment, has S and
+// G at each by one multiplication and addition.
 //
 // Precision. Products of inputs are exact in fp32. bf16 inputs: scores, states
 // and scaled rows enter the next product rounded to bf16, which moves o and the
@@ -47,9 +48,15 @@ struct LinParams {
     SeqMap map;
     int H, L;            // heads; tokens per segment (a multiple of the block)
     bool head_gate;      // gate: one fp32 per head, not per token and head
-    float* seg[2];       // [segment][H][dk][dv]: contributions, then boundary states (0: S, 1: adjoint)
+    float* seg[2];       // [segment][H][dk][dv]: contributions (0: to S, 1: to the adjoint)
+    void* bound[2];      // the same, in the input type: S at segment starts, adjoint at segment ends
     float* seg_decay;    // [segment][H]
-    void* blk[2];        // [block][H][dk][dv] in the input type: S at block starts, adjoint at block ends
+    // Gradient only, per block and direction: the state (adjoint) at its start
+    // (end) as far as it stems from the segment's own tokens, [block][H][dk][dv] in
+    // the input type (not written for the first block walked, where it is zero),
+    // and the product of the decays between the segment's boundary and there.
+    void* blk[2];
+    float* blk_decay[2];
 };
 
 // tokens per block: fp32 tiles are twice as large, and fp32 MFMA makes the
@@ -174,14 +181,14 @@ template <class T, int PARTS> __device__ __forceinline__ void split(typename Fra
 
 // ---------------------------------------------------------------- state walk
 
-// One segment of one head in one direction: the state's transpose (rows dv,
-// columns dk) in accumulators, dk columns split over the waves.
-//   !STORE: from zero; writes the segment's contribution and its decay.
-//   STORE:  from the boundary state; writes the state before every block.
-template <class T, int DK, int DV, int NW, bool STORE>
+// One segment of one head in one direction, from zero: the state's transpose
+// (rows dv, columns dk) in accumulators, dk columns split over the waves. Writes
+// the segment's contribution and its decay; BLOCKS: what it has at every block
+// on the way too.
+template <class T, int DK, int DV, int NW, bool BLOCKS>
 __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
     constexpr int C = lin_block<T>(), NT = 64 * NW, NPW = DK / 16 / NW, MT = DV / 16;
-    constexpr int SX = tile_stride<T>(DV), SY = tile_stride<T>(DK), PARTS = sizeof(T) == 4 ? 1 : STORE ? 2 : 3;
+    constexpr int SX = tile_stride<T>(DV), SY = tile_stride<T>(DK), PARTS = sizeof(T) == 4 ? 1 : 3;
     using V8 = typename Frag<T>::V;
     extern __shared__ __align__(16) unsigned char smem[];
     lds_poison((uint32_t)(sizeof(Decays<C>) + sizeof(T) * C * (SX + SY)));
@@ -189,7 +196,7 @@ __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
     T* sx = reinterpret_cast<T*>(smem + sizeof(Decays<C>));
     T* sy = sx + C * SX;
 
-    const int tid = threadIdx.x, lane = tid % WAVE, w = tid / WAVE, g = lane >> 4, il = lane & 15;
+    const int tid = threadIdx.x, lane = tid % WAVE, w = wave_id(), g = lane >> 4, il = lane & 15;
     const int h = blockIdx.y, rev = blockIdx.z;
     SeqBlock b;
     if (!seq_block(p.map, p.L, blockIdx.x, b)) return;
@@ -203,13 +210,7 @@ __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
 #pragma unroll
     for (int x = 0; x < NPW; ++x)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            if constexpr (STORE)
-                acc[x][m] = *reinterpret_cast<const f32x4*>(p.seg[rev] + at * (DK * DV) +
-                                                            (size_t)(16 * (w * NPW + x) + il) * DV + 16 * m + 4 * g);
-            else
-                acc[x][m] = zero4();
-        }
+        for (int m = 0; m < MT; ++m) acc[x][m] = zero4();
 
     Stage<T, DV, C, NT> stx;
     Stage<T, DK, C, NT> sty;
@@ -226,14 +227,17 @@ __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
     fetch(0);
     for (int step = 0; step < nc; ++step) {
         const int c = rev ? nc - 1 - step : step;
-        if constexpr (STORE) {
-            T* dst = static_cast<T*>(p.blk[rev]) + ((size_t)((long)blockIdx.x * (p.L / C) + c) * p.H + h) * (DK * DV);
+        if constexpr (BLOCKS) {
+            const size_t to = (size_t)((long)blockIdx.x * (p.L / C) + c) * p.H + h;
+            if (tid == 0) p.blk_decay[rev][to] = decay;
+            if (step) {
+                T* dst = static_cast<T*>(p.blk[rev]) + to * (DK * DV);
 #pragma unroll
-            for (int x = 0; x < NPW; ++x)
+                for (int x = 0; x < NPW; ++x)
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    store4(dst + (size_t)(16 * (w * NPW + x) + il) * DV + 16 * m + 4 * g, acc[x][m]);
-            if (step == nc - 1) break;
+                    for (int m = 0; m < MT; ++m)
+                        store4(dst + (size_t)(16 * (w * NPW + x) + il) * DV + 16 * m + 4 * g, acc[x][m]);
+            }
         }
         if (step) __syncthreads();
         stx.store(sx, tid);
@@ -266,23 +270,23 @@ __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
                     for (int x = 0; x < NPW; ++x) acc[x][m] = mma(xf[m], part[x][e], acc[x][m]);
         }
     }
-    if constexpr (!STORE) {
 #pragma unroll
-        for (int x = 0; x < NPW; ++x)
+    for (int x = 0; x < NPW; ++x)
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-                *reinterpret_cast<f32x4*>(p.seg[rev] + at * (DK * DV) + (size_t)(16 * (w * NPW + x) + il) * DV + 16 * m +
-                                          4 * g) = acc[x][m];
-        if (tid == 0 && !rev) p.seg_decay[at] = decay;
-    }
+        for (int m = 0; m < MT; ++m)
+            *reinterpret_cast<f32x4*>(p.seg[rev] + at * (DK * DV) + (size_t)(16 * (w * NPW + x) + il) * DV + 16 * m + 4 * g) =
+                acc[x][m];
+    if (tid == 0 && !rev) p.seg_decay[at] = decay;
 }
 
 // ---------------------------------------------------------------- scan over segments
 
 // Elementwise over dk x dv, one (sequence, head) per blockIdx.x. Direction 0:
-// every segment's contribution is replaced by the state at its start, the end
-// is S_T. Direction 1: by the adjoint at its end, the beginning is dS0.
-__global__ void __launch_bounds__(256) lin_scan_kernel(LinParams p, int dkdv) {
+// from the segments' contributions the state at each segment's start, and S_T.
+// Direction 1: the adjoint at each one's end, and dS0. Summed in fp32; at the
+// boundaries in between the states are kept as they enter products, in the
+// input type.
+template <class T> __global__ void __launch_bounds__(256) lin_scan_kernel(LinParams p, int dkdv) {
     lds_poison(0);
     const int s = blockIdx.x / p.H, h = blockIdx.x % p.H, rev = blockIdx.z;
     const int e = 4 * (blockIdx.y * 256 + threadIdx.x);
@@ -320,7 +324,7 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(LinParams p, int dkdv) {
         for (int u = 0; u < U; ++u) {
             if (b0 + u >= nb) break;
             const int b = rev ? nb - 1 - (b0 + u) : b0 + u;
-            *reinterpret_cast<f32x4*>(p.seg[rev] + ((size_t)(first + b) * p.H + h) * dkdv + e) = cur;
+            store4(static_cast<T*>(p.bound[rev]) + ((size_t)(first + b) * p.H + h) * dkdv + e, cur);
             cur = cur * d[u] + z[u];
         }
     }
@@ -349,7 +353,7 @@ __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
     T* sv = sk + C * SK;
     T* sp = sv + C * SV;   // [i][j] decayed scores
 
-    const int tid = threadIdx.x, lane = tid % WAVE, w = tid / WAVE, g = lane >> 4, il = lane & 15;
+    const int tid = threadIdx.x, lane = tid % WAVE, w = wave_id(), g = lane >> 4, il = lane & 15;
     const int h = blockIdx.y;
     SeqBlock b;
     const bool some = seq_block(p.map, p.L, blockIdx.x, b);
@@ -372,20 +376,23 @@ __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
     };
     if (nc) fetch(0);
     f32x4 S[NPW][MT];
-    const float* init = WHOLE ? (p.S0 ? p.S0 + ends : nullptr)
-                              : p.seg[0] + ((size_t)blockIdx.x * p.H + h) * (DK * DV);
-#pragma unroll
-    for (int x = 0; x < NPW; ++x)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) S[x][m] = zero4();
-    if (init) {
+    auto start = [&](const auto* src) {
 #pragma unroll
         for (int x = 0; x < NPW; ++x)
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    S[x][m][r] = init[(size_t)(16 * m + 4 * g + r) * DV + 16 * (w * NPW + x) + il];
+                    S[x][m][r] = from_el(src[(size_t)(16 * m + 4 * g + r) * DV + 16 * (w * NPW + x) + il]);
+    };
+    if constexpr (WHOLE) {
+#pragma unroll
+        for (int x = 0; x < NPW; ++x)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) S[x][m] = zero4();
+        if (p.S0) start(p.S0 + ends);
+    } else {
+        start(static_cast<const T*>(p.bound[0]) + ((size_t)blockIdx.x * p.H + h) * (DK * DV));
     }
     zero_pad_cols<T, DK>(sq, C, tid, NT);
     zero_pad_cols<T, DK>(sk, C, tid, NT);
@@ -496,71 +503,55 @@ __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
 
 // ---------------------------------------------------------------- gradients
 
-// One block of one head. With the start state S and the end adjoint E:
+// The blocks of one segment of one head. With the start state S and the end
+// adjoint E of a block:
 //   dq_i = G_i S dO_i + sum_{j<=i} D_ij (dO_i . v_j) k_j
 //   dk_j = d_j E v_j  + sum_{i>=j} D_ij (dO_i . v_j) q_i
 //   dv_j = d_j E^T k_j + sum_{i>=j} D_ij (q_i . k_j) dO_i
 // and da_t by its definition as a sum over the pairs (j, i), j < t <= i, of
-// their products without a_t: M_ij = (q_i . k_j)(dO_i . v_j) weighted with
-// a_{j+1}..a_{t-1} and a_{t+1}..a_i, where the start state takes the place of
-// an earlier token (r_i = q_i . S dO_i), the end adjoint that of a later one
-// (c_j = k_j . E v_j), and both together give <S, E>:
-//   R_0[i] = r_i,  R_{t+1}[i] = a_t R_t[i] + M_it        (scan along a row)
-//   da_t = sum_{i>=t} a_{t+1}..a_i R_t[i]                (and down a column)
+// their products without a_t: with M_ij = (q_i . k_j)(dO_i . v_j),
+//   da_t = sum_{i>=t} D_it R_it,   R_it = sum_{j<t} M_ij D_{t-1,j} + G_{t-1} r_i
+//        + d_t (G_{t-1} <S, E> + sum_{j<t} D_{t-1,j} c_j)
+// where the start state takes the place of an earlier token (r_i = q_i . S dO_i)
+// and the end adjoint that of a later one (c_j = k_j . E v_j). R is one more
+// small matrix product.
 template <class T, int DK, int DV, bool DG> struct LinGradTiles {
-    static constexpr int C = lin_block<T>(), NW = (DK > DV ? DK : DV) / 16;
-    static constexpr int SK = tile_stride<T>(DK), SV = tile_stride<T>(DV), SP = tile_stride<T>(C), SM = C + 1;
-    static constexpr int GROWS = DK < 32 ? 32 : DK;
+    // A wave owns MP of the 16-row tiles of dk and dv for a part of a block's
+    // tokens (one of TS). bf16: two row tiles and half the tokens, which reads half
+    // as much LDS as one and all of them; fp32 has no registers for that.
+    static constexpr int C = lin_block<T>(), NM = (DK > DV ? DK : DV) / 16;
+    static constexpr int TS = sizeof(T) == 2 ? 2 : 1, MP = sizeof(T) == 2 && NM > 1 ? 2 : 1, NW = TS * NM / MP;
+    static constexpr int SK = tile_stride<T>(DK), SV = tile_stride<T>(DV), SP = tile_stride<T>(C);
+    static constexpr int EROWS = DK < 32 ? 32 : DK;
     Decays<C> dec;
     alignas(16) T q[C * SK], k[C * SK], v[C * SV], dO[C * SV];
-    alignas(16) T E[GROWS * SV];
-    alignas(16) T p[C * SP], b[C * SP];   // decayed scores and decayed dO . v, [i][j]
-    float M[DG ? C * SM : 1];
-    float r[DG ? NW * C : 1], c[DG ? NW * C : 1], x[NW];
+    alignas(16) T E[EROWS * SV];
+    alignas(16) T p[C * SP], b[C * SP];                       // decayed scores and decayed dO . v, [i][j]
+    alignas(16) T M[DG ? C * SP : 8], D[DG ? C * SP : 8];     // [i][j], and D_{t-1,j} as [t][j]
+    alignas(16) float r[DG ? NM * C : 4], c[DG ? NM * C : 4], x[NM], da[DG ? C / 16 * C : 4];
 };
 
 template <class T, int DK, int DV, bool DG>
-__global__ void __launch_bounds__(4 * (DK > DV ? DK : DV)) lin_grad_kernel(LinParams p) {
+__global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_grad_kernel(LinParams p) {
     using L = LinGradTiles<T, DK, DV, DG>;
-    constexpr int C = L::C, NW = L::NW, NT = 64 * NW, CT = C / 16, SK = L::SK, SV = L::SV, SP = L::SP, SM = L::SM;
-    constexpr int KSK = tile_cols<T>(DK) / 32, KSV = tile_cols<T>(DV) / 32;
+    constexpr int C = L::C, NW = L::NW, MP = L::MP, NT = 64 * NW, CT = C / 16, HT = CT / L::TS, SK = L::SK, SV = L::SV, SP = L::SP;
+    constexpr int KSK = tile_cols<T>(DK) / 32, KSV = tile_cols<T>(DV) / 32, KC = C / 32;
+    constexpr int NS = (DK / 16 + MP - 1) / MP;   // waves that share in sums over dk
     using V8 = typename Frag<T>::V;
     extern __shared__ __align__(16) unsigned char smem[];
     lds_poison((uint32_t)sizeof(L));
     L& s = *reinterpret_cast<L*>(smem);
 
-    const int tid = threadIdx.x, lane = tid % WAVE, w = tid / WAVE, g = lane >> 4, il = lane & 15;
+    const int tid0 = threadIdx.x, w = wave_id();
+    int tid = tid0, lane = tid0 % WAVE, g = lane >> 4, il = lane & 15;
+    const int wm = w % (NW / L::TS) * MP, th = w / (NW / L::TS);   // first row tile of dk and dv, part of the tokens
     const int h = blockIdx.y;
-    const int per = p.L / C;
     SeqBlock b;
-    if (!seq_block(p.map, p.L, blockIdx.x / per, b)) return;
-    const int c = blockIdx.x % per;
-    const int n = min(C, b.n - c * C);
-    if (n <= 0) return;
-    const long t0 = b.t0 + (long)c * C;
-    const size_t r0 = (size_t)t0 * p.H + h, rk = (size_t)p.H * DK, rv = (size_t)p.H * DV;
-    const size_t at = ((size_t)blockIdx.x * p.H + h) * (DK * DV);
+    if (!seq_block(p.map, p.L, blockIdx.x, b)) return;
+    const int nc = (b.n + C - 1) / C;
+    const size_t rk = (size_t)p.H * DK, rv = (size_t)p.H * DV;
 
-    {
-        Stage<T, DK, C, NT> a, bb;
-        Stage<T, DV, C, NT> cc, dd;
-        Stage<T, DV, DK, NT> ee;
-        a.load(static_cast<const T*>(p.q) + r0 * DK, rk, n, tid);
-        bb.load(static_cast<const T*>(p.k) + r0 * DK, rk, n, tid);
-        cc.load(static_cast<const T*>(p.v) + r0 * DV, rv, n, tid);
-        dd.load(static_cast<const T*>(p.dO) + r0 * DV, rv, n, tid);
-        ee.load(static_cast<const T*>(p.blk[1]) + at, DV, DK, tid);
-        if (w == 0) {
-            DecayLoad<T> x(p, h);
-            x.load(p, t0, h, lane, n);
-            block_decays<C, true>(s.dec, x.value(p, lane), lane);
-        }
-        a.store(s.q, tid);
-        bb.store(s.k, tid);
-        cc.store(s.v, tid);
-        dd.store(s.dO, tid);
-        ee.store(s.E, tid);
-    }
+    // what lies beyond a tile's columns, and above the diagonal, stays zero
     zero_pad_cols<T, DK>(s.q, C, tid, NT);
     zero_pad_cols<T, DK>(s.k, C, tid, NT);
     zero_pad_cols<T, DV>(s.v, C, tid, NT);
@@ -568,180 +559,321 @@ __global__ void __launch_bounds__(4 * (DK > DV ? DK : DV)) lin_grad_kernel(LinPa
     zero_pad_cols<T, DV>(s.E, DK, tid, NT);
     if constexpr (DK < 32)   // rows 16..31 of E are contracted over too
         for (int e = tid; e < 16 * SV; e += NT) s.E[16 * SV + e] = T(0);
+    for (int e = tid; e < C * SP; e += NT) {
+        s.p[e] = s.b[e] = T(0);
+        if constexpr (DG) s.M[e] = s.D[e] = T(0);
+    }
 
-    // S rows of this wave's dk tile: dv is contracted
-    V8 sf[KSV];
-    if (w < DK / 16) {
-        const T* src = static_cast<const T*>(p.blk[0]) + at + (size_t)(16 * w + il) * DV + 4 * g;
+    // Boundary states, as they lie in memory until used: E where this thread
+    // stages it, S where this wave has dk rows (dv is contracted). Held for the
+    // segment, and loaded ahead for the next block.
+    using StageE = Stage<T, DV, DK, NT>;
+    using R4 = typename Raw4<T>::V;
+    struct RowS {
+        R4 x[KSV][2];
+        __device__ __forceinline__ void load(const T* src) {
 #pragma unroll
-        for (int ks = 0; ks < KSV; ++ks) {
-            f32x8 x;
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                x[m] = from_el(src[32 * ks + m]);
-                x[4 + m] = DV >= 32 ? from_el(src[32 * ks + (DV >= 32 ? 16 : 0) + m]) : 0.f;
+            for (int ks = 0; ks < KSV; ++ks) {
+                x[ks][0] = *reinterpret_cast<const R4*>(src + 32 * ks);
+                x[ks][1] = DV >= 32 ? *reinterpret_cast<const R4*>(src + 32 * ks + (DV >= 32 ? 16 : 0)) : R4(0);
             }
-            sf[ks] = narrow<T>(x);
         }
-    }
-    __syncthreads();
-
-    // pairs of row tiles, transposed: rows j, columns i
-    for (int e = w; e < CT * (CT + 1) / 2; e += NW) {
-        int ti = 0, tj = e;
-        while (tj > ti) { tj -= ti + 1; ++ti; }
-        f32x4 x = zero4(), y = zero4();
+    };
+    size_t srow[MP];
 #pragma unroll
-        for (int ks = 0; ks < KSK; ++ks)
-            x = mma(frag_nat(s.k, SK, 16 * tj + il, 32 * ks, g), frag_nat(s.q, SK, 16 * ti + il, 32 * ks, g), x);
+    for (int m = 0; m < MP; ++m) srow[m] = (size_t)(min(16 * (wm + m), DK - 16) + il) * DV + 4 * g;
+    const size_t seg = ((size_t)blockIdx.x * p.H + h) * (DK * DV);
+    StageE segE, locE;
+    RowS segS[MP], locS[MP];
+    segE.load(static_cast<const T*>(p.bound[1]) + seg, DV, DK, tid);
 #pragma unroll
-        for (int ks = 0; ks < KSV; ++ks)
-            y = mma(frag_nat(s.v, SV, 16 * tj + il, 32 * ks, g), frag_nat(s.dO, SV, 16 * ti + il, 32 * ks, g), y);
-        const f32x4 d = tile_decays<C>(s.dec, ti, tj, g, il);
-        if constexpr (DG) {
-            float* m = s.M + (16 * ti + il) * SM + 16 * tj + 4 * g;
+    for (int m = 0; m < MP; ++m) {
+        segS[m].load(static_cast<const T*>(p.bound[0]) + seg + srow[m]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) m[r] = x[r] * y[r];
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const bool in = tj < ti || 4 * g + r <= il;
-            x[r] = in ? x[r] * d[r] : 0.f;
-            y[r] = in ? y[r] * d[r] : 0.f;
-        }
-        const int to = (16 * ti + il) * SP + 16 * tj + 4 * g;
-        store4(s.p + to, x);
-        store4(s.b + to, y);
-        if (ti == tj && ti % 2 == 0) {   // the other half of a 32-deep step
-            store4(s.p + to + 16, zero4());
-            store4(s.b + to + 16, zero4());
-        }
+        for (int ks = 0; ks < KSV; ++ks) locS[m].x[ks][0] = locS[m].x[ks][1] = R4(0);   // the first block's own share
     }
 
-    // products with the boundary states
-    f32x4 aq[CT], ak[CT], av[CT];
+    Stage<T, DK, C, NT> stq, stk;
+    Stage<T, DV, C, NT> stv, sto;
+    DecayLoad<T> a(p, h);
+    float preS = 1.f, preE = 1.f;
+    // The next block's loads, in three parts between the phases of this one: a
+    // wave waits where the memory pipe is full, and registers are freest last.
+    auto fetch_qk = [&](int c) {
+        const long t = b.t0 + (long)c * C;
+        const size_t r0 = (size_t)t * p.H + h;
+        const int n = min(C, b.n - c * C);
+        stq.load(static_cast<const T*>(p.q) + r0 * DK, rk, n, tid);
+        stk.load(static_cast<const T*>(p.k) + r0 * DK, rk, n, tid);
+        if (w == 0) a.load(p, t, h, lane, n);
+    };
+    auto fetch_vo = [&](int c) {
+        const size_t r0 = (size_t)(b.t0 + (long)c * C) * p.H + h;
+        const int n = min(C, b.n - c * C);
+        stv.load(static_cast<const T*>(p.v) + r0 * DV, rv, n, tid);
+        sto.load(static_cast<const T*>(p.dO) + r0 * DV, rv, n, tid);
+    };
+    auto fetch_states = [&](int c) {
+        const size_t bs = (size_t)((long)blockIdx.x * (p.L / C) + c) * p.H + h;
+        locE.load(static_cast<const T*>(p.blk[1]) + bs * (DK * DV), DV, c + 1 < nc ? DK : 0, tid);
+        if (c) {
 #pragma unroll
-    for (int tt = 0; tt < CT; ++tt) aq[tt] = ak[tt] = av[tt] = zero4();
-    if (w < DK / 16) {
-        float xe = 0.f;
+            for (int m = 0; m < MP; ++m) locS[m].load(static_cast<const T*>(p.blk[0]) + bs * (DK * DV) + srow[m]);
+        }
+        preS = p.blk_decay[0][bs];
+        preE = p.blk_decay[1][bs];
+    };
+    fetch_qk(0);
+    fetch_vo(0);
+    fetch_states(0);
+    for (int c = 0; c < nc; ++c) {
+        tid = here(tid0);
+        lane = tid % WAVE;
+        g = lane >> 4;
+        il = lane & 15;
+        const long t0 = b.t0 + (long)c * C;
+        const int n = min(C, b.n - c * C);
+        const size_t r0 = (size_t)t0 * p.H + h;
+        if (c) __syncthreads();   // the last block's reads are done, its decays' too
+        stq.store(s.q, tid);
+        stk.store(s.k, tid);
+        stv.store(s.v, tid);
+        sto.store(s.dO, tid);
+        // the states at this block: the segment's, decayed, and its own tokens' share
 #pragma unroll
-        for (int ks = 0; ks < KSV; ++ks) {
-            const V8 ef = frag_kpos(s.E, SV, 16 * w + il, 32 * ks, g);
+        for (int m = 0; m < StageE::N; ++m) {
+            if constexpr (sizeof(T) == 2) {
+                const u32x4 x = locE.r[m], y = raw_here(segE.r[m]);
+                u32x2 lo, hi;
+                store4(reinterpret_cast<T*>(&lo), values(u32x2{y[0], y[1]}) * preE + values(u32x2{x[0], x[1]}));
+                store4(reinterpret_cast<T*>(&hi), values(u32x2{y[2], y[3]}) * preE + values(u32x2{x[2], x[3]}));
+                locE.r[m] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+            } else {
+                locE.r[m] = __builtin_bit_cast(u32x4, values(raw_here(segE.r[m])) * preE + values(locE.r[m]));
+            }
+        }
+        locE.store(s.E, tid);
+        V8 sf[MP][KSV];
+#pragma unroll
+        for (int m = 0; m < MP; ++m)
+#pragma unroll
+            for (int ks = 0; ks < KSV; ++ks)
+                sf[m][ks] = narrow<T>(dtiles_to_frag(values(raw_here(segS[m].x[ks][0])) * preS + values(locS[m].x[ks][0]),
+                                                     values(raw_here(segS[m].x[ks][1])) * preS + values(locS[m].x[ks][1])));
+        if (w == 0) block_decays<C, true>(s.dec, a.value(p, lane), lane);
+        __syncthreads();
+        if (c + 1 < nc) fetch_qk(c + 1);
+
+        // pairs of row tiles, transposed: rows j, columns i
+        for (int e = w; e < CT * (CT + 1) / 2; e += NW) {
+            int ti = 0, tj = e;
+            while (tj > ti) { tj -= ti + 1; ++ti; }
+            f32x4 x = zero4(), y = zero4();
+#pragma unroll
+            for (int ks = 0; ks < KSK; ++ks)
+                x = mma(frag_nat(s.k, SK, 16 * tj + il, 32 * ks, g), frag_nat(s.q, SK, 16 * ti + il, 32 * ks, g), x);
+#pragma unroll
+            for (int ks = 0; ks < KSV; ++ks)
+                y = mma(frag_nat(s.v, SV, 16 * tj + il, 32 * ks, g), frag_nat(s.dO, SV, 16 * ti + il, 32 * ks, g), y);
+            const f32x4 d = tile_decays<C>(s.dec, ti, tj, g, il);
+            const int to = (16 * ti + il) * SP + 16 * tj + 4 * g;
+            f32x4 m = zero4();
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const bool in = tj < ti || 4 * g + r <= il;
+                m[r] = in ? x[r] * y[r] : 0.f;
+                x[r] = in ? x[r] * d[r] : 0.f;
+                y[r] = in ? y[r] * d[r] : 0.f;
+            }
+            store4(s.p + to, x);
+            store4(s.b + to, y);
             if constexpr (DG) {
-                const f32x8 e8 = widen(ef) * widen(sf[ks]);
-                xe += ((e8[0] + e8[1]) + (e8[2] + e8[3])) + ((e8[4] + e8[5]) + (e8[6] + e8[7]));
-            }
-#pragma unroll
-            for (int tt = 0; tt < CT; ++tt) {
-                aq[tt] = mma(sf[ks], frag_kpos(s.dO, SV, 16 * tt + il, 32 * ks, g), aq[tt]);
-                ak[tt] = mma(ef, frag_kpos(s.v, SV, 16 * tt + il, 32 * ks, g), ak[tt]);
+                store4(s.M + to, m);
+                if (16 * ti + il + 1 < C) store4(s.D + to + SP, d);
             }
         }
-        if constexpr (DG) {
-            xe = wave_sum(xe);
-            if (lane == 0) s.x[w] = xe;
-#pragma unroll
-            for (int tt = 0; tt < CT; ++tt) {
-                const int i = 16 * tt + il;
-                float rr = 0.f, cc = 0.f;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    rr += aq[tt][r] * from_el(s.q[i * SK + 16 * w + 4 * g + r]);
-                    cc += ak[tt][r] * from_el(s.k[i * SK + 16 * w + 4 * g + r]);
-                }
-                rr += __shfl_xor(rr, 16, WAVE);
-                rr += __shfl_xor(rr, 32, WAVE);
-                cc += __shfl_xor(cc, 16, WAVE);
-                cc += __shfl_xor(cc, 32, WAVE);
-                if (g == 0) {
-                    s.r[w * C + i] = rr;
-                    s.c[w * C + i] = cc;
-                }
-            }
-        }
-    }
-    if (w < DV / 16) {
-#pragma unroll
-        for (int ks = 0; ks < KSK; ++ks) {
-            const V8 ef = frag_tr(s.E, SV, 32 * ks, 16 * w, g, il);
-#pragma unroll
-            for (int tt = 0; tt < CT; ++tt) av[tt] = mma(ef, frag_kpos(s.k, SK, 16 * tt + il, 32 * ks, g), av[tt]);
-        }
-    }
-#pragma unroll
-    for (int tt = 0; tt < CT; ++tt) {
-        const float gi = s.dec.gam[16 * tt + il], di = s.dec.suf[16 * tt + il];
-        aq[tt] *= gi;
-        ak[tt] *= di;
-        av[tt] *= di;
-    }
-    __syncthreads();
 
-    // products inside the block
-    constexpr int KC = C / 32;
-    if (w < DK / 16) {
-        V8 kf[KC], qf[KC];
+        // products with the boundary states
+        f32x4 aq[MP][HT], ak[MP][HT], av[MP][HT];
+#pragma unroll
+        for (int m = 0; m < MP; ++m)
+#pragma unroll
+            for (int tt = 0; tt < HT; ++tt) aq[m][tt] = ak[m][tt] = av[m][tt] = zero4();
+        if (wm < DK / 16) {
+            float xe = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < KSV; ++ks) {
+                V8 ef[MP];
+#pragma unroll
+                for (int m = 0; m < MP; ++m) {
+                    ef[m] = frag_kpos(s.E, SV, 16 * (wm + m) + il, 32 * ks, g);
+                    if constexpr (DG) xe = dot8(ef[m], sf[m][ks], xe);
+                }
+#pragma unroll
+                for (int tt = 0; tt < HT; ++tt) {
+                    const int i = 16 * (HT * th + tt) + il;
+                    const V8 of = frag_kpos(s.dO, SV, i, 32 * ks, g), vf = frag_kpos(s.v, SV, i, 32 * ks, g);
+#pragma unroll
+                    for (int m = 0; m < MP; ++m) {
+                        aq[m][tt] = mma(sf[m][ks], of, aq[m][tt]);
+                        ak[m][tt] = mma(ef[m], vf, ak[m][tt]);
+                    }
+                }
+            }
+            if constexpr (DG) {
+                if (th == 0) {
+                    xe = wave_sum(xe);
+                    if (lane == 0) s.x[wm / MP] = xe;
+                }
+#pragma unroll
+                for (int tt = 0; tt < HT; ++tt) {
+                    const int i = 16 * (HT * th + tt) + il;
+                    f32x4 x = zero4(), y = zero4();
+#pragma unroll
+                    for (int m = 0; m < MP; ++m) {
+                        x += aq[m][tt] * values(*reinterpret_cast<const R4*>(s.q + i * SK + 16 * (wm + m) + 4 * g));
+                        y += ak[m][tt] * values(*reinterpret_cast<const R4*>(s.k + i * SK + 16 * (wm + m) + 4 * g));
+                    }
+                    float rr = (x[0] + x[1]) + (x[2] + x[3]), cc = (y[0] + y[1]) + (y[2] + y[3]);
+                    rr += __shfl_xor(rr, 16, WAVE);
+                    rr += __shfl_xor(rr, 32, WAVE);
+                    cc += __shfl_xor(cc, 16, WAVE);
+                    cc += __shfl_xor(cc, 32, WAVE);
+                    if (g == 0) {
+                        s.r[wm / MP * C + i] = rr;
+                        s.c[wm / MP * C + i] = cc;
+                    }
+                }
+            }
+        }
+        if (wm < DV / 16) {
+#pragma unroll
+            for (int ks = 0; ks < KSK; ++ks) {
+                V8 ef[MP];
+#pragma unroll
+                for (int m = 0; m < MP; ++m) ef[m] = frag_tr(s.E, SV, 32 * ks, 16 * (wm + m), g, il);
+#pragma unroll
+                for (int tt = 0; tt < HT; ++tt) {
+                    const V8 kf = frag_kpos(s.k, SK, 16 * (HT * th + tt) + il, 32 * ks, g);
+#pragma unroll
+                    for (int m = 0; m < MP; ++m) av[m][tt] = mma(ef[m], kf, av[m][tt]);
+                }
+            }
+        }
+#pragma unroll
+        for (int tt = 0; tt < HT; ++tt) {
+            const int i = 16 * (HT * th + tt) + il;
+            const float gi = s.dec.gam[i], di = s.dec.suf[i];
+#pragma unroll
+            for (int m = 0; m < MP; ++m) {
+                aq[m][tt] *= gi;
+                ak[m][tt] *= di;
+                av[m][tt] *= di;
+            }
+        }
+        __syncthreads();
+        if (c + 1 < nc) fetch_vo(c + 1);
+
+        // products inside the block; a 32-deep step on the wrong side of the
+        // diagonal is skipped
 #pragma unroll
         for (int ks = 0; ks < KC; ++ks) {
-            kf[ks] = frag_tr(s.k, SK, 32 * ks, 16 * w, g, il);
-            qf[ks] = frag_tr(s.q, SK, 32 * ks, 16 * w, g, il);
-        }
+            V8 kf[MP], qf[MP], of[MP];
 #pragma unroll
-        for (int tt = 0; tt < CT; ++tt) {
+            for (int m = 0; m < MP; ++m) {
+                if (wm < DK / 16) {
+                    kf[m] = frag_tr(s.k, SK, 32 * ks, 16 * (wm + m), g, il);
+                    qf[m] = frag_tr(s.q, SK, 32 * ks, 16 * (wm + m), g, il);
+                }
+                if (wm < DV / 16) of[m] = frag_tr(s.dO, SV, 32 * ks, 16 * (wm + m), g, il);
+            }
 #pragma unroll
-            for (int ks = 0; ks <= tt / 2; ++ks) aq[tt] = mma(kf[ks], frag_kpos(s.b, SP, 16 * tt + il, 32 * ks, g), aq[tt]);
+            for (int tt = 0; tt < HT; ++tt) {
+                const int t = HT * th + tt;
+                if (ks <= t / 2 && wm < DK / 16) {
+                    const V8 f = frag_kpos(s.b, SP, 16 * t + il, 32 * ks, g);
 #pragma unroll
-            for (int ks = tt / 2; ks < KC; ++ks)
-                ak[tt] = mma(qf[ks], frag_tr(s.b, SP, 32 * ks, 16 * tt, g, il), ak[tt]);
-            const int i = 16 * tt + il;
-            if (i < n) {
-                const size_t to = (r0 + (size_t)i * p.H) * DK + 16 * w + 4 * g;
-                store4(static_cast<T*>(p.dq) + to, aq[tt]);
-                store4(static_cast<T*>(p.dk) + to, ak[tt]);
+                    for (int m = 0; m < MP; ++m) aq[m][tt] = mma(kf[m], f, aq[m][tt]);
+                }
+                if (ks >= t / 2 && wm < DK / 16) {
+                    const V8 f = frag_tr(s.b, SP, 32 * ks, 16 * t, g, il);
+#pragma unroll
+                    for (int m = 0; m < MP; ++m) ak[m][tt] = mma(qf[m], f, ak[m][tt]);
+                }
+                if (ks >= t / 2 && wm < DV / 16) {
+                    const V8 f = frag_tr(s.p, SP, 32 * ks, 16 * t, g, il);
+#pragma unroll
+                    for (int m = 0; m < MP; ++m) av[m][tt] = mma(of[m], f, av[m][tt]);
+                }
             }
         }
-    }
-    if (w < DV / 16) {
-        V8 of[KC];
 #pragma unroll
-        for (int ks = 0; ks < KC; ++ks) of[ks] = frag_tr(s.dO, SV, 32 * ks, 16 * w, g, il);
+        for (int tt = 0; tt < HT; ++tt) {
+            const int i = 16 * (HT * th + tt) + il;
+            if (i >= n) continue;
 #pragma unroll
-        for (int tt = 0; tt < CT; ++tt) {
-#pragma unroll
-            for (int ks = tt / 2; ks < KC; ++ks)
-                av[tt] = mma(of[ks], frag_tr(s.p, SP, 32 * ks, 16 * tt, g, il), av[tt]);
-            const int i = 16 * tt + il;
-            if (i < n) store4(static_cast<T*>(p.dv) + (r0 + (size_t)i * p.H) * DV + 16 * w + 4 * g, av[tt]);
+            for (int m = 0; m < MP; ++m) {
+                const size_t row = r0 + (size_t)i * p.H;
+                const int col = 16 * (wm + m) + 4 * g;
+                if (wm + m < DK / 16) {
+                    store4(static_cast<T*>(p.dq) + row * DK + col, aq[m][tt]);
+                    store4(static_cast<T*>(p.dk) + row * DK + col, ak[m][tt]);
+                }
+                if (wm + m < DV / 16) store4(static_cast<T*>(p.dv) + row * DV + col, av[m][tt]);
+            }
         }
-    }
 
-    if constexpr (DG) {
-        if (w == 0) {
-            const int i = lane % C;   // C = 32: the upper lanes repeat the lower ones
-            constexpr int NK = DK / 16;
-            float R = 0.f, cl = 0.f, X = 0.f, RC = 0.f;
-            for (int m = 0; m < NK; ++m) {
-                R += s.r[m * C + i];
-                cl += s.c[m * C + i];
-                X += s.x[m];
+        if (c + 1 < nc) fetch_states(c + 1);
+        if constexpr (DG) {
+            // R tiles: rows i, columns t
+            for (int e = w; e < CT * (CT + 1) / 2; e += NW) {
+                int ti = 0, tt = e;
+                while (tt > ti) { tt -= ti + 1; ++ti; }
+                const int t = 16 * tt + il;
+                f32x4 R = zero4();
+                for (int ks = 0; ks <= tt / 2; ++ks)
+                    R = mma(frag_kpos(s.M, SP, 16 * ti + il, 32 * ks, g), frag_kpos(s.D, SP, t, 32 * ks, g), R);
+                f32x4 ri = zero4();
+#pragma unroll
+                for (int m = 0; m < NS; ++m) ri += *reinterpret_cast<const f32x4*>(s.r + m * C + 16 * ti + 4 * g);
+                R += ri * (t ? s.dec.gam[t - 1] : 1.f);
+                float mid = 1.f;
+                for (int m = tt + 1; m < ti; ++m) mid *= s.dec.blk[m];
+                if (tt < ti) mid *= s.dec.col[t];
+                float sum = 0.f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = 16 * ti + 4 * g + r;
+                    const float d = tt < ti ? s.dec.row[i] * mid : 4 * g + r >= il ? s.dec.diag[i * Decays<C>::DST + il] : 0.f;
+                    if (tt < ti || 4 * g + r >= il) sum += R[r] * d;
+                }
+                sum += __shfl_xor(sum, 16, WAVE);
+                sum += __shfl_xor(sum, 32, WAVE);
+                if (g == 0) s.da[ti * C + t] = sum;
             }
-            // along the rows, in place: M_it becomes R_t[i]; the row of the end
-            // adjoint (M_it = c_t, R_0 = <S, E>) is kept by lane t
-            float* row = s.M + i * SM;
-            for (int t = 0; t < C; ++t) {
-                const float m = row[t], at = s.dec.a[t];
-                row[t] = R;
-                if (t == i) RC = X;
-                R = at * R + (t < i ? m : 0.f);
-                X = at * X + __shfl(cl, t, WAVE);
+            __syncthreads();
+            if (w == NW - 1) {
+                const int t = lane % C;   // C = 32: the upper lanes repeat the lower ones
+                float c0 = 0.f, X = 0.f, acc = 0.f;
+                for (int m = 0; m < NS; ++m) {
+                    c0 += s.c[m * C + t];
+                    X += s.x[m];
+                }
+                float part[4] = {X * (t ? s.dec.gam[t - 1] : 1.f), 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < KC; ++ks)
+#pragma unroll
+                    for (int gg = 0; gg < 4; ++gg) {
+                        const f32x8 d = widen(frag_nat(s.D, SP, t, 32 * ks, gg));
+#pragma unroll
+                        for (int m = 0; m < 8; ++m)
+                            part[m & 3] += d[m] * __uint_as_float((uint32_t)__builtin_amdgcn_readlane(
+                                                      (int)__float_as_uint(c0), 32 * ks + 8 * gg + m));
+                    }
+                acc = s.dec.suf[t] * ((part[0] + part[1]) + (part[2] + part[3]));
+                for (int m = t / 16; m < CT; ++m) acc += s.da[m * C + t];
+                if (lane < n) store1(static_cast<T*>(p.dgate) + (size_t)(t0 + lane) * p.H + h, acc);
             }
-            __builtin_amdgcn_wave_barrier();
-            // down the columns
-            float acc = RC;
-            for (int j = C - 1; j >= 0; --j) {
-                if (j >= i) acc = s.M[j * SM + i] + (j == C - 1 ? acc : s.dec.a[j + 1] * acc);
-            }
-            if (lane < n) store1(static_cast<T*>(p.dgate) + (size_t)(t0 + lane) * p.H + h, acc);
         }
     }
 }
@@ -807,21 +939,19 @@ __global__ void __launch_bounds__(NT) lin_decode_kernel(const T* __restrict__ q,
 
 size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Tokens per segment. Enough segments that every CU has two workgroups, at
-// least 128 tokens each so that the extra read of k and v and the states are
-// paid for, and one segment per sequence where sequences are short.
+// Tokens per segment: as few segments as give every CU two workgroups.
 int segment_tokens(int T, int N, int H, bool packed) {
     const long tokens = packed ? T : (long)T * N;
     const long want = tokens * H / 512;
     long L = (want + 63) / 64 * 64;
-    if (L < 128) L = 128;
+    if (L < 64) L = 64;
     const long whole = ((long)T + 63) / 64 * 64;
     return (int)(L < whole ? L : (whole > 0 ? whole : 64));
 }
 bool whole_sequences(int T) { return T <= 256; }
 
 struct LinWorkspace {
-    size_t seg[2], decay, blk[2], total;
+    size_t seg[2], bound[2], decay, blk[2], blk_decay[2], total;
 };
 LinWorkspace workspace_layout(int T, int N, int H, int dk, int dv, bool packed, bool bf16, bool grad, int L) {
     const size_t segs = (size_t)seq_blocks_bound(T, N, L, packed) * H, state = (size_t)dk * dv;
@@ -829,12 +959,17 @@ LinWorkspace workspace_layout(int T, int N, int H, int dk, int dv, bool packed, 
     LinWorkspace w{};
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t r = at; at += al256(bytes); return r; };
+    const size_t es = bf16 ? 2 : 4;
     w.seg[0] = take(segs * state * 4);
+    w.bound[0] = take(segs * state * es);
     w.decay = take(segs * 4);
     if (grad) {
         w.seg[1] = take(segs * state * 4);
-        w.blk[0] = take(blocks * state * (bf16 ? 2 : 4));
-        w.blk[1] = take(blocks * state * (bf16 ? 2 : 4));
+        w.bound[1] = take(segs * state * es);
+        w.blk[0] = take(blocks * state * es);
+        w.blk[1] = take(blocks * state * es);
+        w.blk_decay[0] = take(blocks * 4);
+        w.blk_decay[1] = take(blocks * 4);
     }
     w.total = at;
     return w;
@@ -849,10 +984,10 @@ template <class K> hipError_t launch(K kern, dim3 grid, int threads, size_t lds,
     return hipGetLastError();
 }
 
-template <class T, int DK, int DV, bool STORE>
+template <class T, int DK, int DV, bool BLOCKS>
 hipError_t launch_state(const LinParams& p, int segs, int dirs, hipStream_t st) {
     constexpr int NW = DK / 16 < 4 ? DK / 16 : 4, C = lin_block<T>();
-    return launch(lin_state_kernel<T, DK, DV, NW, STORE>, dim3(segs, p.H, dirs), 64 * NW,
+    return launch(lin_state_kernel<T, DK, DV, NW, BLOCKS>, dim3(segs, p.H, dirs), 64 * NW,
                   sizeof(Decays<C>) + sizeof(T) * C * (tile_stride<T>(DK) + tile_stride<T>(DV)), st, p);
 }
 
@@ -873,7 +1008,7 @@ template <class T, int DK, int DV> hipError_t forward(LinParams p, const LinArgs
     hipError_t e = hipSuccess;
     if (p.map.T > 0) e = launch_state<T, DK, DV, false>(p, segs, 1, a.stream);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(lin_scan_kernel, dim3(p.map.N * p.H, (DK * DV / 4 + 255) / 256, 1), dim3(256), 0, a.stream, p, DK * DV);
+    hipLaunchKernelGGL(lin_scan_kernel<T>, dim3(p.map.N * p.H, (DK * DV / 4 + 255) / 256, 1), dim3(256), 0, a.stream, p, DK * DV);
     e = hipGetLastError();
     if (e != hipSuccess || p.map.T == 0) return e;
     return launch_out<T, DK, DV, false>(p, segs, a.stream);
@@ -883,17 +1018,14 @@ template <class T, int DK, int DV> hipError_t backward(const LinParams& p, const
     const bool packed = p.map.cu != nullptr;
     const int segs = (int)seq_blocks_bound(p.map.T, p.map.N, p.L, packed);
     hipError_t e = hipSuccess;
-    if (p.map.T > 0) e = launch_state<T, DK, DV, false>(p, segs, 2, a.stream);
+    if (p.map.T > 0) e = launch_state<T, DK, DV, true>(p, segs, 2, a.stream);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(lin_scan_kernel, dim3(p.map.N * p.H, (DK * DV / 4 + 255) / 256, 2), dim3(256), 0, a.stream, p, DK * DV);
+    hipLaunchKernelGGL(lin_scan_kernel<T>, dim3(p.map.N * p.H, (DK * DV / 4 + 255) / 256, 2), dim3(256), 0, a.stream, p, DK * DV);
     e = hipGetLastError();
     if (e != hipSuccess || p.map.T == 0) return e;
-    e = launch_state<T, DK, DV, true>(p, segs, 2, a.stream);
-    if (e != hipSuccess) return e;
-    const dim3 grid(segs * (p.L / lin_block<T>()), p.H);
-    constexpr int NT = 4 * (DK > DV ? DK : DV);
-    if (p.head_gate) return launch(lin_grad_kernel<T, DK, DV, false>, grid, NT, sizeof(LinGradTiles<T, DK, DV, false>), a.stream, p);
-    return launch(lin_grad_kernel<T, DK, DV, true>, grid, NT, sizeof(LinGradTiles<T, DK, DV, true>), a.stream, p);
+    const dim3 grid(segs, p.H);
+    if (p.head_gate) return launch(lin_grad_kernel<T, DK, DV, false>, grid, 64 * LinGradTiles<T, DK, DV, false>::NW, sizeof(LinGradTiles<T, DK, DV, false>), a.stream, p);
+    return launch(lin_grad_kernel<T, DK, DV, true>, grid, 64 * LinGradTiles<T, DK, DV, true>::NW, sizeof(LinGradTiles<T, DK, DV, true>), a.stream, p);
 }
 
 template <class T, int DK, int DV> hipError_t decode(const LinDecodeArgs& a) {
@@ -925,7 +1057,9 @@ LinParams make_params(const LinArgs& a) {
     char* base = static_cast<char*>(a.workspace);
     for (int d = 0; d < 2; ++d) {
         p.seg[d] = reinterpret_cast<float*>(base + w.seg[d]);
+        p.bound[d] = base + w.bound[d];
         p.blk[d] = base + w.blk[d];
+        p.blk_decay[d] = reinterpret_cast<float*>(base + w.blk_decay[d]);
     }
     p.seg_decay = reinterpret_cast<float*>(base + w.decay);
     return p;

@@ -496,8 +496,8 @@ template <class T, int D> __global__ void __launch_bounds__(512, 2) swa_dkv_kern
 
     const int tid = threadIdx.x, lane = tid % WAVE, n = lane & 31, h2 = lane >> 5;
     // which 32 keys, which 32 rows of a tile, and which of the two tasks
-    const int w = tid / WAVE % 2, x = tid / WAVE / 2 % 2;
-    const bool grad = tid >= 256;
+    const int w = wave_id() % 2, x = wave_id() / 2 % 2;
+    const bool grad = wave_id() >= 4;
     const int hk = blockIdx.y;
     SeqBlock b;
     int part = 0;
@@ -717,7 +717,7 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
     extern __shared__ __align__(16) unsigned char smem[];
     const uint32_t lds = sizeof(T) * NW * 2 * 32 * ST;
     lds_poison(lds);
-    const int tid = threadIdx.x, lane = tid % WAVE, w = tid / WAVE, n = lane & 31, h2 = lane >> 5;
+    const int tid = threadIdx.x, lane = tid % WAVE, w = wave_id(), n = lane & 31, h2 = lane >> 5;
     T* const tk = reinterpret_cast<T*>(smem) + w * 2 * 32 * ST;
     T* const tv = tk + 32 * ST;
     const int part = blockIdx.x % p.splits, gc = blockIdx.x / p.splits, hk = blockIdx.y, seq = blockIdx.z;

@@ -22,13 +22,14 @@ template <> struct Frag<float> { using V = f32x8; };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// row stride in elements: bf16 D + 16 (rows 8 banks apart modulo 64: the
-// 16-lane groups of a transposing read cover 4 rows x 8 banks), fp32 D + 4
-// (4 rows are 16 banks apart, so the 4 lane groups of a scalar column read
-// cover all banks)
+// row stride in elements: four dwords past a multiple of 32, the banks. Eight
+// consecutive rows are then 4 banks apart and cover all of them with the 16
+// bytes of a nat read each, or with a lane group's 8 dwords of a tr read twice;
+// so are 16 rows with the 8 bytes that two lane groups of a kpos read take. No
+// read above conflicts (with eight dwords, nat and kpos take twice the cycles).
 template <class T> __host__ __device__ constexpr int tile_cols(int d) { return d < 32 ? 32 : d; }
 template <class T> __host__ __device__ constexpr int tile_stride(int d) {
-    return tile_cols<T>(d) + (sizeof(T) == 2 ? 16 : 4);
+    return tile_cols<T>(d) + (sizeof(T) == 2 ? 8 : 4);
 }
 
 __device__ __forceinline__ bf16x8 frag_nat(const uint16_t* t, int st, int row, int k0, int g) {
@@ -72,33 +73,47 @@ __device__ __forceinline__ f32x8 frag_tr(const float* t, int st, int r0, int c0,
     return r;
 }
 
-__device__ __forceinline__ f32x8 widen(const bf16x8& x) {
-    f32x8 r;
-#pragma unroll
-    for (int p = 0; p < 8; ++p) r[p] = (float)x[p];
-    return r;
-}
+__device__ __forceinline__ f32x8 widen(const bf16x8& x) { return __builtin_convertvector(x, f32x8); }
 __device__ __forceinline__ f32x8 widen(const f32x8& x) { return x; }
 
 // fp32 values as an operand of the input type (bf16: rounded to nearest)
 template <class T> __device__ __forceinline__ typename Frag<T>::V narrow(const f32x8& x);
-template <> __device__ __forceinline__ bf16x8 narrow<uint16_t>(const f32x8& x) {
-    bf16x8 r;
-#pragma unroll
-    for (int p = 0; p < 8; ++p) r[p] = (__bf16)x[p];
-    return r;
-}
+template <> __device__ __forceinline__ bf16x8 narrow<uint16_t>(const f32x8& x) { return __builtin_convertvector(x, bf16x8); }
 template <> __device__ __forceinline__ f32x8 narrow<float>(const f32x8& x) { return x; }
+
+// a . b + c over the eight values of two operands, in fp32
+__device__ __forceinline__ float dot8(const bf16x8& a, const bf16x8& b, float c) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int m = 0; m < 8; m += 2)
+        c = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{a[m], a[m + 1]}, bf16x2{b[m], b[m + 1]}, c, false);
+    return c;
+}
+__device__ __forceinline__ float dot8(const f32x8& a, const f32x8& b, float c) {
+#pragma unroll
+    for (int m = 0; m < 8; ++m) c = fmaf(a[m], b[m], c);
+    return c;
+}
 
 // four values to consecutive elements (8 or 16 bytes, aligned)
 __device__ __forceinline__ void store4(uint16_t* p, const f32x4& x) {
     typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-    bf16x4 r;
-#pragma unroll
-    for (int m = 0; m < 4; ++m) r[m] = (__bf16)x[m];
-    *reinterpret_cast<bf16x4*>(p) = r;
+    *reinterpret_cast<bf16x4*>(p) = __builtin_convertvector(x, bf16x4);
 }
 __device__ __forceinline__ void store4(float* p, const f32x4& x) { *reinterpret_cast<f32x4*>(p) = x; }
+
+// four elements as they lie in memory, held whole (arrays of 16-bit elements
+// would take a register each), and their values
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <class T> struct Raw4;
+template <> struct Raw4<uint16_t> { using V = u32x2; };
+template <> struct Raw4<float> { using V = u32x4; };
+__device__ __forceinline__ f32x4 values(const u32x2& x) {
+    return f32x4{__uint_as_float(x[0] << 16), __uint_as_float(x[0] & 0xffff0000u), __uint_as_float(x[1] << 16),
+                 __uint_as_float(x[1] & 0xffff0000u)};
+}
+__device__ __forceinline__ f32x4 values(const u32x4& x) { return __builtin_bit_cast(f32x4, x); }
 
 __device__ __forceinline__ float from_el(uint16_t x) { return bf16_bits_to_f32(x); }
 __device__ __forceinline__ float from_el(float x) { return x; }
@@ -113,7 +128,6 @@ __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
 // rows read as zeros and touch no memory, with no branch around a load.
 template <class T, int D, int R, int NT> struct Stage {
     static constexpr int PER = 16 / (int)sizeof(T), CPR = D / PER, TOT = R * CPR, N = (TOT + NT - 1) / NT;
-    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     u32x4 r[N];
     __device__ __forceinline__ void load(const T* base, size_t stride, int valid, int tid) {
         const uint32_t bytes = (uint32_t)stride * (uint32_t)sizeof(T);
@@ -133,6 +147,25 @@ template <class T, int D, int R, int NT> struct Stage {
         }
     }
 };
+
+// number of the wave in its workgroup, as a scalar: branches and addresses that
+// depend on it stay out of the vector registers
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE); }
+
+// The same value, unknown to the compiler from here on: LDS addresses formed from
+// it inside a loop stay there, where a few additions cost less than the hundreds
+// of registers that hoisting every one of them out of the loop takes (and spills).
+__device__ __forceinline__ int here(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// The same for values held over a loop as they lie in memory, so that what is
+// unpacked from them is not hoisted and held instead.
+template <class V> __device__ __forceinline__ V raw_here(V x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
 
 // zero columns D..31 of a narrow tile
 template <class T, int D> __device__ __forceinline__ void zero_pad_cols(T* tile, int rows, int tid, int nt) {
