@@ -579,7 +579,7 @@ int kda_linattn_decode_step(const void* q, const void* k, const void* v, const v
 
 size_t kda_swa_bwd_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int window, int sinks, int N, int has_cu) {
     if (!swa_sizes_ok(B, Hq, Hkv, T, d, window, sinks, N, has_cu)) return 0;
-    return kda::swa_bwd_workspace_bytes(T, has_cu ? N : B, Hq, Hkv, d, window, sinks);
+    return kda::swa_bwd_workspace_bytes(T, has_cu ? N : B, Hq, Hkv, d, window, sinks, has_cu != 0);
 }
 
 size_t kda_swa_decode_workspace_bytes(int N, int Hq, int Hkv, int d, int window, int sinks) {
@@ -612,7 +612,7 @@ int kda_swa_bwd(const void* q, const void* k, const void* v, const void* o, cons
     if (!aligned(o) || !aligned(lse, 4) || !aligned(dO) || !aligned(grad_q) || !aligned(grad_k) || !aligned(grad_v) ||
         !aligned(workspace))
         return KDA_EALIGN;
-    if (workspace_bytes < kda::swa_bwd_workspace_bytes(T, a.N, Hq, Hkv, d, window, sinks)) return KDA_EINVAL;
+    if (workspace_bytes < kda::swa_bwd_workspace_bytes(T, a.N, Hq, Hkv, d, window, sinks, cu_seqlens != nullptr)) return KDA_EINVAL;
     a.o = o;
     a.lse = lse;
     a.dO = dO;

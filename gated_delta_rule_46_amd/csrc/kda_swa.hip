@@ -30,7 +30,7 @@ struct SwaParams {
     const float* lse;
     void *out, *dq, *dk, *dv;
     float *lse_out, *delta;
-    float* part;            // gradients of sink blocks: [sequence][kv head][block][split][dv, dk][KB][D]
+    float* part;            // gradients of key blocks in parts: [slot][dv, dk][KB][D]
     SeqMap map;
     int Hq, Hkv, G;         // G = Hq / Hkv
     int HW;                 // heads of a group that a workgroup takes together
@@ -38,6 +38,7 @@ struct SwaParams {
     float scale;
     int blocks;             // blocks of rows over all sequences
     int sink_blocks, splits, split_rows;   // gradient: key blocks with sinks, parts of their rows, rows in a part
+    int head_parts;                        // gradient: parts of a group's query heads
 };
 
 __device__ __forceinline__ f32x16 mma32(const bf16x8& a, const bf16x8& b, const f32x16& c) {
@@ -234,10 +235,15 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int x = 0; x < NX; ++x) s[x] = zero16();
+        f32x16 odd = zero16();   // one tile of keys: two chains of products, added
 #pragma unroll
         for (int ks = 0; ks < KD; ++ks)
 #pragma unroll
-            for (int x = 0; x < NX; ++x) s[x] = mma32(kf[x][ks], qf[ks], s[x]);
+            for (int x = 0; x < NX; ++x) {
+                if (NX == 1 && ks % 2) odd = mma32(kf[x][ks], qf[ks], odd);
+                else s[x] = mma32(kf[x][ks], qf[ks], s[x]);
+            }
+        if constexpr (NX == 1) s[0] += odd;
 #pragma unroll
         for (int m = 0; m < MD; ++m) vf[m] = tr32(tv, ST, 0, 32 * m, lane);
         __builtin_amdgcn_sched_barrier(0);
@@ -471,40 +477,61 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
 // A workgroup owns KEY_BLOCK keys of one kv head and walks the rows that see
 // them, over every query head of the group. P is formed as [rows][keys], a lane
 // owning a key: dv^T += dO^T P, dk^T += Q^T dS. Both sums and both operands of 32
-// keys would fill a SIMD's registers with one wave, so two waves share the work
-// of 32 keys and 32 rows of every tile: one holds k, forms P, hands it over
-// through LDS and sums dv; the other holds v, forms dP, and dS and dk from it. The
-// sums of a tile's two halves are joined at the end.
+// keys would fill a SIMD's registers with one wave, so two waves share the work of
+// 32 keys: one holds k, forms P, hands it over through LDS and sums dv; the other
+// holds v, forms dP, and dS and dk from it. A tile has 64 rows, two independent
+// chains of products a wave; it lies in LDS once, the next one in registers, so
+// that two workgroups fit a CU and fill each other's waits.
 // The rows of a block with sinks reach to the end of the sequence: they are cut
 // into parts of their own workgroups, summed afterwards in a fixed order.
 constexpr int KEY_BLOCK = 64, GRAD_ROWS = 64;
 
-template <class T, int D> constexpr size_t dkv_lds() {
-    const size_t tiles = sizeof(T) * 4 * GRAD_ROWS * tile_stride<T>(D) + 16 * GRAD_ROWS + 4 * 16 * 64 * 4;
-    const size_t join = KEY_BLOCK * 2 * D * 4;
-    return tiles > join ? tiles : join;
+// Where a part of a block's gradients is kept. Only blocks with sinks in parts:
+// [sequence][kv head][block][part]; every block, by its heads: [item][kv head][part
+// of the heads], an item being a block or a further part of a block with sinks.
+__host__ __device__ inline size_t part_slot(const SwaParams& p, int item, int seq, int idx, int part, int hk, int hp) {
+    if (p.head_parts > 1) return ((size_t)item * p.Hkv + hk) * p.head_parts + hp;
+    return (((size_t)seq * p.Hkv + hk) * p.sink_blocks + idx) * (1 + p.splits) + part;
 }
 
-template <class T, int D> __global__ void __launch_bounds__(512, 2) swa_dkv_kernel(SwaParams p) {
-    constexpr int RT = GRAD_ROWS, NT = 512, KB = KEY_BLOCK, ST = tile_stride<T>(D), KD = D / 16, MD = D / 32;
+template <class T, int D> constexpr size_t dkv_lds() {
+    return sizeof(T) * 2 * GRAD_ROWS * tile_stride<T>(D) + 8 * GRAD_ROWS + KEY_BLOCK * GRAD_ROWS * 4;
+}
+
+template <class T, int D> __global__ void __launch_bounds__(256, 2) swa_dkv_kernel(SwaParams p) {
+    constexpr int RT = GRAD_ROWS, NX = RT / 32, NT = 256, KB = KEY_BLOCK, ST = tile_stride<T>(D), KD = D / 16, MD = D / 32;
     using V8 = typename Frag<T>::V;
     extern __shared__ __align__(16) unsigned char smem[];
     lds_poison((uint32_t)dkv_lds<T, D>());
-    T* const tiles = reinterpret_cast<T*>(smem);                                   // [2][q, dO][RT][ST]
-    float* const stats = reinterpret_cast<float*>(smem + sizeof(T) * 4 * RT * ST);   // [2][lse, delta][RT]
-    f32x4* const box = reinterpret_cast<f32x4*>(stats + 4 * RT);                     // [32 keys, 32 rows][4][lane]: P
+    T* const tq = reinterpret_cast<T*>(smem);   // q and dO of a tile, [RT][ST] each
+    T* const tg = tq + RT * ST;
+    float* const stats = reinterpret_cast<float*>(tg + RT * ST);   // [lse, delta][RT]
+    f32x4* const box = reinterpret_cast<f32x4*>(stats + 2 * RT);   // [32 keys][32 rows][4][lane]: P
 
     const int tid = threadIdx.x, lane = tid % WAVE, n = lane & 31, h2 = lane >> 5;
-    // which 32 keys, which 32 rows of a tile, and which of the two tasks
-    const int w = wave_id() % 2, x = wave_id() / 2 % 2;
-    const bool grad = wave_id() >= 4;
-    const int hk = blockIdx.y;
+    const int w = wave_id() % 2;   // which 32 keys
+    const bool grad = wave_id() >= 2;
+    // neighbouring key blocks, which read the same rows, on one XCD; parts of
+    // blocks with sinks behind them
+    const int heads = p.Hkv * p.head_parts, items = p.blocks * heads;
+    int hk, item;
+    if ((int)blockIdx.x < items) {
+        const int e = xcd_remap(blockIdx.x, items);
+        hk = e / p.blocks;
+        item = e % p.blocks;
+    } else {
+        hk = (blockIdx.x - items) % heads;
+        item = p.blocks + (blockIdx.x - items) / heads;
+    }
+    const int hp = hk % p.head_parts;
+    hk /= p.head_parts;
+    const int ga = hp * p.G / p.head_parts, gn = (hp + 1) * p.G / p.head_parts - ga;   // the group's heads taken here
     SeqBlock b;
     int part = 0;
-    if ((int)blockIdx.x < p.blocks) {
-        if (!seq_block(p.map, KB, blockIdx.x, b)) return;
+    if (item < p.blocks) {
+        if (!seq_block(p.map, KB, item, b)) return;
     } else {   // parts 1.. of the blocks with sinks, of every sequence
-        const int e = blockIdx.x - p.blocks;
+        const int e = item - p.blocks;
         part = 1 + e % p.splits;
         const int kb = (e / p.splits) % p.sink_blocks, s = e / p.splits / p.sink_blocks;
         if (p.map.cu) {
@@ -523,9 +550,9 @@ template <class T, int D> __global__ void __launch_bounds__(512, 2) swa_dkv_kern
     }
     const int k0 = b.idx * KB, len = b.len;
     const long ts = b.t0 - k0;
-    const bool cut = p.splits > 0 && b.idx < p.sink_blocks;
+    const bool sink = p.splits > 0 && b.idx < p.sink_blocks, cut = sink || p.head_parts > 1;
     // rows of this workgroup: the window's, or the rest of the sequence in parts
-    const long reach = k0 < p.sinks && !cut ? (long)len : min((long)k0 + KB - 1 + p.window, (long)len);
+    const long reach = k0 < p.sinks && !sink ? (long)len : min((long)k0 + KB - 1 + p.window, (long)len);
     int ra = k0, rb = (int)reach;
     if (part > 0) {
         const long a = reach + (long)(part - 1) * p.split_rows;
@@ -546,13 +573,13 @@ template <class T, int D> __global__ void __launch_bounds__(512, 2) swa_dkv_kern
 #pragma unroll
     for (int m = 0; m < MD; ++m) acc[m] = zero16();
 
-    const int t0 = ra / RT, per = rb > ra ? (rb - 1) / RT - t0 + 1 : 0, count = per * p.G;
+    const int t0 = ra / RT, per = rb > ra ? (rb - 1) / RT - t0 + 1 : 0, count = per * gn;
     const size_t rs = (size_t)p.Hq * D;
     Stage<T, D, RT, NT> sq, sg;
     float stat = 0.f;
     int stat_rows = 0;
     auto fetch = [&](int it) {
-        const int h = hk * p.G + it / per, r0 = (t0 + it % per) * RT;
+        const int h = hk * p.G + ga + it / per, r0 = (t0 + it % per) * RT;
         const size_t at = (size_t)(ts + r0) * p.Hq + h;
         sq.load(static_cast<const T*>(p.q) + at * D, rs, rb - r0, tid);
         sg.load(static_cast<const T*>(p.dO) + at * D, rs, rb - r0, tid);
@@ -560,139 +587,149 @@ template <class T, int D> __global__ void __launch_bounds__(512, 2) swa_dkv_kern
         stat_rows = rb - r0;
         if (tid < 2 * RT) stat = (tid < RT ? p.lse : p.delta)[at + (size_t)min(tid % RT, stat_rows - 1) * p.Hq];
     };
-    auto put = [&](int it) {
-        T* t = tiles + (it & 1) * 2 * RT * ST;
-        sq.store(t, tid);
-        sg.store(t + RT * ST, tid);
-        if (tid < 2 * RT) stats[(it & 1) * 2 * RT + tid] =
-            tid % RT >= stat_rows ? 0.f : tid < RT ? stat * LOG2E : stat;
+    auto put = [&] {
+        sq.store(tq, tid);
+        sg.store(tg, tid);
+        if (tid < 2 * RT) stats[tid] = tid % RT >= stat_rows ? 0.f : tid < RT ? stat * LOG2E : stat;
     };
-    f32x4* const mine = box + (w + 2 * x) * (4 * WAVE) + lane;
-    const f32x16 none = zero16();
-    auto product = [&](const T* t) {   // rows of this half against the lane's key
-        f32x16 s = none;
-#pragma unroll
-        for (int ks = 0; ks < KD; ++ks) s = mma32(nat32<T>(t, ST, 32 * x, 16 * ks, n, h2), own[ks], s);
-        return s;
-    };
-    auto sum = [&](const T* t, const f32x16& s) {
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            const V8 f = rows16<T>(s, kb);
-#pragma unroll
-            for (int m = 0; m < MD; ++m) acc[m] = mma32(tr32(t, ST, 32 * x + 16 * kb, 32 * m, lane), f, acc[m]);
-        }
-    };
-    // P from the scores, and over to the other wave
-    auto weigh = [&](f32x16& s, const float* sl, int i0, auto masked) {
-        const Mask mask(i0 + 4 * h2, key, p.window, p.sinks);   // offsets count down from the first row
-        const int from = ra - i0 - 4 * h2;
-#pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4) {
-            const f32x4 l4 = *reinterpret_cast<const f32x4*>(sl + 8 * r4 + 4 * h2);
-            f32x4 e;
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int o = 8 * r4 + m;   // row - (i0 + 4 h2)
-                const bool in = !masked.value || (o >= from && -o <= mask.last && (-o > mask.first || key < p.sinks));
-                e[m] = in ? fast_exp2(fmaf(s[4 * r4 + m], c, -l4[m])) : 0.f;
-                s[4 * r4 + m] = e[m];
-            }
-            mine[r4 * WAVE] = e;
-        }
-    };
+    f32x4* const mine = box + w * (NX * 4 * WAVE) + lane;
+    const float* const sl = stats;
     if (count) {
         fetch(0);
-        put(0);
+        put();
         __syncthreads();
     }
     for (int it = 0; it < count; ++it) {
         if (it + 1 < count) fetch(it + 1);
-        const T* tq = tiles + (it & 1) * 2 * RT * ST;
-        const T* tg = tq + RT * ST;
-        const float* sl = stats + (it & 1) * 2 * RT + 32 * x;
-        const int i0 = (t0 + it % per) * RT + 32 * x, j0 = k0 + 32 * w;
-        const Seen se = seen(i0, i0 + 31, j0, j0 + 31, p.window, p.sinks);
-        const bool some = !se.none && i0 + 31 >= ra && i0 < rb;
-        f32x16 s = none;
+        const int i0 = (t0 + it % per) * RT, j0 = k0 + 32 * w;
+        const Seen se = seen(i0, i0 + RT - 1, j0, j0 + 31, p.window, p.sinks);
+        const bool some = !se.none && i0 + RT - 1 >= ra && i0 < rb;
+        f32x16 s[NX];
         if (some) {
-            s = product(grad ? tg : tq);
-            if (!grad) {
-                if (se.all && i0 >= ra) weigh(s, sl, i0, std::false_type()); else weigh(s, sl, i0, std::true_type());
+            const T* t = grad ? tg : tq;
+#pragma unroll
+            for (int x = 0; x < NX; ++x) s[x] = zero16();
+#pragma unroll
+            for (int ks = 0; ks < KD; ++ks)
+#pragma unroll
+                for (int x = 0; x < NX; ++x) s[x] = mma32(nat32<T>(t, ST, 32 * x, 16 * ks, n, h2), own[ks], s[x]);
+            if (!grad) {   // P, and over to the other wave
+                auto weigh = [&](auto masked) {
+#pragma unroll
+                    for (int x = 0; x < NX; ++x) {
+                        // row - key and row - ra of the lane's first row; later ones count up
+                        const int back = i0 + 32 * x + 4 * h2 - key, from = ra - (i0 + 32 * x + 4 * h2);
+#pragma unroll
+                        for (int r4 = 0; r4 < 4; ++r4) {
+                            const f32x4 l4 = *reinterpret_cast<const f32x4*>(sl + 32 * x + 8 * r4 + 4 * h2);
+                            f32x4 e;
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) {
+                                const int o = 8 * r4 + m;
+                                const bool in = !masked.value || (o >= from && o >= -back &&
+                                                                  (o < p.window - back || key < p.sinks));
+                                e[m] = in ? fast_exp2(fmaf(s[x][4 * r4 + m], c, -l4[m])) : 0.f;
+                                s[x][4 * r4 + m] = e[m];
+                            }
+                            mine[(4 * x + r4) * WAVE] = e;
+                        }
+                    }
+                };
+                if (se.all && i0 >= ra) weigh(std::false_type()); else weigh(std::true_type());
             }
         }
         __syncthreads();
         if (some) {
             if (grad) {
 #pragma unroll
-                for (int r4 = 0; r4 < 4; ++r4) {
-                    const f32x4 d4 = *reinterpret_cast<const f32x4*>(sl + RT + 8 * r4 + 4 * h2);
-                    const f32x4 e = mine[r4 * WAVE];
-                    // where P is zero for a hidden row, dP may be anything
+                for (int x = 0; x < NX; ++x)
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) s[4 * r4 + m] = e[m] == 0.f ? 0.f : e[m] * (s[4 * r4 + m] - d4[m]);
-                }
+                    for (int r4 = 0; r4 < 4; ++r4) {
+                        const f32x4 d4 = *reinterpret_cast<const f32x4*>(sl + RT + 32 * x + 8 * r4 + 4 * h2);
+                        const f32x4 e = mine[(4 * x + r4) * WAVE];
+                        // where P is zero for a hidden row, dP may be anything
+#pragma unroll
+                        for (int m = 0; m < 4; ++m)
+                            s[x][4 * r4 + m] = e[m] == 0.f ? 0.f : e[m] * (s[x][4 * r4 + m] - d4[m]);
+                    }
             }
-            sum(grad ? tq : tg, s);
+            const T* t = grad ? tq : tg;
+#pragma unroll
+            for (int kb = 0; kb < 2 * NX; ++kb) {
+                const V8 f = rows16<T>(s[kb / 2], kb % 2);
+#pragma unroll
+                for (int m = 0; m < MD; ++m) acc[m] = mma32(tr32(t, ST, 16 * kb, 32 * m, lane), f, acc[m]);
+            }
         }
         if (it + 1 < count) {
-            put(it + 1);
+            __syncthreads();
+            put();
             __syncthreads();
         }
     }
-    // the second half's sums to the first half's waves, four values a lane and step
-    __syncthreads();
-    f32x4* const so = reinterpret_cast<f32x4*>(smem) + (w + 2 * grad) * (MD * 4 * WAVE) + lane;
-    if (x) {
-#pragma unroll
-        for (int m = 0; m < MD; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                so[(4 * m + r) * WAVE] = f32x4{acc[m][4 * r], acc[m][4 * r + 1], acc[m][4 * r + 2], acc[m][4 * r + 3]};
-    }
-    __syncthreads();
-    if (x) return;
-    float* const part_out = p.part + ((((size_t)b.seq * p.Hkv + hk) * p.sink_blocks + b.idx) * (1 + p.splits) + part) * (2 * KB * D) +
-                            (size_t)grad * (KB * D) + (size_t)(32 * w + n) * D + 4 * h2;
+    float* const part_out = p.part + part_slot(p, item, b.seq, b.idx, part, hk, hp) * (2 * KB * D) + (size_t)grad * (KB * D) +
+                            (size_t)(32 * w + n) * D + 4 * h2;
     T* const out = static_cast<T*>(grad ? p.dk : p.dv) + ((size_t)(ts + key) * p.Hkv + hk) * D + 4 * h2;
     const float f = grad ? p.scale : 1.f;
 #pragma unroll
     for (int m = 0; m < MD; ++m)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const f32x4 y = f32x4{acc[m][4 * r], acc[m][4 * r + 1], acc[m][4 * r + 2], acc[m][4 * r + 3]} + so[(4 * m + r) * WAVE];
+            const f32x4 y = f32x4{acc[m][4 * r], acc[m][4 * r + 1], acc[m][4 * r + 2], acc[m][4 * r + 3]};
             if (cut) *reinterpret_cast<f32x4*>(part_out + 32 * m + 8 * r) = y;
             else if (live) store4(out + 32 * m + 8 * r, y * f);
         }
 }
 
-// the parts of the blocks with sinks, summed in order
-template <class T, int D> __global__ void __launch_bounds__(256) swa_sink_sum_kernel(SwaParams p) {
+// the parts of a block, summed in order
+template <class T, int D> __global__ void __launch_bounds__(256) swa_part_sum_kernel(SwaParams p) {
     constexpr int KB = KEY_BLOCK;
     lds_poison(0);
-    const int kb = blockIdx.x % p.sink_blocks, hk = blockIdx.y, s = blockIdx.x / p.sink_blocks;
-    int len;
-    long ts;
-    if (p.map.cu) {
-        const int c0 = seq_offset(p.map, s);
-        ts = c0;
-        len = max(seq_offset(p.map, s + 1) - c0, 0);
-    } else {
-        ts = (long)s * p.map.T;
-        len = p.map.T;
+    const int hk = blockIdx.y;
+    SeqBlock b;
+    int item = blockIdx.x;
+    if (p.head_parts > 1) {
+        if (!seq_block(p.map, KB, item, b)) return;
+    } else {   // the blocks with sinks of every sequence
+        b.seq = blockIdx.x / p.sink_blocks;
+        b.idx = blockIdx.x % p.sink_blocks;
+        if (p.map.cu) {
+            const int c0 = seq_offset(p.map, b.seq);
+            b.t0 = c0;
+            b.len = max(seq_offset(p.map, b.seq + 1) - c0, 0);
+        } else {
+            b.t0 = (long)b.seq * p.map.T;
+            b.len = p.map.T;
+        }
+        b.t0 += (long)b.idx * KB;
     }
     const int e = 4 * (blockIdx.z * 256 + threadIdx.x);
-    const int key = kb * KB + e / D;
-    if (e >= KB * D || key >= len) return;
-    const float* src = p.part + (((size_t)s * p.Hkv + hk) * p.sink_blocks + kb) * (1 + p.splits) * (size_t)(2 * KB * D) + e;
-    f32x4 a = zero4(), c = zero4();
-    for (int m = 0; m <= p.splits; ++m) {
-        a += *reinterpret_cast<const f32x4*>(src + (size_t)m * (2 * KB * D));
-        c += *reinterpret_cast<const f32x4*>(src + (size_t)m * (2 * KB * D) + KB * D);
+    if (e >= KB * D || b.idx * KB + e / D >= b.len) return;
+    f32x4 v = zero4(), k = zero4();
+    const int parts = (p.splits > 0 && b.idx < p.sink_blocks ? 1 + p.splits : 1) * p.head_parts;
+    const int more = p.blocks + (b.seq * p.sink_blocks + b.idx) * p.splits - 1;   // item of part 1, less 1
+    constexpr int U = 4;   // parts in flight
+    for (int q0 = 0; q0 < parts; q0 += U) {
+        f32x4 x[U], y[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int part = (q0 + u) / p.head_parts, hp = (q0 + u) % p.head_parts;
+            x[u] = y[u] = zero4();
+            if (q0 + u >= parts) continue;
+            const float* src =
+                p.part + part_slot(p, part ? more + part : item, b.seq, b.idx, part, hk, hp) * (2 * KB * D) + e;
+            x[u] = *reinterpret_cast<const f32x4*>(src);
+            y[u] = *reinterpret_cast<const f32x4*>(src + KB * D);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            v += x[u];
+            k += y[u];
+        }
     }
-    const size_t to = ((size_t)(ts + key) * p.Hkv + hk) * D + e % D;
-    store4(static_cast<T*>(p.dv) + to, a);
-    store4(static_cast<T*>(p.dk) + to, c * p.scale);
+    const size_t to = ((size_t)(b.t0 + e / D) * p.Hkv + hk) * D + e % D;
+    store4(static_cast<T*>(p.dv) + to, v);
+    store4(static_cast<T*>(p.dk) + to, k * p.scale);
 }
 
 // ---------------------------------------------------------------- one token over a cache
@@ -849,22 +886,37 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
     }
 }
 
-// joins the parts of one query head; four values a thread
-template <class T, int D> __global__ void __launch_bounds__(64) swa_join_kernel(SwaDecodeParams p) {
+// Joins the parts of one query head: four values a thread, the parts spread over
+// the rest of the workgroup (a thread that walked them all would wait for each).
+template <class T, int D> __global__ void __launch_bounds__(256) swa_join_kernel(SwaDecodeParams p) {
     lds_poison(0);
-    const size_t at = (size_t)blockIdx.x * (64 / (D / 4)) + threadIdx.x / (D / 4);
-    if (at >= (size_t)p.N * p.Hq) return;
-    const int d = threadIdx.x % (D / 4) * 4;
-    float m = -INFINITY, l = 0.f;
+    constexpr int CG = D / 4, RG = 256 / CG;
+    __shared__ float s_l[RG];
+    __shared__ __align__(16) float s_o[RG][D];
+    const size_t at = blockIdx.x;
+    const int cg = threadIdx.x % CG, rg = threadIdx.x / CG;
+    float m = -INFINITY;
     for (int y = 0; y < p.splits; ++y) m = fmaxf(m, p.pm[at * p.splits + y]);
     const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
     f32x4 acc = zero4();
-    for (int y = 0; y < p.splits; ++y) {
+    for (int y = rg; y < p.splits; y += RG) {
         const float f = fast_exp2(p.pm[at * p.splits + y] - base);
         l += f * p.pl[at * p.splits + y];
-        acc += *reinterpret_cast<const f32x4*>(p.po + (at * p.splits + y) * D + d) * f;
+        acc += *reinterpret_cast<const f32x4*>(p.po + (at * p.splits + y) * D + 4 * cg) * f;
     }
-    store4(static_cast<T*>(p.o) + at * D + d, p.pos[at / p.Hq] < 0 ? zero4() : acc * (1.f / l));
+    if (cg == 0) s_l[rg] = l;
+    *reinterpret_cast<f32x4*>(&s_o[rg][4 * cg]) = acc;
+    __syncthreads();
+    if (rg) return;
+    l = 0.f;
+    acc = zero4();
+#pragma unroll
+    for (int y = 0; y < RG; ++y) {
+        l += s_l[y];
+        acc += *reinterpret_cast<const f32x4*>(&s_o[y][4 * cg]);
+    }
+    store4(static_cast<T*>(p.o) + at * D + 4 * cg, p.pos[at / p.Hq] < 0 ? zero4() : acc * (1.f / l));
 }
 
 // ---------------------------------------------------------------- a prompt's keys into a cache
@@ -942,11 +994,30 @@ SwaParams make_params(const SwaArgs& a, int NW) {
     return p;
 }
 
-template <class T, int D> hipError_t forward(const SwaArgs& a) {
-    constexpr int NW = 4;
+// Waves a workgroup of the forward: four, which share every key tile, where that
+// gives two workgroups to a CU; else two, or one (for rows up to 256 bytes, which
+// one wave has the registers to stage), over fewer rows each. 1,025 packed rows
+// of 6 heads, d = 64, fp32: 0.030 ms with four, 0.023 ms with one.
+template <class T, int D, int NW> hipError_t forward_waves(const SwaArgs& a) {
     const SwaParams p = make_params(a, NW);
+    if constexpr (NW > (D * sizeof(T) > 256 ? 2 : 1))
+        if ((long)p.blocks * (p.Hq / p.HW) < 512) return forward_waves<T, D, NW / 2>(a);
     return launch(swa_fwd_kernel<T, D, NW>, dim3(p.blocks * (p.Hq / p.HW)), 64 * NW,
                   sizeof(T) * 4 * swa_tile<T>() * tile_stride<T>(D), a.stream, p);
+}
+template <class T, int D> hipError_t forward(const SwaArgs& a) { return forward_waves<T, D, 4>(a); }
+
+// How the gradients of k and v are cut up, and the slots that their parts take.
+// Heads of a group are split until there are four workgroups to a CU, two at a
+// time: 4,096 rows, 16 and 4 heads, d = 128, window 512, 4 sinks: 0.169 ms whole,
+// 0.135 in two parts, 0.109 in four.
+size_t grad_parts(int T, int N, int G, int Hkv, int window, int sinks, bool packed, SwaParams& p) {
+    sink_parts(T, window, sinks, p.sink_blocks, p.splits, p.split_rows);
+    p.blocks = (int)seq_blocks_bound(T, N, KEY_BLOCK, packed);
+    const long items = (long)p.blocks + (long)N * p.sink_blocks * p.splits;
+    p.head_parts = (int)std::max(1L, std::min((long)G, (1023 + items * Hkv) / (items * Hkv)));
+    if (p.head_parts > 1) return (size_t)items * Hkv * p.head_parts;
+    return (size_t)N * Hkv * p.sink_blocks * (p.splits ? 1 + p.splits : 0);
 }
 
 template <class T, int D> hipError_t backward(const SwaArgs& a) {
@@ -955,14 +1026,15 @@ template <class T, int D> hipError_t backward(const SwaArgs& a) {
     char* ws = static_cast<char*>(a.workspace);
     p.delta = reinterpret_cast<float*>(ws);
     p.part = reinterpret_cast<float*>(ws + al256((size_t)a.N * a.T * a.Hq * 4));
-    sink_parts(a.T, p.window, p.sinks, p.sink_blocks, p.splits, p.split_rows);
     const size_t lds = sizeof(T) * 4 * swa_tile<T>() * tile_stride<T>(D);
     hipError_t e = launch(swa_dq_kernel<T, D, NW>, dim3(p.blocks * (p.Hq / p.HW)), 64 * NW, lds, a.stream, p);
     if (e != hipSuccess) return e;
-    p.blocks = (int)seq_blocks_bound(a.T, a.N, KEY_BLOCK, a.cu_seqlens != nullptr);
-    e = launch(swa_dkv_kernel<T, D>, dim3(p.blocks + a.N * p.sink_blocks * p.splits, p.Hkv), 512, dkv_lds<T, D>(), a.stream, p);
-    if (e != hipSuccess || p.splits == 0) return e;
-    return launch(swa_sink_sum_kernel<T, D>, dim3(a.N * p.sink_blocks, p.Hkv, (KEY_BLOCK * D / 4 + 255) / 256), 256, 0,
+    grad_parts(a.T, a.N, p.G, p.Hkv, p.window, p.sinks, a.cu_seqlens != nullptr, p);
+    const unsigned items = (unsigned)(p.blocks + a.N * p.sink_blocks * p.splits);
+    e = launch(swa_dkv_kernel<T, D>, dim3(items * p.Hkv * p.head_parts), 256, dkv_lds<T, D>(), a.stream, p);
+    if (e != hipSuccess || (p.splits == 0 && p.head_parts == 1)) return e;
+    return launch(swa_part_sum_kernel<T, D>,
+                  dim3(p.head_parts > 1 ? p.blocks : a.N * p.sink_blocks, p.Hkv, (KEY_BLOCK * D / 4 + 255) / 256), 256, 0,
                   a.stream, p);
 }
 
@@ -990,8 +1062,7 @@ template <class T, int D> hipError_t decode(const SwaDecodeArgs& a) {
     hipError_t e = launch(swa_decode_kernel<T, D, NW>, dim3(p.splits * p.GC, p.Hkv, p.N), 64 * NW, std::max(tiles, join),
                           a.stream, p);
     if (e != hipSuccess || p.splits == 1) return e;
-    constexpr int HB = 64 / (D / 4);
-    return launch(swa_join_kernel<T, D>, dim3((unsigned)((heads + HB - 1) / HB)), 64, 0, a.stream, p);
+    return launch(swa_join_kernel<T, D>, dim3((unsigned)heads), 256, 0, a.stream, p);
 }
 
 #define KDA_SWA_DIM(d, D, ...)                                         \
@@ -1005,12 +1076,10 @@ template <class T, int D> hipError_t decode(const SwaDecodeArgs& a) {
 
 }  // namespace
 
-size_t swa_bwd_workspace_bytes(int T, int N, int Hq, int Hkv, int d, int window, int sinks) {
-    int blocks, splits, rows;
-    sink_parts(T, std::min(window, T), std::min(sinks, T), blocks, splits, rows);
-    const size_t n = al256((size_t)N * T * Hq * 4) +
-                     (splits ? (size_t)N * Hkv * blocks * (1 + splits) * 2 * KEY_BLOCK * d * 4 : 0);
-    return n ? n : 256;
+size_t swa_bwd_workspace_bytes(int T, int N, int Hq, int Hkv, int d, int window, int sinks, bool packed) {
+    SwaParams p{};
+    const size_t slots = T > 0 ? grad_parts(T, N, Hq / Hkv, Hkv, std::min(window, T), std::min(sinks, T), packed, p) : 0;
+    return al256((size_t)N * T * Hq * 4 + 1) + slots * 2 * KEY_BLOCK * d * 4;
 }
 
 size_t swa_decode_workspace_bytes(int N, int Hq, int Hkv, int d, int window, int sinks) {
