@@ -78,7 +78,7 @@ bool swa_sizes_ok(int B, int Hq, int Hkv, int T, int d, int window, int sinks, i
     if (B <= 0 || T < 0 || window < 1 || sinks < 0 || !swa_heads_ok(Hq, Hkv, d)) return false;
     if (has_cu && (B != 1 || N <= 0)) return false;
     const int64_t n = has_cu ? N : B, rows = has_cu ? T : n * T;
-    return n <= 65535 && n * (T + 128LL) <= INT32_MAX && (rows / 128 + n + 1) * Hq <= INT32_MAX;
+    return n <= 65535 && n * (T + 128LL) <= INT32_MAX && (rows / 64 + n + 1) * Hq < (1 << 24);   // workgroups of 256
 }
 
 // The checks that the window-attention calls over sequences share, and the
@@ -612,7 +612,8 @@ int kda_swa_bwd(const void* q, const void* k, const void* v, const void* o, cons
     if (!aligned(o) || !aligned(lse, 4) || !aligned(dO) || !aligned(grad_q) || !aligned(grad_k) || !aligned(grad_v) ||
         !aligned(workspace))
         return KDA_EALIGN;
-    if (workspace_bytes < kda::swa_bwd_workspace_bytes(T, a.N, Hq, Hkv, d, window, sinks, cu_seqlens != nullptr)) return KDA_EINVAL;
+    if (workspace_bytes < kda::swa_bwd_workspace_bytes(T, a.N, Hq, Hkv, d, window, sinks, cu_seqlens != nullptr))
+        return KDA_EINVAL;
     a.o = o;
     a.lse = lse;
     a.dO = dO;

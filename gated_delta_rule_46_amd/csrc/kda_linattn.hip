@@ -33,6 +33,8 @@
 // final states S_T and dS_0, which are fp32, take the scaled rows as three bf16
 // numbers (24 mantissa bits: as exact as an fp32 sum). fp32 inputs: fp32 MFMA
 // throughout.
+#include <type_traits>
+
 #include "kda_launch.h"
 #include "kda_tiles.h"
 
@@ -58,6 +60,13 @@ struct LinParams {
     void* blk[2];
     float* blk_decay[2];
 };
+
+// Number of the first block (of C tokens) of a segment; a sequence's blocks follow
+// each other, numbered as segments are, with C in place of L.
+__device__ __forceinline__ long first_block(const LinParams& p, const SeqBlock& b, int C) {
+    const long before = p.map.cu ? (b.t0 - (long)b.idx * p.L) / C + b.seq : (long)b.seq * ((p.map.T + C - 1) / C);
+    return before + (long)b.idx * (p.L / C);
+}
 
 // tokens per block: fp32 tiles are twice as large, and fp32 MFMA makes the
 // quadratic part dearer
@@ -201,6 +210,7 @@ __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
     SeqBlock b;
     if (!seq_block(p.map, p.L, blockIdx.x, b)) return;
     const int nc = (b.n + C - 1) / C;
+    const long block0 = BLOCKS ? first_block(p, b, C) : 0;
     const size_t at = (size_t)blockIdx.x * p.H + h;
     const T* X = static_cast<const T*>(rev ? p.dO : p.v);
     const T* Y = static_cast<const T*>(rev ? p.q : p.k);
@@ -228,7 +238,7 @@ __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
     for (int step = 0; step < nc; ++step) {
         const int c = rev ? nc - 1 - step : step;
         if constexpr (BLOCKS) {
-            const size_t to = (size_t)((long)blockIdx.x * (p.L / C) + c) * p.H + h;
+            const size_t to = (size_t)(block0 + c) * p.H + h;
             if (tid == 0) p.blk_decay[rev][to] = decay;
             if (step) {
                 T* dst = static_cast<T*>(p.blk[rev]) + to * (DK * DV);
@@ -549,6 +559,7 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
     SeqBlock b;
     if (!seq_block(p.map, p.L, blockIdx.x, b)) return;
     const int nc = (b.n + C - 1) / C;
+    const long block0 = first_block(p, b, C);
     const size_t rk = (size_t)p.H * DK, rv = (size_t)p.H * DV;
 
     // what lies beyond a tile's columns, and above the diagonal, stays zero
@@ -614,7 +625,7 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
         sto.load(static_cast<const T*>(p.dO) + r0 * DV, rv, n, tid);
     };
     auto fetch_states = [&](int c) {
-        const size_t bs = (size_t)((long)blockIdx.x * (p.L / C) + c) * p.H + h;
+        const size_t bs = (size_t)(block0 + c) * p.H + h;
         locE.load(static_cast<const T*>(p.blk[1]) + bs * (DK * DV), DV, c + 1 < nc ? DK : 0, tid);
         if (c) {
 #pragma unroll
@@ -955,7 +966,7 @@ struct LinWorkspace {
 };
 LinWorkspace workspace_layout(int T, int N, int H, int dk, int dv, bool packed, bool bf16, bool grad, int L) {
     const size_t segs = (size_t)seq_blocks_bound(T, N, L, packed) * H, state = (size_t)dk * dv;
-    const size_t blocks = segs * (L / (bf16 ? 64 : 32));
+    const size_t blocks = (size_t)seq_blocks_bound(T, N, bf16 ? lin_block<uint16_t>() : lin_block<float>(), packed) * H;
     LinWorkspace w{};
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t r = at; at += al256(bytes); return r; };
@@ -975,25 +986,28 @@ LinWorkspace workspace_layout(int T, int N, int H, int dk, int dv, bool packed, 
     return w;
 }
 
-template <class K> hipError_t launch(K kern, dim3 grid, int threads, size_t lds, hipStream_t stream, const LinParams& p) {
+// (a launch has fewer than 2^32 threads along x)
+template <class K, class... A>
+hipError_t launch(K kern, size_t x, unsigned y, unsigned z, int threads, size_t lds, hipStream_t stream, A... args) {
+    if (x * threads > 0xffffffffu) return hipErrorInvalidConfiguration;
     if (lds > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(kern, grid, dim3(threads), lds, stream, p);
+    hipLaunchKernelGGL(kern, dim3((unsigned)x, y, z), dim3(threads), lds, stream, args...);
     return hipGetLastError();
 }
 
 template <class T, int DK, int DV, bool BLOCKS>
 hipError_t launch_state(const LinParams& p, int segs, int dirs, hipStream_t st) {
     constexpr int NW = DK / 16 < 4 ? DK / 16 : 4, C = lin_block<T>();
-    return launch(lin_state_kernel<T, DK, DV, NW, BLOCKS>, dim3(segs, p.H, dirs), 64 * NW,
+    return launch(lin_state_kernel<T, DK, DV, NW, BLOCKS>, segs, p.H, dirs, 64 * NW,
                   sizeof(Decays<C>) + sizeof(T) * C * (tile_stride<T>(DK) + tile_stride<T>(DV)), st, p);
 }
 
 template <class T, int DK, int DV, bool WHOLE> hipError_t launch_out(const LinParams& p, int segs, hipStream_t st) {
     constexpr int NW = DV / 16 < 4 ? DV / 16 : 4, C = lin_block<T>();
-    return launch(lin_out_kernel<T, DK, DV, NW, WHOLE>, dim3(segs, p.H), 64 * NW,
+    return launch(lin_out_kernel<T, DK, DV, NW, WHOLE>, segs, p.H, 1, 64 * NW,
                   sizeof(Decays<C>) + sizeof(T) * C * (2 * tile_stride<T>(DK) + tile_stride<T>(DV) + tile_stride<T>(C)), st,
                   p);
 }
@@ -1008,8 +1022,7 @@ template <class T, int DK, int DV> hipError_t forward(LinParams p, const LinArgs
     hipError_t e = hipSuccess;
     if (p.map.T > 0) e = launch_state<T, DK, DV, false>(p, segs, 1, a.stream);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(lin_scan_kernel<T>, dim3(p.map.N * p.H, (DK * DV / 4 + 255) / 256, 1), dim3(256), 0, a.stream, p, DK * DV);
-    e = hipGetLastError();
+    e = launch(lin_scan_kernel<T>, (size_t)p.map.N * p.H, (DK * DV / 4 + 255) / 256, 1, 256, 0, a.stream, p, DK * DV);
     if (e != hipSuccess || p.map.T == 0) return e;
     return launch_out<T, DK, DV, false>(p, segs, a.stream);
 }
@@ -1020,20 +1033,21 @@ template <class T, int DK, int DV> hipError_t backward(const LinParams& p, const
     hipError_t e = hipSuccess;
     if (p.map.T > 0) e = launch_state<T, DK, DV, true>(p, segs, 2, a.stream);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(lin_scan_kernel<T>, dim3(p.map.N * p.H, (DK * DV / 4 + 255) / 256, 2), dim3(256), 0, a.stream, p, DK * DV);
-    e = hipGetLastError();
+    e = launch(lin_scan_kernel<T>, (size_t)p.map.N * p.H, (DK * DV / 4 + 255) / 256, 2, 256, 0, a.stream, p, DK * DV);
     if (e != hipSuccess || p.map.T == 0) return e;
-    const dim3 grid(segs, p.H);
-    if (p.head_gate) return launch(lin_grad_kernel<T, DK, DV, false>, grid, 64 * LinGradTiles<T, DK, DV, false>::NW, sizeof(LinGradTiles<T, DK, DV, false>), a.stream, p);
-    return launch(lin_grad_kernel<T, DK, DV, true>, grid, 64 * LinGradTiles<T, DK, DV, true>::NW, sizeof(LinGradTiles<T, DK, DV, true>), a.stream, p);
+    auto go = [&](auto kern, auto dg) {
+        using L = LinGradTiles<T, DK, DV, dg.value>;
+        return launch(kern, segs, p.H, 1, 64 * L::NW, sizeof(L), a.stream, p);
+    };
+    if (p.head_gate) return go(lin_grad_kernel<T, DK, DV, false>, std::false_type());
+    return go(lin_grad_kernel<T, DK, DV, true>, std::true_type());
 }
 
 template <class T, int DK, int DV> hipError_t decode(const LinDecodeArgs& a) {
     const int pairs = a.N * a.H;
     auto go = [&](auto kern, int threads, int cols) {
-        hipLaunchKernelGGL(kern, dim3(pairs, DV / cols), dim3(threads), 0, a.stream, (const T*)a.q, (const T*)a.k,
-                           (const T*)a.v, a.gate, a.S, (T*)a.o, a.H, DV, (int)a.head_gate);
-        return hipGetLastError();
+        return launch(kern, pairs, DV / cols, 1, threads, 0, a.stream, (const T*)a.q, (const T*)a.k, (const T*)a.v, a.gate,
+                      a.S, (T*)a.o, a.H, DV, (int)a.head_gate);
     };
     constexpr int NT = DK * DV / 4 < 512 ? DK * DV / 4 : 512;
     // under two heads per CU the columns of a head are split over workgroups

@@ -24,13 +24,15 @@
  *    The caller owns every buffer.
  *  - Element type of q, k, v, gate and beta is selected by `dtype`:
  *    KDA_BF16 (bfloat16 bits) or KDA_F32. States S0, S_T, S and outputs o
- *    are always fp32.
+ *    are always fp32, but for o of kda_linattn_* and kda_swa_*, which has
+ *    that type too.
  *  - `stream` is a hipStream_t (NULL = the default stream). Work is enqueued
  *    and the call returns without synchronising.
  *  - Arguments are validated before any HIP call; nothing is enqueued when
  *    validation fails. Device-side contents (cu_seqlens offsets, NaN/Inf in
  *    inputs) are not checked: NaN/Inf propagate.
- *  - Supported sizes: dk, dv in {16, 32, 64, 128}; chunk in {16, 32, 64}.
+ *  - Supported sizes: dk, dv in {16, 32, 64, 128}; chunk in {16, 32, 64}
+ *    (kda_swa_*: d in {32, 64, 128}).
  *  - The library never allocates, frees or synchronises device memory in a
  *    compute call: every call that needs scratch space takes a caller-owned
  *    workspace, and a NULL workspace (or a short one) is KDA_EINVAL.
@@ -344,8 +346,8 @@ int kda_chunk_fwd_gauge(const void* q, const void* k, const void* v, const void*
  * scaling.
  *
  * Unlike the delta rule's calls, o and the gradients have the input dtype
- * (bf16 halves what the call writes); states are fp32. Rows of o at or behind
- * cu_seqlens[N] are left as they are. A NaN or Inf at a token reaches every
+ * (bf16 halves what the call writes); states are fp32. S_T may be S0. Rows of o
+ * at or behind cu_seqlens[N] are left as they are. A NaN or Inf at a token reaches every
  * later output of its sequence, and may reach earlier ones of its block of 64
  * tokens.
  *
@@ -368,7 +370,8 @@ int kda_linattn_fwd(const void* q, const void* k, const void* v, const void* gat
  * is a constant: grad_gate must be NULL (for a learned one, pass it
  * per token and sum). grad_gate is the derivative with respect to the decay
  * itself, an ordinary one at zero and negative decays. Nothing of a forward
- * call is reused. dO and the gradients must be 16-byte aligned (grad_gate and
+ * call is reused, and rows at or behind cu_seqlens[N] are left as they are. dO
+ * and the gradients must be 16-byte aligned (grad_gate and
  * states: their element). workspace: kda_linattn_bwd_workspace_bytes(...)
  * bytes (segment states, and the state and adjoint of every block), required.
  */
@@ -407,7 +410,8 @@ int kda_linattn_decode_step(const void* q, const void* k, const void* v, const v
  * that row in the forward and the decode step.
  *
  * Every pointer 16-byte aligned (lse, cu_seqlens: their element). At most
- * 65,535 sequences and heads, N * (T + 128) < 2^31 (KDA_ENOTSUP otherwise).
+ * 65,535 sequences and heads, N * (T + 128) < 2^31, and fewer than 2^24 blocks of
+ * 64 rows over all sequences and query heads (KDA_ENOTSUP otherwise).
  * Needs no workspace. Returns KDA_OK or a negative status.
  */
 int kda_swa_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv, int T, int d,
@@ -417,8 +421,8 @@ int kda_swa_fwd(const void* q, const void* k, const void* v, void* o, float* lse
  * Gradient of kda_swa_fwd for L = sum <o, dO>: o and lse as the forward left
  * them, dO [B, T, Hq, d]. grad_q, grad_k, grad_v in the input dtype and
  * layouts, those of a kv head summed over its query heads; sums run in a fixed
- * order (repeated calls agree bit for bit). workspace:
- * kda_swa_bwd_workspace_bytes(...) bytes, required.
+ * order (repeated calls agree bit for bit); rows at or behind cu_seqlens[N] are
+ * left as they are. workspace: kda_swa_bwd_workspace_bytes(...) bytes, required.
  */
 size_t kda_swa_bwd_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int window, int sinks, int N,
                                    int has_cu_seqlens);
