@@ -245,8 +245,11 @@ __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
 #pragma unroll
                 for (int x = 0; x < NPW; ++x)
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
-                        store4(dst + (size_t)(16 * (w * NPW + x) + il) * DV + 16 * m + 4 * g, acc[x][m]);
+                    for (int m = 0; m < MT; m += 2) {
+                        T* row = dst + (size_t)(16 * (w * NPW + x) + il) * DV + 16 * m;
+                        if constexpr (MT > 1) store_pair(row, acc[x][m], acc[x][m + 1], g);
+                        else store4(row + 4 * g, acc[x][m]);
+                    }
             }
         }
         if (step) __syncthreads();
@@ -470,9 +473,12 @@ __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
                 for (int x = 0; x < NPW; ++x) acc[x][tt] = mma(vf[x][ks], pf, acc[x][tt]);
             }
             if (16 * tt + il < n) {
-                T* out = static_cast<T*>(p.o) + ((size_t)(b.t0 + c * C + 16 * tt + il) * p.H + h) * DV + 4 * g;
+                T* out = static_cast<T*>(p.o) + ((size_t)(b.t0 + c * C + 16 * tt + il) * p.H + h) * DV;
 #pragma unroll
-                for (int x = 0; x < NPW; ++x) store4(out + 16 * (w * NPW + x), acc[x][tt]);
+                for (int x = 0; x < NPW; x += 2) {
+                    if constexpr (NPW > 1) store_pair(out + 16 * (w * NPW + x), acc[x][tt], acc[x + 1][tt], g);
+                    else store4(out + 16 * w + 4 * g, acc[x][tt]);
+                }
             }
         }
         if (WHOLE || c + 1 < nc) {
@@ -581,27 +587,28 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
     using StageE = Stage<T, DV, DK, NT>;
     using R4 = typename Raw4<T>::V;
     struct RowS {
-        R4 x[KSV][2];
-        __device__ __forceinline__ void load(const T* src) {
+        Raw8<T> x[KSV];
+        __device__ __forceinline__ void load(const T* src, bool in) {
 #pragma unroll
             for (int ks = 0; ks < KSV; ++ks) {
-                x[ks][0] = *reinterpret_cast<const R4*>(src + 32 * ks);
-                x[ks][1] = DV >= 32 ? *reinterpret_cast<const R4*>(src + 32 * ks + (DV >= 32 ? 16 : 0)) : R4(0);
+                x[ks].clear();
+                if (in) x[ks].load(src + 32 * ks);
             }
         }
     };
+    const bool cols = DV >= 32 || g < 2;   // 16 columns: the other lane groups hold the padding
     size_t srow[MP];
 #pragma unroll
-    for (int m = 0; m < MP; ++m) srow[m] = (size_t)(min(16 * (wm + m), DK - 16) + il) * DV + 4 * g;
+    for (int m = 0; m < MP; ++m) srow[m] = (size_t)(min(16 * (wm + m), DK - 16) + il) * DV + 8 * (cols ? g : 0);
     const size_t seg = ((size_t)blockIdx.x * p.H + h) * (DK * DV);
     StageE segE, locE;
     RowS segS[MP], locS[MP];
     segE.load(static_cast<const T*>(p.bound[1]) + seg, DV, DK, tid);
 #pragma unroll
     for (int m = 0; m < MP; ++m) {
-        segS[m].load(static_cast<const T*>(p.bound[0]) + seg + srow[m]);
+        segS[m].load(static_cast<const T*>(p.bound[0]) + seg + srow[m], cols);
 #pragma unroll
-        for (int ks = 0; ks < KSV; ++ks) locS[m].x[ks][0] = locS[m].x[ks][1] = R4(0);   // the first block's own share
+        for (int ks = 0; ks < KSV; ++ks) locS[m].x[ks].clear();   // the first block's own share
     }
 
     Stage<T, DK, C, NT> stq, stk;
@@ -629,7 +636,7 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
         locE.load(static_cast<const T*>(p.blk[1]) + bs * (DK * DV), DV, c + 1 < nc ? DK : 0, tid);
         if (c) {
 #pragma unroll
-            for (int m = 0; m < MP; ++m) locS[m].load(static_cast<const T*>(p.blk[0]) + bs * (DK * DV) + srow[m]);
+            for (int m = 0; m < MP; ++m) locS[m].load(static_cast<const T*>(p.blk[0]) + bs * (DK * DV) + srow[m], cols);
         }
         preS = p.blk_decay[0][bs];
         preE = p.blk_decay[1][bs];
@@ -669,8 +676,7 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
         for (int m = 0; m < MP; ++m)
 #pragma unroll
             for (int ks = 0; ks < KSV; ++ks)
-                sf[m][ks] = narrow<T>(dtiles_to_frag(values(raw_here(segS[m].x[ks][0])) * preS + values(locS[m].x[ks][0]),
-                                                     values(raw_here(segS[m].x[ks][1])) * preS + values(locS[m].x[ks][1])));
+                sf[m][ks] = narrow<T>(values(raw_here(segS[m].x[ks])) * preS + values(locS[m].x[ks]));
         if (w == 0) block_decays<C, true>(s.dec, a.value(p, lane), lane);
         __syncthreads();
         if (c + 1 < nc) fetch_qk(c + 1);
@@ -717,13 +723,13 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
                 V8 ef[MP];
 #pragma unroll
                 for (int m = 0; m < MP; ++m) {
-                    ef[m] = frag_kpos(s.E, SV, 16 * (wm + m) + il, 32 * ks, g);
+                    ef[m] = frag_nat(s.E, SV, 16 * (wm + m) + il, 32 * ks, g);
                     if constexpr (DG) xe = dot8(ef[m], sf[m][ks], xe);
                 }
 #pragma unroll
                 for (int tt = 0; tt < HT; ++tt) {
                     const int i = 16 * (HT * th + tt) + il;
-                    const V8 of = frag_kpos(s.dO, SV, i, 32 * ks, g), vf = frag_kpos(s.v, SV, i, 32 * ks, g);
+                    const V8 of = frag_nat(s.dO, SV, i, 32 * ks, g), vf = frag_nat(s.v, SV, i, 32 * ks, g);
 #pragma unroll
                     for (int m = 0; m < MP; ++m) {
                         aq[m][tt] = mma(sf[m][ks], of, aq[m][tt]);
@@ -822,16 +828,18 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
         for (int tt = 0; tt < HT; ++tt) {
             const int i = 16 * (HT * th + tt) + il;
             if (i >= n) continue;
-#pragma unroll
-            for (int m = 0; m < MP; ++m) {
-                const size_t row = r0 + (size_t)i * p.H;
-                const int col = 16 * (wm + m) + 4 * g;
-                if (wm + m < DK / 16) {
-                    store4(static_cast<T*>(p.dq) + row * DK + col, aq[m][tt]);
-                    store4(static_cast<T*>(p.dk) + row * DK + col, ak[m][tt]);
+            const size_t row = r0 + (size_t)i * p.H;
+            auto put = [&](void* to, int width, const f32x4 (&y)[MP][HT]) {
+                T* at = static_cast<T*>(to) + row * width + 16 * wm;
+                if (wm >= width / 16) return;
+                if constexpr (MP == 2) {
+                    if (width > 16) return store_pair(at, y[0][tt], y[MP - 1][tt], g);
                 }
-                if (wm + m < DV / 16) store4(static_cast<T*>(p.dv) + row * DV + col, av[m][tt]);
-            }
+                store4(at + 4 * g, y[0][tt]);
+            };
+            put(p.dq, DK, aq);
+            put(p.dk, DK, ak);
+            put(p.dv, DV, av);
         }
 
         if (c + 1 < nc) fetch_states(c + 1);

@@ -90,6 +90,28 @@ template <class T> __device__ __forceinline__ typename Frag<T>::V rows16(const f
 }
 __device__ __forceinline__ int result_row(int r, int h) { return 8 * (r >> 2) + 4 * h + (r & 3); }
 
+// A lane's values of a result tile, times f, to 32 consecutive columns of a row:
+// bf16 halves of 8 columns are swapped with the other half of the wave first, so
+// that they go out 16 bytes a lane instead of 8.
+template <class T> __device__ __forceinline__ void store_tile(T* row, const f32x16& y, float f, int h) {
+#pragma unroll
+    for (int r = 0; r < 4; r += 2) {
+        const f32x4 a = f32x4{y[4 * r], y[4 * r + 1], y[4 * r + 2], y[4 * r + 3]} * f;
+        const f32x4 b = f32x4{y[4 * r + 4], y[4 * r + 5], y[4 * r + 6], y[4 * r + 7]} * f;
+        if constexpr (sizeof(T) == 2) {
+            u32x2 u, v;
+            store4(reinterpret_cast<T*>(&u), a);
+            store4(reinterpret_cast<T*>(&v), b);
+            const auto s0 = __builtin_amdgcn_permlane32_swap(u[0], v[0], false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(u[1], v[1], false, false);
+            *reinterpret_cast<uint4*>(row + 8 * (r + h)) = make_uint4(s0[0], s1[0], s0[1], s1[1]);
+        } else {
+            store4(row + 8 * r + 4 * h, a);
+            store4(row + 8 * r + 8 + 4 * h, b);
+        }
+    }
+}
+
 // 8 consecutive elements of a row in global memory, or zeros
 template <class T> __device__ __forceinline__ typename Frag<T>::V load8(const T* p, bool in) {
     constexpr int N = sizeof(T) / 2;
@@ -347,12 +369,9 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
     }
     const float inv = 1.f / sum;
     if (live) {
-        T* out = static_cast<T*>(p.out) + ((size_t)(ts + row) * p.Hq + h) * D + 4 * h2;
+        T* out = static_cast<T*>(p.out) + ((size_t)(ts + row) * p.Hq + h) * D;
 #pragma unroll
-        for (int m = 0; m < MD; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                store4(out + 32 * m + 8 * r, f32x4{O[m][4 * r], O[m][4 * r + 1], O[m][4 * r + 2], O[m][4 * r + 3]} * inv);
+        for (int m = 0; m < MD; ++m) store_tile<T>(out + 32 * m, O[m], inv, h2);
         if (p.lse_out && h2 == 0) p.lse_out[(size_t)(ts + row) * p.Hq + h] = (top + log2f(sum)) * LN2;
     }
 }
@@ -463,12 +482,9 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
         }
     }
     if (live) {
-        T* out = static_cast<T*>(p.dq) + ((size_t)(ts + row) * p.Hq + h) * D + 4 * h2;
+        T* out = static_cast<T*>(p.dq) + ((size_t)(ts + row) * p.Hq + h) * D;
 #pragma unroll
-        for (int m = 0; m < MD; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                store4(out + 32 * m + 8 * r, f32x4{A[m][4 * r], A[m][4 * r + 1], A[m][4 * r + 2], A[m][4 * r + 3]} * p.scale);
+        for (int m = 0; m < MD; ++m) store_tile<T>(out + 32 * m, A[m], p.scale, h2);
     }
 }
 
@@ -693,17 +709,13 @@ template <class T, int D> __global__ void __launch_bounds__(256, 2) swa_dkv_kern
         }
     }
     float* const part_out = p.part + part_slot(p, item, sp.first + part, b.idx, hk, hp) * (2 * KB * D) + (size_t)grad * (KB * D) +
-                            (size_t)(32 * w + n) * D + 4 * h2;
-    T* const out = static_cast<T*>(grad ? p.dk : p.dv) + ((size_t)(ts + key) * p.Hkv + hk) * D + 4 * h2;
-    const float f = grad ? p.scale : 1.f;
+                            (size_t)(32 * w + n) * D;
+    T* const out = static_cast<T*>(grad ? p.dk : p.dv) + ((size_t)(ts + key) * p.Hkv + hk) * D;
 #pragma unroll
-    for (int m = 0; m < MD; ++m)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const f32x4 y = f32x4{acc[m][4 * r], acc[m][4 * r + 1], acc[m][4 * r + 2], acc[m][4 * r + 3]};
-            if (cut) *reinterpret_cast<f32x4*>(part_out + 32 * m + 8 * r) = y;
-            else if (live) store4(out + 32 * m + 8 * r, y * f);
-        }
+    for (int m = 0; m < MD; ++m) {
+        if (cut) store_tile<float>(part_out + 32 * m, acc[m], 1.f, h2);
+        else if (live) store_tile<T>(out + 32 * m, acc[m], grad ? p.scale : 1.f, h2);
+    }
 }
 
 // the parts of a block, summed in order

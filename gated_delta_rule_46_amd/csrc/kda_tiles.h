@@ -102,6 +102,23 @@ __device__ __forceinline__ void store4(uint16_t* p, const f32x4& x) {
 }
 __device__ __forceinline__ void store4(float* p, const f32x4& x) { *reinterpret_cast<f32x4*>(p) = x; }
 
+// Columns 4 g + (0..3) of two neighbouring 16-column tiles of a row: the lane groups
+// swap halves, so that bf16 goes out 16 bytes a lane, 64 in a row, instead of 8 and 32.
+__device__ __forceinline__ void store_pair(uint16_t* row, const f32x4& x, const f32x4& y, int g) {
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+    const u2 a = __builtin_bit_cast(u2, __builtin_convertvector(x, bf16x4));
+    const u2 b = __builtin_bit_cast(u2, __builtin_convertvector(y, bf16x4));
+    // odd groups of the first operand against even ones of the second
+    const auto s0 = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const auto s1 = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    *reinterpret_cast<uint4*>(row + 16 * (g & 1) + 8 * (g >> 1)) = make_uint4(s0[0], s1[0], s0[1], s1[1]);
+}
+__device__ __forceinline__ void store_pair(float* row, const f32x4& x, const f32x4& y, int g) {
+    *reinterpret_cast<f32x4*>(row + 4 * g) = x;
+    *reinterpret_cast<f32x4*>(row + 16 + 4 * g) = y;
+}
+
 // four elements as they lie in memory, held whole (arrays of 16-bit elements
 // would take a register each), and their values
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -109,11 +126,30 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 template <class T> struct Raw4;
 template <> struct Raw4<uint16_t> { using V = u32x2; };
 template <> struct Raw4<float> { using V = u32x4; };
+// eight of them, in pieces of 16 bytes
+template <class T> struct Raw8 {
+    u32x4 x[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int m = 0; m < (int)sizeof(T) / 2; ++m) x[m] = reinterpret_cast<const u32x4*>(p)[m];
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int m = 0; m < (int)sizeof(T) / 2; ++m) x[m] = u32x4(0);
+    }
+};
 __device__ __forceinline__ f32x4 values(const u32x2& x) {
     return f32x4{__uint_as_float(x[0] << 16), __uint_as_float(x[0] & 0xffff0000u), __uint_as_float(x[1] << 16),
                  __uint_as_float(x[1] & 0xffff0000u)};
 }
 __device__ __forceinline__ f32x4 values(const u32x4& x) { return __builtin_bit_cast(f32x4, x); }
+__device__ __forceinline__ f32x8 values8(const f32x4& a, const f32x4& b) {
+    return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+__device__ __forceinline__ f32x8 values(const Raw8<uint16_t>& r) {
+    return values8(values(u32x2{r.x[0][0], r.x[0][1]}), values(u32x2{r.x[0][2], r.x[0][3]}));
+}
+__device__ __forceinline__ f32x8 values(const Raw8<float>& r) { return values8(values(r.x[0]), values(r.x[1])); }
 
 __device__ __forceinline__ float from_el(uint16_t x) { return bf16_bits_to_f32(x); }
 __device__ __forceinline__ float from_el(float x) { return x; }
@@ -165,6 +201,11 @@ __device__ __forceinline__ int here(int x) {
 template <class V> __device__ __forceinline__ V raw_here(V x) {
     asm volatile("" : "+v"(x));
     return x;
+}
+template <class T> __device__ __forceinline__ Raw8<T> raw_here(Raw8<T> r) {
+#pragma unroll
+    for (int m = 0; m < (int)sizeof(T) / 2; ++m) r.x[m] = raw_here(r.x[m]);
+    return r;
 }
 
 // zero columns D..31 of a narrow tile
