@@ -842,7 +842,8 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
             put(p.dv, DV, av);
         }
 
-        if (c + 1 < nc) fetch_states(c + 1);
+        if constexpr (!DG)
+            if (c + 1 < nc) fetch_states(c + 1);
         if constexpr (DG) {
             // R tiles: rows i, columns t
             for (int e = w; e < CT * (CT + 1) / 2; e += NW) {
@@ -870,6 +871,7 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
                 sum += __shfl_xor(sum, 32, WAVE);
                 if (g == 0) s.da[ti * C + t] = sum;
             }
+            if (c + 1 < nc) fetch_states(c + 1);
             __syncthreads();
             if (w == NW - 1) {
                 const int t = lane % C;   // C = 32: the upper lanes repeat the lower ones

@@ -167,7 +167,10 @@ template <class T, int D, int R, int NT> struct Stage {
     u32x4 r[N];
     __device__ __forceinline__ void load(const T* base, size_t stride, int valid, int tid) {
         const uint32_t bytes = (uint32_t)stride * (uint32_t)sizeof(T);
-        const auto rsrc = make_rsrc(base, (uint32_t)min(max(valid, 0), R) * bytes);
+        // said to be the same in every lane: a clamp is vector arithmetic, and a
+        // descriptor in vector registers costs a loop around each load
+        const uint32_t size = __builtin_amdgcn_readfirstlane(min(max(valid, 0), R) * (int)bytes);
+        const auto rsrc = make_rsrc(base, size);
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const int e = tid + n * NT;
