@@ -68,8 +68,8 @@ __device__ __forceinline__ long first_block(const LinParams& p, const SeqBlock& 
     return before + (long)b.idx * (p.L / C);
 }
 
-// tokens per block: fp32 tiles are twice as large, and fp32 MFMA makes the
-// quadratic part dearer
+// tokens per block: fp32 tiles are twice as large (64 would not fit the gradient's
+// LDS), and fp32 MFMA makes the quadratic part dearer
 template <class T> constexpr int lin_block() { return sizeof(T) == 2 ? 64 : 32; }
 
 // ---------------------------------------------------------------- decays of a block
@@ -193,7 +193,8 @@ template <class T, int PARTS> __device__ __forceinline__ void split(typename Fra
 // One segment of one head in one direction, from zero: the state's transpose
 // (rows dv, columns dk) in accumulators, dk columns split over the waves. Writes
 // the segment's contribution and its decay; BLOCKS: what it has at every block
-// on the way too.
+// on the way too. Bound by bytes: B = 2, T = 4096, H = 16, d = 128, bf16, both directions
+// with BLOCKS 57 us (285 MB, 5.0 TB/s); forward of T = 8192 without 43 us (134 + 34 MB).
 template <class T, int DK, int DV, int NW, bool BLOCKS>
 __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
     constexpr int C = lin_block<T>(), NT = 64 * NW, NPW = DK / 16 / NW, MT = DV / 16;
@@ -294,7 +295,8 @@ __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
 
 // ---------------------------------------------------------------- scan over segments
 
-// Elementwise over dk x dv, one (sequence, head) per blockIdx.x. Direction 0:
+// Elementwise over dk x dv, one (sequence, head) per blockIdx.x; bound by the latency of
+// a chain of loads as long as a sequence has segments (eight in flight). Direction 0:
 // from the segments' contributions the state at each segment's start, and S_T.
 // Direction 1: the adjoint at each one's end, and dS0. Summed in fp32; at the
 // boundaries in between the states are kept as they enter products, in the
@@ -350,7 +352,8 @@ template <class T> __global__ void __launch_bounds__(256) lin_scan_kernel(LinPar
 // ---------------------------------------------------------------- forward outputs
 
 // One segment of one head: the state (rows dk, columns dv) in accumulators, dv
-// columns split over the waves; its D tiles are ready A operands of S^T q.
+// columns split over the waves; its D tiles are ready A operands of S^T q. B = 2, T =
+// 8192, H = 16, d = 128, bf16: 59 us (285 MB, 4.8 TB/s).
 // WHOLE: the segment is the whole sequence, from S0 to S_T.
 template <class T, int DK, int DV, int NW, bool WHOLE>
 __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
@@ -531,6 +534,9 @@ __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
 // where the start state takes the place of an earlier token (r_i = q_i . S dO_i)
 // and the end adjoint that of a later one (c_j = k_j . E v_j). R is one more
 // small matrix product.
+// One workgroup fills a CU's LDS; of its 109 us at B = 2, T = 4096, H = 16, d = 128, bf16
+// (370 MB of inputs, block states and results: 3.4 TB/s) half is arithmetic and LDS
+// reads of two waves a SIMD, with five barriers a block, half waits for memory.
 template <class T, int DK, int DV, bool DG> struct LinGradTiles {
     // A wave owns MP of the 16-row tiles of dk and dv for a part of a block's
     // tokens (one of TS). bf16: two row tiles and half the tokens, which reads half
@@ -901,20 +907,21 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
 
 // ---------------------------------------------------------------- decode
 
-// S' = a S + k v^T, o = S'^T q = a (S^T q) + (k . q) v, the state streamed once
-// in and once out. One workgroup takes DVW of a head's dv columns; a column
-// needs no other, so few heads spread over more workgroups.
-template <class T, int DK, int DVW, int NT>
+// S' = a S + k v^T, o = S'^T q = a (S^T q) + (k . q) v, the state streamed once in
+// and once out, all of it in flight at once: one workgroup a head, 16 bytes a thread
+// and load. Bound by those bytes: 256 sequences of 32 heads, 128 x 128, 0.204 ms, 5.3
+// TB/s. One head over four workgroups, a quarter of its columns each: 3.3 against 3.4 us
+// at 16 heads, 6.3 against 5.5 at 256, so it is not done.
+template <class T, int DK, int DV, int NT>
 __global__ void __launch_bounds__(NT) lin_decode_kernel(const T* __restrict__ q, const T* __restrict__ k,
                                                         const T* __restrict__ v, const void* __restrict__ gate,
-                                                        float* __restrict__ S, T* __restrict__ o, int H, int DV,
-                                                        int head_gate) {
-    constexpr int CG = DVW / 4, RG = NT / CG, RPT = DK / RG, NW = NT / WAVE;
+                                                        float* __restrict__ S, T* __restrict__ o, int H, int head_gate) {
+    constexpr int CG = DV / 4, RG = NT / CG, RPT = DK / RG, NW = NT / WAVE;
     static_assert(NT % WAVE == 0 && DK % RG == 0 && RPT >= 1, "decode tiling");
     lds_poison(0);
-    __shared__ float s_k[DK], s_q[DK], s_v[DVW], s_red[NW][DVW], s_kq[NW];
+    __shared__ float s_k[DK], s_q[DK], s_v[DV], s_red[NW][DV], s_kq[NW];
     const size_t pair = blockIdx.x;
-    const int c0 = blockIdx.y * DVW, t = threadIdx.x, cg = t % CG, rg = t / CG, lane = t % WAVE, w = t / WAVE;
+    const int t = threadIdx.x, cg = t % CG, rg = t / CG, lane = t % WAVE, w = t / WAVE;
     float kq = 0.f;
     for (int e = t; e < DK; e += NT) {
         const float kv = ld_in(k + pair * DK + e), qv = ld_in(q + pair * DK + e);
@@ -922,9 +929,9 @@ __global__ void __launch_bounds__(NT) lin_decode_kernel(const T* __restrict__ q,
         s_q[e] = qv;
         kq += kv * qv;
     }
-    for (int e = t; e < DVW; e += NT) s_v[e] = ld_in(v + pair * DV + c0 + e);
+    for (int e = t; e < DV; e += NT) s_v[e] = ld_in(v + pair * DV + e);
     const float a = head_gate ? static_cast<const float*>(gate)[pair % H] : ld_in(static_cast<const T*>(gate) + pair);
-    f32x4* Sp = reinterpret_cast<f32x4*>(S + pair * DK * DV + c0);
+    f32x4* Sp = reinterpret_cast<f32x4*>(S + pair * DK * DV);
     const size_t rs = DV / 4;
     f32x4 sv[RPT];
 #pragma unroll
@@ -947,14 +954,14 @@ __global__ void __launch_bounds__(NT) lin_decode_kernel(const T* __restrict__ q,
         for (int j = 0; j < 4; ++j) y[j] += __shfl_xor(y[j], off, WAVE);
     if (lane < CG) *reinterpret_cast<f32x4*>(&s_red[w][4 * cg]) = y;
     __syncthreads();
-    if (t < DVW) {
+    if (t < DV) {
         float acc = 0.f, dot = 0.f;
 #pragma unroll
         for (int m = 0; m < NW; ++m) {
             acc += s_red[m][t];
             dot += s_kq[m];
         }
-        store1(o + pair * DV + c0 + t, a * acc + dot * s_v[t]);
+        store1(o + pair * DV + t, a * acc + dot * s_v[t]);
     }
 }
 
@@ -972,6 +979,8 @@ int segment_tokens(int T, int N, int H, int dk, int dv, bool packed, bool grad) 
     const long whole = ((long)T + 63) / 64 * 64;
     return (int)(L < whole ? L : (whole > 0 ? whole : 64));
 }
+// Short sequences whole, in one launch. B = 4, H = 16, d = 128: 12.1 against 20.1 us
+// in segments at 128 tokens, 21.0 against 23.7 at 256, 38.3 against 34.8 at 512.
 bool whole_sequences(int T) { return T <= 256; }
 
 struct LinWorkspace {
@@ -1057,16 +1066,9 @@ template <class T, int DK, int DV> hipError_t backward(const LinParams& p, const
 }
 
 template <class T, int DK, int DV> hipError_t decode(const LinDecodeArgs& a) {
-    const int pairs = a.N * a.H;
-    auto go = [&](auto kern, int threads, int cols) {
-        return launch(kern, pairs, DV / cols, 1, threads, 0, a.stream, (const T*)a.q, (const T*)a.k, (const T*)a.v, a.gate,
-                      a.S, (T*)a.o, a.H, DV, (int)a.head_gate);
-    };
     constexpr int NT = DK * DV / 4 < 512 ? DK * DV / 4 : 512;
-    // under two heads per CU the columns of a head are split over workgroups
-    if constexpr (DV > 32 && DK >= 32)
-        if (pairs < 512) return go(lin_decode_kernel<T, DK, 32, (DK * 8 < 512 ? DK * 8 : 512)>, DK * 8 < 512 ? DK * 8 : 512, 32);
-    return go(lin_decode_kernel<T, DK, DV, NT>, NT, DV);
+    return launch(lin_decode_kernel<T, DK, DV, NT>, (size_t)a.N * a.H, 1, 1, NT, 0, a.stream, (const T*)a.q, (const T*)a.k,
+                  (const T*)a.v, a.gate, a.S, (T*)a.o, a.H, (int)a.head_gate);
 }
 
 LinParams make_params(const LinArgs& a) {
