@@ -704,8 +704,8 @@ def linattn_fwd(q, k, v, gate, S0=None, cu_seqlens=None, out: Optional[torch.Ten
     need = linattn_fwd_workspace_bytes(B, H, T, dk, dv, N, varlen, q.dtype)
 
     def call(st):
-        o = torch.empty((B, T, H, dv), device=device, dtype=q.dtype) if out is None else out
-        S = torch.empty((N, H, dk, dv), device=device, dtype=torch.float32) if S_T is None and state_out else S_T
+        o = torch.empty_like(v) if out is None else out
+        S = q.new_empty((N, H, dk, dv), dtype=torch.float32) if S_T is None and state_out else S_T
         ws = _scratch(workspace, need, device)
         rc = _lib().kda_linattn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(), _addr(S0), o.data_ptr(),
                                     _addr(S), B, H, T, dk, dv, _addr(cu_seqlens), N if varlen else 0, dt, kind,
@@ -730,12 +730,12 @@ def linattn_bwd(q, k, v, gate, dO, S0=None, dS_T=None, cu_seqlens=None, want_dS0
     varlen, N = _check_varlen(cu_seqlens, B, device)
     _check_state("S0", S0, N, H, dk, dv, device)
     _check_state("dS_T", dS_T, N, H, dk, dv, device)
-    shapes = {"dq": (B, T, H, dk), "dk": (B, T, H, dk), "dv": (B, T, H, dv)}
+    of = {"dq": q, "dk": k, "dv": v}
     if kind == GATE_SCALAR:
-        shapes["dgate"] = (B, T, H)
+        of["dgate"] = gate
     if out is not None:
-        for name, shape in shapes.items():
-            _like(name, out[name], shape, q.dtype, device)
+        for name, t in of.items():
+            _like(name, out[name], t.shape, q.dtype, device)
         if kind == GATE_HEAD and out.get("dgate") is not None:
             raise ValueError("a constant decay per head has no dgate")
         _check_state("dS0", out.get("dS0"), N, H, dk, dv, device)
@@ -744,9 +744,9 @@ def linattn_bwd(q, k, v, gate, dO, S0=None, dS_T=None, cu_seqlens=None, want_dS0
     def call(st):
         g = out
         if g is None:
-            g = {name: torch.empty(shape, device=device, dtype=q.dtype) for name, shape in shapes.items()}
+            g = {name: torch.empty_like(t) for name, t in of.items()}
             g.setdefault("dgate", None)
-            g["dS0"] = torch.empty((N, H, dk, dv), device=device, dtype=torch.float32) if want_dS0 else None
+            g["dS0"] = q.new_empty((N, H, dk, dv), dtype=torch.float32) if want_dS0 else None
         ws = _scratch(workspace, need, device)
         rc = _lib().kda_linattn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(), _addr(S0), dO.data_ptr(),
                                     _addr(dS_T), g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(),
@@ -770,7 +770,7 @@ def linattn_decode_step(q, k, v, gate, S, out: Optional[torch.Tensor] = None, st
         _like("out", out, (N, H, dv), q.dtype, device)
 
     def call(st):
-        o = torch.empty((N, H, dv), device=device, dtype=q.dtype) if out is None else out
+        o = torch.empty_like(v) if out is None else out
         rc = _lib().kda_linattn_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(), S.data_ptr(),
                                             o.data_ptr(), N, H, dk, dv, dt, kind, st)
         if rc != KDA_OK:
@@ -824,8 +824,8 @@ def swa_fwd(q, k, v, window: int, sinks: int = 0, scale: Optional[float] = None,
         _like("lse", lse, (B, T, Hq), torch.float32, device)
 
     def call(st):
-        o = torch.empty((B, T, Hq, d), device=device, dtype=q.dtype) if out is None else out
-        s = torch.empty((B, T, Hq), device=device, dtype=torch.float32) if lse is None and lse_out else lse
+        o = torch.empty_like(q) if out is None else out
+        s = q.new_empty((B, T, Hq), dtype=torch.float32) if lse is None and lse_out else lse
         rc = _lib().kda_swa_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _addr(s), B, Hq, Hkv, T, d,
                                 _int32(window), _int32(sinks), d ** -0.5 if scale is None else float(scale),
                                 _addr(cu_seqlens), N if varlen else 0, dt, st)
@@ -852,16 +852,16 @@ def swa_bwd(q, k, v, o, lse, dO, window: int, sinks: int = 0, scale: Optional[fl
     _like("dO", dO, (B, T, Hq, d), q.dtype, device)
     _like("lse", lse, (B, T, Hq), torch.float32, device)
     varlen, N = _check_varlen(cu_seqlens, B, device)
-    shapes = {"dq": (B, T, Hq, d), "dk": (B, T, Hkv, d), "dv": (B, T, Hkv, d)}
+    of = {"dq": q, "dk": k, "dv": v}
     if out is not None:
-        for name, shape in shapes.items():
-            _like(name, out[name], shape, q.dtype, device)
+        for name, t in of.items():
+            _like(name, out[name], t.shape, q.dtype, device)
     need = swa_bwd_workspace_bytes(B, Hq, Hkv, T, d, window, sinks, N, varlen)
 
     def call(st):
         g = out
         if g is None:
-            g = {name: torch.empty(shape, device=device, dtype=q.dtype) for name, shape in shapes.items()}
+            g = {name: torch.empty_like(t) for name, t in of.items()}
         ws = _scratch(workspace, need, device)
         rc = _lib().kda_swa_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dO.data_ptr(),
                                 g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(), B, Hq, Hkv, T, d,
@@ -896,7 +896,7 @@ def swa_decode_step(q, k, v, K_cache, V_cache, pos, window: int, sinks: int = 0,
     need = swa_decode_workspace_bytes(N, Hq, Hkv, d, window, sinks)
 
     def call(st):
-        o = torch.empty((N, Hq, d), device=device, dtype=q.dtype) if out is None else out
+        o = torch.empty_like(q) if out is None else out
         ws = _scratch(workspace, need, device)
         rc = _lib().kda_swa_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(),
                                         pos.data_ptr(), o.data_ptr(), N, Hq, Hkv, d, _int32(window), _int32(sinks),
