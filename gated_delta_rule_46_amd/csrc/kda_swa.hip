@@ -504,7 +504,7 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
 // holds v, forms dP, and dS and dk from it. A tile has 64 rows, two independent
 // chains of products a wave; it lies in LDS once, the next one in registers, so
 // that two workgroups fit a CU and fill each other's waits. 4,096 rows, 16 and 4 heads,
-// d = 128, window 512, 4 sinks, bf16: 104 us, 27 more for the sum of the parts.
+// d = 128, window 512, 4 sinks, bf16: 104 us, 22 more for the sum of the parts.
 // The rows of a block with sinks reach to the end of the sequence: in sequences of
 // 2 * sink_rows and more they are cut into equal parts of sink_rows to twice that,
 // each a workgroup, summed afterwards in a fixed order.
@@ -753,7 +753,7 @@ template <class T, int D> __global__ void __launch_bounds__(256) swa_part_sum_ke
     if (e >= KB * D || b.idx * KB + e / D >= b.len) return;
     f32x4 v = zero4(), k = zero4();
     const int parts = max(sp.count, 1) * p.head_parts;
-    constexpr int U = 4;   // parts in flight
+    constexpr int U = 8;   // parts in flight (a block with sinks may have dozens)
     for (int q0 = 0; q0 < parts; q0 += U) {
         f32x4 x[U], y[U];
 #pragma unroll
