@@ -200,24 +200,26 @@ __device__ __forceinline__ void work_item(const SwaParams& p, int& blk, int& hea
 // bf16: 0.186 ms, 695 TFLOP/s of what the window holds (62% of a large library product's
 // rate); bound by the exponentials and the matrix products of two waves a SIMD, which
 // overlap only across waves.
-template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa_fwd_kernel(SwaParams p) {
-    constexpr int KT = swa_tile<T>(), NX = KT / 32, NT = 64 * NW, ST = tile_stride<T>(D), KD = D / 16, MD = D / 32;
+// KS > 1, for few rows: KS waves take the same 32 queries and every KS-th key tile
+// each, and join what they have at the end.
+template <class T, int D, int NW, int KS> __global__ void __launch_bounds__(64 * NW) swa_fwd_kernel(SwaParams p) {
+    constexpr int KT = swa_tile<T>(), KB = KS * KT, NX = KT / 32, NT = 64 * NW, ST = tile_stride<T>(D), KD = D / 16, MD = D / 32;
     using V8 = typename Frag<T>::V;
     extern __shared__ __align__(16) unsigned char smem[];
-    lds_poison((uint32_t)(sizeof(T) * 4 * KT * ST));
-    T* const tiles = reinterpret_cast<T*>(smem);   // [2][k, v][KT][ST]
+    lds_poison((uint32_t)(sizeof(T) * 4 * KB * ST));
+    T* const tiles = reinterpret_cast<T*>(smem);   // [2][k, v][KB][ST]
 
     const int tid = threadIdx.x, lane = tid % WAVE, w = tid / WAVE, n = lane & 31, h2 = lane >> 5;
     int blk, h;
     work_item(p, blk, h);
-    const int rows = 32 * NW / p.HW;
+    const int rows = 32 * (NW / KS) / p.HW, wr = w / KS, wk = w % KS;
     SeqBlock b;
     if (!seq_block(p.map, rows, blk, b)) return;
     const int q0 = b.idx * rows, len = b.len;
     const long ts = b.t0 - q0;
     const int hk = h / p.G;
-    h += w % p.HW;
-    const int i0 = q0 + w / p.HW * 32, row = i0 + n;
+    h += wr % p.HW;
+    const int i0 = q0 + wr / p.HW * 32, row = i0 + n;
     const bool live = row < len;
     // a negative scale goes into q, exactly, so that maxima scale as they stand
     const float c = fabsf(p.scale) * LOG2E;
@@ -234,18 +236,18 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
     const T* K = static_cast<const T*>(p.k) + ((size_t)ts * p.Hkv + hk) * D;
     const T* V = static_cast<const T*>(p.v) + ((size_t)ts * p.Hkv + hk) * D;
     const size_t rs = (size_t)p.Hkv * D;
-    const KeyTiles kt(q0, min(q0 + rows, len) - 1, KT, p.window, p.sinks);
+    const KeyTiles kt(q0, min(q0 + rows, len) - 1, KB, p.window, p.sinks);
 
-    Stage<T, D, KT, NT> sk, sv;
+    Stage<T, D, KB, NT> sk, sv;
     auto fetch = [&](int it) {
-        const int j0 = kt[it] * KT;
+        const int j0 = kt[it] * KB;
         sk.load(K + (size_t)j0 * rs, rs, len - j0, tid);
         sv.load(V + (size_t)j0 * rs, rs, len - j0, tid);
     };
     auto put = [&](int it) {
-        T* t = tiles + (it & 1) * 2 * KT * ST;
+        T* t = tiles + (it & 1) * 2 * KB * ST;
         sk.store(t, tid);
-        sv.store(t + KT * ST, tid);
+        sv.store(t + KB * ST, tid);
     };
     f32x16 O[MD];
 #pragma unroll
@@ -331,9 +333,9 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
     __syncthreads();
     for (int it = 0; it < kt.count; ++it) {
         if (it + 1 < kt.count) fetch(it + 1);
-        const T* tk = tiles + (it & 1) * 2 * KT * ST;
-        const T* tv = tk + KT * ST;
-        const int j0 = kt[it] * KT;
+        const T* tk = tiles + ((it & 1) * 2 * KB + wk * KT) * ST;
+        const T* tv = tk + KB * ST;
+        const int j0 = kt[it] * KB + wk * KT;
         const Seen se = seen(i0, i0 + 31, j0, j0 + KT - 1, p.window, p.sinks);
         if (!se.none && i0 < len) {
             if (se.all) tile(tk, tv, j0, std::false_type()); else tile(tk, tv, j0, std::true_type());
@@ -344,6 +346,33 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
         }
     }
     sum = swap_sum(sum);
+    if constexpr (KS > 1) {   // in the tiles' place: [wave][value][lane]
+        static_assert((16 * MD + 2) * 4 * 64 * NW <= sizeof(T) * 4 * KB * ST, "room for the join");
+        float* const join = reinterpret_cast<float*>(smem) + (size_t)w * (16 * MD + 2) * 64 + lane;
+        __syncthreads();
+        if (wk) {
+            join[0] = top;
+            join[64] = sum;
+#pragma unroll
+            for (int m = 0; m < MD; ++m)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) join[(2 + 16 * m + r) * 64] = O[m][r];
+        }
+        __syncthreads();
+        if (wk) return;
+#pragma unroll
+        for (int y = 1; y < KS; ++y) {
+            const float* other = join + (size_t)y * (16 * MD + 2) * 64;
+            const float next = fmaxf(top, other[0]), base = next == -INFINITY ? 0.f : next;
+            const float fa = fast_exp2(top - base), fb = fast_exp2(other[0] - base);
+            top = next;
+            sum = sum * fa + other[64] * fb;
+#pragma unroll
+            for (int m = 0; m < MD; ++m)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) O[m][r] = O[m][r] * fa + other[(2 + 16 * m + r) * 64] * fb;
+        }
+    }
     // An Inf or NaN in v at a key that a tile holds but a row does not see has
     // entered that row as 0 * v. Rows that are not finite are formed again, one
     // key at a time, from the keys that they see.
@@ -1040,18 +1069,23 @@ SwaParams make_params(const SwaArgs& a, int NW) {
     return p;
 }
 
-// Waves a workgroup of the forward: four, which share every key tile, where that
-// gives two workgroups to a CU; else two, or one (for rows up to 256 bytes, which
-// one wave has the registers to stage), over fewer rows each. 1,025 packed rows
-// of 6 heads, d = 64, fp32: 0.030 ms with four, 0.023 ms with one.
-template <class T, int D, int NW> hipError_t forward_waves(const SwaArgs& a) {
-    const SwaParams p = make_params(a, NW);
-    if constexpr (NW > (D * sizeof(T) > 256 ? 2 : 1))
-        if ((long)p.blocks * (p.Hq / p.HW) < 512) return forward_waves<T, D, NW / 2>(a);
-    return launch(swa_fwd_kernel<T, D, NW>, (size_t)p.blocks * (p.Hq / p.HW), 1, 1, 64 * NW,
-                  sizeof(T) * 4 * swa_tile<T>() * tile_stride<T>(D), a.stream, p);
+// Waves of the forward's workgroup that take the same rows: one, where that gives every
+// CU a workgroup; else two, or four where the tiles fit LDS, over fewer rows each, as
+// long as a row's keys fill the tiles of all. Against workgroups of fewer waves: 1,025
+// rows of 6 heads, d = 64, window 100: fp32 14.6 against 19.8 us, bf16 9.6 against 10.2;
+// 2,048 rows of 8 heads, d = 128, window 512: 56.8 against 87.1 and 19.1 against 23.0.
+// Four where two fill the CUs (1,500 rows of 16 heads, d = 64, window 1024): 43.0
+// against 22.6 us.
+template <class T, int D, int KS> hipError_t forward_split(const SwaArgs& a) {
+    constexpr int NW = 4;
+    constexpr size_t lds = sizeof(T) * 4 * KS * swa_tile<T>() * tile_stride<T>(D);
+    const SwaParams p = make_params(a, NW / KS);
+    if constexpr (KS < 4 && 2 * lds <= 160 * 1024)
+        if ((long)p.blocks * (p.Hq / p.HW) < 256 && p.window + 32 >= 2 * KS * swa_tile<T>())
+            return forward_split<T, D, 2 * KS>(a);
+    return launch(swa_fwd_kernel<T, D, NW, KS>, (size_t)p.blocks * (p.Hq / p.HW), 1, 1, 64 * NW, lds, a.stream, p);
 }
-template <class T, int D> hipError_t forward(const SwaArgs& a) { return forward_waves<T, D, 4>(a); }
+template <class T, int D> hipError_t forward(const SwaArgs& a) { return forward_split<T, D, 1>(a); }
 
 // workgroups of the gradients of k and v, for a kv head and a part of its heads
 long grad_items(const SwaParams& p) { return (long)p.blocks + (long)p.sink_parts * p.sink_blocks; }
