@@ -413,26 +413,26 @@ template <class T, int D, int NW, int KS> __global__ void __launch_bounds__(64 *
 // ---------------------------------------------------------------- gradient with respect to q
 
 // As the forward, with dP^T = V dO^T and dS = P (dP - delta), delta_i = dO_i .
-// o_i (formed here and kept for the other gradients): dq^T = K^T dS^T. 4,096 rows, 16 and
+// o_i (formed here and kept for the other gradients): dq^T = K^T dS^T; KS as there. 4,096 rows, 16 and
 // 4 heads, d = 128, window 512, bf16: 48 us.
-template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa_dq_kernel(SwaParams p) {
-    constexpr int KT = swa_tile<T>(), NT = 64 * NW, ST = tile_stride<T>(D), KD = D / 16, MD = D / 32;
+template <class T, int D, int NW, int KS> __global__ void __launch_bounds__(64 * NW) swa_dq_kernel(SwaParams p) {
+    constexpr int KT = swa_tile<T>(), KB = KS * KT, NT = 64 * NW, ST = tile_stride<T>(D), KD = D / 16, MD = D / 32;
     using V8 = typename Frag<T>::V;
     extern __shared__ __align__(16) unsigned char smem[];
-    lds_poison((uint32_t)(sizeof(T) * 4 * KT * ST));
+    lds_poison((uint32_t)(sizeof(T) * 4 * KB * ST));
     T* const tiles = reinterpret_cast<T*>(smem);
 
     const int tid = threadIdx.x, lane = tid % WAVE, w = tid / WAVE, n = lane & 31, h2 = lane >> 5;
     int blk, h;
     work_item(p, blk, h);
-    const int rows = 32 * NW / p.HW;
+    const int rows = 32 * (NW / KS) / p.HW, wr = w / KS, wk = w % KS;
     SeqBlock b;
     if (!seq_block(p.map, rows, blk, b)) return;
     const int q0 = b.idx * rows, len = b.len;
     const long ts = b.t0 - q0;
     const int hk = h / p.G;
-    h += w % p.HW;
-    const int i0 = q0 + w / p.HW * 32, row = i0 + n;
+    h += wr % p.HW;
+    const int i0 = q0 + wr / p.HW * 32, row = i0 + n;
     const bool live = row < len;
     const float c = p.scale * LOG2E;
 
@@ -453,24 +453,24 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
         delta = swap_sum(delta);
         if (live) {
             lse2 = p.lse[r0] * LOG2E;
-            if (h2 == 0) p.delta[r0] = delta;
+            if (h2 == 0 && wk == 0) p.delta[r0] = delta;
         }
     }
     const T* K = static_cast<const T*>(p.k) + ((size_t)ts * p.Hkv + hk) * D;
     const T* V = static_cast<const T*>(p.v) + ((size_t)ts * p.Hkv + hk) * D;
     const size_t rs = (size_t)p.Hkv * D;
-    const KeyTiles kt(q0, min(q0 + rows, len) - 1, KT, p.window, p.sinks);
+    const KeyTiles kt(q0, min(q0 + rows, len) - 1, KB, p.window, p.sinks);
 
-    Stage<T, D, KT, NT> sk, sv;
+    Stage<T, D, KB, NT> sk, sv;
     auto fetch = [&](int it) {
-        const int j0 = kt[it] * KT;
+        const int j0 = kt[it] * KB;
         sk.load(K + (size_t)j0 * rs, rs, len - j0, tid);
         sv.load(V + (size_t)j0 * rs, rs, len - j0, tid);
     };
     auto put = [&](int it) {
-        T* t = tiles + (it & 1) * 2 * KT * ST;
+        T* t = tiles + (it & 1) * 2 * KB * ST;
         sk.store(t, tid);
-        sv.store(t + KT * ST, tid);
+        sv.store(t + KB * ST, tid);
     };
     f32x16 A[MD];
 #pragma unroll
@@ -500,12 +500,12 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
     __syncthreads();
     for (int it = 0; it < kt.count; ++it) {
         if (it + 1 < kt.count) fetch(it + 1);
-        const T* tk = tiles + (it & 1) * 2 * KT * ST;
-        const T* tv = tk + KT * ST;
+        const T* tk = tiles + ((it & 1) * 2 * KB + wk * KT) * ST;
+        const T* tv = tk + KB * ST;
         if (i0 < len) {
 #pragma unroll
             for (int x = 0; x < KT / 32; ++x) {
-                const int j0 = kt[it] * KT + 32 * x;
+                const int j0 = kt[it] * KB + wk * KT + 32 * x;
                 const Seen se = seen(i0, i0 + 31, j0, j0 + 31, p.window, p.sinks);
                 if (se.none) continue;
                 if (se.all) tile(tk, tv, x, j0, std::false_type()); else tile(tk, tv, x, j0, std::true_type());
@@ -515,6 +515,25 @@ template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa
             put(it + 1);
             __syncthreads();
         }
+    }
+    if constexpr (KS > 1) {
+        static_assert(16 * MD * 4 * 64 * NW <= sizeof(T) * 4 * KB * ST, "room for the join");
+        float* const join = reinterpret_cast<float*>(smem) + (size_t)w * 16 * MD * 64 + lane;
+        __syncthreads();
+        if (wk) {
+#pragma unroll
+            for (int m = 0; m < MD; ++m)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) join[(16 * m + r) * 64] = A[m][r];
+        }
+        __syncthreads();
+        if (wk) return;
+#pragma unroll
+        for (int y = 1; y < KS; ++y)
+#pragma unroll
+            for (int m = 0; m < MD; ++m)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) A[m][r] += join[(size_t)(y * 16 * MD + 16 * m + r) * 64];
     }
     if (live) {
         T* out = static_cast<T*>(p.dq) + ((size_t)(ts + row) * p.Hq + h) * D;
@@ -1069,23 +1088,29 @@ SwaParams make_params(const SwaArgs& a, int NW) {
     return p;
 }
 
-// Waves of the forward's workgroup that take the same rows: one, where that gives every
+// Waves of a workgroup, in the forward and the gradient of q, that take the same rows: one, where that gives every
 // CU a workgroup; else two, or four where the tiles fit LDS, over fewer rows each, as
 // long as a row's keys fill the tiles of all. Against workgroups of fewer waves: 1,025
 // rows of 6 heads, d = 64, window 100: fp32 14.6 against 19.8 us, bf16 9.6 against 10.2;
 // 2,048 rows of 8 heads, d = 128, window 512: 56.8 against 87.1 and 19.1 against 23.0.
 // Four where two fill the CUs (1,500 rows of 16 heads, d = 64, window 1024): 43.0
-// against 22.6 us.
-template <class T, int D, int KS> hipError_t forward_split(const SwaArgs& a) {
+// against 22.6 us. The three gradients of those 1,025 rows against one wave for each: fp32
+// 52.6 against 73.2 us, bf16 29.9 against 33.0.
+template <class T, int D, int KS, class F> hipError_t split_keys(const SwaArgs& a, F f) {
     constexpr int NW = 4;
     constexpr size_t lds = sizeof(T) * 4 * KS * swa_tile<T>() * tile_stride<T>(D);
     const SwaParams p = make_params(a, NW / KS);
+    const size_t wgs = (size_t)p.blocks * (p.Hq / p.HW);
     if constexpr (KS < 4 && 2 * lds <= 160 * 1024)
-        if ((long)p.blocks * (p.Hq / p.HW) < 256 && p.window + 32 >= 2 * KS * swa_tile<T>())
-            return forward_split<T, D, 2 * KS>(a);
-    return launch(swa_fwd_kernel<T, D, NW, KS>, (size_t)p.blocks * (p.Hq / p.HW), 1, 1, 64 * NW, lds, a.stream, p);
+        if (wgs < 256 && p.window + 32 >= 2 * KS * swa_tile<T>()) return split_keys<T, D, 2 * KS>(a, f);
+    return f(p, std::integral_constant<int, KS>(), wgs, 64 * NW, lds);
 }
-template <class T, int D> hipError_t forward(const SwaArgs& a) { return forward_split<T, D, 1>(a); }
+
+template <class T, int D> hipError_t forward(const SwaArgs& a) {
+    return split_keys<T, D, 1>(a, [&](const SwaParams& p, auto ks, size_t wgs, int threads, size_t lds) {
+        return launch(swa_fwd_kernel<T, D, 4, ks.value>, wgs, 1, 1, threads, lds, a.stream, p);
+    });
+}
 
 // workgroups of the gradients of k and v, for a kv head and a part of its heads
 long grad_items(const SwaParams& p) { return (long)p.blocks + (long)p.sink_parts * p.sink_blocks; }
@@ -1107,15 +1132,17 @@ size_t grad_parts(int T, int N, int G, int Hkv, int window, int sinks, bool pack
 size_t all_rows(int T, int N, bool packed) { return packed ? (size_t)T : (size_t)N * T; }
 
 template <class T, int D> hipError_t backward(const SwaArgs& a) {
-    constexpr int NW = 4;
-    SwaParams p = make_params(a, NW);
     const bool packed = a.cu_seqlens != nullptr;
     char* ws = static_cast<char*>(a.workspace);
-    p.delta = reinterpret_cast<float*>(ws);
-    p.part = reinterpret_cast<float*>(ws + al256(all_rows(a.T, a.N, packed) * a.Hq * 4));
-    const size_t lds = sizeof(T) * 4 * swa_tile<T>() * tile_stride<T>(D);
-    hipError_t e = launch(swa_dq_kernel<T, D, NW>, (size_t)p.blocks * (p.Hq / p.HW), 1, 1, 64 * NW, lds, a.stream, p);
+    float* const delta = reinterpret_cast<float*>(ws);
+    hipError_t e = split_keys<T, D, 1>(a, [&](SwaParams p, auto ks, size_t wgs, int threads, size_t lds) {
+        p.delta = delta;
+        return launch(swa_dq_kernel<T, D, 4, ks.value>, wgs, 1, 1, threads, lds, a.stream, p);
+    });
     if (e != hipSuccess) return e;
+    SwaParams p = make_params(a, 1);
+    p.delta = delta;
+    p.part = reinterpret_cast<float*>(ws + al256(all_rows(a.T, a.N, packed) * a.Hq * 4));
     grad_parts(a.T, a.N, p.G, p.Hkv, p.window, p.sinks, packed, p);
     e = launch(swa_dkv_kernel<T, D>, (size_t)grad_items(p) * p.Hkv * p.head_parts, 1, 1, 256, dkv_lds<T, D>(), a.stream, p);
     if (e != hipSuccess || (p.sink_parts == 0 && p.head_parts == 1)) return e;
