@@ -23,16 +23,19 @@
 //   dq_t = S_t dO_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,
 //   da_t = <S_{t-1}, G_t>,  dS_0 = a_1 G_1.
 // The same two launches give S at segment starts and G at segment ends (q, dO
-// in place of k, v, in reverse order); the first keeps what it passes at every
-// block as well, so that the last one, block after block of a segment, has S and
-// G at each by one multiplication and addition.
+// in place of k, v, in reverse order); in reverse the first keeps what it passes
+// at every block as well, so that the last one, block after block of a segment,
+// has G at each by one multiplication and addition, and carries S along.
 //
-// Precision. Products of inputs are exact in fp32. bf16 inputs: scores, states
-// and scaled rows enter the next product rounded to bf16, which moves o and the
-// gradients (bf16 themselves) by less than their own rounding; sums into the
-// final states S_T and dS_0, which are fp32, take the scaled rows as three bf16
-// numbers (24 mantissa bits: as exact as an fp32 sum). fp32 inputs: fp32 MFMA
-// throughout.
+// Precision. States and adjoints are held in fp32 wherever they are kept, and a
+// token's decayed row enters them as three bf16 numbers (24 mantissa bits: as exact
+// as an fp32 sum). bf16 inputs: what enters a product with the inputs is rounded to
+// bf16 there, once: decayed scores, states and adjoints, and in the decay's gradient
+// the products of scores and the decays between. That is as much again as the rounding of
+// the results, bf16 themselves: o, dq, dk and dv are off by 2.35e-3 of their rms, the
+// decay's gradient by 2.66e-3, where their own rounding makes 1.66e-3 (B = 2, H = 16, d =
+// 128, T = 8192 and 4096). Two bf16 numbers an operand would take that away for twice the
+// matrix instructions. fp32 inputs: fp32 MFMA throughout.
 #include <type_traits>
 
 #include "kda_launch.h"
@@ -50,15 +53,15 @@ struct LinParams {
     SeqMap map;
     int H, L;            // heads; tokens per segment (a multiple of the block)
     bool head_gate;      // gate: one fp32 per head, not per token and head
-    float* seg[2];       // [segment][H][dk][dv]: contributions (0: to S, 1: to the adjoint)
-    void* bound[2];      // the same, in the input type: S at segment starts, adjoint at segment ends
+    // [segment][H][dk][dv]: contributions (0: to S, 1: to the adjoint); the scan leaves S
+    // at segment starts and the adjoint at segment ends in their place
+    float* seg[2];
     float* seg_decay;    // [segment][H]
-    // Gradient only, per block and direction: the state (adjoint) at its start
-    // (end) as far as it stems from the segment's own tokens, [block][H][dk][dv] in
-    // the input type (not written for the first block walked, where it is zero),
-    // and the product of the decays between the segment's boundary and there.
-    void* blk[2];
-    float* blk_decay[2];
+    // Gradient only, per block: the adjoint at its end as far as it stems from the
+    // segment's own tokens, [block][H][dk][dv] (not written for a segment's last
+    // block, where it is zero), and the product of the decays between there and
+    // the segment's end.
+    float *blk, *blk_decay;
 };
 
 // Number of the first block (of C tokens) of a segment; a sequence's blocks follow
@@ -192,8 +195,8 @@ template <class T, int PARTS> __device__ __forceinline__ void split(typename Fra
 
 // One segment of one head in one direction, from zero: the state's transpose
 // (rows dv, columns dk) in accumulators, dk columns split over the waves. Writes
-// the segment's contribution and its decay; BLOCKS: what it has at every block
-// on the way too. Bound by bytes: B = 2, T = 4096, H = 16, d = 128, bf16, both directions
+// the segment's contribution and its decay; BLOCKS: in reverse, what it has at
+// every block on the way too. Bound by bytes: B = 2, T = 4096, H = 16, d = 128, bf16, both directions
 // with BLOCKS 57 us (285 MB, 5.0 TB/s); forward of T = 8192 without 43 us (134 + 34 MB).
 template <class T, int DK, int DV, int NW, bool BLOCKS>
 __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
@@ -211,7 +214,8 @@ __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
     SeqBlock b;
     if (!seq_block(p.map, p.L, blockIdx.x, b)) return;
     const int nc = (b.n + C - 1) / C;
-    const long block0 = BLOCKS ? first_block(p, b, C) : 0;
+    const bool keep = BLOCKS && rev;
+    const long block0 = keep ? first_block(p, b, C) : 0;
     const size_t at = (size_t)blockIdx.x * p.H + h;
     const T* X = static_cast<const T*>(rev ? p.dO : p.v);
     const T* Y = static_cast<const T*>(rev ? p.q : p.k);
@@ -223,6 +227,12 @@ __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[x][m] = zero4();
 
+    auto put = [&](float* dst) {
+#pragma unroll
+        for (int x = 0; x < NPW; ++x)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) store4(dst + (size_t)(16 * (w * NPW + x) + il) * DV + 16 * m + 4 * g, acc[x][m]);
+    };
     Stage<T, DV, C, NT> stx;
     Stage<T, DK, C, NT> sty;
     DecayLoad<T> a(p, h);
@@ -238,20 +248,10 @@ __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
     fetch(0);
     for (int step = 0; step < nc; ++step) {
         const int c = rev ? nc - 1 - step : step;
-        if constexpr (BLOCKS) {
+        if (keep) {
             const size_t to = (size_t)(block0 + c) * p.H + h;
-            if (tid == 0) p.blk_decay[rev][to] = decay;
-            if (step) {
-                T* dst = static_cast<T*>(p.blk[rev]) + to * (DK * DV);
-#pragma unroll
-                for (int x = 0; x < NPW; ++x)
-#pragma unroll
-                    for (int m = 0; m < MT; m += 2) {
-                        T* row = dst + (size_t)(16 * (w * NPW + x) + il) * DV + 16 * m;
-                        if constexpr (MT > 1) store_pair(row, acc[x][m], acc[x][m + 1], g);
-                        else store4(row + 4 * g, acc[x][m]);
-                    }
-            }
+            if (tid == 0) p.blk_decay[to] = decay;
+            if (step) put(p.blk + to * (DK * DV));
         }
         if (step) __syncthreads();
         stx.store(sx, tid);
@@ -284,12 +284,7 @@ __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
                     for (int x = 0; x < NPW; ++x) acc[x][m] = mma(xf[m], part[x][e], acc[x][m]);
         }
     }
-#pragma unroll
-    for (int x = 0; x < NPW; ++x)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-            *reinterpret_cast<f32x4*>(p.seg[rev] + at * (DK * DV) + (size_t)(16 * (w * NPW + x) + il) * DV + 16 * m + 4 * g) =
-                acc[x][m];
+    put(p.seg[rev] + at * (DK * DV));
     if (tid == 0 && !rev) p.seg_decay[at] = decay;
 }
 
@@ -298,10 +293,8 @@ __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
 // Elementwise over dk x dv, one (sequence, head) per blockIdx.x; bound by the latency of
 // a chain of loads as long as a sequence has segments (eight in flight). Direction 0:
 // from the segments' contributions the state at each segment's start, and S_T.
-// Direction 1: the adjoint at each one's end, and dS0. Summed in fp32; at the
-// boundaries in between the states are kept as they enter products, in the
-// input type.
-template <class T> __global__ void __launch_bounds__(256) lin_scan_kernel(LinParams p, int dkdv) {
+// Direction 1: the adjoint at each one's end, and dS0. In place, in fp32.
+__global__ void __launch_bounds__(256) lin_scan_kernel(LinParams p, int dkdv) {
     lds_poison(0);
     const int s = blockIdx.x / p.H, h = blockIdx.x % p.H, rev = blockIdx.z;
     const int e = 4 * (blockIdx.y * 256 + threadIdx.x);
@@ -339,7 +332,7 @@ template <class T> __global__ void __launch_bounds__(256) lin_scan_kernel(LinPar
         for (int u = 0; u < U; ++u) {
             if (b0 + u >= nb) break;
             const int b = rev ? nb - 1 - (b0 + u) : b0 + u;
-            store4(static_cast<T*>(p.bound[rev]) + ((size_t)(first + b) * p.H + h) * dkdv + e, cur);
+            store4(p.seg[rev] + ((size_t)(first + b) * p.H + h) * dkdv + e, cur);
             cur = cur * d[u] + z[u];
         }
     }
@@ -392,14 +385,14 @@ __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
     };
     if (nc) fetch(0);
     f32x4 S[NPW][MT];
-    auto start = [&](const auto* src) {
+    auto start = [&](const float* src) {
 #pragma unroll
         for (int x = 0; x < NPW; ++x)
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    S[x][m][r] = from_el(src[(size_t)(16 * m + 4 * g + r) * DV + 16 * (w * NPW + x) + il]);
+                    S[x][m][r] = src[(size_t)(16 * m + 4 * g + r) * DV + 16 * (w * NPW + x) + il];
     };
     if constexpr (WHOLE) {
 #pragma unroll
@@ -408,7 +401,7 @@ __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
             for (int m = 0; m < MT; ++m) S[x][m] = zero4();
         if (p.S0) start(p.S0 + ends);
     } else {
-        start(static_cast<const T*>(p.bound[0]) + ((size_t)blockIdx.x * p.H + h) * (DK * DV));
+        start(p.seg[0] + ((size_t)blockIdx.x * p.H + h) * (DK * DV));
     }
     zero_pad_cols<T, DK>(sq, C, tid, NT);
     zero_pad_cols<T, DK>(sk, C, tid, NT);
@@ -538,11 +531,12 @@ __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
 // (370 MB of inputs, block states and results: 3.4 TB/s) half is arithmetic and LDS
 // reads of two waves a SIMD, with five barriers a block, half waits for memory.
 template <class T, int DK, int DV, bool DG> struct LinGradTiles {
-    // A wave owns MP of the 16-row tiles of dk and dv for a part of a block's
-    // tokens (one of TS). bf16: two row tiles and half the tokens, which reads half
-    // as much LDS as one and all of them; fp32 has no registers for that.
+    // A wave owns one 16-row tile of dk and dv, and so of the state, for a part of a
+    // block's tokens (one of TS): bf16 up to 64 columns takes two halves, which form the
+    // state twice but keep twice the waves busy. B = 2, T = 4096, H = 16, halves against
+    // all tokens: 64 x 64 85 / 107 us, 128 x 64 125 / 132, 64 x 128 136 / 128.
     static constexpr int C = lin_block<T>(), NM = (DK > DV ? DK : DV) / 16;
-    static constexpr int TS = sizeof(T) == 2 ? 2 : 1, MP = sizeof(T) == 2 && NM > 1 ? 2 : 1, NW = TS * NM / MP;
+    static constexpr int TS = sizeof(T) == 2 && DV < 128 ? 2 : 1, NW = TS * NM;
     static constexpr int SK = tile_stride<T>(DK), SV = tile_stride<T>(DV), SP = tile_stride<T>(C);
     static constexpr int EROWS = DK < 32 ? 32 : DK;
     Decays<C> dec;
@@ -556,17 +550,16 @@ template <class T, int DK, int DV, bool DG> struct LinGradTiles {
 template <class T, int DK, int DV, bool DG>
 __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_grad_kernel(LinParams p) {
     using L = LinGradTiles<T, DK, DV, DG>;
-    constexpr int C = L::C, NW = L::NW, MP = L::MP, NT = 64 * NW, CT = C / 16, HT = CT / L::TS, SK = L::SK, SV = L::SV, SP = L::SP;
+    constexpr int C = L::C, NW = L::NW, NT = 64 * NW, CT = C / 16, HT = CT / L::TS, SK = L::SK, SV = L::SV, SP = L::SP;
     constexpr int KSK = tile_cols<T>(DK) / 32, KSV = tile_cols<T>(DV) / 32, KC = C / 32;
-    constexpr int NS = (DK / 16 + MP - 1) / MP;   // waves that share in sums over dk
+    constexpr int KT = DK / 16, VT = DV / 16, PARTS = sizeof(T) == 4 ? 1 : 3;
     using V8 = typename Frag<T>::V;
     extern __shared__ __align__(16) unsigned char smem[];
     lds_poison((uint32_t)sizeof(L));
     L& s = *reinterpret_cast<L*>(smem);
 
-    const int tid0 = threadIdx.x, w = wave_id();
+    const int tid0 = threadIdx.x, w = wave_id(), wm = w % L::NM, th = w / L::NM;   // row tile, part of the tokens
     int tid = tid0, lane = tid0 % WAVE, g = lane >> 4, il = lane & 15;
-    const int wm = w % (NW / L::TS) * MP, th = w / (NW / L::TS);   // first row tile of dk and dv, part of the tokens
     const int h = blockIdx.y;
     SeqBlock b;
     if (!seq_block(p.map, p.L, blockIdx.x, b)) return;
@@ -587,40 +580,26 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
         if constexpr (DG) s.M[e] = s.D[e] = T(0);
     }
 
-    // Boundary states, as they lie in memory until used: E where this thread
-    // stages it, S where this wave has dk rows (dv is contracted). Held for the
-    // segment, and loaded ahead for the next block.
-    using StageE = Stage<T, DV, DK, NT>;
+    // The adjoint, where this thread stages it: the segment's, held throughout, and
+    // a block's own share, loaded ahead for the next block.
+    using StageE = Stage<float, DV, DK, NT>;
     using R4 = typename Raw4<T>::V;
-    struct RowS {
-        Raw8<T> x[KSV];
-        __device__ __forceinline__ void load(const T* src, bool in) {
-#pragma unroll
-            for (int ks = 0; ks < KSV; ++ks) {
-                x[ks].clear();
-                if (in) x[ks].load(src + 32 * ks);
-            }
-        }
-    };
-    const bool cols = DV >= 32 || g < 2;   // 16 columns: the other lane groups hold the padding
-    size_t srow[MP];
-#pragma unroll
-    for (int m = 0; m < MP; ++m) srow[m] = (size_t)(min(16 * (wm + m), DK - 16) + il) * DV + 8 * (cols ? g : 0);
     const size_t seg = ((size_t)blockIdx.x * p.H + h) * (DK * DV);
     StageE segE, locE;
-    RowS segS[MP], locS[MP];
-    segE.load(static_cast<const T*>(p.bound[1]) + seg, DV, DK, tid);
+    segE.load(p.seg[1] + seg, DV, DK, tid);
+    // The state's transpose (rows dv, this wave's columns of dk) in accumulators; its D
+    // tiles are ready A operands of S dO.
+    f32x4 S[VT];
 #pragma unroll
-    for (int m = 0; m < MP; ++m) {
-        segS[m].load(static_cast<const T*>(p.bound[0]) + seg + srow[m], cols);
-#pragma unroll
-        for (int ks = 0; ks < KSV; ++ks) locS[m].x[ks].clear();   // the first block's own share
+    for (int x = 0; x < VT; ++x) {
+        S[x] = zero4();
+        if (wm < KT) S[x] = *reinterpret_cast<const f32x4*>(p.seg[0] + seg + (size_t)(16 * wm + il) * DV + 16 * x + 4 * g);
     }
 
     Stage<T, DK, C, NT> stq, stk;
     Stage<T, DV, C, NT> stv, sto;
     DecayLoad<T> a(p, h);
-    float preS = 1.f, preE = 1.f;
+    float preE = 1.f;
     // The next block's loads, in three parts between the phases of this one: a
     // wave waits where the memory pipe is full, and registers are freest last.
     auto fetch_qk = [&](int c) {
@@ -637,19 +616,14 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
         stv.load(static_cast<const T*>(p.v) + r0 * DV, rv, n, tid);
         sto.load(static_cast<const T*>(p.dO) + r0 * DV, rv, n, tid);
     };
-    auto fetch_states = [&](int c) {
+    auto fetch_state = [&](int c) {
         const size_t bs = (size_t)(block0 + c) * p.H + h;
-        locE.load(static_cast<const T*>(p.blk[1]) + bs * (DK * DV), DV, c + 1 < nc ? DK : 0, tid);
-        if (c) {
-#pragma unroll
-            for (int m = 0; m < MP; ++m) locS[m].load(static_cast<const T*>(p.blk[0]) + bs * (DK * DV) + srow[m], cols);
-        }
-        preS = p.blk_decay[0][bs];
-        preE = p.blk_decay[1][bs];
+        locE.load(p.blk + bs * (DK * DV), DV, c + 1 < nc ? DK : 0, tid);
+        preE = p.blk_decay[bs];
     };
     fetch_qk(0);
     fetch_vo(0);
-    fetch_states(0);
+    fetch_state(0);
     for (int c = 0; c < nc; ++c) {
         tid = here(tid0);
         lane = tid % WAVE;
@@ -663,26 +637,14 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
         stk.store(s.k, tid);
         stv.store(s.v, tid);
         sto.store(s.dO, tid);
-        // the states at this block: the segment's, decayed, and its own tokens' share
+        // the adjoint at this block: the segment's, decayed, and its own tokens' share
 #pragma unroll
         for (int m = 0; m < StageE::N; ++m) {
-            if constexpr (sizeof(T) == 2) {
-                const u32x4 x = locE.r[m], y = raw_here(segE.r[m]);
-                u32x2 lo, hi;
-                store4(reinterpret_cast<T*>(&lo), values(u32x2{y[0], y[1]}) * preE + values(u32x2{x[0], x[1]}));
-                store4(reinterpret_cast<T*>(&hi), values(u32x2{y[2], y[3]}) * preE + values(u32x2{x[2], x[3]}));
-                locE.r[m] = u32x4{lo[0], lo[1], hi[0], hi[1]};
-            } else {
-                locE.r[m] = __builtin_bit_cast(u32x4, values(raw_here(segE.r[m])) * preE + values(locE.r[m]));
-            }
+            const int e = tid + m * NT;
+            if (StageE::TOT % NT == 0 || e < StageE::TOT)
+                store4(s.E + (e / StageE::CPR) * SV + (e % StageE::CPR) * 4,
+                       values(raw_here(segE.r[m])) * preE + values(locE.r[m]));
         }
-        locE.store(s.E, tid);
-        V8 sf[MP][KSV];
-#pragma unroll
-        for (int m = 0; m < MP; ++m)
-#pragma unroll
-            for (int ks = 0; ks < KSV; ++ks)
-                sf[m][ks] = narrow<T>(values(raw_here(segS[m].x[ks])) * preS + values(locS[m].x[ks]));
         if (w == 0) block_decays<C, true>(s.dec, a.value(p, lane), lane);
         __syncthreads();
         if (c + 1 < nc) fetch_qk(c + 1);
@@ -716,83 +678,59 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
             }
         }
 
-        // products with the boundary states
-        f32x4 aq[MP][HT], ak[MP][HT], av[MP][HT];
+        // products with the boundary states, rounded to the input type here
+        f32x4 aq[HT], ak[HT], av[HT];
 #pragma unroll
-        for (int m = 0; m < MP; ++m)
-#pragma unroll
-            for (int tt = 0; tt < HT; ++tt) aq[m][tt] = ak[m][tt] = av[m][tt] = zero4();
-        if (wm < DK / 16) {
+        for (int tt = 0; tt < HT; ++tt) aq[tt] = ak[tt] = av[tt] = zero4();
+        if (wm < KT) {
             float xe = 0.f;
 #pragma unroll
             for (int ks = 0; ks < KSV; ++ks) {
-                V8 ef[MP];
-#pragma unroll
-                for (int m = 0; m < MP; ++m) {
-                    ef[m] = frag_nat(s.E, SV, 16 * (wm + m) + il, 32 * ks, g);
-                    if constexpr (DG) xe = dot8(ef[m], sf[m][ks], xe);
-                }
+                const V8 sf = narrow<T>(dtiles_to_frag(S[2 * ks], 2 * ks + 1 < VT ? S[(2 * ks + 1) % VT] : zero4()));
+                const V8 ef = frag_kpos(s.E, SV, 16 * wm + il, 32 * ks, g);
+                if constexpr (DG) xe = dot8(ef, sf, xe);
 #pragma unroll
                 for (int tt = 0; tt < HT; ++tt) {
                     const int i = 16 * (HT * th + tt) + il;
-                    const V8 of = frag_nat(s.dO, SV, i, 32 * ks, g), vf = frag_nat(s.v, SV, i, 32 * ks, g);
-#pragma unroll
-                    for (int m = 0; m < MP; ++m) {
-                        aq[m][tt] = mma(sf[m][ks], of, aq[m][tt]);
-                        ak[m][tt] = mma(ef[m], vf, ak[m][tt]);
-                    }
+                    aq[tt] = mma(sf, frag_kpos(s.dO, SV, i, 32 * ks, g), aq[tt]);
+                    ak[tt] = mma(ef, frag_kpos(s.v, SV, i, 32 * ks, g), ak[tt]);
                 }
             }
             if constexpr (DG) {
-                if (th == 0) {
-                    xe = wave_sum(xe);
-                    if (lane == 0) s.x[wm / MP] = xe;
-                }
+                xe = wave_sum(xe);
+                if (th == 0 && lane == 0) s.x[wm] = xe;
 #pragma unroll
                 for (int tt = 0; tt < HT; ++tt) {
                     const int i = 16 * (HT * th + tt) + il;
-                    f32x4 x = zero4(), y = zero4();
-#pragma unroll
-                    for (int m = 0; m < MP; ++m) {
-                        x += aq[m][tt] * values(*reinterpret_cast<const R4*>(s.q + i * SK + 16 * (wm + m) + 4 * g));
-                        y += ak[m][tt] * values(*reinterpret_cast<const R4*>(s.k + i * SK + 16 * (wm + m) + 4 * g));
-                    }
+                    const f32x4 x = aq[tt] * values(*reinterpret_cast<const R4*>(s.q + i * SK + 16 * wm + 4 * g));
+                    const f32x4 y = ak[tt] * values(*reinterpret_cast<const R4*>(s.k + i * SK + 16 * wm + 4 * g));
                     float rr = (x[0] + x[1]) + (x[2] + x[3]), cc = (y[0] + y[1]) + (y[2] + y[3]);
                     rr += __shfl_xor(rr, 16, WAVE);
                     rr += __shfl_xor(rr, 32, WAVE);
                     cc += __shfl_xor(cc, 16, WAVE);
                     cc += __shfl_xor(cc, 32, WAVE);
                     if (g == 0) {
-                        s.r[wm / MP * C + i] = rr;
-                        s.c[wm / MP * C + i] = cc;
+                        s.r[wm * C + i] = rr;
+                        s.c[wm * C + i] = cc;
                     }
                 }
             }
         }
-        if (wm < DV / 16) {
+        if (wm < VT) {
 #pragma unroll
             for (int ks = 0; ks < KSK; ++ks) {
-                V8 ef[MP];
+                const V8 ef = frag_tr(s.E, SV, 32 * ks, 16 * wm, g, il);
 #pragma unroll
-                for (int m = 0; m < MP; ++m) ef[m] = frag_tr(s.E, SV, 32 * ks, 16 * (wm + m), g, il);
-#pragma unroll
-                for (int tt = 0; tt < HT; ++tt) {
-                    const V8 kf = frag_kpos(s.k, SK, 16 * (HT * th + tt) + il, 32 * ks, g);
-#pragma unroll
-                    for (int m = 0; m < MP; ++m) av[m][tt] = mma(ef[m], kf, av[m][tt]);
-                }
+                for (int tt = 0; tt < HT; ++tt) av[tt] = mma(ef, frag_kpos(s.k, SK, 16 * (HT * th + tt) + il, 32 * ks, g), av[tt]);
             }
         }
 #pragma unroll
         for (int tt = 0; tt < HT; ++tt) {
             const int i = 16 * (HT * th + tt) + il;
             const float gi = s.dec.gam[i], di = s.dec.suf[i];
-#pragma unroll
-            for (int m = 0; m < MP; ++m) {
-                aq[m][tt] *= gi;
-                ak[m][tt] *= di;
-                av[m][tt] *= di;
-            }
+            aq[tt] *= gi;
+            ak[tt] *= di;
+            av[tt] *= di;
         }
         __syncthreads();
         if (c + 1 < nc) fetch_vo(c + 1);
@@ -801,33 +739,18 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
         // diagonal is skipped
 #pragma unroll
         for (int ks = 0; ks < KC; ++ks) {
-            V8 kf[MP], qf[MP], of[MP];
-#pragma unroll
-            for (int m = 0; m < MP; ++m) {
-                if (wm < DK / 16) {
-                    kf[m] = frag_tr(s.k, SK, 32 * ks, 16 * (wm + m), g, il);
-                    qf[m] = frag_tr(s.q, SK, 32 * ks, 16 * (wm + m), g, il);
-                }
-                if (wm < DV / 16) of[m] = frag_tr(s.dO, SV, 32 * ks, 16 * (wm + m), g, il);
+            V8 kf, qf, of;
+            if (wm < KT) {
+                kf = frag_tr(s.k, SK, 32 * ks, 16 * wm, g, il);
+                qf = frag_tr(s.q, SK, 32 * ks, 16 * wm, g, il);
             }
+            if (wm < VT) of = frag_tr(s.dO, SV, 32 * ks, 16 * wm, g, il);
 #pragma unroll
             for (int tt = 0; tt < HT; ++tt) {
                 const int t = HT * th + tt;
-                if (ks <= t / 2 && wm < DK / 16) {
-                    const V8 f = frag_kpos(s.b, SP, 16 * t + il, 32 * ks, g);
-#pragma unroll
-                    for (int m = 0; m < MP; ++m) aq[m][tt] = mma(kf[m], f, aq[m][tt]);
-                }
-                if (ks >= t / 2 && wm < DK / 16) {
-                    const V8 f = frag_tr(s.b, SP, 32 * ks, 16 * t, g, il);
-#pragma unroll
-                    for (int m = 0; m < MP; ++m) ak[m][tt] = mma(qf[m], f, ak[m][tt]);
-                }
-                if (ks >= t / 2 && wm < DV / 16) {
-                    const V8 f = frag_tr(s.p, SP, 32 * ks, 16 * t, g, il);
-#pragma unroll
-                    for (int m = 0; m < MP; ++m) av[m][tt] = mma(of[m], f, av[m][tt]);
-                }
+                if (ks <= t / 2 && wm < KT) aq[tt] = mma(kf, frag_kpos(s.b, SP, 16 * t + il, 32 * ks, g), aq[tt]);
+                if (ks >= t / 2 && wm < KT) ak[tt] = mma(qf, frag_tr(s.b, SP, 32 * ks, 16 * t, g, il), ak[tt]);
+                if (ks >= t / 2 && wm < VT) av[tt] = mma(of, frag_tr(s.p, SP, 32 * ks, 16 * t, g, il), av[tt]);
             }
         }
 #pragma unroll
@@ -835,21 +758,36 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
             const int i = 16 * (HT * th + tt) + il;
             if (i >= n) continue;
             const size_t row = r0 + (size_t)i * p.H;
-            auto put = [&](void* to, int width, const f32x4 (&y)[MP][HT]) {
-                T* at = static_cast<T*>(to) + row * width + 16 * wm;
-                if (wm >= width / 16) return;
-                if constexpr (MP == 2) {
-                    if (width > 16) return store_pair(at, y[0][tt], y[MP - 1][tt], g);
-                }
-                store4(at + 4 * g, y[0][tt]);
-            };
-            put(p.dq, DK, aq);
-            put(p.dk, DK, ak);
-            put(p.dv, DV, av);
+            if (wm < KT) {
+                store4(static_cast<T*>(p.dq) + row * DK + 16 * wm + 4 * g, aq[tt]);
+                store4(static_cast<T*>(p.dk) + row * DK + 16 * wm + 4 * g, ak[tt]);
+            }
+            if (wm < VT) store4(static_cast<T*>(p.dv) + row * DV + 16 * wm + 4 * g, av[tt]);
         }
 
+        // the state at the next block
+        if (c + 1 < nc && wm < KT) {
+            constexpr int U = VT < 4 ? VT : 4;   // no accumulator twice in a row
+            const float tot = s.dec.total;
+#pragma unroll
+            for (int x = 0; x < VT; ++x) S[x] *= tot;
+#pragma unroll
+            for (int ks = 0; ks < KC; ++ks) {
+                V8 part[PARTS], vf[U];
+                split<T, PARTS>(part, widen(frag_tr(s.k, SK, 32 * ks, 16 * wm, g, il)) * factors(s.dec.suf, 32 * ks, g));
+#pragma unroll
+                for (int x = 0; x < VT; x += U) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) vf[u] = frag_tr(s.v, SV, 32 * ks, 16 * (x + u), g, il);
+#pragma unroll
+                    for (int e = 0; e < PARTS; ++e)
+#pragma unroll
+                        for (int u = 0; u < U; ++u) S[x + u] = mma(vf[u], part[e], S[x + u]);
+                }
+            }
+        }
         if constexpr (!DG)
-            if (c + 1 < nc) fetch_states(c + 1);
+            if (c + 1 < nc) fetch_state(c + 1);
         if constexpr (DG) {
             // R tiles: rows i, columns t
             for (int e = w; e < CT * (CT + 1) / 2; e += NW) {
@@ -861,7 +799,7 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
                     R = mma(frag_kpos(s.M, SP, 16 * ti + il, 32 * ks, g), frag_kpos(s.D, SP, t, 32 * ks, g), R);
                 f32x4 ri = zero4();
 #pragma unroll
-                for (int m = 0; m < NS; ++m) ri += *reinterpret_cast<const f32x4*>(s.r + m * C + 16 * ti + 4 * g);
+                for (int m = 0; m < KT; ++m) ri += *reinterpret_cast<const f32x4*>(s.r + m * C + 16 * ti + 4 * g);
                 R += ri * (t ? s.dec.gam[t - 1] : 1.f);
                 float mid = 1.f;
                 for (int m = tt + 1; m < ti; ++m) mid *= s.dec.blk[m];
@@ -877,12 +815,12 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
                 sum += __shfl_xor(sum, 32, WAVE);
                 if (g == 0) s.da[ti * C + t] = sum;
             }
-            if (c + 1 < nc) fetch_states(c + 1);
+            if (c + 1 < nc) fetch_state(c + 1);
             __syncthreads();
             if (w == NW - 1) {
                 const int t = lane % C;   // C = 32: the upper lanes repeat the lower ones
                 float c0 = 0.f, X = 0.f, acc = 0.f;
-                for (int m = 0; m < NS; ++m) {
+                for (int m = 0; m < KT; ++m) {
                     c0 += s.c[m * C + t];
                     X += s.x[m];
                 }
@@ -984,7 +922,7 @@ int segment_tokens(int T, int N, int H, int dk, int dv, bool packed, bool grad) 
 bool whole_sequences(int T) { return T <= 256; }
 
 struct LinWorkspace {
-    size_t seg[2], bound[2], decay, blk[2], blk_decay[2], total;
+    size_t seg[2], decay, blk, blk_decay, total;
 };
 LinWorkspace workspace_layout(int T, int N, int H, int dk, int dv, bool packed, bool bf16, bool grad, int L) {
     const size_t segs = (size_t)seq_blocks_bound(T, N, L, packed) * H, state = (size_t)dk * dv;
@@ -992,17 +930,12 @@ LinWorkspace workspace_layout(int T, int N, int H, int dk, int dv, bool packed, 
     LinWorkspace w{};
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t r = at; at += al256(bytes); return r; };
-    const size_t es = bf16 ? 2 : 4;
     w.seg[0] = take(segs * state * 4);
-    w.bound[0] = take(segs * state * es);
     w.decay = take(segs * 4);
     if (grad) {
         w.seg[1] = take(segs * state * 4);
-        w.bound[1] = take(segs * state * es);
-        w.blk[0] = take(blocks * state * es);
-        w.blk[1] = take(blocks * state * es);
-        w.blk_decay[0] = take(blocks * 4);
-        w.blk_decay[1] = take(blocks * 4);
+        w.blk = take(blocks * state * 4);
+        w.blk_decay = take(blocks * 4);
     }
     w.total = at;
     return w;
@@ -1044,7 +977,7 @@ template <class T, int DK, int DV> hipError_t forward(LinParams p, const LinArgs
     hipError_t e = hipSuccess;
     if (p.map.T > 0) e = launch_state<T, DK, DV, false>(p, segs, 1, a.stream);
     if (e != hipSuccess) return e;
-    e = launch(lin_scan_kernel<T>, (size_t)p.map.N * p.H, (DK * DV / 4 + 255) / 256, 1, 256, 0, a.stream, p, DK * DV);
+    e = launch(lin_scan_kernel, (size_t)p.map.N * p.H, (DK * DV / 4 + 255) / 256, 1, 256, 0, a.stream, p, DK * DV);
     if (e != hipSuccess || p.map.T == 0) return e;
     return launch_out<T, DK, DV, false>(p, segs, a.stream);
 }
@@ -1055,7 +988,7 @@ template <class T, int DK, int DV> hipError_t backward(const LinParams& p, const
     hipError_t e = hipSuccess;
     if (p.map.T > 0) e = launch_state<T, DK, DV, true>(p, segs, 2, a.stream);
     if (e != hipSuccess) return e;
-    e = launch(lin_scan_kernel<T>, (size_t)p.map.N * p.H, (DK * DV / 4 + 255) / 256, 2, 256, 0, a.stream, p, DK * DV);
+    e = launch(lin_scan_kernel, (size_t)p.map.N * p.H, (DK * DV / 4 + 255) / 256, 2, 256, 0, a.stream, p, DK * DV);
     if (e != hipSuccess || p.map.T == 0) return e;
     auto go = [&](auto kern, auto dg) {
         using L = LinGradTiles<T, DK, DV, dg.value>;
@@ -1084,12 +1017,9 @@ LinParams make_params(const LinArgs& a) {
     p.L = segment_tokens(a.T, a.N, a.H, a.dk, a.dv, packed, grad);
     const LinWorkspace w = workspace_layout(a.T, a.N, a.H, a.dk, a.dv, packed, a.bf16, grad, p.L);
     char* base = static_cast<char*>(a.workspace);
-    for (int d = 0; d < 2; ++d) {
-        p.seg[d] = reinterpret_cast<float*>(base + w.seg[d]);
-        p.bound[d] = base + w.bound[d];
-        p.blk[d] = base + w.blk[d];
-        p.blk_decay[d] = reinterpret_cast<float*>(base + w.blk_decay[d]);
-    }
+    for (int d = 0; d < 2; ++d) p.seg[d] = reinterpret_cast<float*>(base + w.seg[d]);
+    p.blk = reinterpret_cast<float*>(base + w.blk);
+    p.blk_decay = reinterpret_cast<float*>(base + w.blk_decay);
     p.seg_decay = reinterpret_cast<float*>(base + w.decay);
     return p;
 }

@@ -126,31 +126,11 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 template <class T> struct Raw4;
 template <> struct Raw4<uint16_t> { using V = u32x2; };
 template <> struct Raw4<float> { using V = u32x4; };
-// eight of them, in pieces of 16 bytes
-template <class T> struct Raw8 {
-    u32x4 x[sizeof(T) / 2];
-    __device__ __forceinline__ void load(const T* p) {
-#pragma unroll
-        for (int m = 0; m < (int)sizeof(T) / 2; ++m) x[m] = reinterpret_cast<const u32x4*>(p)[m];
-    }
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int m = 0; m < (int)sizeof(T) / 2; ++m) x[m] = u32x4(0);
-    }
-};
 __device__ __forceinline__ f32x4 values(const u32x2& x) {
     return f32x4{__uint_as_float(x[0] << 16), __uint_as_float(x[0] & 0xffff0000u), __uint_as_float(x[1] << 16),
                  __uint_as_float(x[1] & 0xffff0000u)};
 }
 __device__ __forceinline__ f32x4 values(const u32x4& x) { return __builtin_bit_cast(f32x4, x); }
-__device__ __forceinline__ f32x8 values8(const f32x4& a, const f32x4& b) {
-    return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-}
-__device__ __forceinline__ f32x8 values(const Raw8<uint16_t>& r) {
-    return values8(values(u32x2{r.x[0][0], r.x[0][1]}), values(u32x2{r.x[0][2], r.x[0][3]}));
-}
-__device__ __forceinline__ f32x8 values(const Raw8<float>& r) { return values8(values(r.x[0]), values(r.x[1])); }
-
 __device__ __forceinline__ float from_el(uint16_t x) { return bf16_bits_to_f32(x); }
 __device__ __forceinline__ float from_el(float x) { return x; }
 __device__ __forceinline__ void store1(uint16_t* p, float x) {
@@ -205,12 +185,6 @@ template <class V> __device__ __forceinline__ V raw_here(V x) {
     asm volatile("" : "+v"(x));
     return x;
 }
-template <class T> __device__ __forceinline__ Raw8<T> raw_here(Raw8<T> r) {
-#pragma unroll
-    for (int m = 0; m < (int)sizeof(T) / 2; ++m) r.x[m] = raw_here(r.x[m]);
-    return r;
-}
-
 // zero columns D..31 of a narrow tile
 template <class T, int D> __device__ __forceinline__ void zero_pad_cols(T* tile, int rows, int tid, int nt) {
     if constexpr (D < 32) {
