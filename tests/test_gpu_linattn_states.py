@@ -99,6 +99,30 @@ def test_start_state_in_32_bits(kda, dk, dv):  # noqa: F811
 
 
 @pytest.mark.parametrize("dk,dv", SIZES)
+def test_decayed_rows_in_32_bits(kda, dk, dv):  # noqa: F811
+    """S0, decayed, and a token's row, decayed by as much, almost cancel."""
+    assert min(tokens_per_segment(kda, dk, dv, False)) >= 128
+    g, x, i = torch.Generator().manual_seed(dk + dv + 1), zeros(dk, dv), 9
+    v, y = almost(g, B, H, dv)
+    x["S0"] = torch.zeros(B, H, dk, dv)
+    x["S0"][:, :, i] = y
+    x["k"][:, 60, :, i] = 1
+    x["v"][:, 60] = v.float()
+    x["gate"][:, 61:64] = decays(g)
+    x["q"][..., i] = one_hot(g, 1)[..., 0]
+    x = to_gpu(x)
+    o, S_T = kda.linattn_fwd(x["q"], x["k"], x["v"], x["gate"], S0=x["S0"])
+    ro, rS, _ = mixers.linattn(x["q"], x["k"], x["v"], x["gate"], x["S0"], mixers.spans(B, T))
+    near("S_T", S_T, rS, HELD)
+    near("o", o[:, 64:], ro[:, 64:], READ)
+    # one short sequence in one launch
+    part = {n: t[:, :100].contiguous() for n, t in x.items() if n != "S0"}
+    o, S_T = kda.linattn_fwd(part["q"], part["k"], part["v"], part["gate"], S0=x["S0"])
+    near("S_T", S_T, rS, HELD)
+    near("o", o[:, 64:], ro[:, 64:100], READ)
+
+
+@pytest.mark.parametrize("dk,dv", SIZES)
 def test_gradient_of_queries_in_32_bits(kda, dk, dv):  # noqa: F811
     """The same state, as dq = S dO reads it."""
     assert min(tokens_per_segment(kda, dk, dv, True)) >= 128
