@@ -26,6 +26,10 @@ bool lin_sizes_ok(int B, int H, int T, int dk, int dv, int N, int has_cu, int dt
     const int64_t n = has_cu ? N : B;
     return n * H <= INT32_MAX && n * (T + 128LL) <= INT32_MAX;
 }
+bool lin_grad_sizes_ok(int B, int H, int T, int dk, int dv, int N, int has_cu, int dtype) {
+    return lin_sizes_ok(B, H, T, dk, dv, N, has_cu, dtype) &&
+           kda::lin_grad_fits(T, has_cu ? N : B, H, dk, dv, has_cu != 0, dtype == KDA_BF16);
+}
 
 // The checks that the linear-attention forward and backward share, and the
 // fields that they fill.
@@ -515,7 +519,7 @@ size_t kda_linattn_fwd_workspace_bytes(int B, int H, int T, int dk, int dv, int 
 }
 
 size_t kda_linattn_bwd_workspace_bytes(int B, int H, int T, int dk, int dv, int N, int has_cu, int dtype) {
-    return lin_sizes_ok(B, H, T, dk, dv, N, has_cu, dtype)
+    return lin_grad_sizes_ok(B, H, T, dk, dv, N, has_cu, dtype)
                ? kda::lin_workspace_bytes(B, H, T, dk, dv, has_cu != 0, N, dtype == KDA_BF16, true) : 0;
 }
 
@@ -542,6 +546,7 @@ int kda_linattn_bwd(const void* q, const void* k, const void* v, const void* gat
     kda::LinArgs a{};
     const int st = lin_args(&a, q, k, v, gate, S0, B, H, T, dk, dv, cu_seqlens, N, dtype, gate_kind, workspace, stream);
     if (st != KDA_OK) return st;
+    if (!lin_grad_sizes_ok(B, H, T, dk, dv, a.N, cu_seqlens != nullptr, dtype)) return KDA_ENOTSUP;
     if (T > 0 && (!dO || !grad_q || !grad_k || !grad_v || (!grad_gate && !a.head_gate))) return KDA_EINVAL;
     if (a.head_gate && grad_gate) return KDA_EINVAL;
     const uintptr_t es = dtype == KDA_BF16 ? 2 : 4;

@@ -163,6 +163,9 @@ hipError_t launch_cbwd(const BwdArgs& a);
 hipError_t launch_chunk_fwd(const ChunkArgs& a);
 
 size_t lin_workspace_bytes(int B, int H, int T, int dk, int dv, bool packed, int N, bool bf16, bool grad);
+// whether the gradient's largest launch fits a grid
+bool lin_grad_fits(int T, int N, int H, int dk, int dv, bool packed, bool bf16);
+constexpr int lin_decode_threads(int dk, int dv) { return dk * dv / 4 < 512 ? dk * dv / 4 : 512; }   // a head's workgroup
 hipError_t launch_lin_fwd(const LinArgs& a);
 hipError_t launch_lin_bwd(const LinArgs& a);
 hipError_t launch_lin_decode(const LinDecodeArgs& a);

@@ -290,14 +290,15 @@ __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
 
 // ---------------------------------------------------------------- scan over segments
 
-// Elementwise over dk x dv, one (sequence, head) per blockIdx.x; bound by the latency of
+// Elementwise over dk x dv, one (sequence, head) per (blockIdx.x, y); bound by the latency of
 // a chain of loads as long as a sequence has segments (eight in flight). Direction 0:
 // from the segments' contributions the state at each segment's start, and S_T.
 // Direction 1: the adjoint at each one's end, and dS0. In place, in fp32.
+__host__ __device__ constexpr int scan_parts(int dkdv) { return (dkdv / 4 + 255) / 256; }   // workgroups
 __global__ void __launch_bounds__(256) lin_scan_kernel(LinParams p, int dkdv) {
     lds_poison(0);
-    const int s = blockIdx.x / p.H, h = blockIdx.x % p.H, rev = blockIdx.z;
-    const int e = 4 * (blockIdx.y * 256 + threadIdx.x);
+    const int s = blockIdx.x, h = blockIdx.y, parts = scan_parts(dkdv), rev = blockIdx.z / parts;
+    const int e = 4 * (blockIdx.z % parts * 256 + threadIdx.x);
     if (e >= dkdv) return;
     int first, len;
     if (p.map.cu) {
@@ -943,7 +944,9 @@ LinWorkspace workspace_layout(int T, int N, int H, int dk, int dv, bool packed, 
     return w;
 }
 
-// (a launch has fewer than 2^32 threads along x)
+// A launch has fewer than 2^32 threads along x. The sizes that the calls accept
+// (N * (T + 128) < 2^31) give fewer than 2^24 segments, at most 512 more than
+// sequences, so that only the gradient's 512 and 1,024 threads can exceed it.
 template <class K, class... A>
 hipError_t launch(K kern, size_t x, unsigned y, unsigned z, int threads, size_t lds, hipStream_t stream, A... args) {
     if (x * threads > 0xffffffffu) return hipErrorInvalidConfiguration;
@@ -979,7 +982,7 @@ template <class T, int DK, int DV> hipError_t forward(LinParams p, const LinArgs
     hipError_t e = hipSuccess;
     if (p.map.T > 0) e = launch_state<T, DK, DV, false>(p, segs, 1, a.stream);
     if (e != hipSuccess) return e;
-    e = launch(lin_scan_kernel, (size_t)p.map.N * p.H, (DK * DV / 4 + 255) / 256, 1, 256, 0, a.stream, p, DK * DV);
+    e = launch(lin_scan_kernel, p.map.N, p.H, scan_parts(DK * DV), 256, 0, a.stream, p, DK * DV);
     if (e != hipSuccess || p.map.T == 0) return e;
     return launch_out<T, DK, DV, false>(p, segs, a.stream);
 }
@@ -990,7 +993,7 @@ template <class T, int DK, int DV> hipError_t backward(const LinParams& p, const
     hipError_t e = hipSuccess;
     if (p.map.T > 0) e = launch_state<T, DK, DV, true>(p, segs, 2, a.stream);
     if (e != hipSuccess) return e;
-    e = launch(lin_scan_kernel, (size_t)p.map.N * p.H, (DK * DV / 4 + 255) / 256, 2, 256, 0, a.stream, p, DK * DV);
+    e = launch(lin_scan_kernel, p.map.N, p.H, 2 * scan_parts(DK * DV), 256, 0, a.stream, p, DK * DV);
     if (e != hipSuccess || p.map.T == 0) return e;
     auto go = [&](auto kern, auto dg) {
         using L = LinGradTiles<T, DK, DV, dg.value>;
@@ -1001,7 +1004,7 @@ template <class T, int DK, int DV> hipError_t backward(const LinParams& p, const
 }
 
 template <class T, int DK, int DV> hipError_t decode(const LinDecodeArgs& a) {
-    constexpr int NT = DK * DV / 4 < 512 ? DK * DV / 4 : 512;
+    constexpr int NT = lin_decode_threads(DK, DV);
     return launch(lin_decode_kernel<T, DK, DV, NT>, (size_t)a.N * a.H, 1, 1, NT, 0, a.stream, (const T*)a.q, (const T*)a.k,
                   (const T*)a.v, a.gate, a.S, (T*)a.o, a.H, (int)a.head_gate);
 }
@@ -1033,6 +1036,16 @@ size_t lin_workspace_bytes(int B, int H, int T, int dk, int dv, bool packed, int
     if (!grad && T > 0 && whole_sequences(T)) return 256;
     const size_t n = workspace_layout(T, N, H, dk, dv, packed, bf16, grad, segment_tokens(T, N, H, dk, dv, packed, grad)).total;
     return n ? n : 256;
+}
+
+bool lin_grad_fits(int T, int N, int H, int dk, int dv, bool packed, bool bf16) {
+    const long segs = seq_blocks_bound(T, N, segment_tokens(T, N, H, dk, dv, packed, true), packed);
+    const long threads = KDA_SWITCH_DIM(dk, DK, [&] {
+        return KDA_SWITCH_DIM(dv, DV, [&] {
+            return 64L * (bf16 ? LinGradTiles<uint16_t, DK, DV, true>::NW : LinGradTiles<float, DK, DV, true>::NW);
+        });
+    });
+    return segs * threads <= 0xffffffffL;
 }
 
 hipError_t launch_lin_fwd(const LinArgs& a) {

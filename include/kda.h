@@ -373,7 +373,8 @@ int kda_linattn_fwd(const void* q, const void* k, const void* v, const void* gat
  * call is reused, and rows at or behind cu_seqlens[N] are left as they are. dO
  * and the gradients must be 16-byte aligned (grad_gate and
  * states: their element). workspace: kda_linattn_bwd_workspace_bytes(...)
- * bytes (segment states, and the state and adjoint of every block), required.
+ * bytes (segment states, and the adjoint of every block), required. At most
+ * 4,000,000 sequences (KDA_ENOTSUP beyond what one launch takes).
  */
 size_t kda_linattn_bwd_workspace_bytes(int B, int H, int T, int dk, int dv, int N, int has_cu_seqlens, int dtype);
 int kda_linattn_bwd(const void* q, const void* k, const void* v, const void* gate, const float* S0, const void* dO,

@@ -1,0 +1,18 @@
+"""Calls of linear and window attention beyond what one launch takes are refused by
+their checks, before anything is enqueued (no GPU: every call here fails its checks)."""
+import pytest
+
+from gated_delta_rule_46_amd import kda
+from test_mixers_abi import FAKE, lib, lin_bwd  # noqa: F401 (fixture)
+
+
+@pytest.mark.parametrize("dk,dv,dtype", [(128, 64, kda.KDA_BF16), (128, 128, kda.KDA_F32), (16, 128, kda.KDA_BF16)])
+def test_linear_gradient_of_millions_of_sequences(lib, dk, dv, dtype):  # noqa: F811
+    """A workgroup of 512 or 1,024 threads a segment, one segment a sequence at least."""
+    for kw in (dict(B=2 ** 23, N=0), dict(B=1, N=2 ** 23, cu=FAKE)):
+        assert lin_bwd(lib, T=1, H=1, dk=dk, dv=dv, dtype=dtype, **kw) == kda.KDA_ENOTSUP
+        assert lib.kda_linattn_bwd_workspace_bytes(kw["B"], 1, 1, dk, dv, kw["N"], int(kw["N"] > 0), dtype) == 0
+        # within the forward's sizes, and within the gradient's for smaller states
+        assert lib.kda_linattn_fwd_workspace_bytes(kw["B"], 1, 1, dk, dv, kw["N"], int(kw["N"] > 0), dtype) > 0
+        assert lib.kda_linattn_bwd_workspace_bytes(kw["B"], 1, 1, 16, 16, kw["N"], int(kw["N"] > 0), dtype) > 0
+    assert lib.kda_linattn_bwd_workspace_bytes(4000000, 1, 1, dk, dv, 0, 0, dtype) > 0
