@@ -569,7 +569,8 @@ int kda_linattn_bwd(const void* q, const void* k, const void* v, const void* gat
 int kda_linattn_decode_step(const void* q, const void* k, const void* v, const void* gate, float* S, void* o, int N,
                             int H, int dk, int dv, int dtype, int gate_kind, void* stream) {
     if (N <= 0 || H <= 0) return KDA_EINVAL;
-    if (!size_ok(dk) || !size_ok(dv) || (int64_t)N * H > INT32_MAX) return KDA_ENOTSUP;
+    if (!size_ok(dk) || !size_ok(dv)) return KDA_ENOTSUP;
+    if ((int64_t)N * H > (int64_t)UINT32_MAX / kda::lin_decode_threads(dk, dv)) return KDA_ENOTSUP;   // one launch
     if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ENOTSUP;
     if (gate_kind != KDA_GATE_SCALAR && gate_kind != KDA_GATE_HEAD) return KDA_ENOTSUP;
     if (!q || !k || !v || !gate || !S || !o) return KDA_EINVAL;

@@ -387,7 +387,7 @@ int kda_linattn_bwd(const void* q, const void* k, const void* v, const void* gat
  * updated in place (16-byte aligned; every other pointer to its element).
  * q, k [N, H, dk]; v, o [N, H, dv] in the input dtype; gate [N, H] in the
  * input dtype (KDA_GATE_SCALAR) or [H] fp32 (KDA_GATE_HEAD). o must not alias
- * S or the inputs.
+ * S or the inputs. N * H * min(dk * dv / 4, 512) < 2^32 (KDA_ENOTSUP otherwise).
  */
 int kda_linattn_decode_step(const void* q, const void* k, const void* v, const void* gate, float* S, void* o, int N,
                             int H, int dk, int dv, int dtype, int gate_kind, void* stream);

@@ -16,3 +16,10 @@ def test_linear_gradient_of_millions_of_sequences(lib, dk, dv, dtype):  # noqa: 
         assert lib.kda_linattn_fwd_workspace_bytes(kw["B"], 1, 1, dk, dv, kw["N"], int(kw["N"] > 0), dtype) > 0
         assert lib.kda_linattn_bwd_workspace_bytes(kw["B"], 1, 1, 16, 16, kw["N"], int(kw["N"] > 0), dtype) > 0
     assert lib.kda_linattn_bwd_workspace_bytes(4000000, 1, 1, dk, dv, 0, 0, dtype) > 0
+
+
+@pytest.mark.parametrize("N,H,dk,dv", [(2 ** 22, 2, 128, 128), (2 ** 23, 1, 16, 128), (2 ** 26, 1, 16, 16), (1, 2 ** 25, 32, 16),
+                                       (2 ** 31 - 1, 2 ** 31 - 1, 64, 64)])
+def test_linear_step_beyond_a_launch(lib, N, H, dk, dv):  # noqa: F811
+    assert lib.kda_linattn_decode_step(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, N, H, dk, dv, kda.KDA_BF16, kda.GATE_SCALAR,
+                                       None) == kda.KDA_ENOTSUP
