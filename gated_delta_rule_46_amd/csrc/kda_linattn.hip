@@ -860,7 +860,8 @@ __global__ void __launch_bounds__(NT) lin_decode_kernel(const T* __restrict__ q,
     constexpr int CG = DV / 4, RG = NT / CG, RPT = DK / RG, NW = NT / WAVE;
     static_assert(NT % WAVE == 0 && DK % RG == 0 && RPT >= 1, "decode tiling");
     lds_poison(0);
-    __shared__ float s_k[DK], s_q[DK], s_v[DV], s_red[NW][DV], s_kq[NW];
+    __shared__ float s_k[DK], s_q[DK], s_kq[NW];
+    __shared__ __align__(16) float s_v[DV], s_red[NW][DV];   // read and written four at a time
     const size_t pair = blockIdx.x;
     const int t = threadIdx.x, cg = t % CG, rg = t / CG, lane = t % WAVE, w = t / WAVE;
     float kq = 0.f;
