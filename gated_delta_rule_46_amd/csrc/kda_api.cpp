@@ -585,6 +585,7 @@ int kda_linattn_decode_step(const void* q, const void* k, const void* v, const v
 
 size_t kda_swa_bwd_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int window, int sinks, int N, int has_cu) {
     if (!swa_sizes_ok(B, Hq, Hkv, T, d, window, sinks, N, has_cu)) return 0;
+    if (!kda::swa_grad_fits(T, has_cu ? N : B, Hq, Hkv, window, sinks, has_cu != 0)) return 0;
     return kda::swa_bwd_workspace_bytes(T, has_cu ? N : B, Hq, Hkv, d, window, sinks, has_cu != 0);
 }
 
@@ -614,6 +615,7 @@ int kda_swa_bwd(const void* q, const void* k, const void* v, const void* o, cons
     const int st = swa_args(&a, q, k, v, B, Hq, Hkv, T, d, window, sinks, scale, cu_seqlens, N, dtype, stream);
     if (st != KDA_OK) return st;
     if (T == 0) return KDA_OK;
+    if (!kda::swa_grad_fits(T, a.N, Hq, Hkv, window, sinks, cu_seqlens != nullptr)) return KDA_ENOTSUP;
     if (!o || !lse || !dO || !grad_q || !grad_k || !grad_v || !workspace) return KDA_EINVAL;
     if (!aligned(o) || !aligned(lse, 4) || !aligned(dO) || !aligned(grad_q) || !aligned(grad_k) || !aligned(grad_v) ||
         !aligned(workspace))

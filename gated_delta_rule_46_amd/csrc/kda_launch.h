@@ -170,6 +170,8 @@ hipError_t launch_lin_fwd(const LinArgs& a);
 hipError_t launch_lin_bwd(const LinArgs& a);
 hipError_t launch_lin_decode(const LinDecodeArgs& a);
 
+// whether the gradient's largest launch fits a grid
+bool swa_grad_fits(int T, int N, int Hq, int Hkv, int window, int sinks, bool packed);
 size_t swa_bwd_workspace_bytes(int T, int N, int Hq, int Hkv, int d, int window, int sinks, bool packed);
 size_t swa_decode_workspace_bytes(int N, int Hq, int Hkv, int d, int window, int sinks);
 hipError_t launch_swa_fwd(const SwaArgs& a);

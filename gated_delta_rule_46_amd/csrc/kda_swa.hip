@@ -1190,6 +1190,13 @@ template <class T, int D> hipError_t decode(const SwaDecodeArgs& a) {
 
 }  // namespace
 
+bool swa_grad_fits(int T, int N, int Hq, int Hkv, int window, int sinks, bool packed) {
+    if (T <= 0) return true;
+    SwaParams p{};
+    grad_parts(T, N, Hq / Hkv, Hkv, std::min(window, T), std::min(sinks, T), packed, p);
+    return grad_items(p) * Hkv * p.head_parts * 256 <= 0xffffffffL;
+}
+
 size_t swa_bwd_workspace_bytes(int T, int N, int Hq, int Hkv, int d, int window, int sinks, bool packed) {
     SwaParams p{};
     const size_t slots = T > 0 ? grad_parts(T, N, Hq / Hkv, Hkv, std::min(window, T), std::min(sinks, T), packed, p) : 0;

@@ -424,6 +424,10 @@ int kda_swa_fwd(const void* q, const void* k, const void* v, void* o, float* lse
  * layouts, those of a kv head summed over its query heads; sums run in a fixed
  * order (repeated calls agree bit for bit); rows at or behind cu_seqlens[N] are
  * left as they are. workspace: kda_swa_bwd_workspace_bytes(...) bytes, required.
+ * Besides kda_swa_fwd's sizes: fewer than 2^24 pairs of a kv head and a block of 64
+ * keys, where each block with sinks of a sequence of more than window + 64 tokens
+ * counts once more for every part that its rows are cut into, together at most 64 a
+ * sequence (KDA_ENOTSUP otherwise).
  */
 size_t kda_swa_bwd_workspace_bytes(int B, int Hq, int Hkv, int T, int d, int window, int sinks, int N,
                                    int has_cu_seqlens);

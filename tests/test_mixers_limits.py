@@ -3,7 +3,7 @@ their checks, before anything is enqueued (no GPU: every call here fails its che
 import pytest
 
 from gated_delta_rule_46_amd import kda
-from test_mixers_abi import FAKE, lib, lin_bwd  # noqa: F401 (fixture)
+from test_mixers_abi import FAKE, lib, lin_bwd, swa_bwd  # noqa: F401 (fixture)
 
 
 @pytest.mark.parametrize("dk,dv,dtype", [(128, 64, kda.KDA_BF16), (128, 128, kda.KDA_F32), (16, 128, kda.KDA_BF16)])
@@ -23,3 +23,12 @@ def test_linear_gradient_of_millions_of_sequences(lib, dk, dv, dtype):  # noqa: 
 def test_linear_step_beyond_a_launch(lib, N, H, dk, dv):  # noqa: F811
     assert lib.kda_linattn_decode_step(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, N, H, dk, dv, kda.KDA_BF16, kda.GATE_SCALAR,
                                        None) == kda.KDA_ENOTSUP
+
+
+@pytest.mark.parametrize("kw", [dict(B=65535, T=260, N=0), dict(B=65535, T=4096, N=0, Hq=3, Hkv=3)])
+def test_window_gradient_beyond_a_launch(lib, kw):  # noqa: F811
+    """As many key blocks as the forward takes, and parts of those with sinks besides."""
+    kw = dict(dict(Hq=50, Hkv=50, d=32, window=1, sinks=256), **kw)
+    assert swa_bwd(lib, **kw) == kda.KDA_ENOTSUP
+    size = lambda sinks: lib.kda_swa_bwd_workspace_bytes(kw["B"], kw["Hq"], kw["Hkv"], kw["T"], 32, 1, sinks, 0, 0)  # noqa: E731
+    assert size(256) == 0 and size(0) > 0   # without sinks it is within the forward's sizes
