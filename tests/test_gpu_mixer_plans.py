@@ -1,0 +1,112 @@
+"""Linear attention in the plan that large inputs take, segments of several blocks,
+against the recurrence in 64 bits at head sizes of 16 to 128. Which plan an input takes
+is read off the workspace's size, so that a change of the rules cannot move these cases
+to other plans unseen."""
+import pytest
+import torch
+
+import test_gpu_linattn as lin
+from mixer_checks import close
+from oracle import mixers
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+kda = lin.kda   # the fixture
+
+
+# ---------------------------------------------------------------- linear attention
+
+def blocks_per_segment(kda, x, grad):
+    """At most, by the size of the workspace: fp32 states of every segment and, in the
+    gradient, of every block of 64 (fp32: 32) tokens."""
+    B, T, H, dk = x["q"].shape
+    dv, dt, cu = x["v"].shape[-1], x["q"].dtype, x["cu"]
+    N, state, C = len(x["seqs"]), dk * dv, 64 if dt == BF16 else 32
+    numbers = lambda L: T // L + N + 1 if cu is not None else B * ((T + L - 1) // L)  # noqa: E731
+    if grad:
+        size = kda.linattn_bwd_workspace_bytes(B, H, T, dk, dv, N, cu is not None, dt)
+        segs = (size - numbers(C) * H * (4 * state + 4)) // (8 * state + 4)
+    else:
+        segs = kda.linattn_fwd_workspace_bytes(B, H, T, dk, dv, N, cu is not None, dt) // (4 * state + 4)
+    return min(L for L in range(64, T + 64, 64) if numbers(L) * H <= segs) // C
+
+
+def term_sizes(x):
+    """Per element of o, dq, dk and dv the root of its terms' summed squares, a term being
+    one pair of tokens' or one row's of a boundary state or adjoint. Decays that are zero
+    here and there cut some tokens' sums to one term and leave hundreds to others, whose
+    values and errors are several times the rms over all: each term is rounded by itself,
+    up to 2^-8 of it, so an element is off by tau (five times the root of the mean square
+    of three such roundings) times this size, and by less than tau times the rms only where
+    the size is below it."""
+    q, k, v, dO = (x[n].double() for n in ("q", "k", "v", "dO"))
+    a = x["gate"].double().expand(q.shape[:3])
+    size = {n: torch.zeros_like(t) for n, t in (("o", v), ("dq", q), ("dk", k), ("dv", v))}
+    for s, (b, t0, t1) in enumerate(x["seqs"]):
+        n = t1 - t0
+        if n == 0:
+            continue
+        al, qs, ks, vs, gs = (t[b, t0:t1].transpose(0, 1).contiguous() for t in (a, q, k, v, dO))   # [H, n, .]
+        D = torch.zeros(q.shape[2], n, n, dtype=torch.float64, device=q.device)   # D[i, j] = a_{j+1} .. a_i
+        for i in range(n):
+            if i:
+                D[:, i] = D[:, i - 1] * al[:, i, None]
+            D[:, i, i] = 1.0
+        flip = lambda t: t.transpose(1, 2).contiguous()  # noqa: E731
+        P, R = ((D * (y @ flip(z))).square() for y, z in ((qs, ks), (gs, vs)))
+        first, last = (D[:, :, 0] * al[:, :1]).square()[:, :, None], D[:, n - 1].square()[:, :, None]
+        qs, ks, vs, gs, S0, E = (t.square() for t in (qs, ks, vs, gs, x["S0"][s].double(), x["dS_T"][s].double()))
+        for m, y in (("o", P @ vs + first * (qs @ S0)), ("dq", R @ ks + first * (gs @ flip(S0))),
+                     ("dk", flip(R) @ qs + last * (vs @ flip(E))), ("dv", flip(P) @ gs + last * (ks @ E))):
+            size[m][b, t0:t1] = y.sqrt().transpose(0, 1)
+    return size
+
+
+def check_fwd(kda, x):
+    o, S_T = kda.linattn_fwd(x["q"], x["k"], x["v"], x["gate"], S0=x["S0"], cu_seqlens=x["cu"])
+    ro, rS, _ = mixers.linattn(x["q"], x["k"], x["v"], x["gate"], x["S0"], x["seqs"])
+    close("o", o, ro, x["q"].dtype, size=term_sizes(x)["o"])
+    close("S_T", S_T, rS, x["q"].dtype)
+
+
+def check_bwd(kda, x):
+    g = kda.linattn_bwd(x["q"], x["k"], x["v"], x["gate"], x["dO"], S0=x["S0"], dS_T=x["dS_T"], cu_seqlens=x["cu"])
+    r = mixers.linattn_grad(x["q"], x["k"], x["v"], x["gate"], x["dO"], x["S0"], x["dS_T"], x["seqs"])
+    size = term_sizes(x)
+    for n in ("dq", "dk", "dv", "dgate", "dS0"):
+        if g[n] is not None:
+            close(n, g[n], r[n], x["q"].dtype, size=size.get(n))
+    assert (g["dgate"] is None) == (x["gate"].dim() == 1)
+
+
+LONG = [
+    # B, T, H, dk, dv, lens; more than 33,280 tokens by heads, 16,640 for the gradient
+    (1, 1100, 32, 64, 64, None), (1, 1100, 32, 128, 128, None), (1, 1100, 32, 64, 128, None), (2, 570, 64, 128, 64, None),
+    (1, 1100, 32, 32, 128, None), (1, 0, 32, 128, 128, [700, 1, 0, 333, 66]), (1, 0, 32, 64, 64, [65, 1000, 35]),
+]
+WIDE = [(2, 700, 64, 32, 32, None), (1, 1400, 64, 16, 64, None), (1, 1400, 64, 64, 16, None)]
+
+
+@pytest.mark.parametrize("gate", ["token", "signed", "head"])
+@pytest.mark.parametrize("B,T,H,dk,dv,lens", LONG + WIDE)
+def test_linear_forward_in_segments_of_blocks(kda, B, T, H, dk, dv, lens, gate):
+    x = lin.make(B, T, H, dk, dv, BF16, gate, lens=lens, seed=T + dk)
+    assert blocks_per_segment(kda, x, False) >= 2
+    check_fwd(kda, x)
+
+
+@pytest.mark.parametrize("gate", ["token", "signed", "head"])
+@pytest.mark.parametrize("B,T,H,dk,dv,lens", [(b, t, h // 2 if k > 32 or v > 32 else h, k, v, s) for b, t, h, k, v, s in LONG] + WIDE)
+def test_linear_gradient_in_segments_of_blocks(kda, B, T, H, dk, dv, lens, gate):
+    x = lin.make(B, T, H, dk, dv, BF16, gate, lens=lens, seed=T + dk + 1)
+    assert blocks_per_segment(kda, x, True) >= 2
+    check_bwd(kda, x)
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (128, 32)])
+def test_linear_fp32_in_segments_of_blocks(kda, dk, dv):
+    x = lin.make(1, 1100, 32, dk, dv, F32, "signed", seed=dk)
+    assert blocks_per_segment(kda, x, False) >= 4 and blocks_per_segment(kda, x, True) >= 4
+    check_fwd(kda, x)
+    check_bwd(kda, x)
