@@ -1,18 +1,22 @@
-"""Linear attention in the plan that large inputs take, segments of several blocks,
-against the recurrence in 64 bits at head sizes of 16 to 128. Which plan an input takes
-is read off the workspace's size, so that a change of the rules cannot move these cases
-to other plans unseen."""
+"""Linear attention and window attention in the plans that large inputs take: segments
+of several blocks, and workgroups whose waves share no rows (window attention), against
+the definitions in 64 bits, at head sizes of 64 and 128. Which plan an input takes is
+read off the workspace's size (linear attention) or off the names of the kernels that
+ran, so that a change of the rules cannot move these cases to other plans unseen."""
+import re
+
 import pytest
 import torch
 
 import test_gpu_linattn as lin
-from mixer_checks import close
+import test_gpu_swa as swa
+from mixer_checks import TAU_F32, close
 from oracle import mixers
 
 pytestmark = pytest.mark.gpu
 
 BF16, F32 = torch.bfloat16, torch.float32
-kda = lin.kda   # the fixture
+kda = swa.kda   # the fixture
 
 
 # ---------------------------------------------------------------- linear attention
@@ -110,3 +114,73 @@ def test_linear_fp32_in_segments_of_blocks(kda, dk, dv):
     assert blocks_per_segment(kda, x, False) >= 4 and blocks_per_segment(kda, x, True) >= 4
     check_fwd(kda, x)
     check_bwd(kda, x)
+
+
+# ---------------------------------------------------------------- window attention
+
+def kernels(call):
+    """Names of the library's kernels that `call` launches, or None without a profiler."""
+    from torch.profiler import ProfilerActivity, profile
+    call()
+    torch.cuda.synchronize()
+    with profile(activities=[ProfilerActivity.CUDA]) as p:
+        call()
+        torch.cuda.synchronize()
+    names = [re.search(r"(\w+_kernel<[^>]*>)", e.name) for e in p.events() if "kda::" in e.name]
+    return {n.group(1).replace("unsigned short", "bf16") for n in names if n} or None
+
+
+MANY = [
+    # B, T, Hq, Hkv, d, window, sinks, lens: 256 workgroups of 128 rows by heads and more
+    (1, 1050, 32, 8, 128, 300, 4, None), (1, 1050, 32, 8, 64, 300, 4, None), (1, 0, 32, 8, 128, 200, 70, [700, 2, 0, 348]),
+    (2, 530, 32, 32, 128, 160, 0, None), (1, 1100, 30, 10, 64, 1000, 1, None), (1, 0, 64, 8, 64, 96, 3, [33, 600, 1]),
+]
+FEW = [(1, 1050, 8, 2, 128, 300, 4, None), (1, 800, 2, 1, 128, 400, 0, None)]
+
+
+def check_window(kda, x, window, sinks):
+    """As test_gpu_swa.check, with o held to the root of its terms' summed squares p v where
+    that is above the rms: a sequence's first rows are a mean of few keys, of the size of v,
+    its later ones of hundreds, of a tenth of that and less, and every p is rounded by
+    itself, by up to 2^-8 of it."""
+    kw = dict(window=window, sinks=sinks, cu_seqlens=x["cu"])
+    o, lse = kda.swa_fwd(x["q"], x["k"], x["v"], **kw)
+    g = kda.swa_bwd(x["q"], x["k"], x["v"], o, lse, x["dO"], **kw)
+    scale, dt, group = x["q"].shape[-1] ** -0.5, x["q"].dtype, x["q"].shape[2] // x["k"].shape[2]
+    ro, rl, rg, size = mixers.swa(x["q"], x["k"], x["v"], window, sinks, scale, x["seqs"], x["dO"])
+    size["o"] = torch.zeros_like(ro)
+    for b, t0, t1 in x["seqs"]:
+        hidden = ~mixers.visible(t1 - t0, window, sinks, "cuda")
+        for h in range(ro.shape[2]):
+            y, z = (x[n][b, t0:t1, h // group].double() for n in ("k", "v"))
+            s = torch.mm(x["q"][b, t0:t1, h].double(), y.t().contiguous()) * scale
+            p = torch.exp(s - rl[b, t0:t1, h, None]).masked_fill(hidden, 0.0)
+            size["o"][b, t0:t1, h] = torch.mm(p.square(), z.square()).sqrt()
+    close("o", o, ro, dt, size=size["o"])
+    close("lse", lse, rl, dt, TAU_F32)
+    for n in g:
+        close(n, g[n], rg[n], dt, size=size[n])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B,T,Hq,Hkv,d,window,sinks,lens", MANY + FEW)
+def test_window_wide(kda, B, T, Hq, Hkv, d, window, sinks, lens, dtype):
+    """Most tiles of these lie wholly inside the window."""
+    check_window(kda, swa.make(B, T, Hq, Hkv, d, dtype, lens=lens, seed=T + window), window, sinks)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B,T,Hq,Hkv,d,window,sinks,lens", MANY + FEW)
+def test_window_plans(kda, B, T, Hq, Hkv, d, window, sinks, lens, dtype):
+    few = (B, T, Hq, Hkv, d, window, sinks, lens) in FEW
+    x = swa.make(B, T, Hq, Hkv, d, dtype, lens=lens)
+    kw = dict(window=window, sinks=sinks, cu_seqlens=x["cu"])
+    o, lse = kda.swa_fwd(x["q"], x["k"], x["v"], **kw)
+    ran = kernels(lambda: (kda.swa_fwd(x["q"], x["k"], x["v"], **kw),
+                           kda.swa_bwd(x["q"], x["k"], x["v"], o, lse, x["dO"], **kw)))
+    if ran is None:
+        pytest.skip("this profiler shows no kernels")
+    print(ran, flush=True)
+    for name in ("swa_fwd_kernel", "swa_dq_kernel"):
+        alone = "%s<%s, %d, 4, 1>" % (name, "bf16" if dtype == BF16 else "float", d)
+        assert (alone in ran) != few, ran
