@@ -10,7 +10,7 @@ import torch
 
 import test_gpu_linattn as lin
 import test_gpu_swa as swa
-from mixer_checks import TAU_F32, close
+from mixer_checks import STEP, TAU_F32, close, tau_for
 from oracle import mixers
 
 pytestmark = pytest.mark.gpu
@@ -114,6 +114,27 @@ def test_linear_fp32_in_segments_of_blocks(kda, dk, dv):
     assert blocks_per_segment(kda, x, False) >= 4 and blocks_per_segment(kda, x, True) >= 4
     check_fwd(kda, x)
     check_bwd(kda, x)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("lens", [None, [300, 0, 1, 299]])
+def test_linear_against_the_delta_rule_without_erasing(kda, lens, dtype):
+    """kda_chunk_fwd_ew and its gradient with nothing erased and all written, on the same
+    inputs. Bars: the sum of both calls' own, 1e-4 (bf16 inputs 2e-2; gradients 1e-4) of
+    the rms there."""
+    x = lin.make(2, 600, 8, 64, 128, dtype, "token", lens=lens, seed=5)
+    args, kw = (x["q"], x["k"], x["v"], x["gate"]), dict(S0=x["S0"], cu_seqlens=x["cu"])
+    gates = torch.zeros_like(x["k"]), torch.ones_like(x["v"])
+    bar = 1e-4 if dtype == F32 else 2e-2
+    o, S_T = kda.linattn_fwd(*args, **kw)
+    ro, rS = kda.chunk_fwd_ew(*args, *gates, gate_kind=kda.GATE_SCALAR, **kw)
+    close("o", o, ro, dtype, tau_for(dtype, dtype) + bar * (1 + STEP[dtype]))
+    close("S_T", S_T, rS, dtype, tau_for(dtype, F32) + bar)
+    g = kda.linattn_bwd(*args, x["dO"], dS_T=x["dS_T"], **kw)
+    r = kda.chunk_bwd_ew(*args, *gates, x["dO"].float(), dS_T=x["dS_T"], gate_kind=kda.GATE_SCALAR, **kw)
+    for n in ("dq", "dk", "dv", "dgate"):
+        close(n, g[n], r[n], dtype, tau_for(dtype, dtype) + 1e-4 * (1 + STEP[dtype]))
+    close("dS0", g["dS0"], r["dS0"], dtype, tau_for(dtype, F32) + 1e-4)
 
 
 # ---------------------------------------------------------------- window attention
