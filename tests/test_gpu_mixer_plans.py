@@ -205,3 +205,24 @@ def test_window_plans(kda, B, T, Hq, Hkv, d, window, sinks, lens, dtype):
     for name in ("swa_fwd_kernel", "swa_dq_kernel"):
         alone = "%s<%s, %d, 4, 1>" % (name, "bf16" if dtype == BF16 else "float", d)
         assert (alone in ran) != few, ran
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,d,window,sinks", [(1, 4, 2, 128, 4000, 3), (3, 16, 4, 64, 1500, 0), (70, 8, 8, 32, 400, 1)])
+def test_step_on_full_caches_fp32(kda, N, Hq, Hkv, d, window, sinks):
+    """Long caches in full precision, in parts and whole."""
+    g = torch.Generator().manual_seed(N)
+    rnd = lambda *s: torch.randn(s, generator=g).cuda()  # noqa: E731
+    slots = window + sinks
+    q, k, v, K, V = rnd(N, Hq, d), rnd(N, Hkv, d), rnd(N, Hkv, d), rnd(N, slots, Hkv, d), rnd(N, slots, Hkv, d)
+    pos = torch.randint(0, 3 * slots, (N,), generator=g).to(torch.int32)
+    o = kda.swa_decode_step(q, k, v, K, V, pos.cuda(), window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    want = torch.zeros(N, Hq, d, dtype=torch.float64, device="cuda")
+    for n, p in enumerate(pos.tolist()):
+        slot = p if p < sinks else sinks + (p - sinks) % window
+        assert torch.equal(K[n, slot], k[n]) and torch.equal(V[n, slot], v[n])
+        m = min(p + 1, slots)
+        for h in range(Hq):
+            s = (K[n, :m, h // (Hq // Hkv)].double() * q[n, h].double()).sum(1) * d ** -0.5
+            want[n, h] = (torch.softmax(s, 0)[:, None] * V[n, :m, h // (Hq // Hkv)].double()).sum(0)
+    close("o", o, want, F32)
