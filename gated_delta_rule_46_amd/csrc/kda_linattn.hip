@@ -196,8 +196,9 @@ template <class T, int PARTS> __device__ __forceinline__ void split(typename Fra
 // One segment of one head in one direction, from zero: the state's transpose
 // (rows dv, columns dk) in accumulators, dk columns split over the waves. Writes
 // the segment's contribution and its decay; BLOCKS: in reverse, what it has at
-// every block on the way too. Bound by bytes: B = 2, T = 4096, H = 16, d = 128, bf16, both directions
-// with BLOCKS 57 us (285 MB, 5.0 TB/s); forward of T = 8192 without 43 us (134 + 34 MB).
+// every block on the way too. Bound by bytes: B = 2, T = 4096, H = 16, d = 128, bf16, both
+// directions with BLOCKS 60 us (286 MB, 4.8 TB/s); forward of T = 8192 without 46 us (169 MB,
+// 3.7 TB/s).
 template <class T, int DK, int DV, int NW, bool BLOCKS>
 __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
     constexpr int C = lin_block<T>(), NT = 64 * NW, NPW = DK / 16 / NW, MT = DV / 16;
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(LinParams p, int dkdv) {
 
 // One segment of one head: the state (rows dk, columns dv) in accumulators, dv
 // columns split over the waves; its D tiles are ready A operands of S^T q. B = 2, T =
-// 8192, H = 16, d = 128, bf16: 59 us (285 MB, 4.8 TB/s).
+// 8192, H = 16, d = 128, bf16: 76 us (303 MB, 4.0 TB/s).
 // WHOLE: the segment is the whole sequence, from S0 to S_T.
 template <class T, int DK, int DV, int NW, bool WHOLE>
 __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
@@ -530,9 +531,9 @@ __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
 // where the start state takes the place of an earlier token (r_i = q_i . S dO_i)
 // and the end adjoint that of a later one (c_j = k_j . E v_j). R is one more
 // small matrix product.
-// One workgroup fills a CU's LDS; of its 109 us at B = 2, T = 4096, H = 16, d = 128, bf16
-// (370 MB of inputs, block states and results: 3.4 TB/s) half is arithmetic and LDS
-// reads of two waves a SIMD, with five barriers a block, half waits for memory.
+// One workgroup fills a CU's LDS: two waves a SIMD, with five barriers a block. Of its 128
+// us at B = 2, T = 4096, H = 16, d = 128, bf16 (387 MB of inputs, block adjoints and
+// results: 3.0 TB/s) a wave waits for half, and the matrix units are busy for 11%.
 template <class T, int DK, int DV, bool DG> struct LinGradTiles {
     // A wave owns one 16-row tile of dk and dv, and so of the state, for a part of a
     // block's tokens (one of TS): bf16 up to 64 columns takes two halves, which form the
@@ -850,8 +851,9 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
 
 // S' = a S + k v^T, o = S'^T q = a (S^T q) + (k . q) v, the state streamed once in
 // and once out, all of it in flight at once: one workgroup a head, 16 bytes a thread
-// and load. Bound by those bytes: 256 sequences of 32 heads, 128 x 128, 0.204 ms, 5.3
-// TB/s. One head over four workgroups, a quarter of its columns each: 3.3 against 3.4 us
+// and load. Bound by those bytes: 256 sequences of 32 heads, 128 x 128, 0.211 ms, 5.1 TB/s
+// of state (three states in turn; 0.202 ms on one, part of which the last-level cache
+// still holds: the stores go past it). One head over four workgroups, a quarter of its columns each: 3.3 against 3.4 us
 // at 16 heads, 6.3 against 5.5 at 256, so it is not done.
 template <class T, int DK, int DV, int NT>
 __global__ void __launch_bounds__(NT) lin_decode_kernel(const T* __restrict__ q, const T* __restrict__ k,
@@ -911,8 +913,9 @@ size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Tokens per segment: as few segments as give every CU two workgroups, or one in
 // the gradient, of which a CU's LDS holds one (over 32 columns). B = 2, T = 4096, H =
-// 16, d = 128: gradient 0.204 ms with 256 segments of a head, 0.220 with 512, 0.256
-// with 1,024; forward at T = 8192: 0.116, 0.111, 0.128 ms.
+// 16: gradient with 256, 512 and 1,024 segments over all heads 182, 209 and 273 us at
+// 128 x 128, 88, 95 and 110 at 64 x 64, 73, 50 and 54 at 32 x 32; forward at T = 8192,
+// 128 x 128: 133, 121, 151 us.
 int segment_tokens(int T, int N, int H, int dk, int dv, bool packed, bool grad) {
     const long tokens = packed ? T : (long)T * N;
     const long want = tokens * H / (grad && (dk > 32 || dv > 32) ? 256 : 512);
@@ -921,8 +924,11 @@ int segment_tokens(int T, int N, int H, int dk, int dv, bool packed, bool grad) 
     const long whole = ((long)T + 63) / 64 * 64;
     return (int)(L < whole ? L : (whole > 0 ? whole : 64));
 }
-// Short sequences whole, in one launch. B = 4, H = 16, d = 128: 12.1 against 20.1 us
-// in segments at 128 tokens, 21.0 against 23.7 at 256, 38.3 against 34.8 at 512.
+// Short sequences whole, in one launch. B = 4, H = 16, d = 128: 14.7 against 23.7 us in
+// segments at 128 tokens, 21.5 against 29.5 at 256, 30.0 against 33.6 at 384, 38.6 against
+// 39.9 at 512. The rule looks at the length alone: where sequences by heads fill the card
+// by themselves (512 and more), whole ones would be faster at any length (B = 32, H = 16, T =
+// 2048: 268 us against 404), since a segment is a sequence there and is walked twice.
 bool whole_sequences(int T) { return T <= 256; }
 
 struct LinWorkspace {

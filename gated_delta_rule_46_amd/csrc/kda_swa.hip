@@ -11,6 +11,12 @@
 // the other half, and the exponentials are the next product's operand as they
 // stand, with no pass through LDS (the contraction takes the keys in the order
 // in which the registers hold them).
+//
+// Scores, statistics and sums are fp32. bf16 inputs: p and, in the gradient, p (dP -
+// delta) enter the second products rounded to bf16, which takes half the instructions of
+// two bf16 numbers and makes about as much error as the rounding of the results: o is off by
+// 2.21e-3 of its rms where its own rounding makes 1.63e-3 (T = 8192, window 1024), the
+// gradients by 2.34e-3 to 2.42e-3 against 1.66e-3 (T = 4096, window 512).
 #include <algorithm>
 #include <type_traits>
 
@@ -197,9 +203,9 @@ __device__ __forceinline__ void work_item(const SwaParams& p, int& blk, int& hea
 
 // NW waves of 32 queries each share the key tiles, staged twice over in LDS
 // (one barrier a tile). B = 2, T = 8192, 16 and 4 heads, d = 128, window 1024, 4 sinks,
-// bf16: 0.186 ms, 695 TFLOP/s of what the window holds (62% of a large library product's
+// bf16: 0.181 ms, 716 TFLOP/s of what the window holds (half of a large library product's
 // rate); bound by the exponentials and the matrix products of two waves a SIMD, which
-// overlap only across waves.
+// overlap only across waves (matrix units busy for 31% of the time).
 // KS > 1, for few rows: KS waves take the same 32 queries and every KS-th key tile
 // each, and join what they have at the end.
 template <class T, int D, int NW, int KS> __global__ void __launch_bounds__(64 * NW) swa_fwd_kernel(SwaParams p) {
@@ -552,7 +558,7 @@ template <class T, int D, int NW, int KS> __global__ void __launch_bounds__(64 *
 // holds v, forms dP, and dS and dk from it. A tile has 64 rows, two independent
 // chains of products a wave; it lies in LDS once, the next one in registers, so
 // that two workgroups fit a CU and fill each other's waits. 4,096 rows, 16 and 4 heads,
-// d = 128, window 512, 4 sinks, bf16: 104 us, 22 more for the sum of the parts.
+// d = 128, window 512, 4 sinks, bf16: 104 us, 23 more for the sum of the parts.
 // The rows of a block with sinks reach to the end of the sequence: in sequences of
 // 2 * sink_rows and more they are cut into equal parts of sink_rows to twice that,
 // each a workgroup, summed afterwards in a fixed order.
@@ -841,7 +847,7 @@ struct SwaDecodeParams {
 // slots through LDS of its own (no barrier), the group's query heads side by
 // side as the columns. The new token's row is read from k and v, and written to
 // its slot by the workgroup whose part holds it. Bound by the cache's bytes: 64 sequences
-// of 2,052 slots, 8 kv heads, d = 128, bf16: 90 us, 5.4 TB/s.
+// of 2,052 slots, 8 kv heads, d = 128, bf16: 88 us, 5.5 TB/s.
 template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa_decode_kernel(SwaDecodeParams p) {
     constexpr int ST = tile_stride<T>(D), KD = D / 16, MD = D / 32, CPR = D * (int)sizeof(T) / 16, PER = 16 / (int)sizeof(T);
     using V8 = typename Frag<T>::V;
@@ -1060,7 +1066,8 @@ size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 // gives a block, but at most 64 parts of all blocks of a sequence; none where the
 // window covers everything anyway. Forward and gradient of 4,096 rows, 16 and 4
 // heads, d = 128, window 512, 4 sinks: 0.339 ms with one walk over all rows for such a
-// block, 0.211 in seven parts.
+// block, 0.211 in seven parts. More than 2,048 sinks are not cut: each of their blocks
+// walks all later rows by itself.
 void sink_cut(int T, int N, int window, int sinks, bool packed, SwaParams& p) {
     p.sink_blocks = p.sink_rows = p.sink_parts = 0;
     if (sinks <= 0 || T <= window + KEY_BLOCK) return;

@@ -1,7 +1,8 @@
 """A short, fixed workload to run under rocprofv3.
 
     python -m gated_delta_rule_46_amd.profile_run [--fwd 3] [--bwd 2] [--bwd-token 0] [--decode 8]
-                                                  [--copy-mib 256]
+                                                  [--copy-mib 256] [--mixers CASE,CASE|all]
+                                                  [--mixer-calls 12] [--rates]
 
 Runs, on cuda:0 and with seeded synthetic inputs: --fwd forward calls on the
 workload --fwd-workload names (ckda: Complex KDA, B=2, H=16, T=8192, d=128,
@@ -13,12 +14,67 @@ workload (N=256, H=32, d=128, fp32 state in place), and --copy-mib MiB of
 plain device-to-device copy (one read and one write of that many bytes per
 call, three calls), whose counter readings calibrate FETCH_SIZE and
 WRITE_SIZE against a known byte count.
+
+--mixers runs listed cases of perf/operators.py (linear attention and window
+attention), --mixer-calls calls of each on three sets of inputs in turn; alone,
+with --fwd 0 --bwd 0 --decode 0. --rates prints what large copies and
+large matrix products reach on this card, and both one-token state updates
+(decode_step, linattn_decode_step) on one state and on three in turn.
 """
 from __future__ import annotations
 
 import argparse
+import importlib.util
 import os
 import sys
+
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def operators():
+    """perf/operators.py, set to the library's own calls."""
+    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    m.own = True
+    return m
+
+
+def timed(torch, call, calls):
+    """Seconds a call, of `calls` in a row after as many untimed ones."""
+    for i in range(calls):
+        call(i)
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    a.record()
+    for i in range(calls):
+        call(i)
+    b.record()
+    torch.cuda.synchronize()
+    return a.elapsed_time(b) / 1e3 / calls
+
+
+def print_rates(torch, kda):
+    for gib in (1, 2, 4):
+        src = torch.ones(gib << 30, device="cuda", dtype=torch.uint8)
+        dst = torch.empty_like(src)
+        print("copy of %d GiB: %.2f TB/s read and written" % (gib, 2 * (gib << 30) / timed(torch, lambda i: dst.copy_(src), 20) / 1e12),
+              flush=True)
+        del src, dst
+    for dtype, n in ((torch.bfloat16, 8192), (torch.bfloat16, 16384), (torch.float32, 8192)):
+        x, y = (torch.randn(n, n, device="cuda", dtype=dtype) for _ in range(2))
+        print("product of %d x %d %s: %.0f TFLOP/s" % (n, n, str(dtype)[6:], 2 * n ** 3 / timed(torch, lambda i: x @ y, 10) / 1e12),
+              flush=True)
+    N, H, d = 256, 32, 128
+    sets = [[torch.randn(N, H, d, device="cuda").bfloat16() for _ in range(3)]
+            + [torch.rand(N, H, device="cuda").bfloat16() for _ in range(2)] + [torch.randn(N, H, d, d, device="cuda")]
+            for _ in range(3)]
+    for n in (1, 3):
+        for name, call in (("decode_step", lambda i: kda.decode_step(*sets[i % n])),
+                           ("linattn_decode_step", lambda i: kda.linattn_decode_step(*sets[i % n][:4], sets[i % n][5]))):
+            s = timed(torch, call, 60)
+            print("%s, 256 x 32 x 128 x 128, %d state(s) in turn: %.1f us, %.2f TB/s of state"
+                  % (name, n, s * 1e6, 8 * N * H * d * d / s / 1e12), flush=True)
 
 
 def main(argv=None) -> int:
@@ -29,9 +85,12 @@ def main(argv=None) -> int:
     ap.add_argument("--bwd-token", type=int, default=0)
     ap.add_argument("--decode", type=int, default=8)
     ap.add_argument("--copy-mib", type=int, default=256)
+    ap.add_argument("--mixers", default="")
+    ap.add_argument("--mixer-calls", type=int, default=12)
+    ap.add_argument("--rates", action="store_true")
     args = ap.parse_args(argv)
 
-    sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    sys.path.insert(0, ROOT)
     import torch
     from gated_delta_rule_46_amd import inputs, kda
 
@@ -79,6 +138,19 @@ def main(argv=None) -> int:
         torch.cuda.synchronize()
         print("decode steps: %d" % args.decode, flush=True)
         del S, steps, od
+    if args.mixers:
+        m = operators()
+        for case in m.listed():
+            if args.mixers != "all" and case["name"] not in args.mixers.split(","):
+                continue
+            states = [m.prepare(case, seed) for seed in range(3)]
+            for i in range(args.mixer_calls):
+                m.run(states[i % 3])
+            torch.cuda.synchronize()
+            print("%s calls: %d" % (case["name"], args.mixer_calls), flush=True)
+            del states
+    if args.rates:
+        print_rates(torch, kda)
     if args.copy_mib > 0:
         src = torch.ones(args.copy_mib << 20, device=dev, dtype=torch.uint8)
         dst = torch.empty_like(src)

@@ -3,6 +3,7 @@
     python -m gated_delta_rule_46_amd.profile_summary stats DIR OUT.md --title T --command C [--note N]
     python -m gated_delta_rule_46_amd.profile_summary traffic FETCH_DIR WRITE_DIR NAME --command C [--command C2]
     python -m gated_delta_rule_46_amd.profile_summary mfma PMC_DIR STATS_DIR OUT.md --command C
+    python -m gated_delta_rule_46_amd.profile_summary mixers DIR OUT.md --command C [--command C2]
 
 ``stats`` turns the kernel-stats CSV of a ``rocprofv3 --kernel-trace --stats
 --output-format csv`` run into a markdown table (calls, average, minimum and
@@ -23,6 +24,14 @@ GRBM_GUI_ACTIVE) and the kernel durations of a stats run, and tabulates per
 kernel the MFMA work (fp16 MOPS x 512 flops, fp32 16x16x4 instructions x
 2048 flops), its rate, MFMA busy (SQ_VALU_MFMA_BUSY_CYCLES over GRBM_GUI_ACTIVE
 / 8 XCDs x 1024 SIMDs) and VALU issue per wave.
+
+``mixers`` reads, for each case of ``profile_run.py --mixers CASE``, the runs
+DIR/trace_CASE (--kernel-trace), DIR/fetch_CASE and DIR/write_CASE (--pmc
+FETCH_SIZE, --pmc WRITE_SIZE, calibrated on the copies of the same run) and
+DIR/sq_CASE (--pmc SQ_VALU_MFMA_BUSY_CYCLES SQ_ACTIVE_INST_VALU SQ_WAVE_CYCLES
+SQ_WAIT_ANY GRBM_GUI_ACTIVE), and tabulates its kernels: median and shortest
+duration, bytes read and written, MFMA busy, and the shares of a wave's cycles
+that issue VALU instructions and that wait.
 """
 from __future__ import annotations
 
@@ -201,6 +210,50 @@ def cmd_mfma(a) -> int:
     return 0
 
 
+def _counters(d: str):
+    """Mean counter values per dispatch: {kernel: {counter: value}}."""
+    acc = {}
+    for r in _rows(os.path.join(d, "**", "*counter_collection.csv")):
+        acc.setdefault(r["Kernel_Name"], {}).setdefault(r["Counter_Name"], []).append(float(r["Counter_Value"]))
+    return {k: {c: sum(v) / len(v) for c, v in d.items()} for k, d in acc.items()}
+
+
+def cmd_mixers(a) -> int:
+    out = ["# Linear attention and window attention: kernels by case", "",
+           "Commands for each CASE, a listed case of `perf/operators.py` (MI355X, gfx950, one GPU; every counter set in a run "
+           "of its own; `$REPO` is the repository root):", "", "```"] + list(a.command) + ["```", "",
+           "Per dispatch. Durations: median and shortest of the traced run. Bytes: FETCH_SIZE and WRITE_SIZE, calibrated on the "
+           "copies of the same run, from and to HBM and its cache (a mean of the run's calls, on three sets of inputs in turn). "
+           "TB/s: both over the median. MFMA busy: SQ_VALU_MFMA_BUSY_CYCLES / (GRBM_GUI_ACTIVE / 8 XCDs x 1024 SIMDs). VALU and "
+           "wait: SQ_ACTIVE_INST_VALU and SQ_WAIT_ANY over SQ_WAVE_CYCLES.", "",
+           "| case | kernel | calls | median us | min us | read MB | written MB | TB/s | MFMA busy | VALU | wait |",
+           "|---|---|---|---|---|---|---|---|---|---|---|"]
+    cases = sorted(os.path.basename(d)[6:] for d in glob.glob(os.path.join(a.dir, "trace_*")))
+    for case in cases:
+        times = {}
+        for r in _rows(os.path.join(a.dir, "trace_" + case, "**", "*kernel_trace.csv")):
+            times.setdefault(r["Kernel_Name"], []).append((int(r["End_Timestamp"]) - int(r["Start_Timestamp"])) / 1e3)
+        moved = []
+        for what, counter in (("fetch_", "FETCH_SIZE"), ("write_", "WRITE_SIZE")):
+            mean, top = _per_kernel(os.path.join(a.dir, what + case), counter)
+            scale = (a.copy_mib << 20) / max(x for k, x in top.items() if "copyBuffer" in k)
+            moved.append({k: x * scale / 1e6 for k, (x, _) in mean.items()})
+        sq = _counters(os.path.join(a.dir, "sq_" + case))
+        for k in sorted((k for k in times if "kda::" in k), key=lambda k: -sorted(times[k])[len(times[k]) // 2]):
+            t = sorted(times[k])
+            us, c = t[len(t) // 2], sq.get(k, {})
+            rd, wr = (m.get(k, 0.0) for m in moved)
+            wave = c.get("SQ_WAVE_CYCLES", 0.0) or 1.0
+            out.append("| %s | %s | %d | %.1f | %.1f | %.1f | %.1f | %.2f | %.2f | %.2f | %.2f |" % (
+                case, _short(k).replace("kda::", "").replace("unsigned short", "bf16"), len(t), us, t[0], rd, wr, (rd + wr) / us,
+                c.get("SQ_VALU_MFMA_BUSY_CYCLES", 0.0) / (c.get("GRBM_GUI_ACTIVE", 0.0) / 8 * 1024 or 1.0),
+                c.get("SQ_ACTIVE_INST_VALU", 0.0) / wave, c.get("SQ_WAIT_ANY", 0.0) / wave))
+    with open(a.out, "w") as f:
+        f.write("\n".join(out) + "\n")
+    print("wrote", a.out)
+    return 0
+
+
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     sub = ap.add_subparsers(dest="mode", required=True)
@@ -224,8 +277,13 @@ def main(argv=None) -> int:
     m.add_argument("out")
     m.add_argument("--title", default="Complex KDA forward and backward (B=2, H=16, T=8192, d=128), decode")
     m.add_argument("--command", action="append", required=True)
+    x = sub.add_parser("mixers")
+    x.add_argument("dir")
+    x.add_argument("out")
+    x.add_argument("--command", action="append", required=True)
+    x.add_argument("--copy-mib", type=int, default=256)
     a = ap.parse_args(argv)
-    return {"stats": cmd_stats, "traffic": cmd_traffic, "mfma": cmd_mfma}[a.mode](a)
+    return {"stats": cmd_stats, "traffic": cmd_traffic, "mfma": cmd_mfma, "mixers": cmd_mixers}[a.mode](a)
 
 
 if __name__ == "__main__":

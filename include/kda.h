@@ -341,9 +341,11 @@ int kda_chunk_fwd_gauge(const void* q, const void* k, const void* v, const void*
  * v, S0, S_T, cu_seqlens and N as for kda_chunk_fwd, so states and packed
  * batches are shared. gate_kind: KDA_GATE_SCALAR (gate [B, T, H] in the input
  * dtype) or KDA_GATE_HEAD (gate [H], fp32 whatever the dtype: decays near one
- * have no bf16 neighbours). Any finite decay is allowed, zero and negative
- * ones included; products of decays are formed directly. There is no query
- * scaling.
+ * have no bf16 neighbours). Any decay is allowed, zero and negative ones
+ * included, as long as the product of the decays over every run of a sequence's
+ * tokens is finite in fp32 (it is wherever they are at most one in magnitude):
+ * these products are formed directly, whatever they multiply. There is no
+ * query scaling.
  *
  * Unlike the delta rule's calls, o and the gradients have the input dtype
  * (bf16 halves what the call writes); states are fp32. S_T may be S0. Rows of o
@@ -367,8 +369,9 @@ int kda_linattn_fwd(const void* q, const void* k, const void* v, const void* gat
  * dO [B, T, H, dv] in the input dtype; dS_T [N, H, dk, dv] fp32 or NULL (zero).
  * Outputs: grad_q, grad_k, grad_v and grad_gate in the input dtype and
  * layouts, grad_S0 fp32 or NULL when not wanted. With KDA_GATE_HEAD the decay
- * is a constant: grad_gate must be NULL (for a learned one, pass it
- * per token and sum). grad_gate is the derivative with respect to the decay
+ * is a constant: grad_gate must be NULL (a learned one goes in per token, in
+ * the input dtype, and its gradient is summed; with bf16 inputs that rounds it,
+ * 0.999 to 1, and with fp32 inputs it does not). grad_gate is the derivative with respect to the decay
  * itself, an ordinary one at zero and negative decays. Nothing of a forward
  * call is reused, and rows at or behind cu_seqlens[N] are left as they are. dO
  * and the gradients must be 16-byte aligned (grad_gate and
@@ -406,6 +409,9 @@ int kda_linattn_decode_step(const void* q, const void* k, const void* v, const v
  * cu_seqlens[N] are left as they are. d in {32, 64, 128}; scale finite. o and
  * the gradients have the input dtype. Sums and softmax statistics are fp32;
  * bf16 inputs enter the second product with probabilities rounded to bf16.
+ * Sums are divided by that of the exponentials at the end: 256 times the sum
+ * of |v| over the keys that a row sees has to be finite in fp32 (the step of one
+ * token: the sum itself).
  *
  * A NaN or Inf in k or v of a token that a row does not see does not reach
  * that row in the forward and the decode step.
