@@ -77,10 +77,11 @@ template <class T> constexpr int lin_block() { return sizeof(T) == 2 ? 64 : 32; 
 
 // ---------------------------------------------------------------- decays of a block
 
-template <int CTRL> __device__ __forceinline__ float dpp_or_one(float x) {
-    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp((int)0x3f800000, (int)__float_as_uint(x), CTRL, 0xF,
-                                                                 0xF, false));
+template <int CTRL> __device__ __forceinline__ float dpp_or(float x, float other) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp((int)__float_as_uint(other), (int)__float_as_uint(x), CTRL,
+                                                                 0xF, 0xF, false));
 }
+template <int CTRL> __device__ __forceinline__ float dpp_or_one(float x) { return dpp_or<CTRL>(x, 1.f); }
 
 template <int C> struct alignas(16) Decays {   // arrays are read four at a time
     static constexpr int DST = 20;   // row stride of diag
@@ -154,6 +155,43 @@ __device__ __forceinline__ f32x4 tile_decays(const Decays<C>& s, int ti, int tj,
     for (int m = tj + 1; m < ti; ++m) f *= s.blk[m];
     f32x4 d = *reinterpret_cast<const f32x4*>(s.col + 16 * tj + 4 * g);
     return d * f;
+}
+
+// D_{t-1,j} of column t = 16 tt + il, rows j = 16 tj + 4g + r; zero from j = t on
+template <int C>
+__device__ __forceinline__ f32x4 tile_decays_before(const Decays<C>& s, int tt, int tj, int g, int il) {
+    const int t = 16 * tt + il;
+    if (tj > tt) return zero4();
+    if (tj == tt) {
+        f32x4 d = *reinterpret_cast<const f32x4*>(s.diag + max(t - 1, 0) * Decays<C>::DST + 4 * g);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (4 * g + r >= il) d[r] = 0.f;
+        return d;
+    }
+    float f = il ? s.row[t - 1] : 1.f;
+    for (int m = tj + 1; m < tt; ++m) f *= s.blk[m];
+    return *reinterpret_cast<const f32x4*>(s.col + 16 * tj + 4 * g) * f;
+}
+
+// sum_{j<t} D_{t-1,j} c_j for a lane's token t, c its own term
+template <int C> __device__ __forceinline__ float decayed_sum(const Decays<C>& s, float c, int t) {
+    float z = c * s.col[t], y = c, a = s.a[t];
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) z += __shfl_xor(z, m, WAVE);   // of 16 tokens, decayed to their end
+    // inside 16 tokens: (a, y) of consecutive runs, joined
+    y += a * dpp_or<0x111>(y, 0.f); a *= dpp_or_one<0x111>(a);
+    y += a * dpp_or<0x112>(y, 0.f); a *= dpp_or_one<0x112>(a);
+    y += a * dpp_or<0x114>(y, 0.f); a *= dpp_or_one<0x114>(a);
+    y += a * dpp_or<0x118>(y, 0.f);
+    y = dpp_or<0x111>(y, 0.f);   // up to t - 1
+    float before = 0.f;
+#pragma unroll
+    for (int m = 0; m < C / 16 - 1; ++m) {
+        const float zm = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(z), 16 * m));
+        if (m < t / 16) before = before * s.blk[m] + zm;
+    }
+    return y + (t % 16 ? s.row[t - 1] : 1.f) * before;
 }
 
 // A lane's decay as it lies in memory, and its value: apart, so that the load
@@ -530,7 +568,9 @@ __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
 //        + d_t (G_{t-1} <S, E> + sum_{j<t} D_{t-1,j} c_j)
 // where the start state takes the place of an earlier token (r_i = q_i . S dO_i)
 // and the end adjoint that of a later one (c_j = k_j . E v_j). R is one more
-// small matrix product.
+// small matrix product, of M and the decays as two bf16 numbers each (bf16 inputs), and
+// <S, E> is summed in fp32: with both rounded to one, short sequences had the decay's
+// gradient off by up to 2.4 times its own rounding.
 // One workgroup fills a CU's LDS: two waves a SIMD, with five barriers a block. Of its 128
 // us at B = 2, T = 4096, H = 16, d = 128, bf16 (387 MB of inputs, block adjoints and
 // results: 3.0 TB/s) a wave waits for half, and the matrix units are busy for 11%.
@@ -547,8 +587,9 @@ template <class T, int DK, int DV, bool DG> struct LinGradTiles {
     alignas(16) T q[C * SK], k[C * SK], v[C * SV], dO[C * SV];
     alignas(16) T E[EROWS * SV];
     alignas(16) T p[C * SP], b[C * SP];                       // decayed scores and decayed dO . v, [i][j]
-    alignas(16) T M[DG ? C * SP : 8], D[DG ? C * SP : 8];     // [i][j], and D_{t-1,j} as [t][j]
-    alignas(16) float r[DG ? NM * C : 4], c[DG ? NM * C : 4], x[NM], da[DG ? C / 16 * C : 4];
+    static constexpr int MN = sizeof(T) == 2 ? 2 : 1;         // M and what its rounding leaves, [i][j]
+    alignas(16) T M[MN][DG ? C * SP : 8];
+    alignas(16) float r[DG ? NM * C : 4], c[DG ? NM * C : 4], x[NW], da[DG ? C / 16 * C : 4];
 };
 
 template <class T, int DK, int DV, bool DG>
@@ -581,23 +622,29 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
         for (int e = tid; e < 16 * SV; e += NT) s.E[16 * SV + e] = T(0);
     for (int e = tid; e < C * SP; e += NT) {
         s.p[e] = s.b[e] = T(0);
-        if constexpr (DG) s.M[e] = s.D[e] = T(0);
+        if constexpr (DG)
+            for (int y = 0; y < L::MN; ++y) s.M[y][e] = T(0);
     }
 
-    // The adjoint, where this thread stages it: the segment's, held throughout, and
-    // a block's own share, loaded ahead for the next block.
-    using StageE = Stage<float, DV, DK, NT>;
-    using R4 = typename Raw4<T>::V;
-    const size_t seg = ((size_t)blockIdx.x * p.H + h) * (DK * DV);
-    StageE segE, locE;
-    segE.load(p.seg[1] + seg, DV, DK, tid);
     // The state's transpose (rows dv, this wave's columns of dk) in accumulators; its D
-    // tiles are ready A operands of S dO.
-    f32x4 S[VT];
+    // tiles are ready A operands of S dO. The adjoint on its way to LDS in the same
+    // order (EN tiles of a wave): the segment's, held throughout, and a block's own
+    // share, loaded ahead for the next block.
+    using R4 = typename Raw4<T>::V;
+    constexpr int EN = VT < L::TS ? 1 : VT / L::TS;
+    const int x0 = th * EN, erow = 16 * wm + il;
+    const bool stages = wm < KT && x0 < VT;
+    const size_t seg = ((size_t)blockIdx.x * p.H + h) * (DK * DV), own = (size_t)erow * DV + 4 * g;
+    f32x4 S[VT], segE[EN], locE[EN];
 #pragma unroll
     for (int x = 0; x < VT; ++x) {
         S[x] = zero4();
-        if (wm < KT) S[x] = *reinterpret_cast<const f32x4*>(p.seg[0] + seg + (size_t)(16 * wm + il) * DV + 16 * x + 4 * g);
+        if (wm < KT) S[x] = *reinterpret_cast<const f32x4*>(p.seg[0] + seg + own + 16 * x);
+    }
+#pragma unroll
+    for (int x = 0; x < EN; ++x) {
+        segE[x] = zero4();
+        if (stages) segE[x] = *reinterpret_cast<const f32x4*>(p.seg[1] + seg + own + 16 * (x0 + x));
     }
 
     Stage<T, DK, C, NT> stq, stk;
@@ -622,7 +669,12 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
     };
     auto fetch_state = [&](int c) {
         const size_t bs = (size_t)(block0 + c) * p.H + h;
-        locE.load(p.blk + bs * (DK * DV), DV, c + 1 < nc ? DK : 0, tid);
+#pragma unroll
+        for (int x = 0; x < EN; ++x) {
+            locE[x] = zero4();
+            if (stages && c + 1 < nc)
+                locE[x] = *reinterpret_cast<const f32x4*>(p.blk + bs * (DK * DV) + own + 16 * (x0 + x));
+        }
         preE = p.blk_decay[bs];
     };
     fetch_qk(0);
@@ -642,12 +694,26 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
         stv.store(s.v, tid);
         sto.store(s.dO, tid);
         // the adjoint at this block: the segment's, decayed, and its own tokens' share
+        float xe = 0.f;
+        if (stages) {
 #pragma unroll
-        for (int m = 0; m < StageE::N; ++m) {
-            const int e = tid + m * NT;
-            if (StageE::TOT % NT == 0 || e < StageE::TOT)
-                store4(s.E + (e / StageE::CPR) * SV + (e % StageE::CPR) * 4,
-                       values(raw_here(segE.r[m])) * preE + values(locE.r[m]));
+            for (int x = 0; x < EN; ++x) {
+                const f32x4 e = segE[x] * preE + locE[x];
+                store4(s.E + (16 * wm + il) * SV + 16 * (x0 + x) + 4 * g, e);
+                if constexpr (DG) {
+                    f32x4 y = S[x];
+                    if constexpr (L::TS == 2) {   // the wave's half, without an index into registers
+                        const f32x4 z = raw_here(S[(x + EN) % VT]);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) y[r] = th ? z[r] : y[r];
+                    }
+                    xe += (e[0] * y[0] + e[1] * y[1]) + (e[2] * y[2] + e[3] * y[3]);
+                }
+            }
+        }
+        if constexpr (DG) {
+            xe = wave_sum(xe);
+            if (lane == 0) s.x[w] = xe;
         }
         if (w == 0) block_decays<C, true>(s.dec, a.value(p, lane), lane);
         __syncthreads();
@@ -677,8 +743,12 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
             store4(s.p + to, x);
             store4(s.b + to, y);
             if constexpr (DG) {
-                store4(s.M + to, m);
-                if (16 * ti + il + 1 < C) store4(s.D + to + SP, d);
+                store4(s.M[0] + to, m);
+                if constexpr (L::MN == 2) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) m[r] -= (float)(__bf16)m[r];
+                    store4(s.M[1] + to, m);
+                }
             }
         }
 
@@ -687,12 +757,10 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
 #pragma unroll
         for (int tt = 0; tt < HT; ++tt) aq[tt] = ak[tt] = av[tt] = zero4();
         if (wm < KT) {
-            float xe = 0.f;
 #pragma unroll
             for (int ks = 0; ks < KSV; ++ks) {
                 const V8 sf = narrow<T>(dtiles_to_frag(S[2 * ks], 2 * ks + 1 < VT ? S[(2 * ks + 1) % VT] : zero4()));
                 const V8 ef = frag_kpos(s.E, SV, 16 * wm + il, 32 * ks, g);
-                if constexpr (DG) xe = dot8(ef, sf, xe);
 #pragma unroll
                 for (int tt = 0; tt < HT; ++tt) {
                     const int i = 16 * (HT * th + tt) + il;
@@ -701,8 +769,6 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
                 }
             }
             if constexpr (DG) {
-                xe = wave_sum(xe);
-                if (th == 0 && lane == 0) s.x[wm] = xe;
 #pragma unroll
                 for (int tt = 0; tt < HT; ++tt) {
                     const int i = 16 * (HT * th + tt) + il;
@@ -799,8 +865,17 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
                 while (tt > ti) { tt -= ti + 1; ++ti; }
                 const int t = 16 * tt + il;
                 f32x4 R = zero4();
-                for (int ks = 0; ks <= tt / 2; ++ks)
-                    R = mma(frag_kpos(s.M, SP, 16 * ti + il, 32 * ks, g), frag_kpos(s.D, SP, t, 32 * ks, g), R);
+                for (int ks = 0; ks <= tt / 2; ++ks) {
+                    V8 d[L::MN];
+                    split<T, L::MN>(d, dtiles_to_frag(tile_decays_before<C>(s.dec, tt, 2 * ks, g, il),
+                                                      tile_decays_before<C>(s.dec, tt, 2 * ks + 1, g, il)));
+                    const V8 m = frag_kpos(s.M[0], SP, 16 * ti + il, 32 * ks, g);
+                    R = mma(m, d[0], R);
+                    if constexpr (L::MN == 2) {
+                        R = mma(m, d[1], R);
+                        R = mma(frag_kpos(s.M[1], SP, 16 * ti + il, 32 * ks, g), d[0], R);
+                    }
+                }
                 f32x4 ri = zero4();
 #pragma unroll
                 for (int m = 0; m < KT; ++m) ri += *reinterpret_cast<const f32x4*>(s.r + m * C + 16 * ti + 4 * g);
@@ -823,23 +898,10 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
             __syncthreads();
             if (w == NW - 1) {
                 const int t = lane % C;   // C = 32: the upper lanes repeat the lower ones
-                float c0 = 0.f, X = 0.f, acc = 0.f;
-                for (int m = 0; m < KT; ++m) {
-                    c0 += s.c[m * C + t];
-                    X += s.x[m];
-                }
-                float part[4] = {X * (t ? s.dec.gam[t - 1] : 1.f), 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int ks = 0; ks < KC; ++ks)
-#pragma unroll
-                    for (int gg = 0; gg < 4; ++gg) {
-                        const f32x8 d = widen(frag_nat(s.D, SP, t, 32 * ks, gg));
-#pragma unroll
-                        for (int m = 0; m < 8; ++m)
-                            part[m & 3] += d[m] * __uint_as_float((uint32_t)__builtin_amdgcn_readlane(
-                                                      (int)__float_as_uint(c0), 32 * ks + 8 * gg + m));
-                    }
-                acc = s.dec.suf[t] * ((part[0] + part[1]) + (part[2] + part[3]));
+                float c0 = 0.f, X = 0.f;
+                for (int m = 0; m < KT; ++m) c0 += s.c[m * C + t];
+                for (int m = 0; m < NW; ++m) X += s.x[m];
+                float acc = s.dec.suf[t] * (X * (t ? s.dec.gam[t - 1] : 1.f) + decayed_sum<C>(s.dec, c0, t));
                 for (int m = t / 16; m < CT; ++m) acc += s.da[m * C + t];
                 if (lane < n) store1(static_cast<T*>(p.dgate) + (size_t)(t0 + lane) * p.H + h, acc);
             }

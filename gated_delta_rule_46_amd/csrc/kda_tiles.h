@@ -81,20 +81,6 @@ template <class T> __device__ __forceinline__ typename Frag<T>::V narrow(const f
 template <> __device__ __forceinline__ bf16x8 narrow<uint16_t>(const f32x8& x) { return __builtin_convertvector(x, bf16x8); }
 template <> __device__ __forceinline__ f32x8 narrow<float>(const f32x8& x) { return x; }
 
-// a . b + c over the eight values of two operands, in fp32
-__device__ __forceinline__ float dot8(const bf16x8& a, const bf16x8& b, float c) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-#pragma unroll
-    for (int m = 0; m < 8; m += 2)
-        c = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{a[m], a[m + 1]}, bf16x2{b[m], b[m + 1]}, c, false);
-    return c;
-}
-__device__ __forceinline__ float dot8(const f32x8& a, const f32x8& b, float c) {
-#pragma unroll
-    for (int m = 0; m < 8; ++m) c = fmaf(a[m], b[m], c);
-    return c;
-}
-
 // four values to consecutive elements (8 or 16 bytes, aligned)
 __device__ __forceinline__ void store4(uint16_t* p, const f32x4& x) {
     typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
