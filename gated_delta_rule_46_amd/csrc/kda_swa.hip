@@ -418,10 +418,16 @@ template <class T, int D, int NW, int KS> __global__ void __launch_bounds__(64 *
 
 // ---------------------------------------------------------------- gradient with respect to q
 
-// As the forward, with dP^T = V dO^T and dS = P (dP - delta), delta_i = dO_i .
-// o_i (formed here and kept for the other gradients): dq^T = K^T dS^T; KS as there. 4,096 rows, 16 and
-// 4 heads, d = 128, window 512, bf16: 48 us.
+// As the forward, with dP^T = V dO^T and dS = P (dP - delta), delta_i = dO_i . o_i
+// (formed here and kept for the other gradients): dq^T = K^T dS^T; KS as there. With o in
+// bf16 that product takes o's rounding into every dS, which where a row attends to few
+// keys is as large as dP itself: dq and dk were off by up to 2.3 times their own
+// rounding, with scores of deviation 4 also in windows of 1,024. bf16 rows therefore
+// walk their keys once more, for delta_i = sum_j p_ij dP_ij in fp32: off by 1.44 at most. 4,096
+// rows, 16 and 4 heads, d = 128, window 512, bf16: 63 us, 48 without; the whole gradient of
+// windows of 32, 128 and 1,024 71, 141 and 1,416 us against 72, 138 and 1,174.
 template <class T, int D, int NW, int KS> __global__ void __launch_bounds__(64 * NW) swa_dq_kernel(SwaParams p) {
+    constexpr bool SUMMED = sizeof(T) == 2;
     constexpr int KT = swa_tile<T>(), KB = KS * KT, NT = 64 * NW, ST = tile_stride<T>(D), KD = D / 16, MD = D / 32;
     using V8 = typename Frag<T>::V;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -444,8 +450,8 @@ template <class T, int D, int NW, int KS> __global__ void __launch_bounds__(64 *
 
     V8 qf[KD], gf[KD];
     float delta = 0.f, lse2 = 0.f;
+    const size_t r0 = (size_t)(ts + (live ? row : 0)) * p.Hq + h;
     {
-        const size_t r0 = (size_t)(ts + (live ? row : 0)) * p.Hq + h;
         const T* sq = static_cast<const T*>(p.q) + r0 * D + 8 * h2;
         const T* sg = static_cast<const T*>(p.dO) + r0 * D + 8 * h2;
         const T* so = static_cast<const T*>(p.o) + r0 * D + 8 * h2;
@@ -453,14 +459,12 @@ template <class T, int D, int NW, int KS> __global__ void __launch_bounds__(64 *
         for (int ks = 0; ks < KD; ++ks) {
             qf[ks] = load8<T>(sq + 16 * ks, live);
             gf[ks] = load8<T>(sg + 16 * ks, live);
-            const f32x8 x = widen(gf[ks]) * widen(load8<T>(so + 16 * ks, live));
-            delta += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+            if constexpr (!SUMMED) {
+                const f32x8 x = widen(gf[ks]) * widen(load8<T>(so + 16 * ks, live));
+                delta += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+            }
         }
-        delta = swap_sum(delta);
-        if (live) {
-            lse2 = p.lse[r0] * LOG2E;
-            if (h2 == 0 && wk == 0) p.delta[r0] = delta;
-        }
+        if (live) lse2 = p.lse[r0] * LOG2E;
     }
     const T* K = static_cast<const T*>(p.k) + ((size_t)ts * p.Hkv + hk) * D;
     const T* V = static_cast<const T*>(p.v) + ((size_t)ts * p.Hkv + hk) * D;
@@ -478,6 +482,58 @@ template <class T, int D, int NW, int KS> __global__ void __launch_bounds__(64 *
         sk.store(t, tid);
         sv.store(t + KB * ST, tid);
     };
+    // delta of a tile's keys
+    auto sum_tile = [&](const T* tk, const T* tv, int x, int j0, auto masked) {
+        f32x16 s = zero16(), d = zero16();
+#pragma unroll
+        for (int ks = 0; ks < KD; ++ks) {
+            s = mma32(nat32<T>(tk, ST, 32 * x, 16 * ks, n, h2), qf[ks], s);
+            d = mma32(nat32<T>(tv, ST, 32 * x, 16 * ks, n, h2), gf[ks], d);
+        }
+        const Mask mask(row, j0 + 4 * h2, p.window, p.sinks);
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const float e = fast_exp2(fmaf(s[r], c, -lse2)) * d[r];
+            part[r & 3] += !masked.value || mask(result_row(r, 0)) ? e : 0.f;
+        }
+        delta += (part[0] + part[1]) + (part[2] + part[3]);
+    };
+    if constexpr (SUMMED) {
+        fetch(0);
+        put(0);
+        __syncthreads();
+        for (int it = 0; it < kt.count; ++it) {
+            if (it + 1 < kt.count) fetch(it + 1);
+            const T* tk = tiles + ((it & 1) * 2 * KB + wk * KT) * ST;
+            const T* tv = tk + KB * ST;
+            if (i0 < len) {
+#pragma unroll
+                for (int x = 0; x < KT / 32; ++x) {
+                    const int j0 = kt[it] * KB + wk * KT + 32 * x;
+                    const Seen se = seen(i0, i0 + 31, j0, j0 + 31, p.window, p.sinks);
+                    if (se.none) continue;
+                    if (se.all) sum_tile(tk, tv, x, j0, std::false_type()); else sum_tile(tk, tv, x, j0, std::true_type());
+                }
+            }
+            if (it + 1 < kt.count) {
+                put(it + 1);
+                __syncthreads();
+            }
+        }
+    }
+    delta = swap_sum(delta);
+    if constexpr (SUMMED) {
+        __shared__ float s_delta[NW][32];
+        if (KS > 1 && h2 == 0) s_delta[w][n] = delta;
+        __syncthreads();   // the last tiles are read, too
+        if constexpr (KS > 1) {
+            delta = 0.f;
+#pragma unroll
+            for (int y = 0; y < KS; ++y) delta += s_delta[w - wk + y][n];
+        }
+    }
+    if (live && h2 == 0 && wk == 0) p.delta[r0] = delta;
     f32x16 A[MD];
 #pragma unroll
     for (int m = 0; m < MD; ++m) A[m] = zero16();

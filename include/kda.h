@@ -426,7 +426,8 @@ int kda_swa_fwd(const void* q, const void* k, const void* v, void* o, float* lse
 
 /*
  * Gradient of kda_swa_fwd for L = sum <o, dO>: o and lse as the forward left
- * them, dO [B, T, Hq, d]. grad_q, grad_k, grad_v in the input dtype and
+ * them (with bf16 inputs o is not read: its rounding would enter every
+ * gradient), dO [B, T, Hq, d]. grad_q, grad_k, grad_v in the input dtype and
  * layouts, those of a kv head summed over its query heads; sums run in a fixed
  * order (repeated calls agree bit for bit); rows at or behind cu_seqlens[N] are
  * left as they are. workspace: kda_swa_bwd_workspace_bytes(...) bytes, required.

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import test_gpu_linattn as lin
+import test_gpu_swa as swa
 from oracle import mixers
 from test_gpu_linattn import kda  # noqa: F401 (fixture)
 
@@ -39,4 +40,33 @@ def test_linear(kda, B, T, H, dk, dv, lens, states):  # noqa: F811
     r = mixers.linattn_grad(*args, x["dO"], x["S0"], x["dS_T"], x["seqs"])
     check("o", o, ro)
     for n in ("dq", "dk", "dv", "dgate"):
+        check(n, g[n], r[n])
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,d,window,sinks,lens", [
+    (1, 0, 24, 3, 128, 144, 7, [2, 3, 1, 4]), (4, 27, 4, 2, 128, 93, 130, None), (1, 0, 3, 1, 128, 88, 0, [123, 153, 51, 180, 132, 175]),
+    (1, 0, 8, 2, 32, 2, 0, [60, 3, 50, 1]), (1, 0, 8, 8, 128, 5, 0, [23, 16, 26, 30]), (1, 0, 9, 3, 64, 101, 64, [213, 36, 88, 244]),
+    (2, 92, 4, 2, 64, 357, 7, None), (1, 2231, 3, 1, 32, 2, 0, None), (2, 57, 4, 4, 128, 1, 7, None), (3, 424, 9, 3, 64, 126, 130, None),
+    (1, 1050, 32, 8, 128, 300, 4, None), (1, 1400, 4, 1, 64, 1000, 0, None), (1, 600, 32, 32, 128, 3, 1, None)])
+def test_window(kda, B, T, Hq, Hkv, d, window, sinks, lens):  # noqa: F811
+    x = swa.make(B, T, Hq, Hkv, d, BF16, lens=lens, seed=T + window)
+    kw = dict(window=window, sinks=sinks, cu_seqlens=x["cu"])
+    o, lse = kda.swa_fwd(x["q"], x["k"], x["v"], **kw)
+    g = kda.swa_bwd(x["q"], x["k"], x["v"], o, lse, x["dO"], **kw)
+    ro, _, r, _ = mixers.swa(x["q"], x["k"], x["v"], window, sinks, d ** -0.5, x["seqs"], x["dO"])
+    check("o", o, ro)
+    for n in g:
+        check(n, g[n], r[n])
+
+
+@pytest.mark.parametrize("T,window,sinks", [(1024, 1024, 0), (2048, 512, 4)])
+def test_window_of_sharp_scores(kda, T, window, sinks):  # noqa: F811
+    """Scores of deviation 4: a row's weight lies on few of its keys."""
+    x = swa.make(1, T, 4, 1, 128, BF16, seed=T)
+    x["q"] = x["q"] * 4
+    o, lse = kda.swa_fwd(x["q"], x["k"], x["v"], window=window, sinks=sinks)
+    g = kda.swa_bwd(x["q"], x["k"], x["v"], o, lse, x["dO"], window=window, sinks=sinks)
+    ro, _, r, _ = mixers.swa(x["q"], x["k"], x["v"], window, sinks, 128 ** -0.5, x["seqs"], x["dO"])
+    check("o", o, ro)
+    for n in g:
         check(n, g[n], r[n])
