@@ -82,6 +82,20 @@ template <int CTRL> __device__ __forceinline__ float dpp_or(float x, float other
                                                                  0xF, 0xF, false));
 }
 template <int CTRL> __device__ __forceinline__ float dpp_or_one(float x) { return dpp_or<CTRL>(x, 1.f); }
+template <int CTRL> __device__ __forceinline__ double dpp_or_one(double x) {
+    const auto u = __builtin_bit_cast(u32x2, x);
+    return __builtin_bit_cast(
+        double, u32x2{(uint32_t)__builtin_amdgcn_update_dpp(0, (int)u[0], CTRL, 0xF, 0xF, false),
+                      (uint32_t)__builtin_amdgcn_update_dpp((int)0x3ff00000, (int)u[1], CTRL, 0xF, 0xF, false)});
+}
+__device__ __forceinline__ float lane_value(float x, int lane) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), lane));
+}
+__device__ __forceinline__ double lane_value(double x, int lane) {
+    const auto u = __builtin_bit_cast(u32x2, x);
+    return __builtin_bit_cast(double, u32x2{(uint32_t)__builtin_amdgcn_readlane((int)u[0], lane),
+                                            (uint32_t)__builtin_amdgcn_readlane((int)u[1], lane)});
+}
 
 template <int C> struct alignas(16) Decays {   // arrays are read four at a time
     static constexpr int DST = 20;   // row stride of diag
@@ -94,50 +108,57 @@ template <int C> struct alignas(16) Decays {   // arrays are read four at a time
     float total;
 };
 
-template <int C, int D> __device__ __forceinline__ void diag_step(float* row, int il, float a, float& acc) {
+template <int C, int D, class R> __device__ __forceinline__ void diag_step(float* row, int il, R a, R& acc) {
     if constexpr (D < 16) {
         if constexpr (D == 1) acc *= a; else acc *= dpp_or_one<0x110 + D - 1>(a);   // row_shr: a_{i-D+1}
-        if (il >= D) row[il - D] = acc;
+        if (il >= D) row[il - D] = (float)acc;
         diag_step<C, D + 1>(row, il, a, acc);
     }
 }
 
-// One wave, lane = token, `a` its decay (1 past the sequence's end).
-template <int C, bool DIAG> __device__ __forceinline__ void block_decays(Decays<C>& s, float a, int lane) {
-    float p = a, u = a;
+// One wave, lane = token, `a` its decay (1 past the sequence's end). Products in R.
+template <int C, bool DIAG, class R> __device__ __forceinline__ void products_of_decays(Decays<C>& s, R a, int lane) {
+    R p = a, u = a;
     p *= dpp_or_one<0x111>(p); p *= dpp_or_one<0x112>(p); p *= dpp_or_one<0x114>(p); p *= dpp_or_one<0x118>(p);
     u *= dpp_or_one<0x101>(u); u *= dpp_or_one<0x102>(u); u *= dpp_or_one<0x104>(u); u *= dpp_or_one<0x108>(u);
-    const float ux = dpp_or_one<0x101>(u);
-    float b[4];
+    const R ux = dpp_or_one<0x101>(u);
+    R b[4];
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
-        b[m] = 16 * m < C ? __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(p), 16 * m + 15)) : 1.f;
+    for (int m = 0; m < 4; ++m) b[m] = 16 * m < C ? lane_value(p, 16 * m + 15) : R(1);
     const int blk = lane >> 4;
-    float pre = 1.f, post = 1.f;
+    R pre = 1, post = 1;
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
         if (m < blk) pre *= b[m];
         if (m > blk) post *= b[m];
     }
     if (lane < C) {
-        s.gam[lane] = pre * p;
-        s.suf[lane] = ux * post;
-        s.a[lane] = a;
+        s.gam[lane] = (float)(pre * p);
+        s.suf[lane] = (float)(ux * post);
+        s.a[lane] = (float)a;
         if constexpr (DIAG) {
-            s.row[lane] = p;
-            s.col[lane] = ux;
+            s.row[lane] = (float)p;
+            s.col[lane] = (float)ux;
             float* r = s.diag + lane * Decays<C>::DST;
             const int il = lane & 15;
             r[il] = 1.f;
-            float acc = 1.f;
+            R acc = 1;
             diag_step<C, 1>(r, il, a, acc);
         }
     }
     if (lane == 0) {
-        s.total = (b[0] * b[1]) * (b[2] * b[3]);
+        s.total = (float)((b[0] * b[1]) * (b[2] * b[3]));
 #pragma unroll
-        for (int m = 0; m < 4; ++m) s.blk[m] = b[m];
+        for (int m = 0; m < 4; ++m) s.blk[m] = (float)b[m];
     }
+}
+// A constant decay's products are formed in 64 bits: in fp32 every one of a power's
+// squarings rounds the same way at every block, which had slow heads off by 1e-5 of
+// their states after 3,000 tokens. Other decays' roundings differ, and stay in fp32.
+template <int C, bool DIAG>
+__device__ __forceinline__ void block_decays(Decays<C>& s, const LinParams& p, float a, int lane) {
+    if (p.head_gate) products_of_decays<C, DIAG>(s, (double)a, lane);
+    else products_of_decays<C, DIAG>(s, a, lane);
 }
 
 // D_ij of a 16x16 tile in D-tile order: column i = 16 ti + il, rows j = 16 tj + 4g + r
@@ -188,7 +209,7 @@ template <int C> __device__ __forceinline__ float decayed_sum(const Decays<C>& s
     float before = 0.f;
 #pragma unroll
     for (int m = 0; m < C / 16 - 1; ++m) {
-        const float zm = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(z), 16 * m));
+        const float zm = lane_value(z, 16 * m);
         if (m < t / 16) before = before * s.blk[m] + zm;
     }
     return y + (t % 16 ? s.row[t - 1] : 1.f) * before;
@@ -295,7 +316,7 @@ __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
         if (step) __syncthreads();
         stx.store(sx, tid);
         sty.store(sy, tid);
-        if (w == 0) block_decays<C, false>(dec, a.value(p, lane), lane);
+        if (w == 0) block_decays<C, false>(dec, p, a.value(p, lane), lane);
         __syncthreads();
         if (step + 1 < nc) fetch(step + 1);
         const float tot = dec.total;
@@ -452,7 +473,7 @@ __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
         stq.store(sq, tid);
         stk.store(sk, tid);
         stv.store(sv, tid);
-        if (w == 0) block_decays<C, true>(dec, a.value(p, lane), lane);
+        if (w == 0) block_decays<C, true>(dec, p, a.value(p, lane), lane);
         __syncthreads();
         if (c + 1 < nc) fetch(c + 1);
 
@@ -715,7 +736,7 @@ __global__ void __launch_bounds__((64 * LinGradTiles<T, DK, DV, DG>::NW)) lin_gr
             xe = wave_sum(xe);
             if (lane == 0) s.x[w] = xe;
         }
-        if (w == 0) block_decays<C, true>(s.dec, a.value(p, lane), lane);
+        if (w == 0) block_decays<C, true>(s.dec, p, a.value(p, lane), lane);
         __syncthreads();
         if (c + 1 < nc) fetch_qk(c + 1);
 

@@ -70,3 +70,27 @@ def test_window_of_sharp_scores(kda, T, window, sinks):  # noqa: F811
     check("o", o, ro)
     for n in g:
         check(n, g[n], r[n])
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+@pytest.mark.parametrize("T", [200, 1000])
+def test_slow_constant_decays(kda, T, dtype):  # noqa: F811
+    """Constant decays from 1/2 to 1 - 2^-12.9, per head: states carry no rounding that adds
+    up from token to token. A state is multiplied once a block (32 tokens and more) by a
+    product of decays rounded to fp32, half a step off at most and always the same: over
+    the mean age of a state's terms, up to T / 2 tokens, (T / 64) 2^-24; besides that fp32
+    sums, a few 2^-24, at most 5e-7 in the root mean square (mixer_checks, TAU_F32 / 5 sigma
+    would be 4e-6 for single elements). One rounding a token instead: T / 2 of them."""
+    H = 24
+    x = lin.make(2, T, H, 32, 64, dtype, "head", seed=T)
+    x["gate"] = (1 - 2.0 ** -(1 + torch.arange(H, dtype=torch.float64) / 2)).float().cuda()
+    args = (x["q"], x["k"], x["v"], x["gate"])
+    _, S_T = kda.linattn_fwd(*args, S0=x["S0"])
+    g = kda.linattn_bwd(*args, x["dO"], S0=x["S0"], dS_T=x["dS_T"])
+    _, rS, _ = mixers.linattn(*args, x["S0"], x["seqs"])
+    r = mixers.linattn_grad(*args, x["dO"], x["S0"], x["dS_T"], x["seqs"])
+    bar = T / 64 * 2.0 ** -24 + 5e-7
+    for name, a, b in (("S_T", S_T, rS), ("dS0", g["dS0"], r["dS0"])):
+        off = (a.double() - b).square().mean((0, 2, 3)).sqrt() / b.square().mean((0, 2, 3)).sqrt()
+        print(name, ["%.1e" % e for e in off.tolist()], flush=True)
+        assert off.max() <= bar, (name, off.max().item(), bar)
