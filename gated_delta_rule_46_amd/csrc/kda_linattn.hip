@@ -30,11 +30,10 @@
 // Precision. States and adjoints are held in fp32 wherever they are kept, and a
 // token's decayed row enters them as three bf16 numbers (24 mantissa bits: as exact
 // as an fp32 sum). bf16 inputs: what enters a product with the inputs is rounded to
-// bf16 there, once: decayed scores, states and adjoints, and in the decay's gradient
-// the products of scores and the decays between. That is as much again as the rounding of
-// the results, bf16 themselves: o, dq, dk and dv are off by 2.35e-3 of their rms, the
-// decay's gradient by 2.66e-3, where their own rounding makes 1.66e-3 (B = 2, H = 16, d =
-// 128, T = 8192 and 4096). Two bf16 numbers an operand would take that away for twice the
+// bf16 there, once: decayed scores, states and adjoints. That is as much again as the
+// rounding of the results, bf16 themselves: o, dq, dk and dv are off by 2.35e-3 of their
+// rms, the decay's gradient by 1.83e-3, where their own rounding makes 1.66e-3 (B = 2, H =
+// 16, d = 128, T = 8192 and 4096). Two bf16 numbers an operand would take that away for twice the
 // matrix instructions. fp32 inputs: fp32 MFMA throughout.
 #include <type_traits>
 
@@ -414,7 +413,7 @@ __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
     constexpr int C = lin_block<T>(), NT = 64 * NW, NPW = DV / 16 / NW, MT = DK / 16, CT = C / 16;
     constexpr int KS = tile_cols<T>(DK) / 32, SK = tile_stride<T>(DK), SV = tile_stride<T>(DV), SP = tile_stride<T>(C);
     // a decayed row enters the state, carried over a segment, as one number of the input
-    // type (113.6 us), two (117.0) or three, which alone are as exact as the fp32 state (120.7)
+    // type (114.6 us), two (117.3) or three, which alone are as exact as the fp32 state (121.5)
     constexpr int PARTS = sizeof(T) == 2 ? 3 : 1;
     using V8 = typename Frag<T>::V;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -599,7 +598,8 @@ template <class T, int DK, int DV, bool DG> struct LinGradTiles {
     // A wave owns one 16-row tile of dk and dv, and so of the state, for a part of a
     // block's tokens (one of TS): bf16 up to 64 columns takes two halves, which form the
     // state twice but keep twice the waves busy. B = 2, T = 4096, H = 16, halves against
-    // all tokens: 64 x 64 85 / 107 us, 128 x 64 125 / 132, 64 x 128 136 / 128.
+    // all tokens: 16 x 16 60 / 85 us, 64 x 64 92 / 113, 128 x 64 133 / 136, 64 x 128
+    // 168 / 139, 128 x 128 251 / 185.
     static constexpr int C = lin_block<T>(), NM = (DK > DV ? DK : DV) / 16;
     static constexpr int TS = sizeof(T) == 2 && DV < 128 ? 2 : 1, NW = TS * NM;
     static constexpr int SK = tile_stride<T>(DK), SV = tile_stride<T>(DV), SP = tile_stride<T>(C);
@@ -996,9 +996,9 @@ size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Tokens per segment: as few segments as give every CU two workgroups, or one in
 // the gradient, of which a CU's LDS holds one (over 32 columns). B = 2, T = 4096, H =
-// 16: gradient with 256, 512 and 1,024 segments over all heads 182, 209 and 273 us at
-// 128 x 128, 88, 95 and 110 at 64 x 64, 73, 50 and 54 at 32 x 32; forward at T = 8192,
-// 128 x 128: 133, 121, 151 us.
+// 16: gradient with 256, 512 and 1,024 segments over all heads 185, 217 and 280 us at
+// 128 x 128, 92, 99 and 113 at 64 x 64, 82, 55 and 58 at 32 x 32; forward at T = 8192,
+// 128 x 128: 133, 121, 150 us.
 int segment_tokens(int T, int N, int H, int dk, int dv, bool packed, bool grad) {
     const long tokens = packed ? T : (long)T * N;
     const long want = tokens * H / (grad && (dk > 32 || dv > 32) ? 256 : 512);
@@ -1007,11 +1007,11 @@ int segment_tokens(int T, int N, int H, int dk, int dv, bool packed, bool grad) 
     const long whole = ((long)T + 63) / 64 * 64;
     return (int)(L < whole ? L : (whole > 0 ? whole : 64));
 }
-// Short sequences whole, in one launch. B = 4, H = 16, d = 128: 14.7 against 23.7 us in
-// segments at 128 tokens, 21.5 against 29.5 at 256, 30.0 against 33.6 at 384, 38.6 against
-// 39.9 at 512. The rule looks at the length alone: where sequences by heads fill the card
+// Short sequences whole, in one launch. B = 4, H = 16, d = 128: 14.2 against 23.6 us in
+// segments at 128 tokens, 21.7 against 29.2 at 256, 30.5 against 33.5 at 384, 39.3 against
+// 39.3 at 512. The rule looks at the length alone: where sequences by heads fill the card
 // by themselves (512 and more), whole ones would be faster at any length (B = 32, H = 16, T =
-// 2048: 268 us against 404), since a segment is a sequence there and is walked twice.
+// 2048: 265 us against 409), since a segment is a sequence there and is walked twice.
 bool whole_sequences(int T) { return T <= 256; }
 
 struct LinWorkspace {

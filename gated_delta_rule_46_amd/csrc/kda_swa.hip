@@ -16,7 +16,7 @@
 // delta) enter the second products rounded to bf16, which takes half the instructions of
 // two bf16 numbers and makes about as much error as the rounding of the results: o is off by
 // 2.21e-3 of its rms where its own rounding makes 1.63e-3 (T = 8192, window 1024), the
-// gradients by 2.34e-3 to 2.42e-3 against 1.66e-3 (T = 4096, window 512).
+// gradients by 2.34e-3 to 2.36e-3 against 1.66e-3 (T = 4096, window 512).
 #include <algorithm>
 #include <type_traits>
 
@@ -203,8 +203,8 @@ __device__ __forceinline__ void work_item(const SwaParams& p, int& blk, int& hea
 
 // NW waves of 32 queries each share the key tiles, staged twice over in LDS
 // (one barrier a tile). B = 2, T = 8192, 16 and 4 heads, d = 128, window 1024, 4 sinks,
-// bf16: 0.181 ms, 716 TFLOP/s of what the window holds (half of a large library product's
-// rate); bound by the exponentials and the matrix products of two waves a SIMD, which
+// bf16: 0.18 to 0.19 ms, 670 to 716 TFLOP/s of what the window holds (half of a large library
+// product's rate); bound by the exponentials and the matrix products of two waves a SIMD, which
 // overlap only across waves (matrix units busy for 31% of the time).
 // KS > 1, for few rows: KS waves take the same 32 queries and every KS-th key tile
 // each, and join what they have at the end.
@@ -424,7 +424,7 @@ template <class T, int D, int NW, int KS> __global__ void __launch_bounds__(64 *
 // keys is as large as dP itself: dq and dk were off by up to 2.3 times their own
 // rounding, with scores of deviation 4 also in windows of 1,024. bf16 rows therefore
 // walk their keys once more, for delta_i = sum_j p_ij dP_ij in fp32: off by 1.44 at most. 4,096
-// rows, 16 and 4 heads, d = 128, window 512, bf16: 63 us, 48 without; the whole gradient of
+// rows, 16 and 4 heads, d = 128, window 512, bf16: 66 us, 48 without; the whole gradient of
 // windows of 32, 128 and 1,024 71, 141 and 1,416 us against 72, 138 and 1,174.
 template <class T, int D, int NW, int KS> __global__ void __launch_bounds__(64 * NW) swa_dq_kernel(SwaParams p) {
     constexpr bool SUMMED = sizeof(T) == 2;
@@ -903,7 +903,7 @@ struct SwaDecodeParams {
 // slots through LDS of its own (no barrier), the group's query heads side by
 // side as the columns. The new token's row is read from k and v, and written to
 // its slot by the workgroup whose part holds it. Bound by the cache's bytes: 64 sequences
-// of 2,052 slots, 8 kv heads, d = 128, bf16: 88 us, 5.5 TB/s.
+// of 2,052 slots, 8 kv heads, d = 128, bf16: 88 to 90 us, 5.4 TB/s.
 template <class T, int D, int NW> __global__ void __launch_bounds__(64 * NW) swa_decode_kernel(SwaDecodeParams p) {
     constexpr int ST = tile_stride<T>(D), KD = D / 16, MD = D / 32, CPR = D * (int)sizeof(T) / 16, PER = 16 / (int)sizeof(T);
     using V8 = typename Frag<T>::V;

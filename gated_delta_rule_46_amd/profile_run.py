@@ -56,10 +56,11 @@ def timed(torch, call, calls):
 
 def print_rates(torch, kda):
     for gib in (1, 2, 4):
-        src = torch.ones(gib << 30, device="cuda", dtype=torch.uint8)
+        src = torch.ones(gib << 28, device="cuda")
         dst = torch.empty_like(src)
-        print("copy of %d GiB: %.2f TB/s read and written" % (gib, 2 * (gib << 30) / timed(torch, lambda i: dst.copy_(src), 20) / 1e12),
-              flush=True)
+        for name, call in (("copy_", lambda i: dst.copy_(src)), ("multiplied by one", lambda i: torch.mul(src, 1.0, out=dst))):
+            print("copy of %d GiB, %s: %.2f TB/s read and written" % (gib, name, 2 * (gib << 30) / timed(torch, call, 20) / 1e12),
+                  flush=True)
         del src, dst
     for dtype, n in ((torch.bfloat16, 8192), (torch.bfloat16, 16384), (torch.float32, 8192)):
         x, y = (torch.randn(n, n, device="cuda", dtype=dtype) for _ in range(2))
