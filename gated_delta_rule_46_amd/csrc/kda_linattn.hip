@@ -349,11 +349,13 @@ __global__ void __launch_bounds__(64 * NW) lin_state_kernel(LinParams p) {
 
 // ---------------------------------------------------------------- scan over segments
 
+// workgroups of a state
+__host__ __device__ constexpr int scan_parts(int dkdv) { return (dkdv / 4 + 255) / 256; }
+
 // Elementwise over dk x dv, one (sequence, head) per (blockIdx.x, y); bound by the latency of
 // a chain of loads as long as a sequence has segments (eight in flight). Direction 0:
 // from the segments' contributions the state at each segment's start, and S_T.
 // Direction 1: the adjoint at each one's end, and dS0. In place, in fp32.
-__host__ __device__ constexpr int scan_parts(int dkdv) { return (dkdv / 4 + 255) / 256; }   // workgroups
 __global__ void __launch_bounds__(256) lin_scan_kernel(LinParams p, int dkdv) {
     lds_poison(0);
     const int s = blockIdx.x, h = blockIdx.y, parts = scan_parts(dkdv), rev = blockIdx.z / parts;
@@ -591,7 +593,7 @@ __global__ void __launch_bounds__(64 * NW) lin_out_kernel(LinParams p) {
 // small matrix product, of M and the decays as two bf16 numbers each (bf16 inputs), and
 // <S, E> is summed in fp32: with both rounded to one, short sequences had the decay's
 // gradient off by up to 2.4 times its own rounding.
-// One workgroup fills a CU's LDS: two waves a SIMD, with five barriers a block. Of its 128
+// One workgroup fills a CU's LDS: two waves a SIMD, with four barriers a block. Of its 128
 // us at B = 2, T = 4096, H = 16, d = 128, bf16 (387 MB of inputs, block adjoints and
 // results: 3.0 TB/s) a wave waits for half, and the matrix units are busy for 11%.
 template <class T, int DK, int DV, bool DG> struct LinGradTiles {

@@ -371,8 +371,8 @@ int kda_linattn_fwd(const void* q, const void* k, const void* v, const void* gat
  * layouts, grad_S0 fp32 or NULL when not wanted. With KDA_GATE_HEAD the decay
  * is a constant: grad_gate must be NULL (a learned one goes in per token, in
  * the input dtype, and its gradient is summed; with bf16 inputs that rounds it,
- * 0.999 to 1, and with fp32 inputs it does not). grad_gate is the derivative with respect to the decay
- * itself, an ordinary one at zero and negative decays. Nothing of a forward
+ * 0.999 to 1, and with fp32 inputs it does not). grad_gate is the derivative
+ * with respect to the decay itself, an ordinary one at zero and negative decays. Nothing of a forward
  * call is reused, and rows at or behind cu_seqlens[N] are left as they are. dO
  * and the gradients must be 16-byte aligned (grad_gate and
  * states: their element). workspace: kda_linattn_bwd_workspace_bytes(...)
