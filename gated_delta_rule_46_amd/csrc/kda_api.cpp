@@ -117,6 +117,51 @@ int swa_args(kda::SwaArgs* a, const void* q, const void* k, const void* v, int B
     return KDA_OK;
 }
 
+bool glr_sizes_ok(int B, int T, int C, int N, int has_cu, int dtype) {
+    if (B <= 0 || T < 0 || C <= 0 || C > (1 << 20)) return false;
+    if (dtype != KDA_F32 && dtype != KDA_BF16) return false;
+    if (has_cu && (B != 1 || N <= 0)) return false;
+    const int64_t n = has_cu ? N : B;
+    return n * (T + 128LL) <= INT32_MAX && kda::glr_fits(T, (int)n, C, has_cu != 0, dtype == KDA_BF16);
+}
+// bf16 inputs may have fp32 decays
+bool glr_types_ok(int dtype, int gate_dtype) {
+    return gate_dtype == KDA_F32 ? dtype == KDA_F32 || dtype == KDA_BF16 : gate_dtype == KDA_BF16 && dtype == KDA_BF16;
+}
+// what arrays of rows of C elements of the input type are aligned to
+uintptr_t glr_align(int C, int dtype) { return C % (dtype == KDA_BF16 ? 8 : 4) == 0 ? 16 : dtype == KDA_BF16 ? 2 : 4; }
+
+// The checks that the gated linear recurrence's forward and backward share, and
+// the fields that they fill.
+int glr_args(kda::GlrArgs* a, const void* gate, const void* x, const float* h0, int B, int T, int C,
+             const int32_t* cu_seqlens, int N, int dtype, int gate_dtype, void* workspace, size_t workspace_bytes,
+             bool grad, void* stream) {
+    if (B <= 0 || T < 0 || C <= 0) return KDA_EINVAL;
+    const bool packed = cu_seqlens != nullptr;
+    if (packed ? (B != 1 || N <= 0) : (N != 0 && N != B)) return KDA_EINVAL;
+    if (!packed) N = B;
+    if (!glr_types_ok(dtype, gate_dtype) || !glr_sizes_ok(B, T, C, N, packed, dtype)) return KDA_ENOTSUP;
+    if (T > 0 && (!gate || !x)) return KDA_EINVAL;
+    const uintptr_t al = glr_align(C, dtype);
+    if (T > 0 && (!aligned(gate, al < 4 && gate_dtype == KDA_F32 ? 4 : al) || !aligned(x, al))) return KDA_EALIGN;
+    if ((h0 && !aligned(h0, 4)) || (packed && !aligned(cu_seqlens, 4))) return KDA_EALIGN;
+    if (workspace && !aligned(workspace)) return KDA_EALIGN;
+    if (!workspace || workspace_bytes < kda::glr_workspace_bytes(T, N, C, packed, dtype == KDA_BF16, grad)) return KDA_EINVAL;
+    *a = kda::GlrArgs{};
+    a->gate = gate;
+    a->x = x;
+    a->h0 = h0;
+    a->T = T;
+    a->C = C;
+    a->cu_seqlens = cu_seqlens;
+    a->N = N;
+    a->bf16 = dtype == KDA_BF16;
+    a->gate_bf16 = gate_dtype == KDA_BF16;
+    a->workspace = workspace;
+    a->stream = reinterpret_cast<hipStream_t>(stream);
+    return KDA_OK;
+}
+
 }  // namespace
 
 namespace kda {
@@ -659,6 +704,61 @@ int kda_swa_cache_fill(const void* k, const void* v, void* K_cache, void* V_cach
     if (!aligned(K_cache) || !aligned(V_cache)) return KDA_EALIGN;
     return hip_status(kda::launch_swa_cache_fill(kda::SwaFillArgs{k, v, K_cache, V_cache, T, a.N, Hkv, d, window, sinks,
                                                                   cu_seqlens, a.bf16, a.stream}));
+}
+
+size_t kda_glr_fwd_workspace_bytes(int B, int T, int C, int N, int has_cu, int dtype) {
+    return glr_sizes_ok(B, T, C, N, has_cu, dtype)
+               ? kda::glr_workspace_bytes(T, has_cu ? N : B, C, has_cu != 0, dtype == KDA_BF16, false) : 0;
+}
+
+size_t kda_glr_bwd_workspace_bytes(int B, int T, int C, int N, int has_cu, int dtype) {
+    return glr_sizes_ok(B, T, C, N, has_cu, dtype)
+               ? kda::glr_workspace_bytes(T, has_cu ? N : B, C, has_cu != 0, dtype == KDA_BF16, true) : 0;
+}
+
+int kda_glr_fwd(const void* gate, const void* x, const float* h0, void* h, float* h_T, int B, int T, int C,
+                const int32_t* cu_seqlens, int N, int dtype, int gate_dtype, void* workspace, size_t workspace_bytes,
+                void* stream) {
+    kda::GlrArgs a{};
+    const int st = glr_args(&a, gate, x, h0, B, T, C, cu_seqlens, N, dtype, gate_dtype, workspace, workspace_bytes, false, stream);
+    if (st != KDA_OK) return st;
+    if (T > 0 && !h) return KDA_EINVAL;
+    if ((T > 0 && !aligned(h, glr_align(C, dtype))) || (h_T && !aligned(h_T, 4))) return KDA_EALIGN;
+    if (T == 0 && !h_T) return KDA_OK;
+    a.h = h;
+    a.hT = h_T;
+    return hip_status(kda::launch_glr_fwd(a));
+}
+
+int kda_glr_bwd(const void* gate, const void* x, const float* h0, const void* dh, const float* dh_T, void* grad_gate,
+                void* grad_x, float* grad_h0, int B, int T, int C, const int32_t* cu_seqlens, int N, int dtype,
+                int gate_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    kda::GlrArgs a{};
+    const int st = glr_args(&a, gate, x, h0, B, T, C, cu_seqlens, N, dtype, gate_dtype, workspace, workspace_bytes, true, stream);
+    if (st != KDA_OK) return st;
+    if (T > 0 && (!dh || !grad_gate || !grad_x)) return KDA_EINVAL;
+    const uintptr_t al = glr_align(C, dtype);
+    if (T > 0 && (!aligned(dh, al) || !aligned(grad_gate, al < 4 && gate_dtype == KDA_F32 ? 4 : al) || !aligned(grad_x, al)))
+        return KDA_EALIGN;
+    if ((dh_T && !aligned(dh_T, 4)) || (grad_h0 && !aligned(grad_h0, 4))) return KDA_EALIGN;
+    if (T == 0 && !grad_h0) return KDA_OK;
+    a.dh = dh;
+    a.dhT = dh_T;
+    a.g_gate = grad_gate;
+    a.g_x = grad_x;
+    a.g_h0 = grad_h0;
+    return hip_status(kda::launch_glr_bwd(a));
+}
+
+int kda_glr_decode_step(const void* gate, const void* x, float* h, void* o, int N, int C, int dtype, int gate_dtype,
+                        void* stream) {
+    if (N <= 0 || C <= 0) return KDA_EINVAL;
+    if (!glr_types_ok(dtype, gate_dtype) || (int64_t)N * C > INT32_MAX) return KDA_ENOTSUP;
+    if (!gate || !x || !h || !o) return KDA_EINVAL;
+    const uintptr_t es = dtype == KDA_BF16 ? 2 : 4;
+    if (!aligned(gate, gate_dtype == KDA_BF16 ? 2 : 4) || !aligned(x, es) || !aligned(h, 4) || !aligned(o, es)) return KDA_EALIGN;
+    kda::GlrDecodeArgs a{gate, x, h, o, N, C, dtype == KDA_BF16, gate_dtype == KDA_BF16, reinterpret_cast<hipStream_t>(stream)};
+    return hip_status(kda::launch_glr_decode(a));
 }
 
 }  // extern "C"

@@ -125,6 +125,30 @@ struct SwaFillArgs {
     hipStream_t stream;
 };
 
+// Gated linear recurrence per channel; the gradient's fields are null in a forward
+// call and the other way round.
+struct GlrArgs {
+    const void *gate, *x, *dh;
+    const float *h0, *dhT;                  // initial state, adjoint of the final one, or null
+    void *h, *g_gate, *g_x;                 // h and g_x in the type of x, g_gate in that of gate
+    float *hT, *g_h0;                       // or null
+    int T, C;
+    const int32_t* cu_seqlens;              // device, N+1 entries, or null
+    int N;                                  // number of sequences (B when cu_seqlens is null)
+    bool bf16, gate_bf16;
+    void* workspace;
+    hipStream_t stream;
+};
+
+struct GlrDecodeArgs {
+    const void *gate, *x;
+    float* h;
+    void* o;
+    int N, C;
+    bool bf16, gate_bf16;
+    hipStream_t stream;
+};
+
 // Bytes of intermediates one (chunk, head) pair occupies in the workspace.
 size_t chunk_block_bytes(int dk, int dv, int chunk, bool bf16);
 // Upper bound on the number of chunks over all sequences.
@@ -178,5 +202,11 @@ hipError_t launch_swa_fwd(const SwaArgs& a);
 hipError_t launch_swa_bwd(const SwaArgs& a);
 hipError_t launch_swa_decode(const SwaDecodeArgs& a);
 hipError_t launch_swa_cache_fill(const SwaFillArgs& a);
+
+bool glr_fits(int T, int N, int C, bool packed, bool bf16);   // whether every launch fits a grid
+size_t glr_workspace_bytes(int T, int N, int C, bool packed, bool bf16, bool grad);
+hipError_t launch_glr_fwd(const GlrArgs& a);
+hipError_t launch_glr_bwd(const GlrArgs& a);
+hipError_t launch_glr_decode(const GlrDecodeArgs& a);
 
 }  // namespace kda

@@ -32,7 +32,8 @@ EXPORTS = ("kda_chunk_fwd", "kda_chunk_fwd_stage", "kda_chunk_fwd_workspace_byte
            "kda_decode_step_ew", "kda_chunk_bwd_cw", "kda_chunk_bwd_cw_workspace_bytes", "kda_chunk_bwd_ew",
            "kda_chunk_bwd_ew_workspace_bytes", "kda_linattn_fwd", "kda_linattn_fwd_workspace_bytes", "kda_linattn_bwd",
            "kda_linattn_bwd_workspace_bytes", "kda_linattn_decode_step", "kda_swa_fwd", "kda_swa_bwd",
-           "kda_swa_bwd_workspace_bytes", "kda_swa_decode_step", "kda_swa_decode_workspace_bytes", "kda_swa_cache_fill")
+           "kda_swa_bwd_workspace_bytes", "kda_swa_decode_step", "kda_swa_decode_workspace_bytes", "kda_swa_cache_fill",
+           "kda_glr_fwd", "kda_glr_fwd_workspace_bytes", "kda_glr_bwd", "kda_glr_bwd_workspace_bytes", "kda_glr_decode_step")
 
 
 class KDAError(RuntimeError):
@@ -117,6 +118,15 @@ def load(path: str):
     lib.kda_swa_decode_workspace_bytes.argtypes = [i] * 6
     lib.kda_swa_cache_fill.restype = i
     lib.kda_swa_cache_fill.argtypes = [vp] * 4 + [i] * 6 + [vp, i, i, vp]
+    for name in ("kda_glr_fwd_workspace_bytes", "kda_glr_bwd_workspace_bytes"):
+        getattr(lib, name).restype = sz
+        getattr(lib, name).argtypes = [i] * 6
+    lib.kda_glr_fwd.restype = i
+    lib.kda_glr_fwd.argtypes = [vp] * 5 + [i] * 3 + [vp, i, i, i, vp, sz, vp]
+    lib.kda_glr_bwd.restype = i
+    lib.kda_glr_bwd.argtypes = [vp] * 8 + [i] * 3 + [vp, i, i, i, vp, sz, vp]
+    lib.kda_glr_decode_step.restype = i
+    lib.kda_glr_decode_step.argtypes = [vp] * 4 + [i] * 4 + [vp]
     lib.kda_chunk_fwd_noalloc.restype = i
     lib.kda_chunk_fwd_noalloc.argtypes = [vp] * 8 + [i] * 6 + [vp, i, i, i, vp]
     return lib
@@ -926,3 +936,120 @@ def swa_cache_fill(k, v, K_cache, V_cache, window: int, sinks: int = 0, cu_seqle
             raise KDAError(rc, "kda_swa_cache_fill")
 
     _run(device, stream, call)
+
+
+# ---------------------------------------------------------------- gated linear recurrence
+
+def _check_glr(gate, x, cu_seqlens, lead):
+    """Shapes, dtypes and devices of a recurrence whose x has `lead` dims before
+    the channels. Returns (those dims, C)."""
+    if x.dim() != lead + 1:
+        raise ValueError("x must have %d dims, got %s" % (lead + 1, tuple(x.shape)))
+    if cu_seqlens is not None and x.shape[0] != 1:
+        raise ValueError("packed sequences (cu_seqlens) need B = 1, got %d" % x.shape[0])
+    _check_input("x", x, x.dtype, x.device)
+    _like("gate", gate, x.shape, torch.float32 if gate.dtype == torch.float32 else x.dtype, x.device)
+    return x.shape[:-1], x.shape[-1]
+
+
+def _check_vector_state(name, t, N, C, device):
+    if t is not None:
+        _like(name, t, (N, C), torch.float32, device)
+
+
+def glr_fwd_workspace_bytes(B: int, T: int, C: int, N: int = 0, varlen: bool = False,
+                            dtype: torch.dtype = torch.bfloat16) -> int:
+    code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    return _lib().kda_glr_fwd_workspace_bytes(B, T, C, N, int(varlen), code)
+
+
+def glr_bwd_workspace_bytes(B: int, T: int, C: int, N: int = 0, varlen: bool = False,
+                            dtype: torch.dtype = torch.bfloat16) -> int:
+    code = KDA_BF16 if dtype == torch.bfloat16 else KDA_F32
+    return _lib().kda_glr_bwd_workspace_bytes(B, T, C, N, int(varlen), code)
+
+
+def glr_fwd(gate, x, h0=None, cu_seqlens=None, out: Optional[torch.Tensor] = None, state_out: bool = True,
+            h_T: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+            stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Gated linear recurrence per channel, h_t = a_t h_{t-1} + x_t (kda_glr_fwd).
+    x [B,T,C]; gate [B,T,C] in the same dtype or fp32; h0 [N,C] fp32 or None;
+    cu_seqlens int32 [N+1] on the device (B must be 1) or None. Returns (h in the
+    dtype of x, h_T fp32 or None)."""
+    (B, T), C = _check_glr(gate, x, cu_seqlens, 2)
+    device, dt = x.device, _dtype_code(x)
+    varlen, N = _check_varlen(cu_seqlens, B, device)
+    _check_vector_state("h0", h0, N, C, device)
+    _check_vector_state("h_T", h_T, N, C, device)
+    if out is not None:
+        _like("out", out, x.shape, x.dtype, device)
+    need = glr_fwd_workspace_bytes(B, T, C, N, varlen, x.dtype)
+
+    def call(st):
+        h = torch.empty_like(x) if out is None else out
+        S = x.new_empty((N, C), dtype=torch.float32) if h_T is None and state_out else h_T
+        ws = _scratch(workspace, need, device)
+        rc = _lib().kda_glr_fwd(gate.data_ptr(), x.data_ptr(), _addr(h0), h.data_ptr(), _addr(S), B, T, C,
+                                _addr(cu_seqlens), N if varlen else 0, dt, _dtype_code(gate), ws.data_ptr(),
+                                ws.numel() * ws.element_size(), st)
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_glr_fwd")
+        return h, S
+
+    return _run(device, stream, call)
+
+
+def glr_bwd(gate, x, dh, h0=None, dh_T=None, cu_seqlens=None, want_dh0: bool = True, out: Optional[dict] = None,
+            workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradient of glr_fwd for L = sum(h * dh) + sum(h_T * dh_T) (kda_glr_bwd).
+    Inputs as for glr_fwd; dh [B,T,C] in the dtype of x; dh_T fp32 [N,C] or None.
+    Returns a dict of dgate (dtype of gate), dx (dtype of x) and dh0 (fp32, None
+    when not wanted). ``out`` may supply that dict's tensors."""
+    (B, T), C = _check_glr(gate, x, cu_seqlens, 2)
+    device, dt = x.device, _dtype_code(x)
+    _like("dh", dh, x.shape, x.dtype, device)
+    varlen, N = _check_varlen(cu_seqlens, B, device)
+    _check_vector_state("h0", h0, N, C, device)
+    _check_vector_state("dh_T", dh_T, N, C, device)
+    if out is not None:
+        _like("dgate", out["dgate"], x.shape, gate.dtype, device)
+        _like("dx", out["dx"], x.shape, x.dtype, device)
+        _check_vector_state("dh0", out.get("dh0"), N, C, device)
+    need = glr_bwd_workspace_bytes(B, T, C, N, varlen, x.dtype)
+
+    def call(st):
+        g = out
+        if g is None:
+            g = {"dgate": torch.empty_like(gate), "dx": torch.empty_like(x),
+                 "dh0": x.new_empty((N, C), dtype=torch.float32) if want_dh0 else None}
+        ws = _scratch(workspace, need, device)
+        rc = _lib().kda_glr_bwd(gate.data_ptr(), x.data_ptr(), _addr(h0), dh.data_ptr(), _addr(dh_T),
+                                g["dgate"].data_ptr(), g["dx"].data_ptr(), _addr(g.get("dh0")), B, T, C,
+                                _addr(cu_seqlens), N if varlen else 0, dt, _dtype_code(gate), ws.data_ptr(),
+                                ws.numel() * ws.element_size(), st)
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_glr_bwd")
+        return g
+
+    return _run(device, stream, call)
+
+
+def glr_decode_step(gate, x, h, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One step of the gated linear recurrence, h [N,C] fp32 updated in place
+    (kda_glr_decode_step). x [N,C]; gate [N,C] in the same dtype or fp32. Returns
+    the new state in the dtype of x."""
+    (N,), C = _check_glr(gate, x, None, 1)
+    device, dt = x.device, _dtype_code(x)
+    _like("h", h, (N, C), torch.float32, device)
+    if out is not None:
+        _like("out", out, x.shape, x.dtype, device)
+
+    def call(st):
+        o = torch.empty_like(x) if out is None else out
+        rc = _lib().kda_glr_decode_step(gate.data_ptr(), x.data_ptr(), h.data_ptr(), o.data_ptr(), N, C, dt,
+                                        _dtype_code(gate), st)
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_glr_decode_step")
+        return o
+
+    return _run(device, stream, call)

@@ -469,6 +469,53 @@ int kda_swa_decode_step(const void* q, const void* k, const void* v, void* K_cac
 int kda_swa_cache_fill(const void* k, const void* v, void* K_cache, void* V_cache, int B, int Hkv, int T, int d,
                        int window, int sinks, const int32_t* cu_seqlens, int N, int dtype, void* stream);
 
+/*
+ * Gated linear recurrence for each channel,
+ *   h_t = a_t h_{t-1} + x_t,
+ * for layers whose state is a vector: the recurrence without keys and values.
+ * Layouts: gate, x, h [B, T, C]; h0, h_T [N, C] fp32 (NULL: from zero; not
+ * wanted); cu_seqlens and N as for kda_chunk_fwd. h has the type of x (`dtype`),
+ * states are fp32. gate_dtype: KDA_F32, or KDA_BF16 with bf16 x (decays near one
+ * have no bf16 neighbours, so that fp32 decays go with either). Any decay is
+ * allowed, zero and negative ones included, as long as the product of the
+ * decays over every run of a sequence's tokens is finite in fp32: these products
+ * are formed directly. h_T may be h0, h must not alias an input. Rows of h at or
+ * behind cu_seqlens[N] are left as they are. A NaN or Inf at a token reaches the
+ * later outputs of its sequence and channel, no others.
+ *
+ * C <= 2^20, and N * (T + 128) < 2^31; KDA_ENOTSUP beyond, and where one launch
+ * does not take the blocks of 64 tokens and 64 channels. Arrays of rows are 16-byte aligned where C is
+ * a multiple of 8 (fp32 x: of 4), else to their element; the workspace is 16-byte aligned,
+ * states to their element. workspace: kda_glr_fwd_workspace_bytes(...) bytes,
+ * required. Returns KDA_OK or a negative status.
+ */
+size_t kda_glr_fwd_workspace_bytes(int B, int T, int C, int N, int has_cu_seqlens, int dtype);
+int kda_glr_fwd(const void* gate, const void* x, const float* h0, void* h, float* h_T, int B, int T, int C,
+                const int32_t* cu_seqlens, int N, int dtype, int gate_dtype, void* workspace, size_t workspace_bytes,
+                void* stream);
+
+/*
+ * Gradient of kda_glr_fwd for L = sum_t <h_t, dh_t> + sum_seq <h_T, dh_T>: dh
+ * [B, T, C] in the type of x, dh_T [N, C] fp32 or NULL (zero). grad_gate in the
+ * type of gate, grad_x in that of x, grad_h0 [N, C] fp32 or NULL when not
+ * wanted. Nothing of a forward call is reused: the states are formed again in
+ * fp32. Outputs must not alias inputs; rows at or behind cu_seqlens[N] are left
+ * as they are. A NaN or Inf in x reaches grad_gate of the later tokens only. workspace:
+ * kda_glr_bwd_workspace_bytes(...) bytes, required.
+ */
+size_t kda_glr_bwd_workspace_bytes(int B, int T, int C, int N, int has_cu_seqlens, int dtype);
+int kda_glr_bwd(const void* gate, const void* x, const float* h0, const void* dh, const float* dh_T, void* grad_gate,
+                void* grad_x, float* grad_h0, int B, int T, int C, const int32_t* cu_seqlens, int N, int dtype,
+                int gate_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One step of the same recurrence for N sequences: gate, x, o [N, C], h [N, C]
+ * fp32 updated in place; o is h in the type of x. Every pointer aligned to its
+ * element; o must not alias h or the inputs. N * C < 2^31.
+ */
+int kda_glr_decode_step(const void* gate, const void* x, float* h, void* o, int N, int C, int dtype, int gate_dtype,
+                        void* stream);
+
 /* Static text for a status code (never NULL). */
 const char* kda_strerror(int status);
 
