@@ -18,7 +18,7 @@ LIB = os.path.join(HERE, "libkda.so")
 POISON_LIB = os.path.join(HERE, "libkda_lds_poison.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["kda_api.cpp", "kda_decode.hip", "kda_chunk.hip", "kda_bwd.hip", "kda_gauge.hip", "kda_noalloc.hip", "kda_cbwd.hip",
-           "kda_linattn.hip", "kda_swa.hip", "kda_glr.hip"]
+           "kda_linattn.hip", "kda_swa.hip", "kda_glr.hip", "kda_paged.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

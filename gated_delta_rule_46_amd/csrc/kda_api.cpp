@@ -162,6 +162,47 @@ int glr_args(kda::GlrArgs* a, const void* gate, const void* x, const float* h0, 
     return KDA_OK;
 }
 
+bool paged_heads_ok(int Hq, int Hkv, int d) {
+    return Hq <= 65535 && (d == 32 || d == 64 || d == 128) && Hkv > 0 && Hq > 0 && Hq % Hkv == 0;
+}
+bool paged_sizes_ok(int B, int Hq, int Hkv, int T, int d, int N, int has_cu) {
+    if (B <= 0 || T < 0 || !paged_heads_ok(Hq, Hkv, d)) return false;
+    if (has_cu && (B != 1 || N <= 0)) return false;
+    const int64_t n = has_cu ? N : B;
+    return n * (T + 128LL) <= INT32_MAX && (T + 128LL) * (Hq / Hkv) <= INT32_MAX;
+}
+
+// The checks that the calls on a paged cache share, and the fields that they fill.
+int paged_args(kda::PagedArgs* a, const void* q, const int32_t* table, const int32_t* ctx, int B, int T, int Hq, int Hkv,
+               int d, int num_pages, int page_size, int width, const int32_t* cu_seqlens, int N, int dtype,
+               void* stream) {
+    if (B <= 0 || T < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || num_pages <= 0 || page_size <= 0 || width <= 0) return KDA_EINVAL;
+    const bool packed = cu_seqlens != nullptr;
+    if (packed ? (B != 1 || N <= 0) : (N != 0 && N != B)) return KDA_EINVAL;
+    if (!packed) N = B;
+    if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ENOTSUP;
+    if (!paged_sizes_ok(B, Hq, Hkv, T, d, N, packed) || (int64_t)num_pages * page_size > INT32_MAX) return KDA_ENOTSUP;
+    if (T > 0 && (!table || !ctx)) return KDA_EINVAL;
+    if (T > 0 && (!aligned(q) || !aligned(table, 4) || !aligned(ctx, 4))) return KDA_EALIGN;
+    if (packed && !aligned(cu_seqlens, 4)) return KDA_EALIGN;
+    *a = kda::PagedArgs{};
+    a->q = q;
+    a->table = table;
+    a->ctx = ctx;
+    a->T = T;
+    a->Hq = Hq;
+    a->Hkv = Hkv;
+    a->d = d;
+    a->num_pages = num_pages;
+    a->page_size = page_size;
+    a->width = width;
+    a->cu_seqlens = cu_seqlens;
+    a->N = N;
+    a->bf16 = dtype == KDA_BF16;
+    a->stream = reinterpret_cast<hipStream_t>(stream);
+    return KDA_OK;
+}
+
 }  // namespace
 
 namespace kda {
@@ -759,6 +800,64 @@ int kda_glr_decode_step(const void* gate, const void* x, float* h, void* o, int 
     if (!aligned(gate, gate_dtype == KDA_BF16 ? 2 : 4) || !aligned(x, es) || !aligned(h, 4) || !aligned(o, es)) return KDA_EALIGN;
     kda::GlrDecodeArgs a{gate, x, h, o, N, C, dtype == KDA_BF16, gate_dtype == KDA_BF16, reinterpret_cast<hipStream_t>(stream)};
     return hip_status(kda::launch_glr_decode(a));
+}
+
+int kda_paged_append(const void* q, const void* k, const void* v, const int32_t* pos, const float* freqs, void* q_out,
+                     void* K_pages, void* V_pages, const int32_t* block_table, const int32_t* ctx_len, int B, int T,
+                     int Hq, int Hkv, int d, int rot_dim, int pairing, int num_pages, int page_size, int table_width,
+                     const int32_t* cu_seqlens, int N, int dtype, void* stream) {
+    kda::PagedArgs a{};
+    const int st = paged_args(&a, q, block_table, ctx_len, B, T, q ? Hq : Hkv, Hkv, d, num_pages, page_size, table_width,
+                              cu_seqlens, N, dtype, stream);
+    if (st != KDA_OK) return st;
+    if (rot_dim < 0 || rot_dim > d || (rot_dim > 0) != (freqs != nullptr) || (T > 0 && !q != !q_out)) return KDA_EINVAL;
+    if (rot_dim % 16 || (pairing != KDA_PAIRS_HALVES && pairing != KDA_PAIRS_NEIGHBOURS)) return KDA_ENOTSUP;
+    if (T == 0) return KDA_OK;
+    if (!k || !v || !K_pages || !V_pages) return KDA_EINVAL;
+    if (!aligned(k) || !aligned(v) || !aligned(q_out) || !aligned(K_pages) || !aligned(V_pages) || !aligned(pos, 4) ||
+        !aligned(freqs, 4))
+        return KDA_EALIGN;
+    a.k = k;
+    a.v = v;
+    a.pos = pos;
+    a.freqs = freqs;
+    a.out = q_out;
+    a.Kw = K_pages;
+    a.Vw = V_pages;
+    a.rot_dim = rot_dim;
+    a.neighbours = pairing == KDA_PAIRS_NEIGHBOURS;
+    return hip_status(kda::launch_paged_append(a));
+}
+
+size_t kda_paged_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int d, int N, int has_cu) {
+    if (!paged_sizes_ok(B, Hq, Hkv, T, d, N, has_cu) || !kda::paged_attn_fits(T, has_cu ? N : B, Hq, Hkv, has_cu != 0)) return 0;
+    return kda::paged_attn_workspace_bytes(T, has_cu ? N : B, Hq, Hkv, d, has_cu != 0);
+}
+
+int kda_paged_attn(const void* q, const void* K_pages, const void* V_pages, const int32_t* block_table,
+                   const int32_t* ctx_len, const int32_t* tree, int tree_words, void* o, float* lse, int B, int T,
+                   int Hq, int Hkv, int d, float scale, int num_pages, int page_size, int table_width,
+                   const int32_t* cu_seqlens, int N, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    kda::PagedArgs a{};
+    const int st = paged_args(&a, q, block_table, ctx_len, B, T, Hq, Hkv, d, num_pages, page_size, table_width,
+                              cu_seqlens, N, dtype, stream);
+    if (st != KDA_OK) return st;
+    if (!(scale - scale == 0.f) || (tree && tree_words <= 0)) return KDA_EINVAL;
+    if (!kda::paged_attn_fits(T, a.N, Hq, Hkv, cu_seqlens != nullptr)) return KDA_ENOTSUP;
+    if (T == 0) return KDA_OK;
+    if (!q || !K_pages || !V_pages || !o || !workspace) return KDA_EINVAL;
+    if (!aligned(K_pages) || !aligned(V_pages) || !aligned(tree, 4) || !aligned(o) || !aligned(lse, 4) || !aligned(workspace))
+        return KDA_EALIGN;
+    if (workspace_bytes < kda::paged_attn_workspace_bytes(T, a.N, Hq, Hkv, d, cu_seqlens != nullptr)) return KDA_EINVAL;
+    a.Kp = K_pages;
+    a.Vp = V_pages;
+    a.tree = tree;
+    a.words = tree ? tree_words : 0;
+    a.out = o;
+    a.lse = lse;
+    a.scale = scale;
+    a.workspace = workspace;
+    return hip_status(kda::launch_paged_attn(a));
 }
 
 }  // extern "C"

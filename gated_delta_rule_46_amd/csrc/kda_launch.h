@@ -149,6 +149,28 @@ struct GlrDecodeArgs {
     hipStream_t stream;
 };
 
+// New tokens and a paged cache: the append's fields are null in attention and the
+// other way round.
+struct PagedArgs {
+    const void *q, *k, *v;
+    const void *Kp, *Vp;                    // pages that are read
+    void *Kw, *Vw;                          // pages that are written
+    const int32_t *table, *ctx, *pos, *tree;
+    const float* freqs;
+    void* out;                              // q rotated (null: none), or o
+    float* lse;                             // or null
+    int T, Hq, Hkv, d, rot_dim;
+    bool neighbours;                        // pairs (2i, 2i+1), else (i, i + rot_dim / 2)
+    int words;                              // of a token's tree bits
+    float scale;
+    int num_pages, page_size, width;        // width: pages of a row of the table
+    const int32_t* cu_seqlens;              // device, N+1 entries, or null
+    int N;                                  // number of sequences (B when cu_seqlens is null)
+    bool bf16;
+    void* workspace;
+    hipStream_t stream;
+};
+
 // Bytes of intermediates one (chunk, head) pair occupies in the workspace.
 size_t chunk_block_bytes(int dk, int dv, int chunk, bool bf16);
 // Upper bound on the number of chunks over all sequences.
@@ -208,5 +230,10 @@ size_t glr_workspace_bytes(int T, int N, int C, bool packed, bool bf16, bool gra
 hipError_t launch_glr_fwd(const GlrArgs& a);
 hipError_t launch_glr_bwd(const GlrArgs& a);
 hipError_t launch_glr_decode(const GlrDecodeArgs& a);
+
+bool paged_attn_fits(int T, int N, int Hq, int Hkv, bool packed);   // whether every launch fits a grid
+size_t paged_attn_workspace_bytes(int T, int N, int Hq, int Hkv, int d, bool packed);
+hipError_t launch_paged_append(const PagedArgs& a);
+hipError_t launch_paged_attn(const PagedArgs& a);
 
 }  // namespace kda

@@ -22,6 +22,7 @@ KDA_OK, KDA_EINVAL, KDA_ENOTSUP, KDA_EALIGN, KDA_EHIP, KDA_EWAIT, KDA_ESCRATCH =
 NOALLOC_SCRATCH_BYTES = 128 << 20
 KDA_F32, KDA_BF16 = 0, 1
 GATE_CHANNEL, GATE_SCALAR, GATE_HEAD = 0, 1, 2
+PAIRS_HALVES, PAIRS_NEIGHBOURS = 0, 1
 
 STAGE_PREP, STAGE_STATE, STAGE_ALL = 1, 2, 3
 
@@ -33,7 +34,8 @@ EXPORTS = ("kda_chunk_fwd", "kda_chunk_fwd_stage", "kda_chunk_fwd_workspace_byte
            "kda_chunk_bwd_ew_workspace_bytes", "kda_linattn_fwd", "kda_linattn_fwd_workspace_bytes", "kda_linattn_bwd",
            "kda_linattn_bwd_workspace_bytes", "kda_linattn_decode_step", "kda_swa_fwd", "kda_swa_bwd",
            "kda_swa_bwd_workspace_bytes", "kda_swa_decode_step", "kda_swa_decode_workspace_bytes", "kda_swa_cache_fill",
-           "kda_glr_fwd", "kda_glr_fwd_workspace_bytes", "kda_glr_bwd", "kda_glr_bwd_workspace_bytes", "kda_glr_decode_step")
+           "kda_glr_fwd", "kda_glr_fwd_workspace_bytes", "kda_glr_bwd", "kda_glr_bwd_workspace_bytes", "kda_glr_decode_step",
+           "kda_paged_append", "kda_paged_attn", "kda_paged_attn_workspace_bytes")
 
 
 class KDAError(RuntimeError):
@@ -127,6 +129,12 @@ def load(path: str):
     lib.kda_glr_bwd.argtypes = [vp] * 8 + [i] * 3 + [vp, i, i, i, vp, sz, vp]
     lib.kda_glr_decode_step.restype = i
     lib.kda_glr_decode_step.argtypes = [vp] * 4 + [i] * 4 + [vp]
+    lib.kda_paged_append.restype = i
+    lib.kda_paged_append.argtypes = [vp] * 10 + [i] * 10 + [vp, i, i, vp]
+    lib.kda_paged_attn_workspace_bytes.restype = sz
+    lib.kda_paged_attn_workspace_bytes.argtypes = [i] * 7
+    lib.kda_paged_attn.restype = i
+    lib.kda_paged_attn.argtypes = [vp] * 6 + [i] + [vp] * 2 + [i] * 5 + [f] + [i] * 3 + [vp, i, i, vp, sz, vp]
     lib.kda_chunk_fwd_noalloc.restype = i
     lib.kda_chunk_fwd_noalloc.argtypes = [vp] * 8 + [i] * 6 + [vp, i, i, i, vp]
     return lib
@@ -1051,5 +1059,121 @@ def glr_decode_step(gate, x, h, out: Optional[torch.Tensor] = None, stream=None)
         if rc != KDA_OK:
             raise KDAError(rc, "kda_glr_decode_step")
         return o
+
+    return _run(device, stream, call)
+
+
+# ---------------------------------------------------------------- a paged cache
+
+def _check_paged(rows, K_pages, V_pages, block_table, ctx_len, cu_seqlens):
+    """Shapes, dtypes and devices of a call on a paged cache whose new tokens' rows
+    [B,T,H,d] these are. Returns (B, T, packed, N, Hkv, d, pages, page, width)."""
+    if rows.dim() != 4 or K_pages.dim() != 4:
+        raise ValueError("rows must be [B,T,H,d] and pages [pages,page,Hkv,d], got %s and %s" % (tuple(rows.shape),
+                                                                                                tuple(K_pages.shape)))
+    (B, T, H, d), (pages, page, Hkv, _) = rows.shape, K_pages.shape
+    dtype, device = rows.dtype, rows.device
+    if cu_seqlens is not None and B != 1:
+        raise ValueError("packed sequences (cu_seqlens) need B = 1, got %d" % B)
+    if Hkv == 0 or H % Hkv:
+        raise ValueError("%d heads are not a multiple of the cache's %d" % (H, Hkv))
+    varlen, N = _check_varlen(cu_seqlens, B, device)
+    _like("K_pages", K_pages, (pages, page, Hkv, d), dtype, device)
+    _like("V_pages", V_pages, (pages, page, Hkv, d), dtype, device)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [N,width], got %s" % (tuple(block_table.shape),))
+    _like("block_table", block_table, (N, block_table.shape[1]), torch.int32, device)
+    _like("ctx_len", ctx_len, (N,), torch.int32, device)
+    return B, T, varlen, N, Hkv, d, pages, page, block_table.shape[1]
+
+
+def paged_append(k, v, K_pages, V_pages, block_table, ctx_len, q=None, pos=None, freqs=None, interleaved: bool = False,
+                 cu_seqlens=None, q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """New tokens' k, v [B,T,Hkv,d] to their rows of a paged cache K_pages, V_pages
+    [pages,page,Hkv,d] (kda_paged_append): token i of a sequence to row ctx_len + i,
+    in page block_table[row // page]; k, and q [B,T,Hq,d] if given, rotated by the
+    angles position * freqs (freqs fp32 [rot/2], or None: no rotation; pairs (i, i +
+    rot/2), or neighbours where interleaved). block_table int32 [N,width], ctx_len
+    int32 [N] (negative: left out), pos int32 [B,T] or None (the token's row);
+    cu_seqlens int32 [N+1] on the device (B must be 1) or None. Returns q rotated (q_out,
+    which may be q) or None."""
+    B, T, varlen, N, Hkv, d, pages, page, width = _check_paged(k, K_pages, V_pages, block_table, ctx_len, cu_seqlens)
+    device, dt = k.device, _dtype_code(k)
+    if k.shape[2] != Hkv:
+        raise ValueError("k has %d heads, the cache %d" % (k.shape[2], Hkv))
+    _check_input("k", k, k.dtype, device)
+    _like("v", v, k.shape, k.dtype, device)
+    Hq = Hkv
+    if q is not None:
+        if q.dim() != 4 or q.shape[2] % Hkv:
+            raise ValueError("q must be [B,T,Hq,d], Hq a multiple of %d, got %s" % (Hkv, tuple(q.shape)))
+        Hq = q.shape[2]
+        _like("q", q, (B, T, Hq, d), k.dtype, device)
+        if q_out is not None:
+            _like("q_out", q_out, q.shape, k.dtype, device)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    if pos is not None:
+        _like("pos", pos, (B, T), torch.int32, device)
+    rot = 0
+    if freqs is not None:
+        if freqs.dim() != 1:
+            raise ValueError("freqs must be [rot/2], got %s" % (tuple(freqs.shape),))
+        _check_input("freqs", freqs, torch.float32, device)
+        rot = 2 * freqs.shape[0]
+
+    def call(st):
+        out = torch.empty_like(q) if q is not None and q_out is None else q_out
+        rc = _lib().kda_paged_append(_addr(q), k.data_ptr(), v.data_ptr(), _addr(pos), _addr(freqs) if rot else None,
+                                     _addr(out), K_pages.data_ptr(), V_pages.data_ptr(), block_table.data_ptr(),
+                                     ctx_len.data_ptr(), B, T, Hq, Hkv, d, rot,
+                                     PAIRS_NEIGHBOURS if interleaved else PAIRS_HALVES, pages, page, width,
+                                     _addr(cu_seqlens), N if varlen else 0, dt, st)
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_paged_append")
+        return out
+
+    return _run(device, stream, call)
+
+
+def paged_attn_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, d: int, N: int = 0, varlen: bool = False) -> int:
+    return _lib().kda_paged_attn_workspace_bytes(B, T, Hq, Hkv, d, N, int(varlen))
+
+
+def paged_attn(q, K_pages, V_pages, block_table, ctx_len, tree=None, scale: Optional[float] = None, cu_seqlens=None,
+               out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, lse_out: bool = True,
+               workspace: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Attention of new tokens, appended before, over a paged cache (kda_paged_attn).
+    q [B,T,Hq,d]; every token sees its sequence's ctx_len rows before the new ones, and
+    of the new ones those that tree int32 [B,T,words] names by bits, or without a tree
+    those up to itself. Cache, block_table, ctx_len and cu_seqlens as for paged_append;
+    scale defaults to d ** -0.5. Returns (o in the dtype of q, lse fp32 [B,T,Hq] or
+    None); a row that sees no key has o = 0 and lse = -inf."""
+    B, T, varlen, N, Hkv, d, pages, page, width = _check_paged(q, K_pages, V_pages, block_table, ctx_len, cu_seqlens)
+    device, dt, Hq = q.device, _dtype_code(q), q.shape[2]
+    _check_input("q", q, q.dtype, device)
+    words = 0
+    if tree is not None:
+        if tree.dim() != 3 or tree.shape[2] < 1:
+            raise ValueError("tree must be [B,T,words], got %s" % (tuple(tree.shape),))
+        words = tree.shape[2]
+        _like("tree", tree, (B, T, words), torch.int32, device)
+    if out is not None:
+        _like("out", out, q.shape, q.dtype, device)
+    if lse is not None:
+        _like("lse", lse, (B, T, Hq), torch.float32, device)
+    need = paged_attn_workspace_bytes(B, T, Hq, Hkv, d, N, varlen)
+
+    def call(st):
+        o = torch.empty_like(q) if out is None else out
+        s = q.new_empty((B, T, Hq), dtype=torch.float32) if lse is None and lse_out else lse
+        ws = _scratch(workspace, need, device)
+        rc = _lib().kda_paged_attn(q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(), block_table.data_ptr(),
+                                   ctx_len.data_ptr(), _addr(tree), words, o.data_ptr(), _addr(s), B, T, Hq, Hkv, d,
+                                   d ** -0.5 if scale is None else float(scale), pages, page, width, _addr(cu_seqlens),
+                                   N if varlen else 0, dt, ws.data_ptr(), ws.numel() * ws.element_size(), st)
+        if rc != KDA_OK:
+            raise KDAError(rc, "kda_paged_attn")
+        return o, s
 
     return _run(device, stream, call)

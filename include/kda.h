@@ -516,6 +516,70 @@ int kda_glr_bwd(const void* gate, const void* x, const float* h0, const void* dh
 int kda_glr_decode_step(const void* gate, const void* x, float* h, void* o, int N, int C, int dtype, int gate_dtype,
                         void* stream);
 
+/*
+ * A paged cache for attention over all of a sequence's tokens. K_pages, V_pages
+ * [num_pages, page_size, Hkv, d]; row r of a sequence (its r-th token) lies in
+ * page block_table[seq][r / page_size] at r % page_size; block_table
+ * [N, table_width] int32 on the device. An entry outside [0, num_pages), and a
+ * row behind the table's width, is a page that is not there: nothing is read or
+ * written for it. Any page_size; num_pages * page_size < 2^31. ctx_len [N] int32
+ * on the device: tokens of the sequence in the cache before the new ones; a
+ * negative one leaves the sequence out (a padded batch). New token i of a
+ * sequence has row ctx_len + i.
+ *
+ * New tokens: B sequences of T, or packed (B = 1, cu_seqlens and N as for
+ * kda_chunk_fwd; any number of tokens each, none included); rows at or behind
+ * cu_seqlens[N] are left as they are. d in {32, 64, 128}; Hq a multiple of Hkv,
+ * at most 65,535; N * (T + 128) and (T + 128) * Hq / Hkv < 2^31 (KDA_ENOTSUP
+ * beyond). Arrays of rows, pages and the workspace 16-byte aligned, the rest to
+ * their element.
+ *
+ * kda_paged_append: k and v [B, T, Hkv, d] of the new tokens to their rows, k
+ * rotated by its position on the way, and q [B, T, Hq, d] rotated to q_out (both
+ * NULL: no q; Hq is then not read). The first rot_dim values of a head (a
+ * multiple of 16, at most d; 0 with freqs NULL: no rotation) are rotated in
+ * pairs, pair i by the angle pos * freqs[i] (freqs [rot_dim / 2] fp32 on the
+ * device, radians a token; pos [B, T] int32 on the device, or NULL: the token's
+ * row). pairing: KDA_PAIRS_HALVES (i and i + rot_dim / 2) or KDA_PAIRS_NEIGHBOURS
+ * (2i and 2i + 1):  (x, y) -> (x cos - y sin, x sin + y cos).  Angles are
+ * formed in 64 bits, the rest in fp32, rounded once. v and unrotated values are
+ * copied bit for bit. q_out of a sequence that is left out is zero. Two tokens of
+ * a call must not have the same row of the same page; q_out may be q.
+ */
+#define KDA_PAIRS_HALVES 0
+#define KDA_PAIRS_NEIGHBOURS 1
+int kda_paged_append(const void* q, const void* k, const void* v, const int32_t* pos, const float* freqs, void* q_out,
+                     void* K_pages, void* V_pages, const int32_t* block_table, const int32_t* ctx_len, int B, int T,
+                     int Hq, int Hkv, int d, int rot_dim, int pairing, int num_pages, int page_size, int table_width,
+                     const int32_t* cu_seqlens, int N, int dtype, void* stream);
+
+/*
+ * Softmax attention of the new tokens over such a cache, theirs included (they
+ * have been appended before): every new token sees the ctx_len rows before them,
+ * and of the new ones those that tree names, or with tree NULL those up to
+ * itself. tree [B, T, tree_words] int32 on the device: bit j % 32 of word j / 32
+ * of a token says that it sees new token j of its sequence (itself where its own
+ * bit is set); bits of tokens that the sequence does not have mean nothing, and
+ * tokens behind the words are not seen. One token a sequence is decoding, a tree
+ * checks drafts, tree NULL with more tokens takes a piece of a prompt.
+ *   o_i = sum_j softmax_j(scale q_i . k_j) v_j,  lse_i = log sum_j exp(scale q_i . k_j)
+ * q, o [B, T, Hq, d] in the input dtype, query head h reads kv head
+ * h / (Hq / Hkv); lse [B, T, Hq] fp32 or NULL; scale finite. A row that sees no
+ * key has o = 0 and lse = -Inf, as every row of a sequence that is left out.
+ * Statistics and sums are fp32; 256 times the sum of |v| over the keys that a row
+ * sees has to be finite there. A NaN or Inf in a row of the cache reaches no row
+ * of o that does not see it. Repeated calls agree bit for bit. workspace:
+ * kda_paged_attn_workspace_bytes(...) bytes, required; calls that may overlap
+ * (two streams, two captured graphs) need one each. Returns KDA_OK or a negative
+ * status (KDA_ENOTSUP also where the rows of all heads are more than a launch
+ * takes).
+ */
+size_t kda_paged_attn_workspace_bytes(int B, int T, int Hq, int Hkv, int d, int N, int has_cu_seqlens);
+int kda_paged_attn(const void* q, const void* K_pages, const void* V_pages, const int32_t* block_table,
+                   const int32_t* ctx_len, const int32_t* tree, int tree_words, void* o, float* lse, int B, int T,
+                   int Hq, int Hkv, int d, float scale, int num_pages, int page_size, int table_width,
+                   const int32_t* cu_seqlens, int N, int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static text for a status code (never NULL). */
 const char* kda_strerror(int status);
 

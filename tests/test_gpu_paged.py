@@ -1,0 +1,430 @@
+"""New tokens on their way into a paged cache and attention over it, on the GPU
+against their definitions in 64 bits. Bars of o: those of mixer_checks; of lse and
+of rotated values: counted roundings."""
+import pytest
+import torch
+
+from mixer_checks import close
+from oracle import mixers
+from oracle import recur_paged as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+STEP = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
+
+
+@pytest.fixture(scope="module")
+def kda():
+    from gated_delta_rule_46_amd import kda as k
+    k.library()
+    return k
+
+
+def ancestors(n, g):
+    rows = []
+    for i in range(n):
+        parent = int(torch.randint(-1, i, (1,), generator=g)) if i else -1
+        rows.append((rows[parent] if parent >= 0 else 0) | 1 << i)
+    return rows
+
+
+def words_of(rows, words):
+    flat = [[(r >> 32 * w) & 0xffffffff for w in range(words)] for r in rows]
+    return torch.tensor(flat, dtype=torch.int64).to(torch.int32).reshape(len(rows), words)
+
+
+def make(lens, ctx, Hq, Hkv, d, dtype, page, tree=None, packed=True, seed=0, spare=3, width=None):
+    """tree: None, "tree" or "any" (bits at random, rows without any among them)."""
+    g = torch.Generator().manual_seed(seed)
+    rnd = lambda *s: torch.randn(*s, generator=g).to(dtype).cuda()  # noqa: E731
+    N, T = len(lens), sum(lens)
+    need = [max(0, (c + n + page - 1) // page) for c, n in zip(ctx, lens)]
+    pool = sum(need) + spare
+    order = torch.randperm(pool, generator=g).to(torch.int32)
+    table = torch.full((N, max(max(need), 1) + 1 if width is None else width), -1, dtype=torch.int32)
+    at = 0
+    for n in range(N):
+        table[n, :need[n]] = order[at:at + need[n]]
+        at += need[n]
+    lead = (1, T) if packed else (N, lens[0])
+    x = dict(q=rnd(*lead, Hq, d), k=rnd(*lead, Hkv, d), v=rnd(*lead, Hkv, d), Kp=rnd(pool, page, Hkv, d),
+             Vp=rnd(pool, page, Hkv, d), table=table.cuda(), ctx=torch.tensor(ctx, dtype=torch.int32).cuda(), tree=None, cu=None)
+    cu = torch.tensor([0] + lens).cumsum(0)
+    x["seqs"] = mixers.spans(1, T, cu) if packed else mixers.spans(N, lens[0])
+    if packed:
+        x["cu"] = cu.to(torch.int32).cuda()
+    if tree:
+        words = (max(max(lens), 1) + 31) // 32
+        if tree == "tree":
+            rows = [r for n in lens for r in ancestors(n, g)]
+        else:
+            rows = [int(torch.randint(0, 2 ** 62, (1,), generator=g)) * 3 ** 40 % (1 << 32 * words) if i % 3 else 0
+                    for i in range(T)]
+        x["tree"] = words_of(rows, words).reshape(*lead, words).cuda()
+    return x
+
+
+def attend(kda, x, **kw):
+    return kda.paged_attn(x["q"], x["Kp"], x["Vp"], x["table"], x["ctx"], tree=x["tree"], cu_seqlens=x["cu"], **kw)
+
+
+def check(kda, x, scale=None, **kw):
+    o, lse = attend(kda, x, scale=scale, **kw)
+    torch.cuda.synchronize()
+    d = x["q"].shape[-1]
+    cpu = {n: t.cpu() if torch.is_tensor(t) else t for n, t in x.items()}
+    ro, rl, size, bound = ref.paged_attn(cpu["q"], cpu["Kp"], cpu["Vp"], cpu["table"], cpu["ctx"], cpu["tree"],
+                                         d ** -0.5 if scale is None else scale, x["seqs"])
+    close("o", o.cpu(), ro, x["q"].dtype, size=size)
+    none = torch.isinf(rl)
+    assert torch.equal(torch.isinf(lse.cpu()), none) and (lse.cpu()[none] < 0).all()
+    assert (o.cpu()[none] == 0).all()
+    off = (lse.cpu().double() - rl)[~none].abs() / bound[~none]
+    assert off.numel() == 0 or off.max().item() <= 1, "lse off by %.3g of its bound" % off.max().item()
+    return o, lse
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (4, 1), (6, 2), (8, 8), (40, 1), (35, 5)])
+def test_one_token(kda, Hq, Hkv, d, dtype):
+    """Decoding: contexts around tiles' and units' ends, one of them empty."""
+    check(kda, make([1] * 9, [0, 1, 30, 31, 32, 127, 128, 129, 700], Hq, Hkv, d, dtype, 16, packed=False, seed=d + Hq))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("page", [1, 2, 7, 16, 33, 64, 100, 1024])
+def test_pages(kda, page, dtype):
+    check(kda, make([1, 3, 9], [5, 200, 64], 4, 2, 64, dtype, page, seed=page))
+    check(kda, make([33, 70], [100, 3], 4, 2, 64, dtype, page, tree="tree", seed=page))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("kind", [None, "tree", "any"])
+@pytest.mark.parametrize("lens,ctx", [([5, 1, 40], [70, 33, 512]), ([64], [0]), ([0, 3, 0, 17, 0], [9, 0, 0, 128, 4]),
+                                      ([33, 31, 32], [1, 31, 95]), ([130], [61]), ([1, 1, 90, 2], [300, 0, 10, 50])])
+def test_drafts(kda, lens, ctx, kind, dtype):
+    for Hq, Hkv, d in ((6, 2, 64), (4, 4, 32), (8, 1, 128)):
+        check(kda, make(lens, ctx, Hq, Hkv, d, dtype, 16, tree=kind, seed=len(lens)))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,ctx", [(63, 0), (64, 1), (65, 64), (200, 0), (257, 100), (300, 513)])
+def test_pieces(kda, T, ctx, dtype):
+    check(kda, make([T, T], [ctx, ctx // 2], 4, 2, 64, dtype, 32, packed=False, seed=T))
+    check(kda, make([T], [ctx], 3, 1, 128, dtype, 48, seed=T))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("ctx", [3000, 9001, 20000])
+def test_long_context(kda, ctx, dtype):
+    """The keys of one sequence over many workgroups, rows of one token and of a tree."""
+    check(kda, make([1], [ctx], 4, 2, 64, dtype, 64, packed=False))
+    check(kda, make([20, 1], [ctx, 40], 4, 2, 32, dtype, 16, tree="tree"))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_many_sequences(kda, dtype):
+    """More items than are shared out, and just fewer."""
+    check(kda, make([1] * 300, [(7 * i) % 150 for i in range(300)], 16, 8, 32, dtype, 16, packed=False))
+    check(kda, make([1] * 130, [(11 * i) % 170 for i in range(130)], 16, 8, 32, dtype, 16, packed=False))
+    check(kda, make([(i * 5) % 9 for i in range(260)], [(13 * i) % 90 for i in range(260)], 8, 8, 32, dtype, 16))
+
+
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1.0])
+def test_scales(kda, scale):
+    for dtype in (BF16, F32):
+        check(kda, make([1, 20], [200, 40], 4, 2, 64, dtype, 16, tree="any"), scale=scale)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_pages_that_are_not_there(kda, dtype):
+    x = make([1, 7, 40], [500, 90, 0], 4, 2, 64, dtype, 16)
+    x["table"][0, 3] = -1
+    x["table"][0, 9] = 10 ** 6
+    x["table"][0, 10] = x["Kp"].shape[0]
+    x["table"][1, 5:] = -7
+    x["table"][2] = -1
+    check(kda, x)
+    y = make([1, 7, 40], [500, 90, 0], 4, 2, 64, dtype, 16, width=32)
+    y["table"] = y["table"][:, :3].contiguous()   # the table ends before the sequences do
+    check(kda, y)
+
+
+@pytest.mark.parametrize("kind", [None, "tree"])
+@pytest.mark.parametrize("T", [1, 9, 40])
+def test_left_out(kda, T, kind):
+    x = make([T] * 4, [100, 20, 300, 0], 4, 2, 64, BF16, 16, tree=kind, packed=False)
+    x["ctx"][1] = -1
+    x["ctx"][2] = -2 ** 31
+    o, lse = check(kda, x)
+    assert (o[1:3] == 0).all() and torch.isneginf(lse[1:3]).all()
+
+
+def test_contexts_beyond_the_table(kda):
+    """A context longer than its table holds: the rows that are there are seen."""
+    x = make([1, 4], [100, 50], 4, 2, 64, F32, 16)
+    x["ctx"][0] = 2 ** 31 - 1
+    o, _ = attend(kda, x)
+    y = dict(x, ctx=torch.tensor([x["table"].shape[1] * 16, 50], dtype=torch.int32).cuda())
+    p, _ = attend(kda, y)
+    torch.cuda.synchronize()
+    assert torch.equal(o, p)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_not_finite_rows_that_are_not_seen(kda, bad, dtype):
+    """Rows behind a sequence's end, pages of others, drafts of other branches."""
+    x = make([9, 40], [101, 7], 4, 2, 64, dtype, 16, tree="tree", seed=4)
+    used = torch.zeros(x["Kp"].shape[0] * 16, dtype=torch.bool)
+    for n, (_, t0, t1) in enumerate(x["seqs"]):
+        for r in range(int(x["ctx"][n]) + t1 - t0):
+            used[ref.place(x["table"].cpu(), n, r, 16, len(x["Kp"]))] = True
+    for name in ("Kp", "Vp"):
+        x[name].view(-1, 2, 64)[~used.cuda()] = bad
+    check(kda, x)
+    # a draft that few see: rows that do not see it are as the definition says
+    j = 3
+    at = ref.place(x["table"].cpu(), 1, 7 + j, 16, len(x["Kp"]))
+    x["Vp"].view(-1, 2, 64)[at] = bad
+    x["Kp"].view(-1, 2, 64)[at, 0, :3] = float("nan")
+    o, lse = attend(kda, x)
+    tree = x["tree"].cpu()[0]
+    blind = torch.tensor([t < 9 or not ref.sees(tree[t], t - 9, j) for t in range(49)])
+    cpu = {n: t.cpu() if torch.is_tensor(t) else t for n, t in x.items()}
+    ro, rl, size, _ = ref.paged_attn(cpu["q"], cpu["Kp"], cpu["Vp"], cpu["table"], cpu["ctx"], cpu["tree"], 0.125, x["seqs"])
+    assert blind.any() and not blind.all()
+    close("o", o.cpu()[:, blind], ro[:, blind], dtype, size=size[:, blind])
+    assert not torch.isfinite(o.cpu()[:, ~blind][:, :, :2]).any()
+
+
+def test_words(kda):
+    """More words than a draft needs, bits of tokens that are not there, and too few words."""
+    x = make([40], [20], 4, 2, 64, BF16, 16, tree="any")
+    want, _ = check(kda, x)
+    more = torch.cat([x["tree"], torch.full_like(x["tree"], -1)], -1)
+    more[..., 1] |= -1 << 8   # bits 40 and up
+    o, _ = check(kda, dict(x, tree=more.contiguous()))
+    assert torch.equal(o, want)
+    check(kda, dict(x, tree=x["tree"][..., :1].contiguous()))
+
+
+def test_rows_behind_the_last_sequence_stay(kda):
+    x = make([3, 40], [50, 20], 4, 2, 64, BF16, 16)
+    want, want_lse = attend(kda, x)
+    q = torch.cat([x["q"], torch.full_like(x["q"], float("nan"))], 1)
+    out, lse = torch.full_like(q, 3.0), torch.full(q.shape[:3], 3.0, device="cuda")
+    attend(kda, dict(x, q=q), out=out, lse=lse)
+    close("o", out[:, :43].cpu(), want.cpu().double(), BF16)   # (other row blocks: other sums)
+    assert (out[:, 43:] == 3).all() and (lse[:, 43:] == 3).all()
+    assert (lse[:, :43] - want_lse).abs().max() < 1e-5
+    k, v = (torch.cat([x[n], torch.full_like(x[n], 9.0)], 1) for n in ("k", "v"))
+    Kp, Vp, qo = x["Kp"].clone(), x["Vp"].clone(), torch.full_like(q, 3.0)
+    kda.paged_append(k, v, Kp, Vp, x["table"], x["ctx"], q=q, q_out=qo, cu_seqlens=x["cu"])
+    assert torch.equal(qo[:, :43], x["q"]) and (qo[:, 43:] == 3).all()
+    assert not (Kp == 9.0).all(-1).any() and not (Vp == 9.0).all(-1).any()
+
+
+def test_large_pool(kda):
+    """Offsets beyond 32 bits: elements of the pool, then bytes of it."""
+    page, Hkv, d = 256, 8, 128
+    pages = 2 ** 32 // (page * Hkv * d) + 40   # elements pass 2^32, 8.6 GB each
+    x = make([1, 5], [600, 900], 16, Hkv, d, BF16, page, spare=0)
+    n = len(x["Kp"])
+    Kp, Vp = (torch.empty(pages, page, Hkv, d, dtype=BF16, device="cuda") for _ in range(2))
+    where = torch.tensor([pages - 1 - 5 * i for i in range(n)], device="cuda")
+    Kp[where], Vp[where] = x["Kp"], x["Vp"]
+    table = torch.where(x["table"] >= 0, where[x["table"].clamp_min(0).long()].to(torch.int32), x["table"])
+    o, lse = attend(kda, dict(x, Kp=Kp, Vp=Vp, table=table))
+    want, want_lse = attend(kda, x)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    kda.paged_append(x["k"], x["v"], Kp, Vp, table, x["ctx"], cu_seqlens=x["cu"])
+    kda.paged_append(x["k"], x["v"], x["Kp"], x["Vp"], x["table"], x["ctx"], cu_seqlens=x["cu"])
+    assert torch.equal(Kp[where], x["Kp"]) and torch.equal(Vp[where], x["Vp"])
+
+
+@pytest.mark.parametrize("T,kind", [(1, None), (30, "tree"), (200, None)])
+def test_repeats_and_streams_and_graphs(kda, T, kind):
+    x = make([T] * 3, [3000, 11, 700], 8, 2, 64, BF16, 16, tree=kind, packed=False)
+    want, want_lse = attend(kda, x)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    o, lse = attend(kda, x, stream=side)
+    side.synchronize()
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    given = dict(out=torch.empty_like(want), lse=torch.empty_like(want_lse))
+    assert attend(kda, x, **given) == (given["out"], given["lse"]) and torch.equal(given["out"], want)
+    assert attend(kda, x, lse_out=False)[1] is None
+    with torch.cuda.stream(side):
+        attend(kda, x)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = attend(kda, x)
+        graphs.append((graph, held))
+    for _ in range(3):
+        for graph, held in graphs:
+            held[0].fill_(5.0)
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, held in graphs:
+            assert torch.equal(held[0], want) and torch.equal(held[1], want_lse)
+        x["q"].mul_(2.0)
+        x["q"].mul_(0.5)
+    # a context that has grown since the capture
+    x["ctx"].sub_(5)
+    want, _ = attend(kda, x)
+    graphs[0][0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(graphs[0][1][0], want)
+
+
+# ---------------------------------------------------------------- append
+
+def rounded(name, x, want, size):
+    """Half a step of the type and six roundings in fp32 of what was added: the two
+    products, their sum, and one and a half units each of the cosine and the sine
+    with the turn's own rounding to fp32 (2^-24 of a turn is 2 pi 2^-24 of a radian at
+    most, relative to a sine or cosine of one): ten in all."""
+    off = (x.double() - want).abs()
+    room = STEP[x.dtype] * want.abs() * (1 + 1e-6) + 10 * 2.0 ** -24 * size
+    worst = (off - room).max().item()
+    assert worst <= 0, "%s is off by %.3g more than it may" % (name, worst)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,rot", [(32, 16), (32, 32), (64, 0), (64, 48), (64, 64), (128, 64), (128, 128)])
+def test_append(kda, d, rot, interleaved, dtype):
+    lens, ctx = [5, 0, 1, 33, 3], [11, 4, 0, 100, -1]
+    x = make(lens, ctx, 6, 2, d, dtype, 10, seed=rot)
+    g = torch.Generator().manual_seed(rot)
+    freqs = (10000.0 ** (-torch.arange(rot // 2) / max(rot // 2, 1))).to(F32).cuda() if rot else None
+    for pos in (None, torch.randint(-5, 2000000, (1, sum(lens)), generator=g).to(torch.int32).cuda()):
+        Kp, Vp = x["Kp"].clone(), x["Vp"].clone()
+        q = kda.paged_append(x["k"], x["v"], Kp, Vp, x["table"], x["ctx"], q=x["q"], pos=pos, freqs=freqs,
+                             interleaved=interleaved, cu_seqlens=x["cu"])
+        torch.cuda.synchronize()
+        where = torch.cat([torch.arange(c, c + n) for n, c in zip(lens, ctx)]) if pos is None else pos[0].cpu()
+        turn = (lambda t: ref.rotate(t[0].cpu(), where, freqs.cpu(), interleaved)) if rot else (lambda t: t[0].cpu().double())
+        big = lambda t: t[0].cpu().double().abs().max(-1, keepdim=True)[0] * 2 * (1 if rot else 0)  # noqa: E731
+        wq, wk = turn(x["q"]), turn(x["k"])
+        wq[39:] = 0   # left out
+        rounded("q", q[0].cpu(), wq, big(x["q"]))
+        wK, wV = x["Kp"].cpu().view(-1, 2, d).clone(), x["Vp"].cpu().view(-1, 2, d).clone()
+        gotK, gotV = Kp.cpu().view(-1, 2, d), Vp.cpu().view(-1, 2, d)
+        touched = torch.zeros(len(wK), dtype=torch.bool)
+        t = 0
+        for n, (length, c) in enumerate(zip(lens, ctx)):
+            for r in range(c, c + length):
+                if c >= 0:
+                    at = ref.place(x["table"].cpu(), n, r, 10, len(Kp))
+                    touched[at] = True
+                    rounded("k", gotK[at], wk[t], big(x["k"])[t])
+                    assert torch.equal(gotV[at], x["v"][0, t].cpu())
+                    assert torch.equal(gotK[at, :, rot:], x["k"][0, t, :, rot:].cpu())
+                t += 1
+        assert torch.equal(gotK[~touched], wK[~touched]) and torch.equal(gotV[~touched], wV[~touched])
+
+
+def test_append_without_q_in_place_and_fixed(kda):
+    x = make([4, 4], [30, 7], 8, 2, 64, BF16, 16, packed=False)
+    freqs = torch.rand(32, device="cuda")
+    a, b = [(x["Kp"].clone(), x["Vp"].clone()) for _ in range(2)]
+    want = kda.paged_append(x["k"], x["v"], *a, x["table"], x["ctx"], q=x["q"], freqs=freqs)
+    assert kda.paged_append(x["k"], x["v"], *b, x["table"], x["ctx"], freqs=freqs) is None
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    q = x["q"].clone()
+    assert kda.paged_append(x["k"], x["v"], *b, x["table"], x["ctx"], q=q, q_out=q, freqs=freqs) is q and torch.equal(q, want)
+    cu = torch.tensor([0, 4, 8], dtype=torch.int32, device="cuda")
+    flat = lambda t: t.reshape(1, 8, *t.shape[2:])  # noqa: E731
+    c = (x["Kp"].clone(), x["Vp"].clone())
+    p = kda.paged_append(flat(x["k"]), flat(x["v"]), *c, x["table"], x["ctx"], q=flat(x["q"]), freqs=freqs, cu_seqlens=cu)
+    assert torch.equal(flat(want), p) and torch.equal(a[0], c[0])
+
+
+def test_append_pages_that_are_not_there(kda):
+    x = make([20, 20], [30, 7], 2, 2, 64, BF16, 16)
+    x["table"][0, 2:] = -1
+    x["table"][1, 1] = len(x["Kp"])
+    Kp, Vp = x["Kp"].clone(), x["Vp"].clone()
+    kda.paged_append(x["k"], x["v"], Kp, Vp, x["table"], x["ctx"], cu_seqlens=x["cu"])
+    want_K, want_V = x["Kp"].clone(), x["Vp"].clone()
+    for n, (_, t0, t1) in enumerate(x["seqs"]):
+        for t in range(t0, t1):
+            at = ref.place(x["table"].cpu(), n, int(x["ctx"][n]) + t - t0, 16, len(Kp))
+            if at is not None:
+                want_K.view(-1, 2, 64)[at], want_V.view(-1, 2, 64)[at] = x["k"][0, t], x["v"][0, t]
+    assert torch.equal(Kp, want_K) and torch.equal(Vp, want_V)
+
+
+# ---------------------------------------------------------------- together
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_layer_pair_in_serving(kda, dtype):
+    """Prompts, then single tokens, then a chain of drafts of which some are taken back,
+    through a recurrence and attention over its result, against both run over whole
+    sequences in 64 bits. Every part of the serving run sees what the parts before it left
+    behind: the state, the cache, the table."""
+    H, d, page, N = 2, 32, 8, 3
+    C = H * d
+    prompts, steps, drafts, kept = [30, 1, 77], 3, 6, 4
+    total = [p + steps + kept for p in prompts]
+    g = torch.Generator().manual_seed(7)
+    longest = max(total) + drafts
+    gate = (1 - 0.2 * torch.rand(N, longest, C, generator=g)).to(dtype).cuda()
+    xs = torch.randn(N, longest, C, generator=g).mul(0.3).to(dtype).cuda()
+    freqs = (100.0 ** (-torch.arange(d // 2) / (d // 2))).to(F32).cuda()
+    width = (longest + page - 1) // page
+    order = torch.randperm(N * width + 2, generator=g)[:N * width].to(torch.int32)
+    table = order.view(N, width).cuda()
+    Kp, Vp = (torch.full((N * width + 2, page, H, d), float("nan"), dtype=dtype, device="cuda") for _ in range(2))
+    state = None
+    done = [0] * N
+    outs = [[] for _ in range(N)]
+
+    def step(lens, keep_state=True):
+        nonlocal state
+        cu = torch.tensor([0] + lens, device="cuda").cumsum(0).to(torch.int32)
+        cut = lambda t: torch.cat([t[n, done[n]:done[n] + lens[n]] for n in range(N)])[None].contiguous()  # noqa: E731
+        h, h_T = kda.glr_fwd(cut(gate), cut(xs), h0=state, cu_seqlens=cu)
+        rows = h.view(1, -1, H, d)
+        ctx = torch.tensor(done, dtype=torch.int32, device="cuda")
+        q = kda.paged_append(rows, rows, Kp, Vp, table, ctx, q=rows, freqs=freqs, cu_seqlens=cu)
+        o, _ = kda.paged_attn(q, Kp, Vp, table, ctx, cu_seqlens=cu)
+        if keep_state:
+            state = h_T
+        return [o[0, int(cu[n]):int(cu[n + 1])] for n in range(N)]
+
+    def take(o, count):
+        for n in range(N):
+            outs[n].append(o[n][:count[n]])
+            done[n] += count[n]
+
+    take(step(prompts), prompts)
+    for _ in range(steps):
+        take(step([1] * N), [1] * N)
+    before = state
+    o = step([drafts] * N, keep_state=False)   # drafts, all on one branch; the last ones are taken back
+    take(o, [kept] * N)
+    # the state after the drafts that were kept
+    cut = lambda t: torch.stack([t[n, done[n] - kept:done[n]] for n in range(N)]).contiguous()  # noqa: E731
+    _, state = kda.glr_fwd(cut(gate), cut(xs), h0=before)
+    torch.cuda.synchronize()
+    for n in range(N):
+        seqs = [(0, 0, total[n])]
+        h, h_T, *_ = ref.glr(gate[n:n + 1, :total[n]].cpu(), xs[n:n + 1, :total[n]].cpu(), None, seqs)
+        rows = h[0].view(-1, H, d).to(dtype).double()   # as the layer hands them on
+        rot = ref.rotate(rows, torch.arange(total[n]), freqs.cpu(), False).to(dtype)
+        pages = (total[n] + page - 1) // page
+        fill = lambda t: torch.cat([t, torch.zeros(pages * page - total[n], H, d, dtype=t.dtype)]).view(pages, page, H, d)  # noqa: E731
+        want, _, size, _ = ref.paged_attn(rot[None], fill(rot), fill(rows), torch.arange(pages)[None], [0], None, d ** -0.5, seqs)
+        # inputs of attention differ by a rounding of the type where the two recurrences round
+        # apart, which an output sees times the scores' size (under 8 here): 16 more roundings
+        close("o", torch.cat(outs[n])[None].cpu(), want, dtype, tau=5e-2 if dtype == BF16 else 1e-4, size=size)
+        assert (state[n].cpu().double() - h_T[0]).abs().max() <= 1e-4
