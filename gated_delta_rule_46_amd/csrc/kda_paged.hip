@@ -19,6 +19,16 @@ namespace {
 
 size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// over the four lanes that hold one column of a 16x16 result
+__device__ __forceinline__ float group_max(float v) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return swap_max(fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1])));
+}
+__device__ __forceinline__ float group_sum(float v) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return swap_sum(__uint_as_float(a[0]) + __uint_as_float(a[1]));
+}
+
 // Where token `row` of a sequence lies in the cache: its row over all pages, or
 // -1 where the table names no page for it.
 struct Pages {
@@ -163,16 +173,16 @@ struct AttnParams {
     Pages pages;
     SeqMap map;
     int Hq, Hkv, G, words;
+    int HW, groups;         // kv heads that a workgroup takes together, and such groups
     long capacity;          // of a sequence's pages
     float scale;
     int blocks;             // blocks of rows over all sequences
     int wgs;                // workgroups that share the keys, or 0: one for each item
     int2* span;             // [item]: the first and last workgroup of an item that is shared
-    float *po, *pml;        // parts: [2 * wgs][R][D], [2 * wgs][R][2]
+    float *po, *pml;        // parts: [2 * wgs][HW][R][D], [2 * wgs][HW][R][2]
 };
 
 constexpr int MAX_BLOCKS = 1024;   // of a call whose keys are shared out
-constexpr int WGS = 512;           // two for each CU, what LDS takes
 
 // A block of R rows (token, head of a group) of one sequence.
 struct RowBlock {
@@ -211,114 +221,447 @@ __device__ __forceinline__ int keys_of(const AttnParams& p, const RowBlock& b, i
     return (int)min((long)ctx + (p.tree ? b.n : min(b.n, (b.r0 + R - 1) / p.G + 1)), p.capacity);
 }
 
+// What a workgroup takes: units (KB keys of one item, a block and a group of kv heads)
+// [u, end), counted over the blocks, then the groups; unit u is number it0 of item (v, hg).
+// total: of all.
+struct Work {
+    long u, end, total;
+    int v, hg, it0, wgs, wg;
+    // the workgroup that has a unit
+    __device__ __forceinline__ int owner(long x) const { return (int)(((x + 1) * wgs - 1) / total); }
+};
+// LEAST: units that a workgroup has at least, where there are as many. REMAP: workgroups
+// that follow each other in the order of units on one die. False for one without work.
+template <int R, int KB, int LEAST, int NT, bool REMAP> __device__ __forceinline__ bool find_work(const AttnParams& p, Work& k) {
+    const int tid = threadIdx.x, lane = tid % WAVE, w = tid / WAVE;
+    if (!p.wgs) {
+        k.wg = REMAP ? xcd_remap(blockIdx.x, gridDim.x) : (int)blockIdx.x;
+        k.u = 0;
+        k.end = k.total = k.wgs = 1;
+        k.hg = k.wg / p.blocks;
+        k.v = k.wg % p.blocks;
+        k.it0 = 0;
+        return true;
+    }
+    __shared__ int s_wave[NT / WAVE], s_at[2];
+    const int each = (p.blocks + NT - 1) / NT, b0 = tid * each;   // neighbours that a thread counts
+    constexpr int MOST = (MAX_BLOCKS + NT - 1) / NT;
+    int mine[MOST], sum = 0;
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) {
+        RowBlock rb;
+        mine[i] = 0;
+        if (i < each && b0 + i < p.blocks && row_block(p.map, p.G, R, b0 + i, rb))
+            mine[i] = max((keys_of(p, rb, R) + KB - 1) / KB, 1);
+        sum += mine[i];
+    }
+    int before = sum;
+#pragma unroll
+    for (int o = 1; o < WAVE; o *= 2) {
+        const int y = __shfl_up(before, o, WAVE);
+        if (lane >= o) before += y;
+    }
+    if (lane == 63) s_wave[w] = before;
+    __syncthreads();
+    before -= sum;
+    int of_head = 0;
+#pragma unroll
+    for (int i = 0; i < NT / WAVE; ++i) {
+        before += i < w ? s_wave[i] : 0;
+        of_head += s_wave[i];
+    }
+    of_head = __builtin_amdgcn_readfirstlane(of_head);
+    k.total = (long)of_head * p.groups;
+    k.wgs = (int)min((long)p.wgs, (k.total + LEAST - 1) / LEAST);
+    if ((int)blockIdx.x >= k.wgs) return false;
+    k.wg = REMAP ? xcd_remap(blockIdx.x, k.wgs) : (int)blockIdx.x;
+    k.u = k.total * k.wg / k.wgs;
+    k.end = k.total * (k.wg + 1) / k.wgs;
+    k.hg = (int)(k.u / of_head);
+    const int at = (int)(k.u - (long)k.hg * of_head);
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) {   // one block of one thread holds the unit
+        if (at >= before && at < before + mine[i]) {
+            s_at[0] = b0 + i;
+            s_at[1] = at - before;
+        }
+        before += mine[i];
+    }
+    __syncthreads();
+    k.v = __builtin_amdgcn_readfirstlane(s_at[0]);
+    k.it0 = __builtin_amdgcn_readfirstlane(s_at[1]);
+    return true;
+}
+
+// The new tokens that one row sees, as bits.
+struct Seen {
+    const int32_t* bits;   // the token's words, or null: every token up to `tok`
+    int words, ctx, tok;
+    // of the 32 keys from j0 on
+    __device__ __forceinline__ uint32_t operator()(int j0) const {
+        const int d = j0 - ctx;   // among the new tokens
+        if (bits == nullptr) {
+            const int m = min(max(tok - d + 1, 0), 32);
+            return m == 32 ? ~0u : (1u << m) - 1u;
+        }
+        if (d <= -32) return ~0u;
+        if (d < 0) return ((1u << -d) - 1u) | (uint32_t)bits[0] << -d;
+        const int at = d >> 5, sh = d & 31;
+        const uint32_t x = at < words ? (uint32_t)bits[at] : 0u;
+        const uint32_t y = sh && at + 1 < words ? (uint32_t)bits[at + 1] << (32 - sh) : 0u;
+        return x >> sh | y;
+    }
+};
+
+// ---------------------------------------------------------------- few rows
+
+// Up to 16 RT rows a block, tiles of 16x16 and 32 deep. A wave has one kv head and tiles
+// of 32 keys of its own; the waves of a workgroup take HW heads of the same keys, which lie
+// side by side in memory, and every KS-th tile where there are fewer heads than waves. Keys go from memory to the operand as they lie (a lane
+// has 8 values of one key), values through the wave's own LDS for the transposing
+// read; the next DEPTH tiles' loads are under way while a tile is worked on. A lane
+// owns one row of the scores, whose layout is the next product's operand (kpos order).
+template <class T, int D, int RT> struct Few {
+    // one workgroup a CU, of as many waves as registers leave room for
+    static constexpr int NW = sizeof(T) == 4 && D == 128 ? 4 : 8, DEPTH = RT == 1 ? 2 : 1, R = 16 * RT;
+    static constexpr size_t tiles = sizeof(T) * NW * 32 * tile_stride<T>(D), join = sizeof(float) * NW * R * (D + 4);
+    static constexpr size_t lds = tiles > join ? tiles : join;
+};
+
+template <class T, int D, int RT>
+__global__ void __launch_bounds__((64 * Few<T, D, RT>::NW), (Few<T, D, RT>::NW / 4)) paged_few_kernel(AttnParams p) {
+    using F = Few<T, D, RT>;
+    constexpr int NW = F::NW, NT = 64 * NW, DEPTH = F::DEPTH, R = F::R, KB = 32;
+    constexpr int ST = tile_stride<T>(D), KD = D / 32, MD = D / 16, JS = D + 4;
+    constexpr int PER = 16 / (int)sizeof(T), CPR = D / PER, NL = 32 * CPR / 64;
+    using V8 = typename Frag<T>::V;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ float s_top[NW][R], s_sum[NW][R];
+    lds_poison((uint32_t)F::lds);
+    const int tid = threadIdx.x, lane = tid % WAVE, w = wave_id(), n = lane & 15, g = lane >> 4;
+    T* const tv = reinterpret_cast<T*>(smem) + (size_t)w * 32 * ST;
+    const float c = p.scale * LOG2E;
+    const size_t rs = (size_t)p.Hkv * D;
+    Work k;
+    const int HW = p.HW, KS = NW / HW, wh = w % HW, wk = w / HW;
+    if (!find_work<R, KB, 2, NT, false>(p, k)) return;
+
+    for (long u = k.u; u < k.end && k.hg < p.groups; k.it0 = 0) {
+        RowBlock b;
+        if (!row_block(p.map, p.G, R, k.v, b)) {   // an empty number of a packed batch
+            if (!p.wgs) return;
+            if (++k.v == p.blocks) {
+                k.v = 0;
+                ++k.hg;
+            }
+            continue;
+        }
+        const int ctx = p.ctx[b.seq], keys = keys_of(p, b, R);
+        const int units = max((keys + KB - 1) / KB, 1), it0 = k.it0;
+        const int it1 = p.wgs ? (int)min((long)units, it0 + (k.end - u)) : units;
+        const bool whole = it0 == 0 && it1 == units;
+        const int rows = min(b.rows - b.r0, R);
+        const int hk = k.hg * HW + wh;
+        const T* const K = static_cast<const T*>(p.Kp) + (size_t)hk * D;
+        const T* const V = static_cast<const T*>(p.Vp) + (size_t)hk * D;
+        // row of the block -> its place in q, o
+        auto q_row = [&](int r, int head) {
+            const int rr = b.r0 + r;
+            return (size_t)(b.t0 + rr / p.G) * p.Hq + head * p.G + rr % p.G;
+        };
+        Seen seen[RT];
+        V8 qf[RT][KD];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            const int r = 16 * t + n;
+            const bool live = r < rows;
+            const int tok = (b.r0 + (live ? r : 0)) / p.G;
+            seen[t] = Seen{p.tree ? p.tree + (size_t)(b.t0 + tok) * p.words : nullptr, p.words, ctx, tok};
+#pragma unroll
+            for (int ks = 0; ks < KD; ++ks)
+                qf[t][ks] = load8<T>(static_cast<const T*>(p.q) + q_row(live ? r : 0, hk) * D + 32 * ks + 8 * g, live);
+        }
+        // row in the cache of key (tile's first + lane), or -1
+        auto lookup = [&](int it) {
+            const int j = it * KB + lane;
+            return it < it1 && lane < 32 && j < keys ? p.pages.row(b.seq, j) : -1;
+        };
+        V8 kf[DEPTH][2][KD];
+        u32x4 rv[DEPTH][NL];
+        auto fetch_k = [&](auto d, int where) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const T* const src = K + (size_t)max(__shfl(where, 16 * x + n, WAVE), 0) * rs + 8 * g;
+#pragma unroll
+                for (int ks = 0; ks < KD; ++ks) kf[d.value][x][ks] = load8<T>(src + 32 * ks, true);
+            }
+        };
+        auto fetch_v = [&](auto d, int where) {
+#pragma unroll
+            for (int m = 0; m < NL; ++m) {
+                const int e = lane + 64 * m;
+                rv[d.value][m] = *reinterpret_cast<const u32x4*>(V + (size_t)max(__shfl(where, e / CPR, WAVE), 0) * rs + e % CPR * PER);
+            }
+        };
+        f32x4 O[RT][MD];
+        float top[RT], sum[RT];   // sum: this lane's quarter of the keys
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            top[t] = -INFINITY;
+            sum[t] = 0.f;
+#pragma unroll
+            for (int m = 0; m < MD; ++m) O[t][m] = zero4();
+        }
+        int where[DEPTH], next[DEPTH];   // rows of the tiles under way, and of those behind them
+        auto each = [](auto f) {
+            f(std::integral_constant<int, 0>());
+            if constexpr (DEPTH > 1) f(std::integral_constant<int, DEPTH - 1>());
+        };
+        each([&](auto d) { where[d.value] = lookup(it0 + wk + d.value * KS); });
+        __syncthreads();   // the last item's join is done with
+        each([&](auto d) {
+            fetch_k(d, where[d.value]);
+            fetch_v(d, where[d.value]);
+        });
+        each([&](auto d) { next[d.value] = lookup(it0 + wk + (DEPTH + d.value) * KS); });
+        auto tile = [&](auto d, int it) {
+            const int j0 = it * KB;
+            const uint32_t held = (uint32_t)__ballot(where[d.value] >= 0);
+            const bool more = it + DEPTH * KS < it1;
+            f32x4 s[RT][2];
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    s[t][x] = zero4();
+#pragma unroll
+                    for (int ks = 0; ks < KD; ++ks) s[t][x] = mma(kf[d.value][x][ks], qf[t][ks], s[t][x]);
+                }
+            if (more) fetch_k(d, next[d.value]);
+#pragma unroll
+            for (int m = 0; m < NL; ++m) {
+                const int e = lane + 64 * m, row = e / CPR;
+                if (held != ~0u && !(held >> row & 1u)) rv[d.value][m] = u32x4{0u, 0u, 0u, 0u};   // not this sequence's
+                *reinterpret_cast<u32x4*>(tv + row * ST + e % CPR * PER) = rv[d.value][m];
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the tile is this wave's own
+            __builtin_amdgcn_wave_barrier();
+            if (more) fetch_v(d, next[d.value]);
+            where[d.value] = next[d.value];
+            next[d.value] = lookup(it + 2 * DEPTH * KS);
+            const bool all = held == ~0u && j0 + 31 <= (p.tree ? ctx - 1 : ctx + b.r0 / p.G);   // every row sees every key
+            bf16pair pb[RT];
+            f32x8 pf[RT];
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                const uint32_t see = all ? ~0u : (seen[t](j0) & held) >> 4 * g;
+                float mt = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        s[t][x][r] = see >> (16 * x + r) & 1u ? s[t][x][r] * c : -INFINITY;
+                        mt = __builtin_elementwise_maximum(mt, s[t][x][r]);
+                    }
+                mt = group_max(mt);
+                const float next_top = fmaxf(top[t], mt);
+                const float base = next_top == -INFINITY ? 0.f : next_top;
+                const float down = fast_exp2(top[t] - base);
+                top[t] = next_top;
+                sum[t] *= down;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        pf[t][4 * x + r] = fast_exp2(s[t][x][r] - base);
+                        sum[t] += pf[t][4 * x + r];
+                    }
+                if constexpr (sizeof(T) == 2) pb[t] = split8(pf[t]);
+#pragma unroll
+                for (int m = 0; m < MD; ++m) O[t][m] *= down;
+            }
+#pragma unroll
+            for (int m = 0; m < MD; ++m) {
+                const V8 vf = frag_tr(tv, ST, 0, 16 * m, g, n);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    if constexpr (sizeof(T) == 2) O[t][m] = mma(vf, pb[t].lo, mma(vf, pb[t].hi, O[t][m]));
+                    else O[t][m] = mma(vf, pf[t], O[t][m]);
+                }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        };
+        for (int i = it0; i < it1; i += DEPTH * KS) {
+            const int it = i + wk;
+            each([&](auto d) {
+                if (it + d.value * KS < it1) tile(d, it + d.value * KS);
+            });
+            // Keeps the waves on the same rows. Without it the oldest ones run ahead and end early.
+            __builtin_amdgcn_s_barrier();
+        }
+        float probe = 0.f;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            sum[t] = group_sum(sum[t]);
+#pragma unroll
+            for (int m = 0; m < MD; ++m) probe += (O[t][m][0] + O[t][m][1]) * 0.f + (O[t][m][2] + O[t][m][3]) * 0.f;
+        }
+        // An Inf or NaN in v at a key that a tile holds but a row does not see has entered
+        // that row as 0 * v. Then o is formed again, one key at a time, from what each row sees.
+        if (__any(probe != 0.f)) {
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                const bool live = 16 * t + n < rows;
+                const T* const q = static_cast<const T*>(p.q) + q_row(live ? 16 * t + n : 0, hk) * D;
+                const float base = top[t] == -INFINITY ? 0.f : top[t];
+#pragma unroll
+                for (int m = 0; m < MD; ++m) O[t][m] = zero4();
+                for (int it = it0 + wk; it < it1; it += KS) {
+                    const int at32 = lookup(it);
+                    for (int j = 0; j < 32; ++j) {
+                        const int at = __shfl(at32, j, WAVE);
+                        const bool in = live && at >= 0 && (seen[t](it * KB) >> j & 1u);
+                        if (!__any(in)) continue;
+                        const T* const kr = K + (size_t)max(at, 0) * rs;
+                        const T* const vr = V + (size_t)max(at, 0) * rs + 4 * g;
+                        float dot = 0.f;
+                        for (int x = 0; x < D; x += 8) {
+                            const f32x8 y = widen(load8<T>(q + x, true)) * widen(load8<T>(kr + x, true));
+                            dot += ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
+                        }
+                        const float e = fast_exp2(dot * c - base);
+                        if (!in) continue;
+#pragma unroll
+                        for (int m = 0; m < MD; ++m)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) O[t][m][r] += e * from_el(vr[16 * m + r]);
+                    }
+                }
+            }
+        }
+        // the waves' shares, joined through LDS in the tiles' place: [wave][row][D]
+        float* const so = reinterpret_cast<float*>(smem);
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            if (g == 0) {
+                s_top[w][16 * t + n] = top[t];
+                s_sum[w][16 * t + n] = sum[t];
+            }
+            if (16 * t + n < rows) {
+#pragma unroll
+                for (int m = 0; m < MD; ++m) *reinterpret_cast<f32x4*>(so + (size_t)(w * R + 16 * t + n) * JS + 16 * m + 4 * g) = O[t][m];
+            }
+        }
+        __syncthreads();
+        for (int x = tid; x < HW * rows * (D / 4); x += NT) {
+            const int d = x % (D / 4) * 4, hr = x / (D / 4), h = hr / rows, r = hr - h * rows;
+            float m = -INFINITY, l = 0.f;
+            for (int y = h; y < NW; y += HW) m = fmaxf(m, s_top[y][r]);
+            const float base = m == -INFINITY ? 0.f : m;
+            f32x4 acc = zero4();
+            for (int y = h; y < NW; y += HW) {
+                const float f = fast_exp2(s_top[y][r] - base);
+                l += f * s_sum[y][r];
+                acc += *reinterpret_cast<const f32x4*>(so + (size_t)(y * R + r) * JS + d) * f;
+            }
+            if (whole) {
+                const size_t at = q_row(r, k.hg * HW + h);
+                store4(static_cast<T*>(p.out) + at * D + d, acc * (l == 0.f ? 0.f : 1.f / l));
+                if (p.lse && d == 0) p.lse[at] = (m + log2f(l)) * LN2;
+            } else {
+                const size_t slot = (((size_t)2 * k.wg + (it0 == 0 ? 1 : 0)) * HW + h) * R + r;
+                *reinterpret_cast<f32x4*>(p.po + slot * D + d) = acc;
+                if (d == 0) {
+                    p.pml[2 * slot] = m;
+                    p.pml[2 * slot + 1] = l;
+                }
+            }
+        }
+        if (p.wgs && it0 == 0 && tid == 0)
+            p.span[k.v * p.groups + k.hg] = make_int2(k.wg, k.owner(u + units - 1));
+        u += it1 - it0;
+        if (++k.v == p.blocks) {
+            k.v = 0;
+            ++k.hg;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- more rows
+
 // Rows' tiles of 32 a workgroup has (RW), and the groups of waves (KS = 4 / RW) that
 // take every KS-th tile of keys each.
 template <class T, int RW> struct Shape {
     static constexpr int KS = 4 / RW, R = 32 * RW, KT = sizeof(T) == 2 && RW == 4 ? 64 : 32, KB = KS * KT;
-    static constexpr int NB = RW == 1 ? 1 : 2;   // buffers: a wave by itself needs no second one
 };
-template <class T, int D, int RW> constexpr size_t attn_lds() {
+template <class T, int D, int RW> constexpr size_t rows_lds() {
     using S = Shape<T, RW>;
-    const size_t tiles = sizeof(T) * S::KS * S::NB * 2 * S::KT * tile_stride<T>(D);
+    const size_t tiles = sizeof(T) * S::KS * 2 * 2 * S::KT * tile_stride<T>(D);
     const size_t join = S::KS > 1 ? sizeof(float) * 4 * 64 * (16 * (D / 32) + 2) : 0;
-    return tiles > join ? tiles : join;
+    return std::max(tiles, join);
 }
 
-template <class T, int D, int RW> __global__ void __launch_bounds__(256) paged_attn_kernel(AttnParams p) {
+template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_lds<T, D, RW>() > 80 * 1024 ? 1 : 2)) paged_rows_kernel(AttnParams p) {
     using S = Shape<T, RW>;
-    constexpr int KS = S::KS, R = S::R, KT = S::KT, KB = S::KB, NB = S::NB, NX = KT / 32, GT = 64 * RW;
+    constexpr int KS = S::KS, R = S::R, KT = S::KT, KB = S::KB, NX = KT / 32, GT = 64 * RW;
     constexpr int ST = tile_stride<T>(D), KD = D / 16, MD = D / 32, PER = 16 / (int)sizeof(T), CPR = D / PER, NL = KT * CPR / GT;
     using V8 = typename Frag<T>::V;
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ int s_units[MAX_BLOCKS], s_first[MAX_BLOCKS + 1];
-    lds_poison((uint32_t)attn_lds<T, D, RW>());
+    lds_poison((uint32_t)rows_lds<T, D, RW>());
     const int tid = threadIdx.x, lane = tid % WAVE, w = wave_id(), n = lane & 31, h2 = lane >> 5;
     const int wr = w % RW, wk = w / RW, gt = tid - wk * GT;
-    T* const tiles = reinterpret_cast<T*>(smem) + (size_t)wk * NB * 2 * KT * ST;   // [buffer][k, v][KT][ST]
-    const float c = fabsf(p.scale) * LOG2E;
+    T* const tiles = reinterpret_cast<T*>(smem) + (size_t)wk * 2 * 2 * KT * ST;   // [buffer][k, v][KT][ST]
+    // the scale's sign goes into q, exactly, and so does a scale of zero: maxima scale as they stand
+    const float c = p.scale == 0.f ? 1.f : fabsf(p.scale) * LOG2E;
     const size_t rs = (size_t)p.Hkv * D;
+    const bool chunks = p.pages.page % (GT / CPR) == 0;
 
-    // this workgroup's units (KB keys of one item): [u, end)
-    int v = 0, hk = 0, it0 = 0;
-    long u = 0, end = 0, per = 0;
-    if (p.wgs) {
-        int sum = 0;   // of this thread's blocks: MAX_BLOCKS / 256 neighbours
-        constexpr int B = MAX_BLOCKS / 256;
-        int mine[B];
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-            const int b = tid * B + i;
-            RowBlock rb;
-            mine[i] = 0;
-            if (b < p.blocks && row_block(p.map, p.G, R, b, rb)) mine[i] = max((keys_of(p, rb, R) + KB - 1) / KB, 1);
-            sum += mine[i];
-        }
-        int before = sum;
-#pragma unroll
-        for (int o = 1; o < WAVE; o *= 2) {
-            const int y = __shfl_up(before, o, WAVE);
-            if (lane >= o) before += y;
-        }
-        __shared__ int s_wave[4];
-        if (lane == 63) s_wave[w] = before;
-        __syncthreads();
-        before -= sum;
-        for (int i = 0; i < w; ++i) before += s_wave[i];
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-            s_units[tid * B + i] = mine[i];
-            s_first[tid * B + i] = before;
-            before += mine[i];
-        }
-        if (tid == 255) s_first[MAX_BLOCKS] = before;
-        __syncthreads();
-        const long total = (long)s_first[MAX_BLOCKS] * p.Hkv;
-        per = (total + p.wgs - 1) / p.wgs;
-        u = per * blockIdx.x;
-        end = min(u + per, total);
-        if (u >= end) return;
-        int lo = 0, hi = p.blocks - 1;   // the block that holds unit u
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if ((long)s_first[mid] * p.Hkv <= u) lo = mid; else hi = mid - 1;
-        }
-        // (of blocks with the same first unit the search ends at the last, the one that is not empty)
-        v = __builtin_amdgcn_readfirstlane(lo);
-        const int rem = (int)(u - (long)s_first[v] * p.Hkv), un = s_units[v];
-        hk = __builtin_amdgcn_readfirstlane(rem / un);
-        it0 = __builtin_amdgcn_readfirstlane(rem % un);
-    } else {
-        v = blockIdx.x / p.Hkv;
-        hk = blockIdx.x % p.Hkv;
-        u = 0;
-        end = 1;
-    }
+    Work k;
+    if (!find_work<R, KB, 1, 256, true>(p, k)) return;
+    long u = k.u;
+    const long end = k.end;
+    int v = k.v, hk = k.hg, it0 = k.it0;
 
-    for (; u < end && v < p.blocks; it0 = 0) {
+    for (; u < end && hk < p.Hkv; it0 = 0) {
         RowBlock b;
         if (!row_block(p.map, p.G, R, v, b)) {   // an empty number of a packed batch
             if (!p.wgs) return;
-            ++v;
+            if (++v == p.blocks) {
+                v = 0;
+                ++hk;
+            }
             continue;
         }
         const int ctx = p.ctx[b.seq], keys = keys_of(p, b, R);
         const int units = max((keys + KB - 1) / KB, 1);
         const int it1 = p.wgs ? (int)min((long)units, it0 + (end - u)) : units;
         const bool whole = it0 == 0 && it1 == units;
-        const int rr = b.r0 + 32 * wr + n;
-        const bool live = rr < b.rows;
-        const int tok = (live ? rr : 0) / p.G, head = hk * p.G + (live ? rr : 0) % p.G;
-        const size_t q_at = ((size_t)(b.t0 + tok) * p.Hq + head) * D;
+        // this lane's row; formed where it is needed, so that no register holds it over the loop
+        struct Row {
+            bool live;
+            int tok;
+            size_t at;   // its place in q, o
+        };
+        auto row_of = [&](int n) {
+            const int rr = b.r0 + 32 * wr + n;
+            const bool live = rr < b.rows;
+            const int tok = (live ? rr : 0) / p.G, head = hk * p.G + (live ? rr : 0) % p.G;
+            return Row{live, tok, (size_t)(b.t0 + tok) * p.Hq + head};
+        };
 
         V8 qf[KD];
+        {
+            const Row row = row_of(n);
 #pragma unroll
-        for (int ks = 0; ks < KD; ++ks) {
-            qf[ks] = load8<T>(static_cast<const T*>(p.q) + q_at + 8 * h2 + 16 * ks, live);
-            if (p.scale < 0.f) qf[ks] = -qf[ks];   // exact, so that maxima scale as they stand
+            for (int ks = 0; ks < KD; ++ks) {
+                qf[ks] = load8<T>(static_cast<const T*>(p.q) + row.at * D + 8 * h2 + 16 * ks, row.live);
+                if (p.scale <= 0.f) qf[ks] = p.scale < 0.f ? -qf[ks] : narrow<T>(widen(qf[ks]) * 0.f);
+            }
         }
         const T* const K = static_cast<const T*>(p.Kp) + (size_t)hk * D;
         const T* const V = static_cast<const T*>(p.Vp) + (size_t)hk * D;
-        const int32_t* const bits = p.tree ? p.tree + (size_t)(b.t0 + tok) * p.words : nullptr;
 
         // the row in the cache of key (tile's first + lane), or -1
         auto lookup = [&](int it) {
@@ -326,19 +669,33 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256) paged_a
             return lane < KT && j < keys ? p.pages.row(b.seq, j) : -1;
         };
         u32x4 rk[NL], rv[NL];
+        // Pages of whole chunks (the rows that one load of the group's threads covers) have one
+        // address a chunk, the same in every lane; others an address for each row.
         auto fetch = [&](int where) {
+            const int here_gt = here(gt);
+            if (chunks) {
+                const uint32_t off = (uint32_t)(here_gt / CPR) * (uint32_t)rs + (uint32_t)(here_gt % CPR * PER);
+#pragma unroll
+                for (int m = 0; m < NL; ++m) {
+                    const size_t at = (size_t)max(__builtin_amdgcn_readlane(where, m * (GT / CPR)), 0) * rs;
+                    rk[m] = *reinterpret_cast<const u32x4*>(K + at + off);
+                    rv[m] = *reinterpret_cast<const u32x4*>(V + at + off);
+                }
+                return;
+            }
 #pragma unroll
             for (int m = 0; m < NL; ++m) {
-                const int e = gt + m * GT, at = max(__shfl(where, e / CPR, WAVE), 0);
+                const int e = here_gt + m * GT, at = max(__shfl(where, e / CPR, WAVE), 0);
                 const size_t o = (size_t)at * rs + e % CPR * PER;
                 rk[m] = *reinterpret_cast<const u32x4*>(K + o);
                 rv[m] = *reinterpret_cast<const u32x4*>(V + o);
             }
         };
         auto put = [&](T* t, uint64_t held, bool full) {
+            const int here_gt = here(gt);
 #pragma unroll
             for (int m = 0; m < NL; ++m) {
-                const int e = gt + m * GT, row = e / CPR, at = row * ST + e % CPR * PER;
+                const int e = here_gt + m * GT, row = e / CPR, at = row * ST + e % CPR * PER;
                 if (!full && !(held >> row & 1)) {   // what lies there is not this sequence's
                     rk[m] = u32x4{0u, 0u, 0u, 0u};
                     rv[m] = u32x4{0u, 0u, 0u, 0u};
@@ -347,19 +704,8 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256) paged_a
                 *reinterpret_cast<u32x4*>(t + KT * ST + at) = rv[m];
             }
         };
-        // which of the 32 keys from j0 on this lane's row sees
-        auto visible = [&](int j0) -> uint32_t {
-            const int d = j0 - ctx;   // among the new tokens
-            if (bits == nullptr) {
-                const int m = min(max(tok - d + 1, 0), 32);
-                return m == 32 ? ~0u : (1u << m) - 1u;
-            }
-            if (d <= -32) return ~0u;
-            if (d < 0) return ((1u << -d) - 1u) | (uint32_t)bits[0] << -d;
-            const int at = d >> 5, sh = d & 31;
-            const uint32_t x = at < p.words ? (uint32_t)bits[at] : 0u;
-            const uint32_t y = sh && at + 1 < p.words ? (uint32_t)bits[at + 1] << (32 - sh) : 0u;
-            return x >> sh | y;
+        auto seen_by = [&](int tok) {
+            return Seen{p.tree ? p.tree + (size_t)(b.t0 + tok) * p.words : nullptr, p.words, ctx, tok};
         };
 
         f32x16 O[MD];
@@ -367,27 +713,43 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256) paged_a
         for (int m = 0; m < MD; ++m) O[m] = zero16();
         float top = -INFINITY, sum = 0.f;   // sum: this lane's half of the keys
 
-        auto tile = [&](const T* tk, const T* tv, int j0, uint64_t held, auto masked) {
+        auto tile = [&](const T* tk, const T* tv, int j0, uint64_t held, bool masked) {
+            const int lane = here(tid % WAVE), n = lane & 31, h2 = lane >> 5;
             f32x16 s[NX];
+            V8 vf[MD];
 #pragma unroll
-            for (int x = 0; x < NX; ++x) {
-                s[x] = zero16();
+            for (int x = 0; x < NX; ++x) s[x] = zero16();
+            constexpr int HD = KD > 4 ? KD / 2 : KD;   // operands of half the head at a time: registers
 #pragma unroll
-                for (int ks = 0; ks < KD; ++ks) s[x] = mma32(nat32<T>(tk, ST, 32 * x, 16 * ks, n, h2), qf[ks], s[x]);
+            for (int k0 = 0; k0 < KD; k0 += HD) {
+                V8 kf[NX][HD];
+#pragma unroll
+                for (int ks = 0; ks < HD; ++ks)
+#pragma unroll
+                    for (int x = 0; x < NX; ++x) kf[x][ks] = nat32<T>(tk, ST, 32 * x, 16 * (k0 + ks), n, h2);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int ks = 0; ks < HD; ++ks)
+#pragma unroll
+                    for (int x = 0; x < NX; ++x) s[x] = mma32(kf[x][ks], qf[k0 + ks], s[x]);
+                if (k0 + HD < KD) __builtin_amdgcn_sched_barrier(0);
             }
-            if constexpr (masked.value) {
+#pragma unroll
+            for (int m = 0; m < MD; ++m) vf[m] = tr32(tv, ST, 0, 32 * m, lane);
+            __builtin_amdgcn_sched_barrier(0);
+            if (masked) {
+                const Seen visible = seen_by(row_of(n).tok);
 #pragma unroll
                 for (int x = 0; x < NX; ++x) {
                     const uint32_t see = (visible(j0 + 32 * x) & (uint32_t)(held >> 32 * x)) >> 4 * h2;
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) s[x][r] = see >> result_row(r, 0) & 1u ? s[x][r] * c : -INFINITY;
+                    for (int r = 0; r < 16; ++r) s[x][r] = see >> result_row(r, 0) & 1u ? s[x][r] : -INFINITY;
                 }
             }
-            const float f = masked.value ? 1.f : c;   // what is left to scale
             float mt = tree_max(s[0]);
 #pragma unroll
             for (int x = 1; x < NX; ++x) mt = __builtin_elementwise_maximum(mt, tree_max(s[x]));
-            mt = swap_max(mt * f);
+            mt = swap_max(mt * c);
             // the subtracted maximum may lag behind by 2^8: most tiles leave o as it is
             if (__any(mt > top + 8.f || (top == -INFINITY && mt > top))) {
                 const float next = fmaxf(top, mt);
@@ -405,16 +767,26 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256) paged_a
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    s[x][r] = fast_exp2(fmaf(s[x][r], f, -base));
+                    s[x][r] = fast_exp2(fmaf(s[x][r], c, -base));
                     part[r & 3] += s[x][r];
                 }
                 sum += (part[0] + part[1]) + (part[2] + part[3]);
             }
 #pragma unroll
             for (int kb = 0; kb < KT / 16; ++kb) {
-                const V8 pf = rows16<T>(s[kb / 2], kb % 2);
+                V8 next[MD];
+                if (kb + 1 < KT / 16) {
 #pragma unroll
-                for (int m = 0; m < MD; ++m) O[m] = mma32(tr32(tv, ST, 16 * kb, 32 * m, lane), pf, O[m]);
+                    for (int m = 0; m < MD; ++m) next[m] = tr32(tv, ST, 16 * (kb + 1), 32 * m, lane);
+                }
+                const V8 pf = rows16<T>(s[kb / 2], kb % 2);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int m = 0; m < MD; ++m) O[m] = mma32(vf[m], pf, O[m]);
+                if (kb + 1 < KT / 16) {
+#pragma unroll
+                    for (int m = 0; m < MD; ++m) vf[m] = next[m];
+                }
             }
         };
 
@@ -425,14 +797,9 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256) paged_a
         fetch(where);
         int where_next = it0 + 1 < it1 ? lookup(it0 + 1) : -1;
         for (int it = it0; it < it1; ++it) {
-            T* const t = tiles + (size_t)(NB == 2 ? (it & 1) : 0) * 2 * KT * ST;
+            T* const t = tiles + (size_t)(it & 1) * 2 * KT * ST;
             put(t, held, held == ALL);
-            if constexpr (RW == 1) {   // the tile is this wave's own: its reads and writes are in order
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                __builtin_amdgcn_wave_barrier();
-            } else {
-                __syncthreads();
-            }
+            __syncthreads();
             const uint64_t now = held;
             if (it + 1 < it1) {
                 held = __ballot(where_next >= 0);
@@ -441,13 +808,8 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256) paged_a
             }
             const int j0 = (it * KS + wk) * KT;
             if (now) {
-                const int last_seen = bits ? ctx - 1 : ctx + (b.r0 + 32 * wr) / p.G;   // by every row of this wave
-                if (now == ALL && j0 + KT - 1 <= last_seen) tile(t, t + KT * ST, j0, now, std::false_type());
-                else tile(t, t + KT * ST, j0, now, std::true_type());
-            }
-            if constexpr (RW == 1) {
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                __builtin_amdgcn_wave_barrier();
+                const int last_seen = p.tree ? ctx - 1 : ctx + (b.r0 + 32 * wr) / p.G;   // by every row of this wave
+                tile(t, t + KT * ST, j0, now, now != ALL || j0 + KT - 1 > last_seen);
             }
         }
         sum = swap_sum(sum);
@@ -459,7 +821,9 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256) paged_a
         for (int m = 0; m < MD; ++m)
 #pragma unroll
             for (int r = 0; r < 16; ++r) probe += O[m][r] * 0.f;
-        if (__any(live && probe != 0.f)) {
+        const Row row = row_of(here(n));
+        if (__any(row.live && probe != 0.f)) {
+            const Seen visible = seen_by(row.tok);
             const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
             for (int m = 0; m < MD; ++m) O[m] = zero16();
@@ -467,13 +831,13 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256) paged_a
                 const int rows = lookup(it), j0 = (it * KS + wk) * KT;
                 for (int j = 0; j < KT; ++j) {
                     const int at = __shfl(rows, j, WAVE);
-                    const bool in = live && at >= 0 && (visible(j0 + (j & 32)) >> (j & 31) & 1u);
+                    const bool in = row.live && at >= 0 && (visible(j0 + (j & 32)) >> (j & 31) & 1u);
                     if (!__any(in)) continue;
                     const T* const kr = K + (size_t)max(at, 0) * rs;
                     const T* const vr = V + (size_t)max(at, 0) * rs;
                     float dot = 0.f;
                     for (int x = 0; x < D; x += 8) {
-                        const f32x8 y = widen(load8<T>(static_cast<const T*>(p.q) + q_at + x, true)) * widen(load8<T>(kr + x, true));
+                        const f32x8 y = widen(load8<T>(static_cast<const T*>(p.q) + row.at * D + x, true)) * widen(load8<T>(kr + x, true));
                         dot += ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
                     }
                     const float e = fast_exp2(dot * (p.scale * LOG2E) - base);
@@ -512,15 +876,15 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256) paged_a
                 }
             }
         }
-        if (wk == 0 && live) {
+        if (wk == 0 && row.live) {
             if (whole) {
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                T* out = static_cast<T*>(p.out) + q_at;
+                T* out = static_cast<T*>(p.out) + row.at * D;
 #pragma unroll
                 for (int m = 0; m < MD; ++m) store_tile<T>(out + 32 * m, O[m], inv, h2);
-                if (p.lse && h2 == 0) p.lse[(size_t)(b.t0 + tok) * p.Hq + head] = (top + log2f(sum)) * LN2;
+                if (p.lse && h2 == 0) p.lse[row.at] = (top + log2f(sum)) * LN2;
             } else {
-                const size_t slot = ((size_t)2 * blockIdx.x + (it0 == 0 ? 1 : 0)) * R + 32 * wr + n;
+                const size_t slot = ((size_t)2 * k.wg + (it0 == 0 ? 1 : 0)) * R + 32 * wr + n;
                 float* po = p.po + slot * D + 4 * h2;
 #pragma unroll
                 for (int m = 0; m < MD; ++m)
@@ -534,114 +898,162 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256) paged_a
             }
         }
         if (p.wgs && it0 == 0 && tid == 0)
-            p.span[v * p.Hkv + hk] = make_int2((int)blockIdx.x, (int)((u + units - 1) / per));
+            p.span[v * p.Hkv + hk] = make_int2(k.wg, k.owner(u + units - 1));
         u += it1 - it0;
-        if (++hk == p.Hkv || !p.wgs) {
-            hk = 0;
-            ++v;
+        if (++v == p.blocks) {
+            v = 0;
+            ++hk;
         }
     }
 }
 
-// Joins the parts of one row: four values a thread, the parts spread over the rest of
-// the workgroup.
-template <class T, int D, int RW> __global__ void __launch_bounds__(256) paged_join_kernel(AttnParams p) {
+// Joins the parts of a shared item's rows, four values a thread, in J workgroups: as many
+// rows at a time as a workgroup has room for, or (SPREAD) one row at a time with its parts
+// spread over the workgroup, for few rows in many parts.
+template <class T, int D, int R, bool SPREAD> __global__ void __launch_bounds__(256) paged_join_kernel(AttnParams p, int J) {
     lds_poison(0);
-    constexpr int R = Shape<T, RW>::R, CG = D / 4, RG = 256 / CG;
-    __shared__ float s_l[RG];
-    __shared__ __align__(16) float s_o[RG][D];
-    const int item = blockIdx.x / R, row = blockIdx.x % R, v = item / p.Hkv, hk = item % p.Hkv;
+    constexpr int CG = D / 4, RG = 256 / CG;
+    const int at_head = blockIdx.x / J, j = blockIdx.x % J, v = at_head / p.Hkv, hk = at_head % p.Hkv, wh = hk % p.HW;
     RowBlock b;
-    if (!row_block(p.map, p.G, R, v, b) || b.r0 + row >= b.rows) return;
-    const int2 span = p.span[item];
-    if (span.x == span.y) return;
-    const int parts = span.y - span.x + 1;
-    auto slot = [&](int y) { return ((size_t)2 * (span.x + y) + (y == 0 ? 1 : 0)) * R + row; };
-    const int cg = threadIdx.x % CG, rg = threadIdx.x / CG;
-    float m = -INFINITY;
-    for (int y = 0; y < parts; ++y) m = fmaxf(m, p.pml[2 * slot(y)]);
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    f32x4 acc = zero4();
-    for (int y = rg; y < parts; y += RG) {
-        const float f = fast_exp2(p.pml[2 * slot(y)] - base);
-        l += f * p.pml[2 * slot(y) + 1];
-        acc += *reinterpret_cast<const f32x4*>(p.po + slot(y) * D + 4 * cg) * f;
+    if (!row_block(p.map, p.G, R, v, b)) return;
+    const int2 span = p.span[v * p.groups + hk / p.HW];
+    const int parts = span.y - span.x + 1, tid = threadIdx.x, cg = tid % CG, rg = tid / CG, rows = min(b.rows - b.r0, R);
+    if (parts == 1) return;
+    auto finish = [&](int row, float m, float l, const f32x4& acc) {
+        const int rr = b.r0 + row;
+        const size_t at = (size_t)(b.t0 + rr / p.G) * p.Hq + hk * p.G + rr % p.G;
+        store4(static_cast<T*>(p.out) + at * D + 4 * cg, acc * (l == 0.f ? 0.f : 1.f / l));
+        if (p.lse && cg == 0) p.lse[at] = (m + log2f(l)) * LN2;
+    };
+    auto slot = [&](int y, int row) { return (((size_t)2 * (span.x + y) + (y == 0 ? 1 : 0)) * p.HW + wh) * R + row; };
+    // a row's parts y0, y0 + step, ..
+    auto collect = [&](int row, int y0, int step, float base, float& l, f32x4& acc) {
+        l = 0.f;
+        acc = zero4();
+#pragma unroll 8
+        for (int y = y0; y < parts; y += step) {
+            const float2 ml = *reinterpret_cast<const float2*>(p.pml + 2 * slot(y, row));
+            const f32x4 o = *reinterpret_cast<const f32x4*>(p.po + slot(y, row) * D + 4 * cg);
+            const float f = fast_exp2(ml.x - base);
+            l += f * ml.y;
+            acc += o * f;
+        }
+    };
+    float l;
+    f32x4 acc;
+    if constexpr (!SPREAD) {
+        for (int row = j * RG + rg; row < rows; row += J * RG) {
+            float m = -INFINITY;
+#pragma unroll 8
+            for (int y = 0; y < parts; ++y) m = fmaxf(m, p.pml[2 * slot(y, row)]);
+            collect(row, 0, 1, m == -INFINITY ? 0.f : m, l, acc);
+            finish(row, m, l, acc);
+        }
+        return;
     }
-    if (cg == 0) s_l[rg] = l;
-    *reinterpret_cast<f32x4*>(&s_o[rg][4 * cg]) = acc;
-    __syncthreads();
-    if (rg) return;
-    l = 0.f;
-    acc = zero4();
+    __shared__ float s_m[4], s_l[RG];
+    __shared__ __align__(16) float s_o[RG][D];
+    for (int row = j; row < rows; row += J) {
+        float m = -INFINITY;
+        for (int y = tid; y < parts; y += 256) m = fmaxf(m, p.pml[2 * slot(y, row)]);
 #pragma unroll
-    for (int y = 0; y < RG; ++y) {
-        l += s_l[y];
-        acc += *reinterpret_cast<const f32x4*>(&s_o[y][4 * cg]);
+        for (int o = 32; o; o /= 2) m = fmaxf(m, __shfl_xor(m, o, WAVE));
+        __syncthreads();   // the last row's sums are done with
+        if (tid % WAVE == 0) s_m[tid / WAVE] = m;
+        __syncthreads();
+        m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+        collect(row, rg, RG, m == -INFINITY ? 0.f : m, l, acc);
+        if (cg == 0) s_l[rg] = l;
+        *reinterpret_cast<f32x4*>(&s_o[rg][4 * cg]) = acc;
+        __syncthreads();
+        if (rg) continue;
+        l = 0.f;
+        acc = zero4();
+#pragma unroll
+        for (int y = 0; y < RG; ++y) {
+            l += s_l[y];
+            acc += *reinterpret_cast<const f32x4*>(&s_o[y][4 * cg]);
+        }
+        finish(row, m, l, acc);
     }
-    const int rr = b.r0 + row;
-    const size_t at = (size_t)(b.t0 + rr / p.G) * p.Hq + hk * p.G + rr % p.G;
-    store4(static_cast<T*>(p.out) + at * D + 4 * cg, acc * (l == 0.f ? 0.f : 1.f / l));
-    if (p.lse && cg == 0) p.lse[at] = (m + log2f(l)) * LN2;
 }
 
-template <class K, class... P> hipError_t launch(K kern, size_t x, size_t lds, hipStream_t st, const P&... p) {
-    if (x * 256 > 0xffffffffu) return hipErrorInvalidConfiguration;
+template <class K, class... P> hipError_t launch(K kern, size_t x, int threads, size_t lds, hipStream_t st, const P&... p) {
+    if (x * threads > 0xffffffffu) return hipErrorInvalidConfiguration;
     if (lds > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(kern, dim3((unsigned)x), dim3(256), lds, st, p...);
+    hipLaunchKernelGGL(kern, dim3((unsigned)x), dim3(threads), lds, st, p...);
     return hipGetLastError();
 }
 
-// Row tiles of a workgroup: as many as the longest run of rows that a sequence can
-// have fills (a packed batch: its mean).
-int row_waves(int T, int N, int G, bool packed) {
+// Rows of a block: as many as the longest run of rows that a sequence can have
+// fills (a packed batch: its mean).
+int block_rows(int T, int N, int G, bool packed) {
     const long rows = packed ? ((long)T + N - 1) / N * G : (long)T * G;
-    return rows <= 32 ? 1 : rows <= 64 ? 2 : 4;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+}
+// Workgroups that share the keys: what a CU holds at once, times 256.
+int shared_wgs(int R) { return R <= 32 ? 256 : 512; }
+// kv heads that the waves of a workgroup take side by side
+int heads_together(int Hkv, int waves) {
+    int hw = waves;
+    while (Hkv % hw) hw /= 2;
+    return hw;
 }
 
 struct Plan {
-    int RW;
+    int R;
     long blocks;
     bool shared;
 };
 Plan make_plan(int T, int N, int Hkv, int G, bool packed) {
     Plan pl;
-    pl.RW = row_waves(T, N, G, packed);
-    pl.blocks = row_blocks_bound(T, N, G, 32 * pl.RW, packed);
+    pl.R = block_rows(T, N, G, packed);
+    pl.blocks = row_blocks_bound(T, N, G, pl.R, packed);
     pl.shared = pl.blocks <= MAX_BLOCKS && pl.blocks * Hkv < 2048;
     return pl;
 }
 
-template <class T, int D, int RW> hipError_t attend(const PagedArgs& a, const Plan& pl) {
+template <class T, int D, int R> hipError_t attend(const PagedArgs& a, const Plan& pl) {
     AttnParams p{};
     p.q = a.q; p.Kp = a.Kp; p.Vp = a.Vp; p.ctx = a.ctx; p.tree = a.tree; p.out = a.out; p.lse = a.lse;
     p.pages = make_pages(a);
     p.map = SeqMap{a.cu_seqlens, a.T, a.N};
     p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = a.Hq / a.Hkv; p.words = a.words;
+    p.HW = 1;
+    if constexpr (R <= 32) p.HW = heads_together(a.Hkv, Few<T, D, R / 16>::NW);
+    p.groups = a.Hkv / p.HW;
     p.capacity = std::min((long)a.width * a.page_size, 0x7ffff000L);
     p.scale = a.scale;
     p.blocks = (int)pl.blocks;
-    const size_t items = (size_t)pl.blocks * a.Hkv;
+    const size_t items = (size_t)pl.blocks * p.groups;
     if (pl.shared) {
-        p.wgs = WGS;
+        p.wgs = shared_wgs(R);
         char* ws = static_cast<char*>(a.workspace);
         p.span = reinterpret_cast<int2*>(ws);
         ws += al256(items * 8);
         p.pml = reinterpret_cast<float*>(ws);
-        ws += al256((size_t)2 * WGS * 32 * RW * 8);
+        ws += al256((size_t)2 * p.wgs * p.HW * R * 8);
         p.po = reinterpret_cast<float*>(ws);
     }
-    const hipError_t e = launch(paged_attn_kernel<T, D, RW>, pl.shared ? WGS : items, attn_lds<T, D, RW>(), a.stream, p);
+    const size_t wgs = pl.shared ? p.wgs : items;
+    hipError_t e;
+    if constexpr (R <= 32) e = launch(paged_few_kernel<T, D, R / 16>, wgs, 64 * Few<T, D, R / 16>::NW, Few<T, D, R / 16>::lds, a.stream, p);
+    else e = launch(paged_rows_kernel<T, D, R / 32>, wgs, 256, rows_lds<T, D, R / 32>(), a.stream, p);
     if (e != hipSuccess || !pl.shared) return e;
-    return launch(paged_join_kernel<T, D, RW>, items * 32 * RW, 0, a.stream, p);
+    const size_t heads = (size_t)pl.blocks * a.Hkv;
+    const int rows = a.cu_seqlens ? R : std::min(R, a.T * p.G), room = 1024 / D;   // rows that a block can have
+    if (heads * rows <= 1024) return launch(paged_join_kernel<T, D, R, true>, heads * rows, 256, 0, a.stream, p, rows);
+    const int J = (rows + room - 1) / room;
+    return launch(paged_join_kernel<T, D, R, false>, heads * J, 256, 0, a.stream, p, J);
 }
 
 template <class T, int D> hipError_t attend(const PagedArgs& a) {
     const Plan pl = make_plan(a.T, a.N, a.Hkv, a.Hq / a.Hkv, a.cu_seqlens != nullptr);
-    return pl.RW == 1 ? attend<T, D, 1>(a, pl) : pl.RW == 2 ? attend<T, D, 2>(a, pl) : attend<T, D, 4>(a, pl);
+    return pl.R == 16 ? attend<T, D, 16>(a, pl) : pl.R == 32 ? attend<T, D, 32>(a, pl)
+         : pl.R == 64 ? attend<T, D, 64>(a, pl) : attend<T, D, 128>(a, pl);
 }
 
 template <class T, int D> hipError_t append(const PagedArgs& a) {
@@ -652,7 +1064,7 @@ template <class T, int D> hipError_t append(const PagedArgs& a) {
     p.map = SeqMap{a.cu_seqlens, a.T, a.N};
     p.rows = a.cu_seqlens ? a.T : a.N * a.T;
     p.Hq = a.Hq; p.Hkv = a.Hkv; p.rot = a.rot_dim;
-    return launch(paged_append_kernel<T, D>, (size_t)(p.rows + 3) / 4, 0, a.stream, p, a.neighbours);
+    return launch(paged_append_kernel<T, D>, (size_t)(p.rows + 3) / 4, 256, 0, a.stream, p, a.neighbours);
 }
 
 #define KDA_PAGED_DIM(d, D, ...)                                       \
@@ -668,13 +1080,13 @@ template <class T, int D> hipError_t append(const PagedArgs& a) {
 
 bool paged_attn_fits(int T, int N, int Hq, int Hkv, bool packed) {
     const Plan pl = make_plan(T, N, Hkv, Hq / Hkv, packed);
-    return pl.shared ? pl.blocks * Hkv * 32 * pl.RW < (1 << 24) : pl.blocks * Hkv < (1 << 24);
+    return pl.shared ? pl.blocks * Hkv * pl.R < (1 << 24) : pl.blocks * Hkv < (1 << 24);
 }
 
 size_t paged_attn_workspace_bytes(int T, int N, int Hq, int Hkv, int d, bool packed) {
     const Plan pl = make_plan(T, N, Hkv, Hq / Hkv, packed);
     if (!pl.shared) return 256;
-    const size_t slots = (size_t)2 * WGS * 32 * pl.RW;
+    const size_t slots = (size_t)2 * shared_wgs(pl.R) * pl.R * (pl.R <= 32 ? heads_together(Hkv, 8) : 1);
     return al256((size_t)pl.blocks * Hkv * 8) + al256(slots * 8) + slots * d * 4 + 256;
 }
 
