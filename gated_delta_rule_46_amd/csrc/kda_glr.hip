@@ -2,15 +2,20 @@
 //
 // A stretch of tokens acts on the state that enters it as h -> P h + E, with P
 // the product of its decays and E its end state from nothing, and two stretches
-// compose to another, so that blocks of tokens are taken in parallel: (1) every
-// block's P and E, (2) the state that enters each block, one after the other,
-// (3) every block again from that state. The gradient has the same form
-// backwards: with g the adjoint that enters a token from behind,
+// compose to another, so that blocks of tokens are taken in parallel.
+//
+// Forward: one pass. A block's workgroup keeps its values in registers, leaves the
+// block's P and E for the blocks behind, takes up those that the blocks before have
+// left, and finishes. Gradient: backwards, with g the adjoint that enters a token
+// from behind,
 //   lam_t = dh_t + g,  dx_t = lam_t,  da_t = lam_t h_{t-1},  g <- a_t lam_t,
-// and a block takes g to P g + F. h_{t-1} is formed again from a and x in fp32.
+// a block takes g to P g + F; one kernel forms every block's P, E and F, another goes
+// through every block again from what enters it, which its workgroup forms from the
+// other blocks (a long sequence: a kernel of its own, for all blocks). h_{t-1} is formed
+// again from a and x in fp32.
 //
 // In a block, a thread owns V channels and R consecutive tokens (a slot); slots
-// are joined through LDS in the same way.
+// are joined through LDS in the same way, one channel a thread.
 #include <algorithm>
 #include <type_traits>
 
@@ -21,17 +26,21 @@ namespace kda {
 
 namespace {
 
-constexpr int TILE = 64;    // channels of a workgroup: 128 bytes of a bf16 row
 constexpr int NT = 256;     // threads of a workgroup
+constexpr int WALK = 64;    // gradient: blocks of a sequence whose workgroups form what enters them
+constexpr int GROUP = 16;   // forward: blocks that follow each other by P and E, the last one by its state
 
 struct GlrParams {
     const void *gate, *x, *dh;
     const float *h0, *dhT;
     void *h, *dgate, *dx;
     float *hT, *dh0;
-    float* sum;             // [block][P, E, F or P, E][C]; E and F become what enters the block
+    float* sum;             // gradient: [block][P, E, F][C]; E and F become what enters the block
+    uint64_t *words, *counter;   // forward: [block][C] what a block has left, and the blocks begun; all ones before
     SeqMap map;
     int C, tiles;
+    bool chained;           // sum holds what enters each block
+    bool alone;             // no sequence has more than one block, and sum and words are not there
 };
 
 // V elements of a row as they lie in memory
@@ -83,9 +92,10 @@ template <> struct Raw<float, 1> {
     }
 };
 
-// How a workgroup's threads lie over a block of ROWS tokens and TILE channels.
+// How a workgroup's threads lie over a block of ROWS tokens and TILE channels (256 bytes of
+// a row where rows are read 16 bytes a lane).
 template <int V, int R> struct Lay {
-    static constexpr int CL = TILE / V, SLOTS = NT / CL, ROWS = SLOTS * R;
+    static constexpr int CL = V == 1 ? 64 : 16, TILE = CL * V, SLOTS = NT / CL, ROWS = SLOTS * R;
 };
 
 // A block of an array [tokens, C]: rows of a descriptor that ends behind its
@@ -103,85 +113,161 @@ template <class T> struct Rows {
     __device__ __forceinline__ uint32_t operator[](int r) const { return off + r * step; }
 };
 
-// ---------------------------------------------------------------- blocks' P, E and F
+// ---------------------------------------------------------------- a block
 
-template <class TG, class TX, int V, int R, bool GRAD> __global__ void __launch_bounds__(NT) glr_sum_kernel(GlrParams p) {
+// A thread's slot of a block: its values, what the slot does to h and g, and the joint of
+// the workgroup's slots.
+template <class TG, class TX, int V, int R, bool GRAD> struct Block {
     using L = Lay<V, R>;
-    lds_poison(0);
-    __shared__ float sP[L::SLOTS][TILE], sE[L::SLOTS][TILE], sF[GRAD ? L::SLOTS : 1][TILE];
-    const int v = blockIdx.x / p.tiles, c0 = blockIdx.x % p.tiles * TILE, tid = threadIdx.x;
-    SeqBlock b;
-    if (!seq_block(p.map, L::ROWS, v, b)) return;
-    const int cl = tid % L::CL * V, slot = tid / L::CL, row = slot * R, c = c0 + cl;
-    const bool live = c < p.C;
-    const int n = min(b.n - row, R);   // this slot's tokens (or less than none)
-    const Rows<TG> ga(p.gate, b.t0, b.n, p.C, row, c, live);
-    const Rows<TX> gx(p.x, b.t0, b.n, p.C, row, c, live), gd(p.dh, b.t0, b.n, p.C, row, c, live);
+    static constexpr int TILE = L::TILE, SLOTS = L::SLOTS, K = GRAD ? 3 : 2;
+    struct Shared {
+        float P[SLOTS][TILE], E[SLOTS][TILE], F[GRAD ? SLOTS : 1][TILE];
+    };
     Raw<TG, V> a[R];
     Raw<TX, V> x[R], d[GRAD ? R : 1];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        a[r].load(ga.rs, ga[r]);
-        x[r].load(gx.rs, gx[r]);
-        if constexpr (GRAD) d[r].load(gd.rs, gd[r]);
+    int cl, slot, c, n;   // first channel in the tile and of all, this slot's tokens (or less than none)
+    long t0;
+    int rows;
+    bool live;
+
+    __device__ __forceinline__ void at(const GlrParams& p, long first, int tokens, int c0) {
+        // (said to be the same in every lane: descriptors stay in scalar registers)
+        t0 = ((long)__builtin_amdgcn_readfirstlane((int)(first >> 32)) << 32) | (uint32_t)__builtin_amdgcn_readfirstlane((int)first);
+        rows = __builtin_amdgcn_readfirstlane(tokens);
+        cl = threadIdx.x % L::CL * V;
+        slot = threadIdx.x / L::CL;
+        c = c0 + cl;
+        live = c < p.C;
+        n = min(rows - slot * R, R);
     }
-    float P[V], E[V], F[V];
+    template <class T> __device__ __forceinline__ Rows<T> of(const GlrParams& p, const void* base) const {
+        return Rows<T>(base, t0, rows, p.C, slot * R, c, live);
+    }
+    __device__ __forceinline__ void load(const GlrParams& p) {
+        const Rows<TG> ga = of<TG>(p, p.gate);
+        const Rows<TX> gx = of<TX>(p, p.x);
 #pragma unroll
-    for (int i = 0; i < V; ++i) P[i] = 1.f, E[i] = 0.f, F[i] = 0.f;
+        for (int r = 0; r < R; ++r) {
+            a[r].load(ga.rs, ga[r]);
+            x[r].load(gx.rs, gx[r]);
+        }
+        if constexpr (GRAD) {
+            const Rows<TX> gd = of<TX>(p, p.dh);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        if (r < n) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                E[i] = fmaf(a[r][i], E[i], x[r][i]);
-                P[i] *= a[r][i];
-            }
+            for (int r = 0; r < R; ++r) d[r].load(gd.rs, gd[r]);
         }
     }
-    if constexpr (GRAD) {
+    // the slot's P, E and F
+    __device__ __forceinline__ void put(Shared& s) const {
+        float P[V], E[V], F[V];
 #pragma unroll
-        for (int r = R - 1; r >= 0; --r) {
+        for (int i = 0; i < V; ++i) P[i] = 1.f, E[i] = 0.f, F[i] = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
             if (r < n) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) F[i] = a[r][i] * (d[r][i] + F[i]);
+                for (int i = 0; i < V; ++i) {
+                    E[i] = fmaf(a[r][i], E[i], x[r][i]);
+                    P[i] *= a[r][i];
+                }
             }
         }
-    }
+        if constexpr (GRAD) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        sP[slot][cl + i] = P[i];
-        sE[slot][cl + i] = E[i];
-        if constexpr (GRAD) sF[slot][cl + i] = F[i];
+            for (int r = R - 1; r >= 0; --r) {
+                if (r < n) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) F[i] = a[r][i] * (d[r][i] + F[i]);
+                }
+            }
+        }
+        keep(s.P[slot], P);
+        keep(s.E[slot], E);
+        if constexpr (GRAD) keep(s.F[slot], F);
     }
+    __device__ __forceinline__ void keep(float* to, const float* y) const {
+        if constexpr (V == 1) to[cl] = y[0];
+        else
+#pragma unroll
+            for (int i = 0; i < V; i += 4) *reinterpret_cast<f32x4*>(to + cl + i) = f32x4{y[i], y[i + 1], y[i + 2], y[i + 3]};
+    }
+    __device__ __forceinline__ void take(const float* from, float* y) const {
+        if constexpr (V == 1) y[0] = from[cl];
+        else
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                const f32x4 q = *reinterpret_cast<const f32x4*>(from + cl + i);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) y[i + m] = q[m];
+            }
+    }
+};
+
+// gradient: every block's P, E and F
+template <class TG, class TX, int V, int R> __global__ void __launch_bounds__(NT) glr_sum_kernel(GlrParams p) {
+    using B = Block<TG, TX, V, R, true>;
+    lds_poison(0);
+    __shared__ __align__(16) typename B::Shared s;
+    const int v = blockIdx.x / p.tiles, c0 = blockIdx.x % p.tiles * B::TILE, ch = threadIdx.x % B::TILE;
+    SeqBlock b;
+    if (!seq_block(p.map, B::L::ROWS, v, b)) return;
+    B k;
+    k.at(p, b.t0, b.n, c0);
+    k.load(p);
+    k.put(s);
     __syncthreads();
-    if (tid >= (GRAD ? 2 : 1) * TILE || c0 + tid % TILE >= p.C) return;
-    const int ch = tid % TILE;
-    float* const out = p.sum + (size_t)v * (GRAD ? 3 : 2) * p.C + c0 + ch;
-    if (tid < TILE) {
+    const int part = threadIdx.x / B::TILE;
+    if (part >= 2 || c0 + ch >= p.C) return;
+    float* const out = p.sum + (size_t)v * 3 * p.C + c0 + ch;
+    if (part == 0) {
         float pr = 1.f, e = 0.f;
 #pragma unroll 8
-        for (int s = 0; s < L::SLOTS; ++s) {
-            e = fmaf(sP[s][ch], e, sE[s][ch]);
-            pr *= sP[s][ch];
+        for (int i = 0; i < B::SLOTS; ++i) {
+            e = fmaf(s.P[i][ch], e, s.E[i][ch]);
+            pr *= s.P[i][ch];
         }
         out[0] = pr;
         out[p.C] = e;
     } else {
         float f = 0.f;
 #pragma unroll 8
-        for (int s = L::SLOTS - 1; s >= 0; --s) f = fmaf(sP[s][ch], f, sF[s][ch]);
-        out[2 * p.C] = f;
+        for (int i = B::SLOTS - 1; i >= 0; --i) f = fmaf(s.P[i][ch], f, s.F[i][ch]);
+        out[2 * (size_t)p.C] = f;
     }
 }
 
-// ---------------------------------------------------------------- what enters each block
+// What a run of `count` blocks, each `step` on in p.sum (backwards where negative), does to h
+// (or g): y -> P y + E.
+struct Run { float P, E; };
+__device__ __forceinline__ Run run_of(const float* P, const float* E, long step, int count) {
+    Run r{1.f, 0.f};
+    constexpr int U = 8;
+    for (int b0 = 0; b0 < count; b0 += U) {
+        float pr[U], e[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long o = min(b0 + u, count - 1) * step;
+            pr[u] = P[o];
+            e[u] = E[o];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (b0 + u < count) {
+                r.E = fmaf(pr[u], r.E, e[u]);
+                r.P *= pr[u];
+            }
+        }
+    }
+    return r;
+}
 
-// A wave takes 64 channels of one sequence through its blocks, in the gradient
-// a second wave backwards. The end state and the first adjoint are results.
-template <bool GRAD> __global__ void __launch_bounds__(128) glr_chain_kernel(GlrParams p, int rows) {
+// Gradient of long sequences: what enters each block, in place of its E and F. The first
+// wave takes a channel a lane of one sequence through its blocks, the second backwards.
+__global__ void __launch_bounds__(128) glr_chain_kernel(GlrParams p, int rows) {
     lds_poison(0);
-    const int seq = blockIdx.x / p.tiles, c = blockIdx.x % p.tiles * TILE + threadIdx.x % TILE;
-    const bool back = threadIdx.x >= TILE;
+    const int wide = (p.C + 63) / 64;
+    const int seq = blockIdx.x / wide, c = blockIdx.x % wide * 64 + threadIdx.x % 64;
+    const bool back = threadIdx.x >= 64;
     if (c >= p.C) return;
     int first, len;
     if (p.map.cu) {
@@ -193,8 +279,8 @@ template <bool GRAD> __global__ void __launch_bounds__(128) glr_chain_kernel(Glr
         first = seq * ((len + rows - 1) / rows);
     }
     const int nb = (len + rows - 1) / rows;
-    constexpr int K = GRAD ? 3 : 2, U = 8;
-    const size_t step = (size_t)K * p.C;
+    constexpr int U = 8;
+    const size_t step = (size_t)3 * p.C;
     float* const sum = p.sum + first * step + c;
     const size_t at = (size_t)seq * p.C + c;
     const float* const from = back ? p.dhT : p.h0;
@@ -218,120 +304,275 @@ template <bool GRAD> __global__ void __launch_bounds__(128) glr_chain_kernel(Glr
             }
         }
     }
-    float* const to = back ? p.dh0 : p.hT;
-    if (to) to[at] = h;
+    if (back && p.dh0) p.dh0[at] = h;
 }
 
-// ---------------------------------------------------------------- blocks from what enters them
-
-template <class TG, class TX, int V, int R, bool GRAD> __global__ void __launch_bounds__(NT) glr_block_kernel(GlrParams p) {
-    using L = Lay<V, R>;
+// a call without tokens: states as they came
+__global__ void __launch_bounds__(NT) glr_copy_kernel(const float* from, float* to, size_t n) {
     lds_poison(0);
-    __shared__ float sP[L::SLOTS][TILE], sE[L::SLOTS][TILE], sF[GRAD ? L::SLOTS : 1][TILE];
-    const int v = blockIdx.x / p.tiles, c0 = blockIdx.x % p.tiles * TILE, tid = threadIdx.x;
+    const size_t i = (size_t)blockIdx.x * NT + threadIdx.x;
+    if (i < n) to[i] = from ? from[i] : 0.f;
+}
+
+// gradient: every block from what enters it
+template <class TG, class TX, int V, int R> __global__ void __launch_bounds__(NT) glr_grad_kernel(GlrParams p) {
+    using B = Block<TG, TX, V, R, true>;
+    constexpr int TILE = B::TILE, SLOTS = B::SLOTS;
+    lds_poison(0);
+    __shared__ __align__(16) typename B::Shared s;
+    const int v = blockIdx.x / p.tiles, c0 = blockIdx.x % p.tiles * TILE, ch = threadIdx.x % TILE, part = threadIdx.x / TILE;
     SeqBlock b;
-    if (!seq_block(p.map, L::ROWS, v, b)) return;
-    const int cl = tid % L::CL * V, slot = tid / L::CL, row = slot * R, c = c0 + cl;
-    const bool live = c < p.C;
-    const int n = min(b.n - row, R);
-    const Rows<TG> ga(p.gate, b.t0, b.n, p.C, row, c, live);
-    const Rows<TX> gx(p.x, b.t0, b.n, p.C, row, c, live), gd(p.dh, b.t0, b.n, p.C, row, c, live);
-    Raw<TG, V> a[R];
-    Raw<TX, V> x[R], d[GRAD ? R : 1];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        a[r].load(ga.rs, ga[r]);
-        x[r].load(gx.rs, gx[r]);
-        if constexpr (GRAD) d[r].load(gd.rs, gd[r]);
+    const bool any = seq_block(p.map, B::L::ROWS, v, b);
+    const size_t at = (size_t)b.seq * p.C + c0 + ch;
+    const bool mine = part < 2 && c0 + ch < p.C;   // a channel a thread: the first part forwards, the second backwards
+    if (!any) {
+        if (b.idx == 0 && b.len == 0 && mine && part == 0 && p.dh0) p.dh0[at] = p.dhT ? p.dhT[at] : 0.f;
+        return;
     }
+    B k;
+    k.at(p, b.t0, b.n, c0);
+    k.load(p);
+    const int nb = (b.len + B::L::ROWS - 1) / B::L::ROWS;
+    const long step = 3 * (long)p.C;
+    const float* const sum = p.sum + (size_t)v * step + c0 + ch;   // this block's
     float carry = 0.f;
-    const int ch = tid % TILE;
-    if (tid < (GRAD ? 2 : 1) * TILE && c0 + ch < p.C)
-        carry = p.sum[((size_t)v * (GRAD ? 3 : 2) + 1 + tid / TILE) * p.C + c0 + ch];
-    float P[V], E[V], F[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) P[i] = 1.f, E[i] = 0.f, F[i] = 0.f;
+    if (mine && p.chained) {
+        carry = sum[(size_t)(1 + part) * p.C];
+    } else if (mine) {
+        const int count = part ? nb - 1 - b.idx : b.idx;   // blocks on the way from the sequence's end or start
+        const float* const first = part ? sum + count * step : sum - count * step;
+        const Run r = run_of(first, first + (size_t)(1 + part) * p.C, part ? -step : step, count);
+        const float* const from = part ? p.dhT : p.h0;
+        carry = fmaf(r.P, from ? from[at] : 0.f, r.E);
+    }
+    k.put(s);
+    __syncthreads();
+    if (mine && part == 0) {
+#pragma unroll 8
+        for (int i = 0; i < SLOTS; ++i) {
+            const float e = s.E[i][ch];
+            s.E[i][ch] = carry;
+            carry = fmaf(s.P[i][ch], carry, e);
+        }
+    } else if (mine) {
+#pragma unroll 8
+        for (int i = SLOTS - 1; i >= 0; --i) {
+            const float f = s.F[i][ch];
+            s.F[i][ch] = carry;
+            carry = fmaf(s.P[i][ch], carry, f);
+        }
+        if (p.dh0 && !p.chained && b.idx == 0) p.dh0[at] = carry;
+    }
+    __syncthreads();
+    float E[V], F[V];
+    k.take(s.E[k.slot], E);
+    const Rows<TG> oa = k.template of<TG>(p, p.dgate);
+    const Rows<TX> ox = k.template of<TX>(p, p.dx);
+    float before[R][V];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        if (r < n) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            before[r][i] = E[i];
+            E[i] = fmaf(k.a[r][i], E[i], k.x[r][i]);
+        }
+    }
+    k.take(s.F[k.slot], F);
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r) {
+        if (r < k.n) {
+            float lam[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                E[i] = fmaf(a[r][i], E[i], x[r][i]);
-                P[i] *= a[r][i];
+                lam[i] = k.d[r][i] + F[i];
+                F[i] = k.a[r][i] * lam[i];
+                before[r][i] *= lam[i];
+            }
+            Raw<TX, V>::store(ox.rs, ox[r], lam);
+            Raw<TG, V>::store(oa.rs, oa[r], before[r]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- forward
+
+constexpr uint64_t NOTHING = ~0ull;   // a word that no block has left yet
+
+__global__ void __launch_bounds__(NT) glr_clear_kernel(uint4* p, size_t n) {
+    lds_poison(0);
+    const size_t i = (size_t)blockIdx.x * NT + threadIdx.x;
+    if (i < n) p[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+}
+
+// P and E (or P = 0 and a state) in one word, so that it is there whole or not at all; no
+// NaN is passed on with all bits set
+__device__ __forceinline__ void leave(uint64_t* to, float P, float E) {
+    const uint32_t e = __float_as_uint(E) == ~0u ? 0x7fc00000u : __float_as_uint(E);
+    __hip_atomic_store(to, (uint64_t)e << 32 | __float_as_uint(P), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// What `count` (at most GROUP) words, `step` apart, do to a state, waiting for each to be
+// left. All of them belong to workgroups that started earlier and leave them without waiting
+// for a later one, so that every wait ends; should one ever not, it gives up after some
+// seconds with a NaN.
+__device__ __forceinline__ Run take_up(const uint64_t* w, long step, int count) {
+    Run r{1.f, 0.f};
+    constexpr int U = 8;
+    for (int b0 = 0; b0 < count; b0 += U) {
+        uint64_t y[U];
+        for (int tries = 0;; ++tries) {
+            bool all = true;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                y[u] = __hip_atomic_load(w + (long)min(b0 + u, count - 1) * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) all &= y[u] != NOTHING;
+            if (all || tries == 1 << 22) break;
+            __builtin_amdgcn_s_sleep(4);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (b0 + u < count) {
+                const float P = __uint_as_float((uint32_t)y[u]), E = __uint_as_float((uint32_t)(y[u] >> 32));
+                r.E = fmaf(P, r.E, E);
+                r.P *= P;
             }
         }
     }
-    if constexpr (GRAD) {
+    return r;
+}
+
+// One pass over all blocks. Workgroups take them in the order in which they start (a
+// counter), so that a block's predecessors have started before it. A block leaves P and E;
+// the first of a sequence, which alone reads h0 (h_T may be h0), and every GROUP-th leave
+// the state behind them instead, so that no block looks back over more than GROUP words. Which
+// words a block takes up, and in which order, does not depend on when they came.
+template <class TG, class TX, int V, int R> __global__ void __launch_bounds__(NT) glr_pass_kernel(GlrParams p) {
+    using B = Block<TG, TX, V, R, false>;
+    constexpr int TILE = B::TILE, SLOTS = B::SLOTS;
+    lds_poison(0);
+    __shared__ __align__(16) typename B::Shared s;
+    __shared__ float s_run[2][TILE], s_in[TILE];
+    __shared__ int s_work;
+    int work = blockIdx.x;
+    if (!p.alone) {
+        if (threadIdx.x == 0) s_work = (int)(atomicAdd(reinterpret_cast<uint32_t*>(p.counter), 1u) + 1u);   // from all ones
+        __syncthreads();
+        work = __builtin_amdgcn_readfirstlane(s_work);
+    }
+    const int v = work / p.tiles, c0 = work % p.tiles * TILE, ch = threadIdx.x % TILE, part = threadIdx.x / TILE;
+    SeqBlock b;
+    const bool any = seq_block(p.map, B::L::ROWS, v, b);
+    const size_t at = (size_t)b.seq * p.C + c0 + ch;
+    const bool mine = part < 2 && c0 + ch < p.C;   // a channel a thread, twice
+    if (!any) {
+        if (b.idx == 0 && b.len == 0 && mine && part == 0 && p.hT) p.hT[at] = p.h0 ? p.h0[at] : 0.f;   // no tokens
+        return;
+    }
+    B k;
+    k.at(p, b.t0, b.n, c0);
+    k.load(p);
+    const bool last = b.idx == (b.len - 1) / B::L::ROWS, head = b.idx == 0;
+    const float h0 = head && mine && p.h0 ? p.h0[at] : 0.f;
+    k.put(s);
+    __syncthreads();
+    uint64_t* const word = p.words + (size_t)v * p.C + c0 + ch;   // this block's
+    float P = 1.f, E = 0.f;
+    if (mine && part == 0) {   // slots' P and E become those of the block up to them
+#pragma unroll 8
+        for (int i = 0; i < SLOTS; ++i) {
+            const float pr = s.P[i][ch], e = s.E[i][ch];
+            s.P[i][ch] = P;
+            s.E[i][ch] = E;
+            E = fmaf(pr, E, e);
+            P *= pr;
+        }
+        if (!last && head) leave(word, 0.f, fmaf(P, h0, E));
+        else if (!last && (b.idx + 1) % GROUP) leave(word, P, E);
+    }
+    if (!head) {   // the words from the last state on, in two halves
+        const int first = max(b.idx / GROUP * GROUP - 1, 0), count = b.idx - first, half = (count + 1) / 2;
+        if (mine && part == 1) {
+            const Run r = take_up(word - (long)(count - half) * p.C, p.C, count - half);
+            s_run[0][ch] = r.P;
+            s_run[1][ch] = r.E;
+        }
+        Run r{0.f, 0.f};
+        if (mine && part == 0) r = take_up(word - (long)count * p.C, p.C, half);
+        __syncthreads();
+        if (mine && part == 0) {
+            const float h = fmaf(s_run[0][ch], r.E, s_run[1][ch]);
+            s_in[ch] = h;
+            E = fmaf(P, h, E);
+            if (!last && (b.idx + 1) % GROUP == 0) leave(word, 0.f, E);
+        }
+    } else if (mine && part == 0) {
+        s_in[ch] = h0;
+        E = fmaf(P, h0, E);
+    }
+    if (mine && part == 0 && last && p.hT) p.hT[at] = E;
+    __syncthreads();
+    float h[V], sp[V], se[V];
+    k.take(s_in, h);
+    k.take(s.P[k.slot], sp);
+    k.take(s.E[k.slot], se);
+    const Rows<TX> gh = k.template of<TX>(p, p.h);
 #pragma unroll
-        for (int r = R - 1; r >= 0; --r) {
-            if (r < n) {
+    for (int i = 0; i < V; ++i) h[i] = fmaf(sp[i], h[i], se[i]);
 #pragma unroll
-                for (int i = 0; i < V; ++i) F[i] = a[r][i] * (d[r][i] + F[i]);
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) h[i] = fmaf(k.a[r][i], h[i], k.x[r][i]);
+        Raw<TX, V>::store(gh.rs, gh[r], h);
+    }
+}
+
+// Forward of a batch whose sequences and tiles fill the chip: a workgroup takes a tile of
+// one sequence through all its blocks, the next one's loads under way, and reads everything
+// once.
+template <class TG, class TX, int V, int R> __global__ void __launch_bounds__(NT, 2) glr_stream_kernel(GlrParams p) {
+    using B = Block<TG, TX, V, R, false>;
+    constexpr int TILE = B::TILE, SLOTS = B::SLOTS, ROWS = B::L::ROWS;
+    lds_poison(0);
+    __shared__ __align__(16) typename B::Shared s;
+    const int seq = blockIdx.x / p.tiles, c0 = blockIdx.x % p.tiles * TILE, ch = threadIdx.x;
+    const long first = (long)seq * p.map.T;
+    const size_t at = (size_t)seq * p.C + c0 + ch;
+    const bool mine = ch < TILE && c0 + ch < p.C;
+    float carry = mine && p.h0 ? p.h0[at] : 0.f;
+    B k, next;
+    next.at(p, first, min(p.map.T, ROWS), c0);
+    next.load(p);
+    for (int t = 0; t < p.map.T; t += ROWS) {
+        k = next;
+        if (t + ROWS < p.map.T) {
+            next.at(p, first + t + ROWS, min(p.map.T - t - ROWS, ROWS), c0);
+            next.load(p);
+        }
+        k.put(s);
+        __syncthreads();
+        if (mine) {
+#pragma unroll 8
+            for (int i = 0; i < SLOTS; ++i) {
+                const float e = s.E[i][ch];
+                s.E[i][ch] = carry;
+                carry = fmaf(s.P[i][ch], carry, e);
             }
         }
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        sP[slot][cl + i] = P[i];
-        sE[slot][cl + i] = E[i];
-        if constexpr (GRAD) sF[slot][cl + i] = F[i];
-    }
-    __syncthreads();
-    if (tid < TILE) {
-#pragma unroll 8
-        for (int s = 0; s < L::SLOTS; ++s) {
-            const float e = sE[s][ch];
-            sE[s][ch] = carry;
-            carry = fmaf(sP[s][ch], carry, e);
-        }
-    } else if (GRAD && tid < 2 * TILE) {
-#pragma unroll 8
-        for (int s = L::SLOTS - 1; s >= 0; --s) {
-            const float f = sF[s][ch];
-            sF[s][ch] = carry;
-            carry = fmaf(sP[s][ch], carry, f);
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < V; ++i) E[i] = sE[slot][cl + i];
-    if constexpr (!GRAD) {
-        const Rows<TX> gh(p.h, b.t0, b.n, p.C, row, c, live);
+        __syncthreads();
+        float E[V];
+        k.take(s.E[k.slot], E);
+        __syncthreads();   // the next block's slots come to the same place
+        const Rows<TX> gh = k.template of<TX>(p, p.h);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) E[i] = fmaf(a[r][i], E[i], x[r][i]);
+            for (int i = 0; i < V; ++i) E[i] = fmaf(k.a[r][i], E[i], k.x[r][i]);
             Raw<TX, V>::store(gh.rs, gh[r], E);
         }
-    } else {
-        const Rows<TG> oa(p.dgate, b.t0, b.n, p.C, row, c, live);
-        const Rows<TX> ox(p.dx, b.t0, b.n, p.C, row, c, live);
-        float before[R][V];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                before[r][i] = E[i];
-                E[i] = fmaf(a[r][i], E[i], x[r][i]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) F[i] = sF[slot][cl + i];
-#pragma unroll
-        for (int r = R - 1; r >= 0; --r) {
-            if (r < n) {
-                float lam[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    lam[i] = d[r][i] + F[i];
-                    F[i] = a[r][i] * lam[i];
-                    before[r][i] *= lam[i];
-                }
-                Raw<TX, V>::store(ox.rs, ox[r], lam);
-                Raw<TG, V>::store(oa.rs, oa[r], before[r]);
-            }
-        }
     }
+    if (mine && p.hT) p.hT[at] = carry;
 }
 
 // ---------------------------------------------------------------- one token
@@ -353,7 +594,7 @@ template <class TG, class TX, int V> __global__ void __launch_bounds__(NT) glr_d
 // Channels and tokens of a thread: 16 bytes of the input type where every row
 // starts at a multiple of them, else one channel.
 template <class TX, bool WIDE> constexpr int glr_v() { return WIDE ? 16 / (int)sizeof(TX) : 1; }
-template <bool WIDE> constexpr int glr_r() { return WIDE ? 4 : 16; }
+template <bool WIDE> constexpr int glr_r() { return WIDE ? 8 : 16; }
 
 template <class F> auto with_types(bool bf16, bool gate_bf16, bool wide, F f) {
     using U = uint16_t;
@@ -363,10 +604,7 @@ template <class F> auto with_types(bool bf16, bool gate_bf16, bool wide, F f) {
 }
 
 bool wide_rows(int C, bool bf16) { return C % (bf16 ? 8 : 4) == 0; }
-int block_rows(int C, bool bf16) {
-    if (!wide_rows(C, bf16)) return Lay<1, glr_r<false>()>::ROWS;
-    return bf16 ? Lay<8, glr_r<true>()>::ROWS : Lay<4, glr_r<true>()>::ROWS;
-}
+static_assert(Lay<8, glr_r<true>()>::ROWS == 128 && Lay<4, glr_r<true>()>::ROWS == 128 && Lay<1, glr_r<false>()>::ROWS == 64, "");
 
 hipError_t run(const GlrArgs& a, bool grad) {
     GlrParams p{};
@@ -375,24 +613,41 @@ hipError_t run(const GlrArgs& a, bool grad) {
     p.sum = static_cast<float*>(a.workspace);
     p.map = SeqMap{a.cu_seqlens, a.T, a.N};
     p.C = a.C;
-    p.tiles = (a.C + TILE - 1) / TILE;
-    const int rows = block_rows(a.C, a.bf16);
-    const unsigned wgs = (unsigned)(seq_blocks_bound(a.T, a.N, rows, a.cu_seqlens != nullptr) * p.tiles);
     return with_types(a.bf16, a.gate_bf16, wide_rows(a.C, a.bf16), [&](auto tg, auto tx, auto wide) {
         using TG = decltype(tg);
         using TX = decltype(tx);
         constexpr int V = glr_v<TX, wide.value>(), R = glr_r<wide.value>();
-        if (a.T > 0) {
-            if (grad) hipLaunchKernelGGL((glr_sum_kernel<TG, TX, V, R, true>), dim3(wgs), dim3(NT), 0, a.stream, p);
-            else hipLaunchKernelGGL((glr_sum_kernel<TG, TX, V, R, false>), dim3(wgs), dim3(NT), 0, a.stream, p);
+        using L = Lay<V, R>;
+        p.tiles = (a.C + L::TILE - 1) / L::TILE;
+        const bool packed = a.cu_seqlens != nullptr;
+        const size_t blocks = seq_blocks_bound(a.T, a.N, L::ROWS, packed);
+        const dim3 wgs((unsigned)(blocks * p.tiles)), nt(NT);
+        const int most = (a.T + L::ROWS - 1) / L::ROWS;   // blocks that one sequence can have
+        if (most == 0) {
+            const size_t n = (size_t)a.N * a.C;
+            hipLaunchKernelGGL(glr_copy_kernel, dim3((unsigned)((n + NT - 1) / NT)), nt, 0, a.stream, grad ? a.dhT : a.h0,
+                               grad ? a.g_h0 : a.hT, n);
+            return hipGetLastError();
         }
-        const dim3 chains((unsigned)p.tiles * a.N);
-        if (grad) hipLaunchKernelGGL((glr_chain_kernel<true>), chains, dim3(2 * TILE), 0, a.stream, p, rows);
-        else hipLaunchKernelGGL((glr_chain_kernel<false>), chains, dim3(TILE), 0, a.stream, p, rows);
-        if (a.T > 0) {
-            if (grad) hipLaunchKernelGGL((glr_block_kernel<TG, TX, V, R, true>), dim3(wgs), dim3(NT), 0, a.stream, p);
-            else hipLaunchKernelGGL((glr_block_kernel<TG, TX, V, R, false>), dim3(wgs), dim3(NT), 0, a.stream, p);
+        p.alone = most == 1;
+        p.chained = grad && most > WALK;
+        if (grad) {
+            if (!p.alone) hipLaunchKernelGGL((glr_sum_kernel<TG, TX, V, R>), wgs, nt, 0, a.stream, p);
+            if (p.chained) hipLaunchKernelGGL(glr_chain_kernel, dim3((unsigned)((a.C + 63) / 64) * a.N), dim3(128), 0, a.stream, p, L::ROWS);
+            hipLaunchKernelGGL((glr_grad_kernel<TG, TX, V, R>), wgs, nt, 0, a.stream, p);
+            return hipGetLastError();
         }
+        if (!packed && !p.alone && (long)a.N * p.tiles >= 256) {
+            hipLaunchKernelGGL((glr_stream_kernel<TG, TX, V, R>), dim3(a.N * p.tiles), nt, 0, a.stream, p);
+            return hipGetLastError();
+        }
+        if (!p.alone) {
+            p.words = static_cast<uint64_t*>(a.workspace);
+            p.counter = p.words + blocks * a.C;
+            const size_t n = (blocks * a.C + 2) / 2 + 1;   // 16 bytes each, the counter among them
+            hipLaunchKernelGGL(glr_clear_kernel, dim3((unsigned)((n + NT - 1) / NT)), nt, 0, a.stream, static_cast<uint4*>(a.workspace), n);
+        }
+        hipLaunchKernelGGL((glr_pass_kernel<TG, TX, V, R>), wgs, nt, 0, a.stream, p);
         return hipGetLastError();
     });
 }
@@ -400,12 +655,12 @@ hipError_t run(const GlrArgs& a, bool grad) {
 }  // namespace
 
 bool glr_fits(int T, int N, int C, bool packed, bool bf16) {
-    const long tiles = (C + TILE - 1) / TILE;
-    return (seq_blocks_bound(T, N, block_rows(C, bf16), packed) + N) * tiles * NT <= 0xffffffffL;
+    const long tiles = (C + 63) / 64;
+    return (seq_blocks_bound(T, N, wide_rows(C, bf16) ? 128 : 64, packed) + N) * tiles * NT <= 0xffffffffL;
 }
 
 size_t glr_workspace_bytes(int T, int N, int C, bool packed, bool bf16, bool grad) {
-    return (size_t)seq_blocks_bound(T, N, block_rows(C, bf16), packed) * C * (grad ? 12 : 8) + 256;
+    return (size_t)seq_blocks_bound(T, N, wide_rows(C, bf16) ? 128 : 64, packed) * C * (grad ? 12 : 8) + 256;
 }
 
 hipError_t launch_glr_fwd(const GlrArgs& a) { return run(a, false); }

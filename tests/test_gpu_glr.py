@@ -107,6 +107,26 @@ def test_many_blocks(kda):
 
 
 @pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("B,C,T", [(64, 512, 129), (9, 3700, 260), (256, 5, 300)])
+def test_batches_that_fill_the_chip(kda, B, C, T, types):
+    check(kda, make(B, T, C, *types, seed=C))
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("C", [136, 7])
+@pytest.mark.parametrize("T", [64 * 64, 64 * 64 + 1, 64 * 128, 64 * 128 + 3])
+def test_around_the_longest_walk(kda, T, C, types):
+    check(kda, make(1, T, C, *types, seed=T))
+
+
+def test_packed_long_next_to_short(kda):
+    lens = [3, 0, 5000, 1, 700, 0, 128, 64]
+    check(kda, make(1, 0, 130, BF16, F32, lens=lens))
+    check(kda, make(1, 0, 136, F32, F32, lens=lens, kind="signed"))
+    check(kda, make(1, 0, 8, BF16, BF16, lens=[9000, 2, 0, 300]))
+
+
+@pytest.mark.parametrize("types", TYPES)
 def test_step_continues_the_forward(kda, types):
     x = make(3, 40, 56, *types, seed=5)
     _, h_T = kda.glr_fwd(x["gate"][:, :37].contiguous(), x["x"][:, :37].contiguous(), h0=x["h0"])
@@ -129,8 +149,10 @@ def test_step_sizes(kda, N, C, types):
     within("o", o, want, want.abs())
 
 
-def test_state_in_place_and_given_outputs(kda):
-    x = make(2, 200, 64, BF16, BF16)
+@pytest.mark.parametrize("B,T,C", [(2, 100, 64), (2, 200, 64), (1, 3000, 264), (1, 9000, 16), (130, 300, 256)])
+def test_state_in_place_and_given_outputs(kda, B, T, C):
+    """One block, blocks that form what enters them, a chain of blocks, one workgroup a sequence."""
+    x = make(B, T, C, BF16, BF16)
     h, h_T = kda.glr_fwd(x["gate"], x["x"], h0=x["h0"])
     state, out = x["h0"].clone(), torch.empty_like(h)
     a, b = kda.glr_fwd(x["gate"], x["x"], h0=state, h_T=state, out=out)
