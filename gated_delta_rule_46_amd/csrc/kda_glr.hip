@@ -28,7 +28,7 @@ namespace {
 
 constexpr int NT = 256;     // threads of a workgroup
 constexpr int WALK = 64;    // gradient: blocks of a sequence whose workgroups form what enters them
-constexpr int GROUP = 16;   // forward: blocks that follow each other by P and E, the last one by its state
+constexpr int GROUP = 32;   // forward: blocks that follow each other by P and E, the last one by its state
 
 struct GlrParams {
     const void *gate, *x, *dh;
@@ -595,6 +595,15 @@ template <class TG, class TX, int V> __global__ void __launch_bounds__(NT) glr_d
 // starts at a multiple of them, else one channel.
 template <class TX, bool WIDE> constexpr int glr_v() { return WIDE ? 16 / (int)sizeof(TX) : 1; }
 template <bool WIDE> constexpr int glr_r() { return WIDE ? 8 : 16; }
+// The forward's single pass takes more: fewer blocks look back, with registers for two
+// workgroups a CU. B=2 T=8192 C=2048 bf16, 4, 8, 12 and 16 tokens: 69, 49, 48 and 52 us; B=1
+// T=4096 fp32, 8, 12 and 16: 31, 27 and 24 us; C=2049 bf16, 16, 32, 48 and 64: 38, 29, 24 and 23.
+template <int V> constexpr int pass_r() { return V == 8 ? 12 : V == 4 ? 16 : 64; }
+constexpr int pass_rows(bool wide, bool bf16) {
+    return !wide ? Lay<1, pass_r<1>()>::ROWS : bf16 ? Lay<8, pass_r<8>()>::ROWS : Lay<4, pass_r<4>()>::ROWS;
+}
+constexpr int grad_rows(bool wide) { return wide ? 128 : 64; }
+
 
 template <class F> auto with_types(bool bf16, bool gate_bf16, bool wide, F f) {
     using U = uint16_t;
@@ -604,7 +613,8 @@ template <class F> auto with_types(bool bf16, bool gate_bf16, bool wide, F f) {
 }
 
 bool wide_rows(int C, bool bf16) { return C % (bf16 ? 8 : 4) == 0; }
-static_assert(Lay<8, glr_r<true>()>::ROWS == 128 && Lay<4, glr_r<true>()>::ROWS == 128 && Lay<1, glr_r<false>()>::ROWS == 64, "");
+static_assert(Lay<8, glr_r<true>()>::ROWS == grad_rows(true) && Lay<4, glr_r<true>()>::ROWS == grad_rows(true) &&
+              Lay<1, glr_r<false>()>::ROWS == grad_rows(false), "");
 
 hipError_t run(const GlrArgs& a, bool grad) {
     GlrParams p{};
@@ -620,9 +630,10 @@ hipError_t run(const GlrArgs& a, bool grad) {
         using L = Lay<V, R>;
         p.tiles = (a.C + L::TILE - 1) / L::TILE;
         const bool packed = a.cu_seqlens != nullptr;
-        const size_t blocks = seq_blocks_bound(a.T, a.N, L::ROWS, packed);
+        const int rows = grad ? L::ROWS : pass_rows(wide.value, a.bf16);
+        const size_t blocks = seq_blocks_bound(a.T, a.N, rows, packed);
         const dim3 wgs((unsigned)(blocks * p.tiles)), nt(NT);
-        const int most = (a.T + L::ROWS - 1) / L::ROWS;   // blocks that one sequence can have
+        const int most = (a.T + rows - 1) / rows;   // blocks that one sequence can have
         if (most == 0) {
             const size_t n = (size_t)a.N * a.C;
             hipLaunchKernelGGL(glr_copy_kernel, dim3((unsigned)((n + NT - 1) / NT)), nt, 0, a.stream, grad ? a.dhT : a.h0,
@@ -633,7 +644,7 @@ hipError_t run(const GlrArgs& a, bool grad) {
         p.chained = grad && most > WALK;
         if (grad) {
             if (!p.alone) hipLaunchKernelGGL((glr_sum_kernel<TG, TX, V, R>), wgs, nt, 0, a.stream, p);
-            if (p.chained) hipLaunchKernelGGL(glr_chain_kernel, dim3((unsigned)((a.C + 63) / 64) * a.N), dim3(128), 0, a.stream, p, L::ROWS);
+            if (p.chained) hipLaunchKernelGGL(glr_chain_kernel, dim3((unsigned)((a.C + 63) / 64) * a.N), dim3(128), 0, a.stream, p, rows);
             hipLaunchKernelGGL((glr_grad_kernel<TG, TX, V, R>), wgs, nt, 0, a.stream, p);
             return hipGetLastError();
         }
@@ -647,7 +658,7 @@ hipError_t run(const GlrArgs& a, bool grad) {
             const size_t n = (blocks * a.C + 2) / 2 + 1;   // 16 bytes each, the counter among them
             hipLaunchKernelGGL(glr_clear_kernel, dim3((unsigned)((n + NT - 1) / NT)), nt, 0, a.stream, static_cast<uint4*>(a.workspace), n);
         }
-        hipLaunchKernelGGL((glr_pass_kernel<TG, TX, V, R>), wgs, nt, 0, a.stream, p);
+        hipLaunchKernelGGL((glr_pass_kernel<TG, TX, V, pass_r<V>()>), wgs, nt, 0, a.stream, p);
         return hipGetLastError();
     });
 }
@@ -656,11 +667,12 @@ hipError_t run(const GlrArgs& a, bool grad) {
 
 bool glr_fits(int T, int N, int C, bool packed, bool bf16) {
     const long tiles = (C + 63) / 64;
-    return (seq_blocks_bound(T, N, wide_rows(C, bf16) ? 128 : 64, packed) + N) * tiles * NT <= 0xffffffffL;
+    return (seq_blocks_bound(T, N, grad_rows(wide_rows(C, bf16)), packed) + N) * tiles * NT <= 0xffffffffL;
 }
 
 size_t glr_workspace_bytes(int T, int N, int C, bool packed, bool bf16, bool grad) {
-    return (size_t)seq_blocks_bound(T, N, wide_rows(C, bf16) ? 128 : 64, packed) * C * (grad ? 12 : 8) + 256;
+    const bool wide = wide_rows(C, bf16);
+    return (size_t)seq_blocks_bound(T, N, grad ? grad_rows(wide) : pass_rows(wide, bf16), packed) * C * (grad ? 12 : 8) + 256;
 }
 
 hipError_t launch_glr_fwd(const GlrArgs& a) { return run(a, false); }
