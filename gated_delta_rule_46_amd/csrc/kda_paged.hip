@@ -313,6 +313,13 @@ struct Seen {
     }
 };
 
+// Strides of tiles of values, which only transposing reads touch. Those of a 16x16 product
+// take 16 rows of 8 dwords, those of a 32x32 product 8 rows of 16: rows 8 (16) dwords apart
+// cover the 64 banks evenly, while at tile_stride's 4, which suits reads along rows, they
+// met (half of all LDS cycles of 2,048 rows over 6,144 tokens). fp32 reads single elements.
+template <class T> constexpr int v_stride16(int d) { return sizeof(T) == 2 ? d + 16 : tile_stride<T>(d); }
+template <class T> constexpr int v_stride32(int d) { return sizeof(T) == 2 ? (d == 32 ? 32 : d + 32) : tile_stride<T>(d); }
+
 // ---------------------------------------------------------------- few rows
 
 // Up to 16 RT rows a block, tiles of 16x16 and 32 deep. A wave has one kv head and tiles
@@ -324,7 +331,7 @@ struct Seen {
 template <class T, int D, int RT> struct Few {
     // one workgroup a CU, of as many waves as registers leave room for
     static constexpr int NW = sizeof(T) == 4 && D == 128 ? 4 : 8, DEPTH = RT == 1 ? 2 : 1, R = 16 * RT;
-    static constexpr size_t tiles = sizeof(T) * NW * 32 * tile_stride<T>(D), join = sizeof(float) * NW * R * (D + 4);
+    static constexpr size_t tiles = sizeof(T) * NW * 32 * v_stride16<T>(D), join = sizeof(float) * NW * R * (D + 4);
     static constexpr size_t lds = tiles > join ? tiles : join;
 };
 
@@ -332,7 +339,7 @@ template <class T, int D, int RT>
 __global__ void __launch_bounds__((64 * Few<T, D, RT>::NW), (Few<T, D, RT>::NW / 4)) paged_few_kernel(AttnParams p) {
     using F = Few<T, D, RT>;
     constexpr int NW = F::NW, NT = 64 * NW, DEPTH = F::DEPTH, R = F::R, KB = 32;
-    constexpr int ST = tile_stride<T>(D), KD = D / 32, MD = D / 16, JS = D + 4;
+    constexpr int ST = v_stride16<T>(D), KD = D / 32, MD = D / 16, JS = D + 4;
     constexpr int PER = 16 / (int)sizeof(T), CPR = D / PER, NL = 32 * CPR / 64;
     using V8 = typename Frag<T>::V;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -497,8 +504,10 @@ __global__ void __launch_bounds__((64 * Few<T, D, RT>::NW), (Few<T, D, RT>::NW /
             each([&](auto d) {
                 if (it + d.value * KS < it1) tile(d, it + d.value * KS);
             });
-            // Keeps the waves on the same rows. Without it the oldest ones run ahead and end early.
-            __builtin_amdgcn_s_barrier();
+            // Keeps the waves on the same rows; without it the oldest ones run ahead and end early
+            // (64 sequences of 4,096 tokens, 8 kv heads: 200 against 197 us). With one tile ahead
+            // it costs more than that (8 times 8 tokens over 8,192: 47 against 49).
+            if constexpr (DEPTH > 1) __builtin_amdgcn_s_barrier();
         }
         float probe = 0.f;
 #pragma unroll
@@ -598,7 +607,7 @@ template <class T, int RW> struct Shape {
 };
 template <class T, int D, int RW> constexpr size_t rows_lds() {
     using S = Shape<T, RW>;
-    const size_t tiles = sizeof(T) * S::KS * 2 * 2 * S::KT * tile_stride<T>(D);
+    const size_t tiles = sizeof(T) * S::KS * 2 * S::KT * (tile_stride<T>(D) + v_stride32<T>(D));
     const size_t join = S::KS > 1 ? sizeof(float) * 4 * 64 * (16 * (D / 32) + 2) : 0;
     return std::max(tiles, join);
 }
@@ -606,13 +615,13 @@ template <class T, int D, int RW> constexpr size_t rows_lds() {
 template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_lds<T, D, RW>() > 80 * 1024 ? 1 : 2)) paged_rows_kernel(AttnParams p) {
     using S = Shape<T, RW>;
     constexpr int KS = S::KS, R = S::R, KT = S::KT, KB = S::KB, NX = KT / 32, GT = 64 * RW;
-    constexpr int ST = tile_stride<T>(D), KD = D / 16, MD = D / 32, PER = 16 / (int)sizeof(T), CPR = D / PER, NL = KT * CPR / GT;
+    constexpr int ST = tile_stride<T>(D), SV = v_stride32<T>(D), KD = D / 16, MD = D / 32, PER = 16 / (int)sizeof(T), CPR = D / PER, NL = KT * CPR / GT;
     using V8 = typename Frag<T>::V;
     extern __shared__ __align__(16) unsigned char smem[];
     lds_poison((uint32_t)rows_lds<T, D, RW>());
     const int tid = threadIdx.x, lane = tid % WAVE, w = wave_id(), n = lane & 31, h2 = lane >> 5;
     const int wr = w % RW, wk = w / RW, gt = tid - wk * GT;
-    T* const tiles = reinterpret_cast<T*>(smem) + (size_t)wk * 2 * 2 * KT * ST;   // [buffer][k, v][KT][ST]
+    T* const tiles = reinterpret_cast<T*>(smem) + (size_t)wk * 2 * KT * (ST + SV);   // [buffer][k [KT][ST], v [KT][SV]]
     // the scale's sign goes into q, exactly, and so does a scale of zero: maxima scale as they stand
     const float c = p.scale == 0.f ? 1.f : fabsf(p.scale) * LOG2E;
     const size_t rs = (size_t)p.Hkv * D;
@@ -695,13 +704,13 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_l
             const int here_gt = here(gt);
 #pragma unroll
             for (int m = 0; m < NL; ++m) {
-                const int e = here_gt + m * GT, row = e / CPR, at = row * ST + e % CPR * PER;
+                const int e = here_gt + m * GT, row = e / CPR, col = e % CPR * PER;
                 if (!full && !(held >> row & 1)) {   // what lies there is not this sequence's
                     rk[m] = u32x4{0u, 0u, 0u, 0u};
                     rv[m] = u32x4{0u, 0u, 0u, 0u};
                 }
-                *reinterpret_cast<u32x4*>(t + at) = rk[m];
-                *reinterpret_cast<u32x4*>(t + KT * ST + at) = rv[m];
+                *reinterpret_cast<u32x4*>(t + row * ST + col) = rk[m];
+                *reinterpret_cast<u32x4*>(t + KT * ST + row * SV + col) = rv[m];
             }
         };
         auto seen_by = [&](int tok) {
@@ -735,7 +744,7 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_l
                 if (k0 + HD < KD) __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
-            for (int m = 0; m < MD; ++m) vf[m] = tr32(tv, ST, 0, 32 * m, lane);
+            for (int m = 0; m < MD; ++m) vf[m] = tr32(tv, SV, 0, 32 * m, lane);
             __builtin_amdgcn_sched_barrier(0);
             if (masked) {
                 const Seen visible = seen_by(row_of(n).tok);
@@ -777,7 +786,7 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_l
                 V8 next[MD];
                 if (kb + 1 < KT / 16) {
 #pragma unroll
-                    for (int m = 0; m < MD; ++m) next[m] = tr32(tv, ST, 16 * (kb + 1), 32 * m, lane);
+                    for (int m = 0; m < MD; ++m) next[m] = tr32(tv, SV, 16 * (kb + 1), 32 * m, lane);
                 }
                 const V8 pf = rows16<T>(s[kb / 2], kb % 2);
                 __builtin_amdgcn_sched_barrier(0);
@@ -797,7 +806,7 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_l
         fetch(where);
         int where_next = it0 + 1 < it1 ? lookup(it0 + 1) : -1;
         for (int it = it0; it < it1; ++it) {
-            T* const t = tiles + (size_t)(it & 1) * 2 * KT * ST;
+            T* const t = tiles + (size_t)(it & 1) * KT * (ST + SV);
             put(t, held, held == ALL);
             __syncthreads();
             const uint64_t now = held;

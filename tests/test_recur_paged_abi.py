@@ -1,0 +1,233 @@
+"""Refusals of the gated linear recurrence's and the paged cache's calls, in the C
+ABI and in the binding, the sizes of their workspaces, and what pins their 64-bit
+references (no GPU: every call here fails its checks, or has nothing to do)."""
+import math
+import os
+
+import pytest
+import torch
+
+from gated_delta_rule_46_amd import kda
+from oracle import mixers
+from oracle import recur_paged as ref
+
+FAKE = 0x10000   # aligned, never dereferenced
+OK, EINVAL, ENOTSUP, EALIGN = kda.KDA_OK, kda.KDA_EINVAL, kda.KDA_ENOTSUP, kda.KDA_EALIGN
+BF16, F32 = kda.KDA_BF16, kda.KDA_F32
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(kda.LIB_PATH):
+        from gated_delta_rule_46_amd import build
+        build.build()
+    return kda.library()
+
+
+def glr_fwd(lib, **kw):
+    a = dict(gate=FAKE, x=FAKE, h0=None, h=FAKE, hT=None, B=2, T=8, C=16, cu=None, N=0, dtype=BF16, gate_dtype=BF16, ws=FAKE,
+             wsb=1 << 40, stream=None)
+    a.update(kw)
+    return lib.kda_glr_fwd(*a.values())
+
+
+def glr_bwd(lib, **kw):
+    a = dict(gate=FAKE, x=FAKE, h0=None, dh=FAKE, dhT=None, gg=FAKE, gx=FAKE, gh0=None, B=2, T=8, C=16, cu=None, N=0,
+             dtype=BF16, gate_dtype=BF16, ws=FAKE, wsb=1 << 40, stream=None)
+    a.update(kw)
+    return lib.kda_glr_bwd(*a.values())
+
+
+@pytest.mark.parametrize("call", [glr_fwd, glr_bwd])
+@pytest.mark.parametrize("status,bad", [
+    (EINVAL, dict(B=0)), (EINVAL, dict(T=-1)), (EINVAL, dict(C=0)), (EINVAL, dict(N=3)), (EINVAL, dict(cu=FAKE, N=2)),
+    (EINVAL, dict(B=1, cu=FAKE, N=0)), (EINVAL, dict(gate=None)), (EINVAL, dict(x=None)), (EINVAL, dict(ws=None)),
+    (EINVAL, dict(wsb=255)), (EINVAL, dict(T=1000, wsb=2 * 6 * 16 * 8)),
+    (ENOTSUP, dict(dtype=2)), (ENOTSUP, dict(gate_dtype=2)), (ENOTSUP, dict(dtype=F32)), (ENOTSUP, dict(C=2 ** 20 + 1)),
+    (ENOTSUP, dict(T=2 ** 30)), (ENOTSUP, dict(B=2 ** 24, T=1)), (ENOTSUP, dict(B=1, T=2 ** 20, C=2 ** 20)),
+    (EALIGN, dict(gate=FAKE + 8)), (EALIGN, dict(x=FAKE + 8)), (EALIGN, dict(x=FAKE + 1, C=15)),
+    (EALIGN, dict(gate=FAKE + 2, gate_dtype=F32, C=15)), (EALIGN, dict(gate=FAKE + 8, gate_dtype=F32)),
+    (EALIGN, dict(h0=FAKE + 2)), (EALIGN, dict(ws=FAKE + 8)), (EALIGN, dict(B=1, cu=FAKE + 2, N=2)),
+])
+def test_recurrence_refusals(lib, call, status, bad):
+    assert call(lib, **bad) == status
+
+
+def test_recurrence_refusals_of_each(lib):
+    assert glr_fwd(lib, h=None) == EINVAL and glr_fwd(lib, h=FAKE + 8) == EALIGN and glr_fwd(lib, hT=FAKE + 2) == EALIGN
+    assert glr_fwd(lib, T=0, gate=None, x=None, h=None) == OK   # nothing to do
+    for name in ("dh", "gg", "gx"):
+        assert glr_bwd(lib, **{name: None}) == EINVAL
+        assert glr_bwd(lib, **{name: FAKE + 8}) == EALIGN
+    assert glr_bwd(lib, dhT=FAKE + 1) == EALIGN and glr_bwd(lib, gh0=FAKE + 2) == EALIGN
+    assert glr_bwd(lib, T=0, gate=None, x=None, dh=None, gg=None, gx=None) == OK
+    for f, call in ((kda.glr_fwd_workspace_bytes, glr_fwd), (kda.glr_bwd_workspace_bytes, glr_bwd)):
+        assert call(lib, T=1000, wsb=f(2, 1000, 16) - 1) == EINVAL
+
+
+def test_recurrence_step_refusals(lib):
+    def step(**kw):
+        a = dict(gate=FAKE, x=FAKE, h=FAKE, o=FAKE, N=2, C=16, dtype=BF16, gate_dtype=BF16, stream=None)
+        a.update(kw)
+        return lib.kda_glr_decode_step(*a.values())
+    assert step(N=0) == EINVAL and step(C=-1) == EINVAL
+    assert step(dtype=3) == ENOTSUP and step(dtype=F32) == ENOTSUP and step(N=2 ** 20, C=2 ** 11) == ENOTSUP
+    for name in ("gate", "x", "h", "o"):
+        assert step(**{name: None}) == EINVAL and step(**{name: FAKE + 1}) == EALIGN
+    assert step(gate=FAKE + 2, gate_dtype=F32) == EALIGN and step(h=FAKE + 2) == EALIGN
+
+
+def test_recurrence_workspace(lib):
+    for f in (kda.glr_fwd_workspace_bytes, kda.glr_bwd_workspace_bytes):
+        assert f(0, 8, 16) == 0 and f(1, -1, 16) == 0 and f(1, 8, 0) == 0 and f(2, 8, 16, N=2, varlen=True) == 0
+        assert f(1, 8, 16, N=0, varlen=True) == 0 and f(1, 8, 2 ** 21) == 0
+        assert f(1, 0, 16) >= 256 and f(1, 5000, 64) <= f(1, 5100, 64) <= f(2, 5100, 64)
+    # packed: what the tokens need, and one block more for each sequence
+    assert kda.glr_bwd_workspace_bytes(1, 65536, 128, N=1000, varlen=True) <= (65536 // 128 + 1001) * 128 * 12 + 256
+
+
+def append(lib, **kw):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, pos=None, freqs=FAKE, q_out=FAKE, K=FAKE, V=FAKE, table=FAKE, ctx=FAKE, B=2, T=8, Hq=4,
+             Hkv=2, d=64, rot=64, pairing=0, pages=10, page=16, width=4, cu=None, N=0, dtype=BF16, stream=None)
+    a.update(kw)
+    return lib.kda_paged_append(*a.values())
+
+
+def attn(lib, **kw):
+    a = dict(q=FAKE, K=FAKE, V=FAKE, table=FAKE, ctx=FAKE, tree=None, words=0, o=FAKE, lse=None, B=2, T=8, Hq=4, Hkv=2, d=64,
+             scale=0.125, pages=10, page=16, width=4, cu=None, N=0, dtype=BF16, ws=FAKE, wsb=1 << 40, stream=None)
+    a.update(kw)
+    return lib.kda_paged_attn(*a.values())
+
+
+@pytest.mark.parametrize("call", [append, attn])
+@pytest.mark.parametrize("status,bad", [
+    (EINVAL, dict(B=0)), (EINVAL, dict(T=-1)), (EINVAL, dict(Hq=0)), (EINVAL, dict(Hkv=0)), (EINVAL, dict(Hq=3)),
+    (EINVAL, dict(pages=0)), (EINVAL, dict(page=0)), (EINVAL, dict(width=0)), (EINVAL, dict(N=3)), (EINVAL, dict(cu=FAKE, N=2)),
+    (EINVAL, dict(B=1, cu=FAKE, N=0)), (EINVAL, dict(K=None)), (EINVAL, dict(V=None)), (EINVAL, dict(table=None)),
+    (EINVAL, dict(ctx=None)),
+    (ENOTSUP, dict(d=16)), (ENOTSUP, dict(d=96)), (ENOTSUP, dict(dtype=2)), (ENOTSUP, dict(Hq=131070, Hkv=65535)),
+    (ENOTSUP, dict(pages=2 ** 20, page=2 ** 11)), (ENOTSUP, dict(T=2 ** 30)), (ENOTSUP, dict(B=2 ** 24, T=1)),
+    (ENOTSUP, dict(B=1, T=2 ** 25, Hq=64, Hkv=1)),
+    (EALIGN, dict(q=FAKE + 8)), (EALIGN, dict(K=FAKE + 8)), (EALIGN, dict(V=FAKE + 8)), (EALIGN, dict(table=FAKE + 2)),
+    (EALIGN, dict(ctx=FAKE + 1)), (EALIGN, dict(B=1, cu=FAKE + 2, N=2)),
+])
+def test_paged_refusals(lib, call, status, bad):
+    assert call(lib, **bad) == status
+
+
+def test_append_refusals(lib):
+    for bad in (dict(k=None), dict(v=None), dict(q=None), dict(q_out=None), dict(freqs=None), dict(rot=0), dict(rot=80), dict(rot=-16)):
+        assert append(lib, **bad) == EINVAL
+    for bad in (dict(rot=24), dict(pairing=2)):
+        assert append(lib, **bad) == ENOTSUP
+    for bad in (dict(k=FAKE + 8), dict(v=FAKE + 2), dict(q_out=FAKE + 8), dict(pos=FAKE + 2), dict(freqs=FAKE + 2)):
+        assert append(lib, **bad) == EALIGN
+    none = dict(q=None, k=None, v=None, q_out=None, K=None, V=None, table=None, ctx=None)
+    assert append(lib, T=0, **none) == OK
+
+
+def test_attention_refusals(lib):
+    for bad in (dict(q=None), dict(o=None), dict(ws=None), dict(wsb=255), dict(scale=math.inf), dict(scale=math.nan),
+                dict(tree=FAKE, words=0)):
+        assert attn(lib, **bad) == EINVAL
+    for bad in (dict(o=FAKE + 8), dict(lse=FAKE + 2), dict(tree=FAKE + 2, words=1), dict(ws=FAKE + 8)):
+        assert attn(lib, **bad) == EALIGN
+    need = kda.paged_attn_workspace_bytes(2, 8, 4, 2, 64)
+    assert need > 256 and attn(lib, wsb=need - 1) == EINVAL
+    assert attn(lib, B=1, T=2 ** 22, Hq=4096, Hkv=4096) == ENOTSUP   # more items than a launch takes
+    assert attn(lib, T=0, q=None, K=None, V=None, table=None, ctx=None, o=None, ws=None) == OK
+
+
+def test_attention_workspace(lib):
+    f = kda.paged_attn_workspace_bytes
+    assert f(0, 1, 4, 2, 64) == 0 and f(1, 1, 4, 3, 64) == 0 and f(1, 1, 4, 2, 48) == 0 and f(2, 1, 4, 2, 64, N=2, varlen=True) == 0
+    assert f(1, 1, 4, 2, 64, N=0, varlen=True) == 0
+    # no more than the parts of what the chip holds at once, however long the contexts are
+    for T in (1, 8, 64, 4096):
+        for N in (1, 64):
+            assert 256 <= f(N, T, 32, 8, 128) <= 1024 * 128 * (128 + 2) * 4 + (1 << 20)
+
+
+def test_binding_refusals():
+    """What the binding refuses before it loads the library or asks for a GPU."""
+    def t(*shape, dtype=torch.bfloat16):
+        return torch.zeros(shape, dtype=dtype)
+    with pytest.raises(ValueError, match="dims"):
+        kda.glr_fwd(t(4, 16), t(4, 16))
+    with pytest.raises(ValueError, match="B = 1"):
+        kda.glr_fwd(t(2, 4, 16), t(2, 4, 16), cu_seqlens=torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(TypeError, match="GPU"):
+        kda.glr_bwd(t(2, 4, 16), t(2, 4, 16), t(2, 4, 16))
+    with pytest.raises(TypeError, match="GPU"):
+        kda.glr_decode_step(t(4, 16), t(4, 16), t(4, 16, dtype=torch.float32))
+    i = lambda *shape: torch.zeros(shape, dtype=torch.int32)  # noqa: E731
+    pages, q, k = t(5, 16, 2, 64), t(2, 3, 4, 64), t(2, 3, 2, 64)
+    for bad in (dict(q=t(6, 4, 64)), dict(q=t(2, 3, 3, 64)), dict(K_pages=t(80, 2, 64))):
+        with pytest.raises(ValueError):
+            kda.paged_attn(**dict(dict(q=q, K_pages=pages, V_pages=pages, block_table=i(2, 4), ctx_len=i(2)), **bad))
+    with pytest.raises(ValueError, match="B = 1"):
+        kda.paged_attn(q, pages, pages, i(2, 4), i(2), cu_seqlens=i(3))
+    with pytest.raises(TypeError, match="GPU"):
+        kda.paged_attn(q, pages, pages, i(2, 4), i(2))
+    with pytest.raises(TypeError, match="GPU"):
+        kda.paged_append(k, k, pages, pages, i(2, 4), i(2))
+
+
+# ---------------------------------------------------------------- references
+
+def test_recurrence_reference_against_its_sum():
+    """h_t = sum_s a_{s+1} .. a_t x_s, written out, and its gradient by autograd."""
+    g = torch.Generator().manual_seed(3)
+    a, x, dh = (torch.randn(1, 7, 2, generator=g, dtype=torch.float64) for _ in range(3))
+    h0, dh_T = (torch.randn(1, 2, generator=g, dtype=torch.float64) for _ in range(2))
+    seqs = mixers.spans(1, 7)
+    for t in (a, x, h0):
+        t.requires_grad_()
+    rows = []
+    for t in range(7):
+        rows.append(sum(a[0, s + 1:t + 1].prod(0) * x[0, s] for s in range(t + 1)) + a[0, :t + 1].prod(0) * h0[0])
+    h = torch.stack(rows)[None]
+    want = torch.autograd.grad((h * dh).sum() + (h[:, -1] * dh_T).sum(), [a, x, h0])
+    a, x, h0 = a.detach(), x.detach(), h0.detach()
+    got, last, before, *_ = ref.glr(a, x, h0, seqs)
+    assert torch.allclose(got, h.detach(), atol=1e-12) and torch.allclose(last, h[0, -1:].detach(), atol=1e-12)
+    assert torch.equal(before[0, 0], h0[0]) and torch.allclose(before[0, 1:], got[0, :-1])
+    out, _ = ref.glr_grad(a, x, h0, dh, dh_T, seqs)
+    for n, w in zip(("dgate", "dx", "dh0"), want):
+        assert torch.allclose(out[n], w, atol=1e-12)
+
+
+def test_rotation_reference():
+    """A rotation keeps lengths, leaves the rest alone, and turns scores by distances only."""
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(2, 3, 8, generator=g, dtype=torch.float64)
+    freqs = torch.tensor([1.0, 0.25])
+    for inter in (False, True):
+        y = ref.rotate(x, torch.tensor([5, 9]), freqs, inter)
+        z = ref.rotate(x, torch.tensor([105, 109]), freqs, inter)
+        assert torch.equal(y[..., 4:], x[..., 4:])
+        assert torch.allclose(y.norm(dim=-1), x.norm(dim=-1))
+        assert torch.allclose((y[0] * y[1]).sum(-1), (z[0] * z[1]).sum(-1))
+        i, j = (0, 1) if inter else (0, 2)
+        turned = torch.complex(x[0, 0, i], x[0, 0, j]) * torch.polar(torch.ones((), dtype=torch.float64), torch.tensor(5.0, dtype=torch.float64))
+        assert torch.allclose(torch.complex(y[0, 0, i], y[0, 0, j]), turned)
+
+
+def test_paged_reference_against_one_row_of_keys():
+    """Pages put in order and masked by hand against one softmax."""
+    g = torch.Generator().manual_seed(5)
+    q = torch.randn(1, 3, 4, 32, generator=g, dtype=torch.float64)
+    K, V = (torch.randn(4, 4, 2, 32, generator=g, dtype=torch.float64) for _ in range(2))
+    table, ctx = torch.tensor([[2, 0, 3]], dtype=torch.int32), [6]
+    tree = torch.tensor([[[1], [3], [5]]], dtype=torch.int32)   # token 2 does not see token 1
+    o, lse, _, _ = ref.paged_attn(q, K, V, table, ctx, tree, 0.2, mixers.spans(1, 3))
+    k, v = (torch.cat([x[2], x[0], x[3]])[:9] for x in (K, V))
+    mask = torch.zeros(3, 9, dtype=torch.bool)
+    mask[:, :6] = True
+    for i, row in enumerate(([1, 0, 0], [1, 1, 0], [1, 0, 1])):
+        mask[i, 6:] = torch.tensor(row, dtype=torch.bool)
+    for h in range(4):
+        s = (0.2 * q[0, :, h] @ k[:, h // 2].T).masked_fill(~mask, -math.inf)
+        assert torch.allclose(torch.softmax(s, -1) @ v[:, h // 2], o[0, :, h])
+        assert torch.allclose(torch.logsumexp(s, -1), lse[0, :, h])
