@@ -626,6 +626,10 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_l
     const float c = p.scale == 0.f ? 1.f : fabsf(p.scale) * LOG2E;
     const size_t rs = (size_t)p.Hkv * D;
     const bool chunks = p.pages.page % (GT / CPR) == 0;
+    // this thread's places in a tile: of what it brings, and of its operands
+    const int put_k = gt / CPR * ST + gt % CPR * PER, put_v = gt / CPR * SV + gt % CPR * PER;
+    const int at_k = n * ST + 8 * h2;
+    const int at_v = sizeof(T) == 2 ? (4 * h2 + ((lane & 15) >> 2)) * SV + (lane & 16) + 4 * (lane & 3) : 4 * h2 * SV + n;
 
     Work k;
     if (!find_work<R, KB, 1, 256, true>(p, k)) return;
@@ -700,17 +704,24 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_l
                 rv[m] = *reinterpret_cast<const u32x4*>(V + o);
             }
         };
+        // (rows that are not this sequence's become zeros)
         auto put = [&](T* t, uint64_t held, bool full) {
-            const int here_gt = here(gt);
+            T* const tk = t + put_k;
+            T* const tv = t + KT * ST + put_v;
+            constexpr int RPC = GT / CPR;
+            if (full) {
+#pragma unroll
+                for (int m = 0; m < NL; ++m) {
+                    *reinterpret_cast<u32x4*>(tk + m * RPC * ST) = rk[m];
+                    *reinterpret_cast<u32x4*>(tv + m * RPC * SV) = rv[m];
+                }
+                return;
+            }
 #pragma unroll
             for (int m = 0; m < NL; ++m) {
-                const int e = here_gt + m * GT, row = e / CPR, col = e % CPR * PER;
-                if (!full && !(held >> row & 1)) {   // what lies there is not this sequence's
-                    rk[m] = u32x4{0u, 0u, 0u, 0u};
-                    rv[m] = u32x4{0u, 0u, 0u, 0u};
-                }
-                *reinterpret_cast<u32x4*>(t + row * ST + col) = rk[m];
-                *reinterpret_cast<u32x4*>(t + KT * ST + row * SV + col) = rv[m];
+                const uint32_t keep = held >> (gt / CPR + m * RPC) & 1 ? ~0u : 0u;
+                *reinterpret_cast<u32x4*>(tk + m * RPC * ST) = rk[m] & keep;
+                *reinterpret_cast<u32x4*>(tv + m * RPC * SV) = rv[m] & keep;
             }
         };
         auto seen_by = [&](int tok) {
@@ -723,7 +734,8 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_l
         float top = -INFINITY, sum = 0.f;   // sum: this lane's half of the keys
 
         auto tile = [&](const T* tk, const T* tv, int j0, uint64_t held, bool masked) {
-            const int lane = here(tid % WAVE), n = lane & 31, h2 = lane >> 5;
+            tk += at_k;
+            tv += at_v;
             f32x16 s[NX];
             V8 vf[MD];
 #pragma unroll
@@ -735,7 +747,7 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_l
 #pragma unroll
                 for (int ks = 0; ks < HD; ++ks)
 #pragma unroll
-                    for (int x = 0; x < NX; ++x) kf[x][ks] = nat32<T>(tk, ST, 32 * x, 16 * (k0 + ks), n, h2);
+                    for (int x = 0; x < NX; ++x) kf[x][ks] = nat32<T>(tk, ST, 32 * x, 16 * (k0 + ks), 0, 0);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int ks = 0; ks < HD; ++ks)
@@ -744,7 +756,7 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_l
                 if (k0 + HD < KD) __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
-            for (int m = 0; m < MD; ++m) vf[m] = tr32(tv, SV, 0, 32 * m, lane);
+            for (int m = 0; m < MD; ++m) vf[m] = tr32(tv, SV, 0, 32 * m, 0);
             __builtin_amdgcn_sched_barrier(0);
             if (masked) {
                 const Seen visible = seen_by(row_of(n).tok);
@@ -786,7 +798,7 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_l
                 V8 next[MD];
                 if (kb + 1 < KT / 16) {
 #pragma unroll
-                    for (int m = 0; m < MD; ++m) next[m] = tr32(tv, SV, 16 * (kb + 1), 32 * m, lane);
+                    for (int m = 0; m < MD; ++m) next[m] = tr32(tv, SV, 16 * (kb + 1), 32 * m, 0);
                 }
                 const V8 pf = rows16<T>(s[kb / 2], kb % 2);
                 __builtin_amdgcn_sched_barrier(0);

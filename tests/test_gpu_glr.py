@@ -256,3 +256,20 @@ def test_gradient_against_differences(kda):
             flat[e] = keep
             # second-order term: eps^2 times third derivatives, which are zero in each input by itself
             assert abs(slope - g[out].view(-1)[e].item()) <= 1e-4 * (1 + abs(slope))
+
+
+def test_poisoned_lds(kda):
+    """The build that fills every workgroup's LDS with NaN first: every kernel."""
+    import os
+
+    from gated_delta_rule_46_amd import build
+    assert os.path.exists(build.POISON_LIB)
+    with kda.using_library(build.POISON_LIB):
+        for types in TYPES:
+            for C in (24, 5):
+                check(kda, make(2, 100, C, *types))
+                check(kda, make(1, 0, C, *types, lens=[700, 0, 3, 129]))
+            check(kda, make(1, 64 * 128 + 3, 3, *types))
+            test_step_sizes(kda, 3, 5, types)
+        check(kda, make(130, 270, 256, BF16, BF16))
+        test_no_tokens(kda)

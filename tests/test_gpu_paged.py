@@ -428,3 +428,44 @@ def test_a_layer_pair_in_serving(kda, dtype):
         # apart, which an output sees times the scores' size (under 8 here): 16 more roundings
         close("o", torch.cat(outs[n])[None].cpu(), want, dtype, tau=5e-2 if dtype == BF16 else 1e-4, size=size)
         assert (state[n].cpu().double() - h_T[0]).abs().max() <= 1e-4
+
+
+@pytest.mark.parametrize("T,G,most", [(1, 4, 1.02), (7, 4, 1.02), (12, 4, 1.5), (64, 4, 1.5)])
+def test_mean_error_in_bf16(kda, T, G, most):
+    """Against the rounding of the result alone. Up to 32 rows a kv head the probabilities
+    enter the second product as two bf16 numbers, off by 2^-17: nothing next to the result's
+    2^-8. More rows: as one, whose rounding makes, over random v, as large an error as the
+    result's own (both relative to the same root of squared terms): sqrt(2) of it together."""
+    x = make([T] * 2, [2000, 700], 2 * G, 2, 128, BF16, 16, packed=False, seed=T)
+    o, _ = attend(kda, x)
+    q, Kp, Vp, table = x["q"].double(), x["Kp"].double(), x["Vp"].double(), x["table"].long()
+    off, own = 0.0, 0.0
+    for n in range(2):
+        L = int(x["ctx"][n]) + T
+        pages = table[n, :(L + 15) // 16]
+        hidden = torch.zeros(T, L, dtype=torch.bool, device="cuda")
+        hidden[:, L - T:] = torch.ones(T, T, dtype=torch.bool, device="cuda").triu(1)
+        for h in range(2 * G):
+            K, V = (t[pages].flatten(0, 1)[:L, h // G] for t in (Kp, Vp))
+            s = (q[n, :, h] @ K.t().contiguous() * 128 ** -0.5).masked_fill(hidden, float("-inf"))
+            want = torch.softmax(s, -1) @ V
+            off += (o[n, :, h].double() - want).square().sum().item()
+            own += (want.to(BF16).double() - want).square().sum().item()
+    ratio = (off / own) ** 0.5
+    assert ratio <= most, "%.3f times the rounding of the result" % ratio
+
+
+def test_poisoned_lds(kda):
+    """The build that fills every workgroup's LDS with NaN first: every kernel."""
+    import os
+
+    from gated_delta_rule_46_amd import build
+    assert os.path.exists(build.POISON_LIB)
+    with kda.using_library(build.POISON_LIB):
+        for dtype in (BF16, F32):
+            for d in (32, 64, 128):
+                for lens, ctx in (([1, 1], [700, 3]), ([7, 2], [300, 0]), ([14, 9], [90, 40]), ([50, 3], [100, 0])):
+                    check(kda, make(lens, ctx, 8, 2, d, dtype, 16, tree="tree"))
+            check(kda, make([1] * 300, [(7 * i) % 50 for i in range(300)], 8, 8, 32, dtype, 16, packed=False))
+            test_append(kda, 64, 48, False, dtype)
+            test_append(kda, 64, 48, True, dtype)
