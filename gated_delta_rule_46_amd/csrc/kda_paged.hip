@@ -214,9 +214,8 @@ __device__ __forceinline__ bool row_block(const SeqMap& m, int G, int R, int v, 
     b.rows = b.n * G;
     return b.r0 >= 0 && b.r0 < b.rows;
 }
-// keys that a block's rows may see
-__device__ __forceinline__ int keys_of(const AttnParams& p, const RowBlock& b, int R) {
-    const int ctx = p.ctx[b.seq];
+// keys that a block's rows may see, of a sequence with ctx tokens before the new ones
+__device__ __forceinline__ int keys_of(const AttnParams& p, const RowBlock& b, int ctx, int R) {
     if (ctx < 0) return 0;
     return (int)min((long)ctx + (p.tree ? b.n : min(b.n, (b.r0 + R - 1) / p.G + 1)), p.capacity);
 }
@@ -227,13 +226,18 @@ __device__ __forceinline__ int keys_of(const AttnParams& p, const RowBlock& b, i
 struct Work {
     long u, end, total;
     int v, hg, it0, wgs, wg;
+    bool known;      // b and ctx are those of v
+    RowBlock b;
+    int ctx;
     // the workgroup that has a unit
     __device__ __forceinline__ int owner(long x) const { return (int)(((x + 1) * wgs - 1) / total); }
 };
 // LEAST: units that a workgroup has at least, where there are as many. REMAP: workgroups
-// that follow each other in the order of units on one die. False for one without work.
-template <int R, int KB, int LEAST, int NT, bool REMAP> __device__ __forceinline__ bool find_work(const AttnParams& p, Work& k) {
+// that follow each other in the order of units on one die. False for one without work. lds:
+// 2 MAX_BLOCKS + 1 words, free again behind the next barrier.
+template <int R, int KB, int LEAST, int NT, bool REMAP> __device__ __forceinline__ bool find_work(const AttnParams& p, int* lds, Work& k) {
     const int tid = threadIdx.x, lane = tid % WAVE, w = tid / WAVE;
+    k.known = false;
     if (!p.wgs) {
         k.wg = REMAP ? xcd_remap(blockIdx.x, gridDim.x) : (int)blockIdx.x;
         k.u = 0;
@@ -244,6 +248,15 @@ template <int R, int KB, int LEAST, int NT, bool REMAP> __device__ __forceinline
         return true;
     }
     __shared__ int s_wave[NT / WAVE], s_at[2];
+    // offsets and contexts at once, in place of a search through memory (a call has no more
+    // sequences than blocks)
+    int* const s_ctx = lds;
+    int* const s_cu = lds + MAX_BLOCKS;
+    for (int i = tid; i < p.map.N; i += NT) s_ctx[i] = p.ctx[i];
+    if (p.map.cu)
+        for (int i = tid; i <= p.map.N; i += NT) s_cu[i] = p.map.cu[i];
+    __syncthreads();
+    const SeqMap map{p.map.cu ? s_cu : nullptr, p.map.T, p.map.N};
     const int each = (p.blocks + NT - 1) / NT, b0 = tid * each;   // neighbours that a thread counts
     constexpr int MOST = (MAX_BLOCKS + NT - 1) / NT;
     int mine[MOST], sum = 0;
@@ -251,8 +264,8 @@ template <int R, int KB, int LEAST, int NT, bool REMAP> __device__ __forceinline
     for (int i = 0; i < MOST; ++i) {
         RowBlock rb;
         mine[i] = 0;
-        if (i < each && b0 + i < p.blocks && row_block(p.map, p.G, R, b0 + i, rb))
-            mine[i] = max((keys_of(p, rb, R) + KB - 1) / KB, 1);
+        if (i < each && b0 + i < p.blocks && row_block(map, p.G, R, b0 + i, rb))
+            mine[i] = max((keys_of(p, rb, s_ctx[rb.seq], R) + KB - 1) / KB, 1);
         sum += mine[i];
     }
     int before = sum;
@@ -290,6 +303,12 @@ template <int R, int KB, int LEAST, int NT, bool REMAP> __device__ __forceinline
     __syncthreads();
     k.v = __builtin_amdgcn_readfirstlane(s_at[0]);
     k.it0 = __builtin_amdgcn_readfirstlane(s_at[1]);
+    row_block(map, p.G, R, k.v, k.b);
+    k.b = RowBlock{__builtin_amdgcn_readfirstlane(k.b.seq), __builtin_amdgcn_readfirstlane(k.b.r0),
+                   __builtin_amdgcn_readfirstlane(k.b.rows), __builtin_amdgcn_readfirstlane(k.b.n),
+                   (long)__builtin_amdgcn_readfirstlane((int)k.b.t0)};   // (tokens over the batch: 31 bits)
+    k.ctx = __builtin_amdgcn_readfirstlane(s_ctx[k.b.seq]);
+    k.known = true;
     return true;
 }
 
@@ -351,11 +370,11 @@ __global__ void __launch_bounds__((64 * Few<T, D, RT>::NW), (Few<T, D, RT>::NW /
     const size_t rs = (size_t)p.Hkv * D;
     Work k;
     const int HW = p.HW, KS = NW / HW, wh = w % HW, wk = w / HW;
-    if (!find_work<R, KB, 2, NT, false>(p, k)) return;
+    if (!find_work<R, KB, 2, NT, false>(p, reinterpret_cast<int*>(smem), k)) return;
 
     for (long u = k.u; u < k.end && k.hg < p.groups; k.it0 = 0) {
-        RowBlock b;
-        if (!row_block(p.map, p.G, R, k.v, b)) {   // an empty number of a packed batch
+        RowBlock b = k.b;
+        if (!k.known && !row_block(p.map, p.G, R, k.v, b)) {   // an empty number of a packed batch
             if (!p.wgs) return;
             if (++k.v == p.blocks) {
                 k.v = 0;
@@ -363,7 +382,8 @@ __global__ void __launch_bounds__((64 * Few<T, D, RT>::NW), (Few<T, D, RT>::NW /
             }
             continue;
         }
-        const int ctx = p.ctx[b.seq], keys = keys_of(p, b, R);
+        const int ctx = k.known ? k.ctx : p.ctx[b.seq], keys = keys_of(p, b, ctx, R);
+        k.known = false;
         const int units = max((keys + KB - 1) / KB, 1), it0 = k.it0;
         const int it1 = p.wgs ? (int)min((long)units, it0 + (k.end - u)) : units;
         const bool whole = it0 == 0 && it1 == units;
@@ -632,14 +652,14 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_l
     const int at_v = sizeof(T) == 2 ? (4 * h2 + ((lane & 15) >> 2)) * SV + (lane & 16) + 4 * (lane & 3) : 4 * h2 * SV + n;
 
     Work k;
-    if (!find_work<R, KB, 1, 256, true>(p, k)) return;
+    if (!find_work<R, KB, 1, 256, true>(p, reinterpret_cast<int*>(smem), k)) return;
     long u = k.u;
     const long end = k.end;
     int v = k.v, hk = k.hg, it0 = k.it0;
 
     for (; u < end && hk < p.Hkv; it0 = 0) {
-        RowBlock b;
-        if (!row_block(p.map, p.G, R, v, b)) {   // an empty number of a packed batch
+        RowBlock b = k.b;
+        if (!k.known && !row_block(p.map, p.G, R, v, b)) {   // an empty number of a packed batch
             if (!p.wgs) return;
             if (++v == p.blocks) {
                 v = 0;
@@ -647,7 +667,8 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_l
             }
             continue;
         }
-        const int ctx = p.ctx[b.seq], keys = keys_of(p, b, R);
+        const int ctx = k.known ? k.ctx : p.ctx[b.seq], keys = keys_of(p, b, ctx, R);
+        k.known = false;
         const int units = max((keys + KB - 1) / KB, 1);
         const int it1 = p.wgs ? (int)min((long)units, it0 + (end - u)) : units;
         const bool whole = it0 == 0 && it1 == units;
@@ -783,8 +804,7 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_l
                     for (int r = 0; r < 16; ++r) O[m][r] *= down;
             }
             const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll
-            for (int x = 0; x < NX; ++x) {
+            auto weigh = [&](int x) {   // scores of 32 keys to probabilities
                 float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
@@ -792,7 +812,8 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_l
                     part[r & 3] += s[x][r];
                 }
                 sum += (part[0] + part[1]) + (part[2] + part[3]);
-            }
+            };
+            weigh(0);
 #pragma unroll
             for (int kb = 0; kb < KT / 16; ++kb) {
                 V8 next[MD];
@@ -801,9 +822,11 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_l
                     for (int m = 0; m < MD; ++m) next[m] = tr32(tv, SV, 16 * (kb + 1), 32 * m, 0);
                 }
                 const V8 pf = rows16<T>(s[kb / 2], kb % 2);
-                __builtin_amdgcn_sched_barrier(0);
+                
 #pragma unroll
                 for (int m = 0; m < MD; ++m) O[m] = mma32(vf[m], pf, O[m]);
+                if (kb % 2 == 0 && kb / 2 + 1 < NX) weigh(kb / 2 + 1);
+
                 if (kb + 1 < KT / 16) {
 #pragma unroll
                     for (int m = 0; m < MD; ++m) vf[m] = next[m];
@@ -1037,7 +1060,7 @@ Plan make_plan(int T, int N, int Hkv, int G, bool packed) {
     return pl;
 }
 
-template <class T, int D, int R> hipError_t attend(const PagedArgs& a, const Plan& pl) {
+template <class T, int D, int R> hipError_t attend(const PagedArgs& a, Plan pl) {
     AttnParams p{};
     p.q = a.q; p.Kp = a.Kp; p.Vp = a.Vp; p.ctx = a.ctx; p.tree = a.tree; p.out = a.out; p.lse = a.lse;
     p.pages = make_pages(a);
@@ -1049,6 +1072,7 @@ template <class T, int D, int R> hipError_t attend(const PagedArgs& a, const Pla
     p.capacity = std::min((long)a.width * a.page_size, 0x7ffff000L);
     p.scale = a.scale;
     p.blocks = (int)pl.blocks;
+    if ((p.capacity / 32 + 1) * pl.blocks > 0x7fffffffL) pl.shared = false;   // units are counted in 31 bits
     const size_t items = (size_t)pl.blocks * p.groups;
     if (pl.shared) {
         p.wgs = shared_wgs(R);

@@ -631,6 +631,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _run(device, stream, call):
     """call(stream handle) with the inputs' device current, and on a given stream
     with that stream current too, so that what the call allocates comes from its
@@ -638,10 +641,11 @@ def _run(device, stream, call):
     if stream is not None:
         with torch.cuda.device(device), torch.cuda.stream(stream):
             return call(stream.cuda_stream)
-    if torch.cuda.current_device() == device.index:
-        return call(_raw_stream(device.index))
+    index = device.index
+    if _current_device() == index:
+        return call(_raw_stream(index))
     with torch.cuda.device(device):
-        return call(_raw_stream(device.index))
+        return call(_raw_stream(index))
 
 
 def _addr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -948,16 +952,24 @@ def swa_cache_fill(k, v, K_cache, V_cache, window: int, sinks: int = 0, cu_seqle
 
 # ---------------------------------------------------------------- gated linear recurrence
 
+def _as_it_is(t, dtype, index) -> bool:
+    """Whether a tensor can be handed on: what `_check_input` asks for, in one go."""
+    return t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+
+
 def _check_glr(gate, x, cu_seqlens, lead):
     """Shapes, dtypes and devices of a recurrence whose x has `lead` dims before
-    the channels. Returns (those dims, C)."""
-    if x.dim() != lead + 1:
-        raise ValueError("x must have %d dims, got %s" % (lead + 1, tuple(x.shape)))
-    if cu_seqlens is not None and x.shape[0] != 1:
-        raise ValueError("packed sequences (cu_seqlens) need B = 1, got %d" % x.shape[0])
-    _check_input("x", x, x.dtype, x.device)
-    _like("gate", gate, x.shape, torch.float32 if gate.dtype == torch.float32 else x.dtype, x.device)
-    return x.shape[:-1], x.shape[-1]
+    the channels. Returns x's shape."""
+    shape, dtype, index = x.shape, x.dtype, x.get_device()
+    if len(shape) != lead + 1:
+        raise ValueError("x must have %d dims, got %s" % (lead + 1, tuple(shape)))
+    if cu_seqlens is not None and shape[0] != 1:
+        raise ValueError("packed sequences (cu_seqlens) need B = 1, got %d" % shape[0])
+    gate_dtype = torch.float32 if gate.dtype is torch.float32 else dtype
+    if index < 0 or not x.is_contiguous() or gate.shape != shape or not _as_it_is(gate, gate_dtype, index):
+        _check_input("x", x, dtype, x.device)
+        _like("gate", gate, shape, gate_dtype, x.device)
+    return shape
 
 
 def _check_vector_state(name, t, N, C, device):
@@ -984,7 +996,7 @@ def glr_fwd(gate, x, h0=None, cu_seqlens=None, out: Optional[torch.Tensor] = Non
     x [B,T,C]; gate [B,T,C] in the same dtype or fp32; h0 [N,C] fp32 or None;
     cu_seqlens int32 [N+1] on the device (B must be 1) or None. Returns (h in the
     dtype of x, h_T fp32 or None)."""
-    (B, T), C = _check_glr(gate, x, cu_seqlens, 2)
+    B, T, C = _check_glr(gate, x, cu_seqlens, 2)
     device, dt = x.device, _dtype_code(x)
     varlen, N = _check_varlen(cu_seqlens, B, device)
     _check_vector_state("h0", h0, N, C, device)
@@ -1013,9 +1025,10 @@ def glr_bwd(gate, x, dh, h0=None, dh_T=None, cu_seqlens=None, want_dh0: bool = T
     Inputs as for glr_fwd; dh [B,T,C] in the dtype of x; dh_T fp32 [N,C] or None.
     Returns a dict of dgate (dtype of gate), dx (dtype of x) and dh0 (fp32, None
     when not wanted). ``out`` may supply that dict's tensors."""
-    (B, T), C = _check_glr(gate, x, cu_seqlens, 2)
+    B, T, C = _check_glr(gate, x, cu_seqlens, 2)
     device, dt = x.device, _dtype_code(x)
-    _like("dh", dh, x.shape, x.dtype, device)
+    if dh.shape != x.shape or not _as_it_is(dh, x.dtype, x.get_device()):
+        _like("dh", dh, x.shape, x.dtype, device)
     varlen, N = _check_varlen(cu_seqlens, B, device)
     _check_vector_state("h0", h0, N, C, device)
     _check_vector_state("dh_T", dh_T, N, C, device)
@@ -1046,9 +1059,10 @@ def glr_decode_step(gate, x, h, out: Optional[torch.Tensor] = None, stream=None)
     """One step of the gated linear recurrence, h [N,C] fp32 updated in place
     (kda_glr_decode_step). x [N,C]; gate [N,C] in the same dtype or fp32. Returns
     the new state in the dtype of x."""
-    (N,), C = _check_glr(gate, x, None, 1)
+    N, C = _check_glr(gate, x, None, 1)
     device, dt = x.device, _dtype_code(x)
-    _like("h", h, (N, C), torch.float32, device)
+    if h.shape != x.shape or not _as_it_is(h, torch.float32, x.get_device()):
+        _like("h", h, (N, C), torch.float32, device)
     if out is not None:
         _like("out", out, x.shape, x.dtype, device)
 
@@ -1071,20 +1085,25 @@ def _check_paged(rows, K_pages, V_pages, block_table, ctx_len, cu_seqlens):
     if rows.dim() != 4 or K_pages.dim() != 4:
         raise ValueError("rows must be [B,T,H,d] and pages [pages,page,Hkv,d], got %s and %s" % (tuple(rows.shape),
                                                                                                 tuple(K_pages.shape)))
-    (B, T, H, d), (pages, page, Hkv, _) = rows.shape, K_pages.shape
-    dtype, device = rows.dtype, rows.device
+    (B, T, H, d), (pages, page, Hkv, d_pages) = rows.shape, K_pages.shape
+    dtype, device, index = rows.dtype, rows.device, rows.get_device()
     if cu_seqlens is not None and B != 1:
         raise ValueError("packed sequences (cu_seqlens) need B = 1, got %d" % B)
     if Hkv == 0 or H % Hkv:
         raise ValueError("%d heads are not a multiple of the cache's %d" % (H, Hkv))
     varlen, N = _check_varlen(cu_seqlens, B, device)
-    _like("K_pages", K_pages, (pages, page, Hkv, d), dtype, device)
-    _like("V_pages", V_pages, (pages, page, Hkv, d), dtype, device)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [N,width], got %s" % (tuple(block_table.shape),))
-    _like("block_table", block_table, (N, block_table.shape[1]), torch.int32, device)
-    _like("ctx_len", ctx_len, (N,), torch.int32, device)
-    return B, T, varlen, N, Hkv, d, pages, page, block_table.shape[1]
+    rows_of_table, width = block_table.shape
+    if (index < 0 or d_pages != d or V_pages.shape != K_pages.shape or rows_of_table != N or ctx_len.shape != (N,)
+            or not rows.is_contiguous() or not _as_it_is(K_pages, dtype, index) or not _as_it_is(V_pages, dtype, index)
+            or not _as_it_is(block_table, torch.int32, index) or not _as_it_is(ctx_len, torch.int32, index)):
+        _check_input("rows of the new tokens", rows, dtype, device)
+        _like("K_pages", K_pages, (pages, page, Hkv, d), dtype, device)
+        _like("V_pages", V_pages, (pages, page, Hkv, d), dtype, device)
+        _like("block_table", block_table, (N, width), torch.int32, device)
+        _like("ctx_len", ctx_len, (N,), torch.int32, device)
+    return B, T, varlen, N, Hkv, d, pages, page, width
 
 
 def paged_append(k, v, K_pages, V_pages, block_table, ctx_len, q=None, pos=None, freqs=None, interleaved: bool = False,
@@ -1101,14 +1120,16 @@ def paged_append(k, v, K_pages, V_pages, block_table, ctx_len, q=None, pos=None,
     device, dt = k.device, _dtype_code(k)
     if k.shape[2] != Hkv:
         raise ValueError("k has %d heads, the cache %d" % (k.shape[2], Hkv))
-    _check_input("k", k, k.dtype, device)
-    _like("v", v, k.shape, k.dtype, device)
+    index = k.get_device()
+    if v.shape != k.shape or not _as_it_is(v, k.dtype, index):
+        _like("v", v, k.shape, k.dtype, device)
     Hq = Hkv
     if q is not None:
         if q.dim() != 4 or q.shape[2] % Hkv:
             raise ValueError("q must be [B,T,Hq,d], Hq a multiple of %d, got %s" % (Hkv, tuple(q.shape)))
         Hq = q.shape[2]
-        _like("q", q, (B, T, Hq, d), k.dtype, device)
+        if q.shape != (B, T, Hq, d) or not _as_it_is(q, k.dtype, index):
+            _like("q", q, (B, T, Hq, d), k.dtype, device)
         if q_out is not None:
             _like("q_out", q_out, q.shape, k.dtype, device)
     elif q_out is not None:
@@ -1151,7 +1172,6 @@ def paged_attn(q, K_pages, V_pages, block_table, ctx_len, tree=None, scale: Opti
     None); a row that sees no key has o = 0 and lse = -inf."""
     B, T, varlen, N, Hkv, d, pages, page, width = _check_paged(q, K_pages, V_pages, block_table, ctx_len, cu_seqlens)
     device, dt, Hq = q.device, _dtype_code(q), q.shape[2]
-    _check_input("q", q, q.dtype, device)
     words = 0
     if tree is not None:
         if tree.dim() != 3 or tree.shape[2] < 1:
