@@ -1052,11 +1052,20 @@ struct Plan {
     long blocks;
     bool shared;
 };
+// Keys are shared out among workgroups, or every block of rows and head (group) is a
+// workgroup's own. bf16, 128 channels, 32 / 8 heads, shared and then not, us. Few rows:
+// 400 sequences of 100 to 4,096 tokens 586 and 816, 900 of 100 to 2,048 679 and 784:
+// shared as long as the plan can count the blocks. More rows, items of 64 sequences of
+// 100 to 8,192 tokens with 32 new ones (512 items) 293 and 354, of 100 (800) 446 and 526;
+// from 1,024 items on they fill the chip by themselves, and the parts' sums cost more than
+// the evener split gives: 128 of 2,048 tokens with 16 new ones 222 and 213, prompts of
+// 16 x 512 tokens (16 / 4 heads) 72 and 47.
 Plan make_plan(int T, int N, int Hkv, int G, bool packed) {
     Plan pl;
     pl.R = block_rows(T, N, G, packed);
     pl.blocks = row_blocks_bound(T, N, G, pl.R, packed);
-    pl.shared = pl.blocks <= MAX_BLOCKS && pl.blocks * Hkv < 2048;
+    const long items = pl.blocks * Hkv;
+    pl.shared = pl.blocks <= MAX_BLOCKS && items * pl.R < 1 << 24 && (pl.R <= 32 || items < 1024);
     return pl;
 }
 
@@ -1125,7 +1134,7 @@ template <class T, int D> hipError_t append(const PagedArgs& a) {
 
 bool paged_attn_fits(int T, int N, int Hq, int Hkv, bool packed) {
     const Plan pl = make_plan(T, N, Hkv, Hq / Hkv, packed);
-    return pl.shared ? pl.blocks * Hkv * pl.R < (1 << 24) : pl.blocks * Hkv < (1 << 24);
+    return pl.shared || pl.blocks * Hkv < 1 << 24;
 }
 
 size_t paged_attn_workspace_bytes(int T, int N, int Hq, int Hkv, int d, bool packed) {
