@@ -320,7 +320,8 @@ struct Seen {
     __device__ __forceinline__ uint32_t operator()(int j0) const {
         const int d = j0 - ctx;   // among the new tokens
         if (bits == nullptr) {
-            const int m = min(max(tok - d + 1, 0), 32);
+            // (a context may be any number: tok - d without a sign)
+            const uint32_t m = tok >= d ? min((uint32_t)tok - (uint32_t)d, 31u) + 1u : 0u;
             return m == 32 ? ~0u : (1u << m) - 1u;
         }
         if (d <= -32) return ~0u;
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__((64 * Few<T, D, RT>::NW), (Few<T, D, RT>::NW /
             if (more) fetch_v(d, next[d.value]);
             where[d.value] = next[d.value];
             next[d.value] = lookup(it + 2 * DEPTH * KS);
-            const bool all = held == ~0u && j0 + 31 <= (p.tree ? ctx - 1 : ctx + b.r0 / p.G);   // every row sees every key
+            const bool all = held == ~0u && j0 + 31 - (p.tree ? -1 : b.r0 / p.G) <= ctx;   // every row sees every key
             bf16pair pb[RT];
             f32x8 pf[RT];
 #pragma unroll
@@ -852,8 +853,8 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_l
             }
             const int j0 = (it * KS + wk) * KT;
             if (now) {
-                const int last_seen = p.tree ? ctx - 1 : ctx + (b.r0 + 32 * wr) / p.G;   // by every row of this wave
-                tile(t, t + KT * ST, j0, now, now != ALL || j0 + KT - 1 > last_seen);
+                const int own = p.tree ? -1 : (b.r0 + 32 * wr) / p.G;   // the last new token that every row of this wave sees
+                tile(t, t + KT * ST, j0, now, now != ALL || j0 + KT - 1 - own > ctx);
             }
         }
         sum = swap_sum(sum);
@@ -1134,7 +1135,7 @@ template <class T, int D> hipError_t append(const PagedArgs& a) {
 
 bool paged_attn_fits(int T, int N, int Hq, int Hkv, bool packed) {
     const Plan pl = make_plan(T, N, Hkv, Hq / Hkv, packed);
-    return pl.shared || pl.blocks * Hkv < 1 << 24;
+    return pl.shared || pl.blocks * Hkv < 1 << 23;
 }
 
 size_t paged_attn_workspace_bytes(int T, int N, int Hq, int Hkv, int d, bool packed) {

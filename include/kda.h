@@ -483,11 +483,16 @@ int kda_swa_cache_fill(const void* k, const void* v, void* K_cache, void* V_cach
  * behind cu_seqlens[N] are left as they are. A NaN or Inf at a token reaches the
  * later outputs of its sequence and channel, no others.
  *
- * C <= 2^20, and N * (T + 128) < 2^31; KDA_ENOTSUP beyond, and where one launch
- * does not take the blocks of 64 tokens and 64 channels. Arrays of rows are 16-byte aligned where C is
- * a multiple of 8 (fp32 x: of 4), else to their element; the workspace is 16-byte aligned,
- * states to their element. workspace: kda_glr_fwd_workspace_bytes(...) bytes,
- * required. Returns KDA_OK or a negative status.
+ * C <= 2^20, and N * (T + 128) < 2^31; KDA_ENOTSUP beyond, and where blocks of
+ * 128 tokens (64 where C is no multiple of 8, fp32 x: of 4) and 64 channels are
+ * more than one launch takes. Arrays of rows are 16-byte aligned where C is such a
+ * multiple, else to their element; the workspace is 16-byte aligned, states to
+ * their element. workspace: kda_glr_fwd_workspace_bytes(...) bytes, required; calls
+ * that may overlap (two streams, two captured graphs) need one each. Repeated calls
+ * agree bit for bit. Inside a launch blocks wait for what earlier ones leave in the
+ * workspace; a wait that never ended, as when a call is given a workspace that
+ * another one is using, is given up and leaves NaN. Returns KDA_OK or a negative
+ * status.
  */
 size_t kda_glr_fwd_workspace_bytes(int B, int T, int C, int N, int has_cu_seqlens, int dtype);
 int kda_glr_fwd(const void* gate, const void* x, const float* h0, void* h, float* h_T, int B, int T, int C,
@@ -500,8 +505,9 @@ int kda_glr_fwd(const void* gate, const void* x, const float* h0, void* h, float
  * type of gate, grad_x in that of x, grad_h0 [N, C] fp32 or NULL when not
  * wanted. Nothing of a forward call is reused: the states are formed again in
  * fp32. Outputs must not alias inputs; rows at or behind cu_seqlens[N] are left
- * as they are. A NaN or Inf in x reaches grad_gate of the later tokens only. workspace:
- * kda_glr_bwd_workspace_bytes(...) bytes, required.
+ * as they are. A NaN or Inf in x reaches grad_gate of the later tokens only.
+ * workspace: kda_glr_bwd_workspace_bytes(...) bytes, required, one for each of the
+ * calls that may overlap.
  */
 size_t kda_glr_bwd_workspace_bytes(int B, int T, int C, int N, int has_cu_seqlens, int dtype);
 int kda_glr_bwd(const void* gate, const void* x, const float* h0, const void* dh, const float* dh_T, void* grad_gate,

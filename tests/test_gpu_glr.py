@@ -233,6 +233,23 @@ def test_repeats_and_streams_and_graph(kda):
     assert all(torch.equal(a, b) for a, b in zip(held, want))
 
 
+def test_calls_at_once(kda):
+    """Two streams in turn, a workspace each, over sequences of many blocks."""
+    xs = [make(1, 6000, 520, BF16, BF16, seed=i) for i in range(2)]
+    args = [(x["gate"], x["x"]) for x in xs]
+    want = [kda.glr_fwd(*a, h0=x["h0"]) for a, x in zip(args, xs)]
+    side = [torch.cuda.Stream() for _ in xs]
+    ws = [torch.empty(kda.glr_fwd_workspace_bytes(1, 6000, 520), dtype=torch.uint8, device="cuda") for _ in xs]
+    outs = [[(torch.empty_like(x["x"]), torch.empty_like(x["h0"])) for _ in range(6)] for x in xs]
+    torch.cuda.synchronize()
+    for n in range(6):
+        for i, x in enumerate(xs):
+            kda.glr_fwd(*args[i], h0=x["h0"], out=outs[i][n][0], h_T=outs[i][n][1], workspace=ws[i], stream=side[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(h, want[i][0]) and torch.equal(h_T, want[i][1]) for h, h_T in outs[i])
+
+
 def test_gradient_against_differences(kda):
     """Central differences of the loss in fp32 inputs, formed by the oracle in 64 bits
     so that only the step's own error (its square) is left."""

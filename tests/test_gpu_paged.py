@@ -132,6 +132,38 @@ def test_many_sequences(kda, dtype):
     check(kda, make([(i * 5) % 9 for i in range(260)], [(13 * i) % 90 for i in range(260)], 8, 8, 32, dtype, 16))
 
 
+@pytest.mark.parametrize("kind", [None, "any"])
+def test_items_on_either_side_of_sharing(kda, kind):
+    """Blocks of 64 and 128 rows by kv heads from 1,000 to 1,040, single tokens of more
+    sequences than a plan counts, and just as many."""
+    for N in (125, 130):
+        for T in (10, 20):
+            check(kda, make([T] * N, [(11 * i) % 90 for i in range(N)], 32, 8, 32, BF16, 16, tree=kind, packed=False, seed=N))
+    for N in (1024, 1100):
+        check(kda, make([1] * N, [(7 * i) % 60 for i in range(N)], 4, 2, 32, BF16, 16, tree=kind, packed=False, seed=N))
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_tables_wider_than_units_are_counted(kda, T):
+    """Pages by width past 2^31 rows, for more sequences than 31 bits of units hold."""
+    N, page = 40, 2 ** 20
+    x = make([T] * N, [(7 * i) % 200 for i in range(N)], 2, 1, 32, BF16, 16, packed=False)
+    y = dict(x, Kp=torch.zeros((2, page, 1, 32), dtype=BF16, device="cuda"), Vp=torch.zeros((2, page, 1, 32), dtype=BF16, device="cuda"),
+             table=torch.full((N, 4096), -1, dtype=torch.int32, device="cuda"))
+    g = torch.Generator().manual_seed(T)
+    y["table"][:, 0] = torch.arange(N, device="cuda") % 2
+    for p in ("Kp", "Vp"):
+        y[p][:, :256] = torch.randn((2, 256, 1, 32), generator=g).to(BF16).cuda()
+    o, lse = attend(kda, y)
+    z = dict(y, Kp=y["Kp"][:, :256].contiguous(), Vp=y["Vp"][:, :256].contiguous(), table=y["table"][:, :1].contiguous())
+    torch.cuda.synchronize()
+    check(kda, z)
+    cpu = {n: t.cpu() if torch.is_tensor(t) else t for n, t in z.items()}
+    ro, rl, size, bound = ref.paged_attn(cpu["q"], cpu["Kp"], cpu["Vp"], cpu["table"], cpu["ctx"], None, 32 ** -0.5, x["seqs"])
+    close("o", o.cpu(), ro, BF16, size=size)
+    assert ((lse.cpu().double() - rl).abs() <= bound).all()
+
+
 @pytest.mark.parametrize("scale", [-0.3, 0.0, 1.0])
 def test_scales(kda, scale):
     for dtype in (BF16, F32):
@@ -171,6 +203,20 @@ def test_contexts_beyond_the_table(kda):
     p, _ = attend(kda, y)
     torch.cuda.synchronize()
     assert torch.equal(o, p)
+
+
+@pytest.mark.parametrize("kind", [None, "tree"])
+@pytest.mark.parametrize("T", [4, 9, 70])
+def test_contexts_beyond_a_short_table(kda, T, kind):
+    """The same within one tile: sums with the context must not wrap around."""
+    x = make([T, T], [20, 20], 4, 2, 64, BF16, 16, tree=kind, packed=False)
+    x["table"] = x["table"][:, :1].contiguous()
+    x["ctx"][0] = 2 ** 31 - 1
+    x["ctx"][1] = 2 ** 31 - 2
+    o, lse = attend(kda, x)
+    p, plse = attend(kda, dict(x, ctx=torch.tensor([16, 16], dtype=torch.int32).cuda()))
+    torch.cuda.synchronize()
+    assert torch.equal(o, p) and torch.equal(lse, plse) and lse.isfinite().all()
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
