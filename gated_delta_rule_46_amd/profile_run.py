@@ -16,8 +16,8 @@ call, three calls), whose counter readings calibrate FETCH_SIZE and
 WRITE_SIZE against a known byte count.
 
 --mixers runs listed cases of perf/operators.py (linear attention and window
-attention), --mixer-calls calls of each on three sets of inputs in turn; alone,
-with --fwd 0 --bwd 0 --decode 0. --rates prints what large copies and
+attention) and perf/more_operators.py (gated linear recurrence, paged cache),
+--mixer-calls calls of each on three sets of inputs in turn; alone, with --fwd 0 --bwd 0 --decode 0. --rates prints what large copies and
 large matrix products reach on this card, and both one-token state updates
 (decode_step, linattn_decode_step) on one state and on three in turn.
 """
@@ -32,9 +32,9 @@ import sys
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
-def operators():
-    """perf/operators.py, set to the library's own calls."""
-    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+def operators(name):
+    """perf/<name>.py, set to the library's own calls."""
+    spec = importlib.util.spec_from_file_location(name, os.path.join(ROOT, "perf", name + ".py"))
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
     m.own = True
@@ -140,8 +140,8 @@ def main(argv=None) -> int:
         print("decode steps: %d" % args.decode, flush=True)
         del S, steps, od
     if args.mixers:
-        m = operators()
-        for case in m.listed():
+        files = [operators(name) for name in ("operators", "more_operators")]
+        for m, case in [(m, case) for m in files for case in m.listed()]:
             if args.mixers != "all" and case["name"] not in args.mixers.split(","):
                 continue
             states = [m.prepare(case, seed) for seed in range(3)]

@@ -4,6 +4,7 @@
     python -m gated_delta_rule_46_amd.profile_summary traffic FETCH_DIR WRITE_DIR NAME --command C [--command C2]
     python -m gated_delta_rule_46_amd.profile_summary mfma PMC_DIR STATS_DIR OUT.md --command C
     python -m gated_delta_rule_46_amd.profile_summary mixers DIR OUT.md --command C [--command C2]
+                                                       [--title T] [--cases F]
 
 ``stats`` turns the kernel-stats CSV of a ``rocprofv3 --kernel-trace --stats
 --output-format csv`` run into a markdown table (calls, average, minimum and
@@ -219,8 +220,8 @@ def _counters(d: str):
 
 
 def cmd_mixers(a) -> int:
-    out = ["# Linear attention and window attention: kernels by case", "",
-           "Commands for each CASE, a listed case of `perf/operators.py` (MI355X, gfx950, one GPU; every counter set in a run "
+    out = ["# %s: kernels by case" % a.title, "",
+           "Commands for each CASE, a listed case of `" + a.cases + "` (MI355X, gfx950, one GPU; every counter set in a run "
            "of its own; `$REPO` is the repository root):", "", "```"] + list(a.command) + ["```", "",
            "Per dispatch. Durations: median and shortest of the traced run. Bytes: FETCH_SIZE and WRITE_SIZE, calibrated on the "
            "copies of the same run, from and to HBM and its cache (a mean of the run's calls, on three sets of inputs in turn). "
@@ -280,6 +281,8 @@ def main(argv=None) -> int:
     x = sub.add_parser("mixers")
     x.add_argument("dir")
     x.add_argument("out")
+    x.add_argument("--title", default="Linear attention and window attention")
+    x.add_argument("--cases", default="perf/operators.py")
     x.add_argument("--command", action="append", required=True)
     x.add_argument("--copy-mib", type=int, default=256)
     a = ap.parse_args(argv)
