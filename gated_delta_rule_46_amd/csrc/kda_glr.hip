@@ -15,7 +15,13 @@
 // again from a and x in fp32.
 //
 // In a block, a thread owns V channels and R consecutive tokens (a slot); slots
-// are joined through LDS in the same way, one channel a thread.
+// are joined through LDS in the same way, one channel a thread. States, products of
+// decays and sums are fp32 throughout; results are rounded once.
+//
+// Bound by memory (2 operations an element). bf16, B=2 C=2048: forward of T=8192 45 us for
+// 213 MB at 4.8 TB/s, and 3 to 5 us for the clear before it; gradient of T=4096 20 us (sums,
+// 5.1 TB/s) and 32 us (5.2 TB/s): it reads its inputs twice, as one pass would need both
+// the states from the front and the adjoints from the back.
 #include <algorithm>
 #include <type_traits>
 
@@ -203,7 +209,7 @@ template <class TG, class TX, int V, int R, bool GRAD> struct Block {
     }
 };
 
-// gradient: every block's P, E and F
+// gradient: every block's P, E and F (reads a, x and dh once: 100 MB in 20 us)
 template <class TG, class TX, int V, int R> __global__ void __launch_bounds__(NT) glr_sum_kernel(GlrParams p) {
     using B = Block<TG, TX, V, R, true>;
     lds_poison(0);
@@ -447,7 +453,9 @@ __device__ __forceinline__ Run take_up(const uint64_t* w, long step, int count) 
 // counter), so that a block's predecessors have started before it. A block leaves P and E;
 // the first of a sequence, which alone reads h0 (h_T may be h0), and every GROUP-th leave
 // the state behind them instead, so that no block looks back over more than GROUP words. Which
-// words a block takes up, and in which order, does not depend on when they came.
+// words a block takes up, and in which order, does not depend on when they came. GROUP: one
+// sequence of T=131072, C=256 takes 128, 81 and 71 us with states at every 8th, 16th and 32nd
+// block. A third workgroup a CU would spill (58 us against 49 at B=2 T=8192 C=2048).
 template <class TG, class TX, int V, int R> __global__ void __launch_bounds__(NT) glr_pass_kernel(GlrParams p) {
     using B = Block<TG, TX, V, R, false>;
     constexpr int TILE = B::TILE, SLOTS = B::SLOTS;
@@ -530,7 +538,9 @@ template <class TG, class TX, int V, int R> __global__ void __launch_bounds__(NT
 
 // Forward of a batch whose sequences and tiles fill the chip: a workgroup takes a tile of
 // one sequence through all its blocks, the next one's loads under way, and reads everything
-// once.
+// once. Taken from 256 such pairs on, one a CU: B=32 T=1024 C=1024 bf16 39 us against the
+// single pass's 47, B=16 T=4096 C=2048 157 against 155; with 128 of them it is slower
+// (B=8 T=4096 C=2048, 99 against 86).
 template <class TG, class TX, int V, int R> __global__ void __launch_bounds__(NT, 2) glr_stream_kernel(GlrParams p) {
     using B = Block<TG, TX, V, R, false>;
     constexpr int TILE = B::TILE, SLOTS = B::SLOTS, ROWS = B::L::ROWS;
@@ -577,6 +587,8 @@ template <class TG, class TX, int V, int R> __global__ void __launch_bounds__(NT
 
 // ---------------------------------------------------------------- one token
 
+// The state once in and out, with everything else beside it: 256 sequences of 4,096 channels
+// bf16 4.0 us for 14.7 MB (a launch's own time is most of it).
 template <class TG, class TX, int V> __global__ void __launch_bounds__(NT) glr_decode_kernel(const TG* __restrict__ gate, const TX* __restrict__ x, float* __restrict__ h, TX* __restrict__ o, size_t n) {
     lds_poison(0);
     const size_t at = ((size_t)blockIdx.x * NT + threadIdx.x) * V;
@@ -603,7 +615,6 @@ constexpr int pass_rows(bool wide, bool bf16) {
     return !wide ? Lay<1, pass_r<1>()>::ROWS : bf16 ? Lay<8, pass_r<8>()>::ROWS : Lay<4, pass_r<4>()>::ROWS;
 }
 constexpr int grad_rows(bool wide) { return wide ? 128 : 64; }
-
 
 template <class F> auto with_types(bool bf16, bool gate_bf16, bool wide, F f) {
     using U = uint16_t;

@@ -81,7 +81,10 @@ __device__ __forceinline__ bool token_place(const SeqMap& m, int t, int& seq, in
 // A wave takes a token: cosines and sines of its angles once, then the rows of
 // all its heads, two pieces of 16 bytes a lane that hold each other's partners.
 // Angles are formed and reduced to one turn in 64 bits (position and frequency
-// are exact, their product is at positions where 32 bits have no fraction left).
+// are exact, their product is at positions where 32 bits have no fraction left),
+// the rest is fp32, rounded once. Bound by memory: 7,213 tokens of eight prompts,
+// 16 and 4 heads of 128 channels, bf16 16.9 us at 5.2 TB/s; 46 drafted tokens 4.2 us,
+// most of it the way from the offsets over the table to the rows.
 template <class T, int D> __global__ void __launch_bounds__(256) paged_append_kernel(AppendParams p, bool neighbours) {
     lds_poison(0);
     __shared__ float s_cos[4][64], s_sin[4][64];
@@ -222,7 +225,8 @@ __device__ __forceinline__ int keys_of(const AttnParams& p, const RowBlock& b, i
 
 // What a workgroup takes: units (KB keys of one item, a block and a group of kv heads)
 // [u, end), counted over the blocks, then the groups; unit u is number it0 of item (v, hg).
-// total: of all.
+// total: of all. Contexts are only known on the device: every workgroup counts all blocks'
+// units for itself (2 us at 64 sequences), in place of a launch that does it once.
 struct Work {
     long u, end, total;
     int v, hg, it0, wgs, wg;
@@ -344,10 +348,16 @@ template <class T> constexpr int v_stride32(int d) { return sizeof(T) == 2 ? (d 
 
 // Up to 16 RT rows a block, tiles of 16x16 and 32 deep. A wave has one kv head and tiles
 // of 32 keys of its own; the waves of a workgroup take HW heads of the same keys, which lie
-// side by side in memory, and every KS-th tile where there are fewer heads than waves. Keys go from memory to the operand as they lie (a lane
-// has 8 values of one key), values through the wave's own LDS for the transposing
-// read; the next DEPTH tiles' loads are under way while a tile is worked on. A lane
-// owns one row of the scores, whose layout is the next product's operand (kpos order).
+// side by side in memory, and every KS-th tile where there are fewer heads than waves. Keys
+// go from memory to the operand as they lie (a lane has 8 values of one key), values through
+// the wave's own LDS for the transposing read; the next DEPTH tiles' loads are under way
+// while a tile is worked on. A lane owns one row of the scores, whose layout is the next
+// product's operand (kpos order). bf16 probabilities enter it as two bf16 numbers (3 of 40 us
+// at 8 sequences of 8,192 tokens): o is then off by no more than its own rounding.
+// Bound by memory: one token of 64 sequences of 100 to 4,096 tokens, 32 and 8 heads of 128
+// channels, bf16 115 us at 4.8 TB/s, of 4,096 tokens each 197 us at 5.5. Small calls: 13 us
+// for 2,048 to 8,192 tokens of one sequence, of which 2 are the plan's, 2 to 4 the loads' way
+// and 2 to 4 the join of the waves' shares. Two tiles ahead with 32 rows spill (89 us, one 49).
 template <class T, int D, int RT> struct Few {
     // one workgroup a CU, of as many waves as registers leave room for
     static constexpr int NW = sizeof(T) == 4 && D == 128 ? 4 : 8, DEPTH = RT == 1 ? 2 : 1, R = 16 * RT;
@@ -621,8 +631,17 @@ __global__ void __launch_bounds__((64 * Few<T, D, RT>::NW), (Few<T, D, RT>::NW /
 
 // ---------------------------------------------------------------- more rows
 
-// Rows' tiles of 32 a workgroup has (RW), and the groups of waves (KS = 4 / RW) that
-// take every KS-th tile of keys each.
+// Scores and o of 32 rows a wave on 32x32 tiles: rows stay in registers (a lane owns one),
+// keys and values come through LDS, twice over, for the RW waves that share them. RW: rows'
+// tiles of 32 a workgroup has; KS = 4 / RW groups of waves take every KS-th tile of keys each.
+// bf16 probabilities are rounded to bf16 once, for a single product (o off by 1.4 times its
+// own rounding). Bound by the turns that scores, exponentials and products take within two
+// waves a SIMD: 2,048 tokens over 6,144, 16 and 4 heads of 128 channels, bf16 165 to 178 us
+// (650 to 730 TFLOP/s), matrix units busy for 31%, vector units for 36% of the time, LDS for
+// 23%. Without gain there: 256 rows in eight waves (3 to 6% faster from 2,048 rows and long
+// contexts on, 3 to 5% slower at 256 rows and for short ones), with its two halves of waves a
+// phase apart as well (189 us against 175), two tiles of rows a wave at one wave a SIMD (213),
+// exponentials beside the next tile's scores (207), wave priorities and orders of the loads.
 template <class T, int RW> struct Shape {
     static constexpr int KS = 4 / RW, R = 32 * RW, KT = sizeof(T) == 2 && RW == 4 ? 64 : 32, KB = KS * KT;
 };
@@ -823,11 +842,9 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_l
                     for (int m = 0; m < MD; ++m) next[m] = tr32(tv, SV, 16 * (kb + 1), 32 * m, 0);
                 }
                 const V8 pf = rows16<T>(s[kb / 2], kb % 2);
-                
 #pragma unroll
                 for (int m = 0; m < MD; ++m) O[m] = mma32(vf[m], pf, O[m]);
                 if (kb % 2 == 0 && kb / 2 + 1 < NX) weigh(kb / 2 + 1);
-
                 if (kb + 1 < KT / 16) {
 #pragma unroll
                     for (int m = 0; m < MD; ++m) vf[m] = next[m];
@@ -954,7 +971,8 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_l
 
 // Joins the parts of a shared item's rows, four values a thread, in J workgroups: as many
 // rows at a time as a workgroup has room for, or (SPREAD) one row at a time with its parts
-// spread over the workgroup, for few rows in many parts.
+// spread over the workgroup, for few rows in many parts. Parts are added in their order: the
+// same bits every time. 64 sequences 8.5 us, one of 8,191 tokens 4.8, 2,048 rows 13.7 (60 MB).
 template <class T, int D, int R, bool SPREAD> __global__ void __launch_bounds__(256) paged_join_kernel(AttnParams p, int J) {
     lds_poison(0);
     constexpr int CG = D / 4, RG = 256 / CG;
@@ -1034,7 +1052,10 @@ template <class K, class... P> hipError_t launch(K kern, size_t x, int threads, 
 }
 
 // Rows of a block: as many as the longest run of rows that a sequence can have
-// fills (a packed batch: its mean).
+// fills (a packed batch: its mean). Up to 32 rows go to 16x16 tiles: the other kernel is
+// quicker for 17 to 32 rows of few keys in bf16 at 128 channels (8 sequences of 8 tokens over
+// 8,192: 39 us against 46; 64 over 4,096: 119 and 123) and slower elsewhere (256 of 5 tokens
+// over 2,048: 210 and 199; 32 channels 56 and 49; fp32 140 and 92), and its o is less exact.
 int block_rows(int T, int N, int G, bool packed) {
     const long rows = packed ? ((long)T + N - 1) / N * G : (long)T * G;
     return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;

@@ -24,15 +24,15 @@
  *    The caller owns every buffer.
  *  - Element type of q, k, v, gate and beta is selected by `dtype`:
  *    KDA_BF16 (bfloat16 bits) or KDA_F32. States S0, S_T, S and outputs o
- *    are always fp32, but for o of kda_linattn_* and kda_swa_*, which has
- *    that type too.
+ *    are always fp32, but for o (h) of kda_linattn_*, kda_swa_*, kda_glr_*
+ *    and kda_paged_*, which has that type too.
  *  - `stream` is a hipStream_t (NULL = the default stream). Work is enqueued
  *    and the call returns without synchronising.
  *  - Arguments are validated before any HIP call; nothing is enqueued when
  *    validation fails. Device-side contents (cu_seqlens offsets, NaN/Inf in
  *    inputs) are not checked: NaN/Inf propagate.
  *  - Supported sizes: dk, dv in {16, 32, 64, 128}; chunk in {16, 32, 64}
- *    (kda_swa_*: d in {32, 64, 128}).
+ *    (kda_swa_*, kda_paged_*: d in {32, 64, 128}; kda_glr_*: any C).
  *  - The library never allocates, frees or synchronises device memory in a
  *    compute call: every call that needs scratch space takes a caller-owned
  *    workspace, and a NULL workspace (or a short one) is KDA_EINVAL.
