@@ -147,6 +147,10 @@ def test_attention_workspace(lib):
     for T in (1, 8, 64, 4096):
         for N in (1, 64):
             assert 256 <= f(N, T, 32, 8, 128) <= 1024 * 128 * (128 + 2) * 4 + (1 << 20)
+    # 2^23 blocks of rows by heads would be 2^32 threads
+    assert f(1, 2 ** 20, 1024, 1024, 64) == 0 and f(1, 2 ** 20 - 128, 1024, 1024, 64) == 256
+    # single tokens: shared out as long as a plan can count the sequences
+    assert f(1024, 1, 32, 8, 128) > 256 and f(1025, 1, 32, 8, 128) == 256
 
 
 def test_binding_refusals():
