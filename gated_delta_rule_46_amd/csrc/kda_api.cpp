@@ -849,6 +849,7 @@ int kda_paged_attn(const void* q, const void* K_pages, const void* V_pages, cons
     if (!aligned(K_pages) || !aligned(V_pages) || !aligned(tree, 4) || !aligned(o) || !aligned(lse, 4) || !aligned(workspace))
         return KDA_EALIGN;
     if (workspace_bytes < kda::paged_attn_workspace_bytes(T, a.N, Hq, Hkv, d, cu_seqlens != nullptr)) return KDA_EINVAL;
+    if (o == q) return KDA_EINVAL;   // a row of q is read by several workgroups
     a.Kp = K_pages;
     a.Vp = V_pages;
     a.tree = tree;

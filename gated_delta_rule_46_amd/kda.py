@@ -1168,8 +1168,8 @@ def paged_attn(q, K_pages, V_pages, block_table, ctx_len, tree=None, scale: Opti
     q [B,T,Hq,d]; every token sees its sequence's ctx_len rows before the new ones, and
     of the new ones those that tree int32 [B,T,words] names by bits, or without a tree
     those up to itself. Cache, block_table, ctx_len and cu_seqlens as for paged_append;
-    scale defaults to d ** -0.5. Returns (o in the dtype of q, lse fp32 [B,T,Hq] or
-    None); a row that sees no key has o = 0 and lse = -inf."""
+    out must not be q; scale defaults to d ** -0.5. Returns (o in the dtype of q, lse
+    fp32 [B,T,Hq] or None); a row that sees no key has o = 0 and lse = -inf."""
     B, T, varlen, N, Hkv, d, pages, page, width = _check_paged(q, K_pages, V_pages, block_table, ctx_len, cu_seqlens)
     device, dt, Hq = q.device, _dtype_code(q), q.shape[2]
     words = 0

@@ -570,8 +570,10 @@ int kda_paged_append(const void* q, const void* k, const void* v, const int32_t*
  * checks drafts, tree NULL with more tokens takes a piece of a prompt.
  *   o_i = sum_j softmax_j(scale q_i . k_j) v_j,  lse_i = log sum_j exp(scale q_i . k_j)
  * q, o [B, T, Hq, d] in the input dtype, query head h reads kv head
- * h / (Hq / Hkv); lse [B, T, Hq] fp32 or NULL; scale finite. A row that sees no
- * key has o = 0 and lse = -Inf, as every row of a sequence that is left out.
+ * h / (Hq / Hkv); lse [B, T, Hq] fp32 or NULL; scale finite. o must not alias an
+ * input (several workgroups read a row of q, one writes it; o = q is KDA_EINVAL).
+ * A row that sees no key has o = 0 and lse = -Inf, as every row of a sequence that
+ * is left out.
  * Statistics and sums are fp32; 256 times the sum of |v| over the keys that a row
  * sees has to be finite there. A NaN or Inf in a row of the cache reaches no row
  * of o that does not see it. Repeated calls agree bit for bit. workspace:

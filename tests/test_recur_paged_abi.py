@@ -135,6 +135,7 @@ def test_attention_refusals(lib):
         assert attn(lib, **bad) == EALIGN
     need = kda.paged_attn_workspace_bytes(2, 8, 4, 2, 64)
     assert need > 256 and attn(lib, wsb=need - 1) == EINVAL
+    assert attn(lib, o=FAKE, q=FAKE) == EINVAL   # in place
     assert attn(lib, B=1, T=2 ** 22, Hq=4096, Hkv=4096) == ENOTSUP   # more items than a launch takes
     assert attn(lib, T=0, q=None, K=None, V=None, table=None, ctx=None, o=None, ws=None) == OK
 
