@@ -634,14 +634,16 @@ __global__ void __launch_bounds__((64 * Few<T, D, RT>::NW), (Few<T, D, RT>::NW /
 // Scores and o of 32 rows a wave on 32x32 tiles: rows stay in registers (a lane owns one),
 // keys and values come through LDS, twice over, for the RW waves that share them. RW: rows'
 // tiles of 32 a workgroup has; KS = 4 / RW groups of waves take every KS-th tile of keys each.
-// bf16 probabilities are rounded to bf16 once, for a single product (o off by 1.4 times its
-// own rounding). Bound by the turns that scores, exponentials and products take within two
-// waves a SIMD: 2,048 tokens over 6,144, 16 and 4 heads of 128 channels, bf16 165 to 178 us
-// (650 to 730 TFLOP/s), matrix units busy for 31%, vector units for 36% of the time, LDS for
-// 23%. Without gain there: 256 rows in eight waves (3 to 6% faster from 2,048 rows and long
-// contexts on, 3 to 5% slower at 256 rows and for short ones), with its two halves of waves a
-// phase apart as well (189 us against 175), two tiles of rows a wave at one wave a SIMD (213),
-// exponentials beside the next tile's scores (207), wave priorities and orders of the loads.
+// bf16 probabilities enter the second product as two bf16 numbers here too, so that a token is
+// as exact in a block of many rows as in one of few. Rounded once, for a single product, they
+// put o off by 1.4 times its own rounding (2,048 tokens over 6,144 168 us, two products 206;
+// 2,048 alone 51 and 56; 8 trees of 64 90 and 100). Bound by the turns that scores,
+// exponentials and products take within two waves a SIMD: 2,048 tokens over 6,144, 16 and 4
+// heads of 128 channels, bf16 206 to 216 us (560 to 580 TFLOP/s). Without gain, tried with one
+// product: 256 rows in eight waves (3 to 6% faster from 2,048 rows and long contexts on, 3 to 5%
+// slower at 256 rows and for short ones), with its two halves of waves a phase apart as well (189
+// us against 175), two tiles of rows a wave at one wave a SIMD (213), exponentials beside the
+// next tile's scores (207), wave priorities and orders of the loads.
 template <class T, int RW> struct Shape {
     static constexpr int KS = 4 / RW, R = 32 * RW, KT = sizeof(T) == 2 && RW == 4 ? 64 : 32, KB = KS * KT;
 };
@@ -651,6 +653,30 @@ template <class T, int D, int RW> constexpr size_t rows_lds() {
     const size_t join = S::KS > 1 ? sizeof(float) * 4 * 64 * (16 * (D / 32) + 2) : 0;
     return std::max(tiles, join);
 }
+
+// Half b of a tile of probabilities as operands: fp32 as they are, bf16 as two numbers, the
+// upper half of p's bits and the rest rounded (together off by 2^-15 at most; a NaN of the
+// arithmetic stays one). To round the first as well costs 1 to 2% more.
+template <class T> struct Weights {
+    typename Frag<T>::V hi;
+    __device__ __forceinline__ Weights(const f32x16& x, int b) : hi(rows16<T>(x, b)) {}
+};
+template <> struct Weights<uint16_t> {
+    bf16x8 hi, lo;
+    __device__ __forceinline__ Weights(const f32x16& x, int b) {
+        u32x4 top;
+        f32x8 rest;
+#pragma unroll
+        for (int m = 0; m < 8; m += 2) {
+            const uint32_t y = __float_as_uint(x[8 * b + m]), z = __float_as_uint(x[8 * b + m + 1]);
+            top[m / 2] = __builtin_amdgcn_perm(z, y, 0x07060302u);
+            rest[m] = x[8 * b + m] - __uint_as_float(y & 0xffff0000u);
+            rest[m + 1] = x[8 * b + m + 1] - __uint_as_float(z & 0xffff0000u);
+        }
+        hi = __builtin_bit_cast(bf16x8, top);
+        lo = narrow<uint16_t>(rest);
+    }
+};
 
 template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_lds<T, D, RW>() > 80 * 1024 ? 1 : 2)) paged_rows_kernel(AttnParams p) {
     using S = Shape<T, RW>;
@@ -841,9 +867,13 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_l
 #pragma unroll
                     for (int m = 0; m < MD; ++m) next[m] = tr32(tv, SV, 16 * (kb + 1), 32 * m, 0);
                 }
-                const V8 pf = rows16<T>(s[kb / 2], kb % 2);
+                const Weights<T> pf(s[kb / 2], kb % 2);
 #pragma unroll
-                for (int m = 0; m < MD; ++m) O[m] = mma32(vf[m], pf, O[m]);
+                for (int m = 0; m < MD; ++m) O[m] = mma32(vf[m], pf.hi, O[m]);
+                if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                    for (int m = 0; m < MD; ++m) O[m] = mma32(vf[m], pf.lo, O[m]);
+                }
                 if (kb % 2 == 0 && kb / 2 + 1 < NX) weigh(kb / 2 + 1);
                 if (kb + 1 < KT / 16) {
 #pragma unroll
@@ -1053,9 +1083,10 @@ template <class K, class... P> hipError_t launch(K kern, size_t x, int threads, 
 
 // Rows of a block: as many as the longest run of rows that a sequence can have
 // fills (a packed batch: its mean). Up to 32 rows go to 16x16 tiles: the other kernel is
-// quicker for 17 to 32 rows of few keys in bf16 at 128 channels (8 sequences of 8 tokens over
-// 8,192: 39 us against 46; 64 over 4,096: 119 and 123) and slower elsewhere (256 of 5 tokens
-// over 2,048: 210 and 199; 32 channels 56 and 49; fp32 140 and 92), and its o is less exact.
+// quicker for 32 rows in bf16 at 128 channels (8 sequences of 8 tokens over 8,192, 16 and 4
+// heads: 41 us against 47; 64 over 4,096, 32 and 8 heads: 203 and 216) and slower elsewhere (256
+// of 5 tokens over 2,048: 414 and 380; 64 of 8 at 64 channels 126 and 120, at 32 104 and 88, in
+// fp32 846 and 482).
 int block_rows(int T, int N, int G, bool packed) {
     const long rows = packed ? ((long)T + N - 1) / N * G : (long)T * G;
     return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
@@ -1078,10 +1109,9 @@ struct Plan {
 // workgroup's own. bf16, 128 channels, 32 / 8 heads, shared and then not, us. Few rows:
 // 400 sequences of 100 to 4,096 tokens 586 and 816, 900 of 100 to 2,048 679 and 784:
 // shared as long as the plan can count the blocks. More rows, items of 64 sequences of
-// 100 to 8,192 tokens with 32 new ones (512 items) 293 and 354, of 100 (800) 446 and 526;
-// from 1,024 items on they fill the chip by themselves, and the parts' sums cost more than
-// the evener split gives: 128 of 2,048 tokens with 16 new ones 222 and 213, prompts of
-// 16 x 512 tokens (16 / 4 heads) 72 and 47.
+// 100 to 8,192 tokens with 32 new ones (512 items) 312 and 387; from 1,024 items on they fill
+// the chip by themselves, and the parts' sums cost more than the evener split gives: 128 of
+// 2,048 tokens with 16 new ones 226 and 218, prompts of 16 x 512 tokens (16 / 4 heads) 77 and 54.
 Plan make_plan(int T, int N, int Hkv, int G, bool packed) {
     Plan pl;
     pl.R = block_rows(T, N, G, packed);

@@ -574,9 +574,11 @@ int kda_paged_append(const void* q, const void* k, const void* v, const int32_t*
  * input (several workgroups read a row of q, one writes it; o = q is KDA_EINVAL).
  * A row that sees no key has o = 0 and lse = -Inf, as every row of a sequence that
  * is left out.
- * Statistics and sums are fp32; 256 times the sum of |v| over the keys that a row
- * sees has to be finite there. A NaN or Inf in a row of the cache reaches no row
- * of o that does not see it. Repeated calls agree bit for bit. workspace:
+ * Statistics and sums are fp32, and bf16 probabilities enter the product with v as
+ * two bf16 numbers, whatever the number of rows (o is off by little more than its
+ * own rounding); 256 times the sum of |v| over the keys that a row sees has to be
+ * finite in fp32. A NaN or Inf in a row of the cache reaches no row of o that does
+ * not see it. Repeated calls agree bit for bit. workspace:
  * kda_paged_attn_workspace_bytes(...) bytes, required; calls that may overlap
  * (two streams, two captured graphs) need one each. Returns KDA_OK or a negative
  * status (KDA_ENOTSUP also where the rows of all heads are more than a launch
