@@ -3,7 +3,7 @@ results are off by, next to the rounding of the results themselves."""
 import pytest
 import torch
 
-from test_gpu_paged import BF16, kda, make  # noqa: F401  (kda: the fixture)
+from test_gpu_paged import BF16, F32, kda, make  # noqa: F401  (kda: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,28 @@ def test_rows_of_every_block_are_as_exact(kda, T, G, d):  # noqa: F811
         own += (want.to(BF16).double() - want).square().sum().item()
     ratio = (off / own) ** 0.5
     assert ratio <= 1.02, "%.3f times the rounding of the result" % ratio
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("longest", [100, 10 ** 4, 2 * 10 ** 6])
+def test_cosines_and_sines_in_fp32(kda, longest, interleaved):  # noqa: F811
+    """Pairs (1, 0) rotated are the cosine and the sine themselves. Each is off by one unit of
+    sincospif's (2^-24 below one) and half a unit of the joint with the rest of the angle, 1.5 x
+    2^-24 in all; an angle rounded to fp32 first (up to 2^-25 of a half turn, pi 2^-25) would put
+    it off by 1.57 more."""
+    T, d, page = 65536, 32, 64
+    k = torch.zeros(1, T, 1, d, device="cuda")
+    one = slice(0, d, 2) if interleaved else slice(0, d // 2)
+    k[..., one] = 1
+    pages = [torch.zeros(T // page, page, 1, d, device="cuda") for _ in range(2)]
+    table = torch.arange(T // page, dtype=torch.int32, device="cuda")[None]
+    ctx = torch.zeros(1, dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(longest)
+    pos = torch.randint(0, longest, (1, T), generator=g).to(torch.int32).cuda()
+    freqs = (10000.0 ** (-torch.arange(d // 2) / (d // 2))).to(F32).cuda()
+    q = kda.paged_append(k, k, *pages, table, ctx, q=k, pos=pos, freqs=freqs, interleaved=interleaved)[0, :, 0]
+    angle = pos[0].double()[:, None] * freqs.double()
+    other = slice(1, d, 2) if interleaved else slice(d // 2, d)
+    for got, want in ((q[:, one], angle.cos()), (q[:, other], angle.sin())):
+        worst = (got.double() - want).abs().max().item() * 2 ** 24
+        assert worst <= 1.5, "off by %.3f of 2^-24" % worst
