@@ -25,6 +25,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "kda_bounds.h"
 #include "kda_launch.h"
 #include "kda_tiles.h"
 
@@ -465,9 +466,10 @@ template <class TG, class TX, int V, int R> __global__ void __launch_bounds__(NT
     __shared__ int s_work;
     int work = blockIdx.x;
     if (!p.alone) {
-        if (threadIdx.x == 0) s_work = (int)(atomicAdd(reinterpret_cast<uint32_t*>(p.counter), 1u) + 1u);   // from all ones
+        if (threadIdx.x == 0) s_work = drawn_work(atomicAdd(reinterpret_cast<uint32_t*>(p.counter), 1u), gridDim.x);
         __syncthreads();
         work = __builtin_amdgcn_readfirstlane(s_work);
+        if (work < 0) return;   // another call counts here too
     }
     const int v = work / p.tiles, c0 = work % p.tiles * TILE, ch = threadIdx.x % TILE, part = threadIdx.x / TILE;
     SeqBlock b;

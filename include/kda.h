@@ -490,8 +490,9 @@ int kda_swa_cache_fill(const void* k, const void* v, void* K_cache, void* V_cach
  * their element. workspace: kda_glr_fwd_workspace_bytes(...) bytes, required; calls
  * that may overlap (two streams, two captured graphs) need one each. Repeated calls
  * agree bit for bit. Inside a launch blocks wait for what earlier ones leave in the
- * workspace; a wait that never ended, as when a call is given a workspace that
- * another one is using, is given up and leaves NaN. Returns KDA_OK or a negative
+ * workspace; a wait that never ended is given up after some seconds. Where two calls
+ * use a workspace at once, the results of both are undefined (they may be finite and
+ * wrong); nothing outside their arrays is touched. Returns KDA_OK or a negative
  * status.
  */
 size_t kda_glr_fwd_workspace_bytes(int B, int T, int C, int N, int has_cu_seqlens, int dtype);

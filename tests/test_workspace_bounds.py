@@ -1,0 +1,57 @@
+"""What kernels make of numbers that they read back from a workspace, gone through on the
+host (csrc/kda_bounds.h is compiled here as it stands): with a workspace that two calls use
+at once, which the header leaves undefined, no index leaves the call's own arrays."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "gated_delta_rule_46_amd", "csrc")
+SOURCE = """
+#include "kda_bounds.h"
+extern "C" int drawn_work(unsigned counted, unsigned workgroups) { return kda::drawn_work(counted, workgroups); }
+"""
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    at = tmp_path_factory.mktemp("bounds")
+    src, out = str(at / "bounds.cpp"), str(at / "bounds.so")
+    with open(src, "w") as f:
+        f.write(SOURCE)
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    subprocess.check_call(["g++", "-std=c++17", "-O1", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__", "-I" + CSRC,
+                           "-I" + os.path.join(rocm, "include"), src, "-o", out])
+    lib = ctypes.CDLL(out)
+    lib.drawn_work.argtypes = [ctypes.c_uint, ctypes.c_uint]
+    return lib
+
+
+def place(work, T, N, rows, tiles):
+    """Sequence and first token of the block that a piece of work is, in a batch of N x T tokens."""
+    nb = (T + rows - 1) // rows
+    v = work // tiles
+    return v // nb, v // nb * T + v % nb * rows
+
+
+@pytest.mark.parametrize("T,N,rows,tiles", [(6000, 1, 192, 5), (700, 2, 192, 1), (385, 7, 192, 3), (257, 3, 256, 16)])
+def test_work_of_the_recurrence(lib, T, N, rows, tiles):
+    """A call by itself draws every piece of work once. Two calls that both clear a counter and
+    then both count on it: the second draws on from where the first is."""
+    grid = N * ((T + rows - 1) // rows) * tiles
+    counter, drawn = 0xffffffff, []
+    for _ in range(2 * grid):
+        drawn.append(lib.drawn_work(counter, grid))
+        counter = (counter + 1) & 0xffffffff
+    assert drawn == list(range(grid)) + [-1] * grid
+    assert max(place(w, T, N, rows, tiles)[1] for w in drawn if w >= 0) < N * T
+    assert place(grid, T, N, rows, tiles)[0] >= N   # what the bound keeps out: a sequence behind the last one
+
+
+def test_work_from_another_calls_words(lib):
+    """A counter that another call, of other sizes, has written a value of its own over."""
+    for found in (0, 1, 99, 100, 0x3f800000, 0x7fc00000, 0x7fffffff, 0x80000000, 0xbf800000, 0xfffffffe, 0xffffffff):
+        work = lib.drawn_work(found, 100)
+        assert -1 <= work < 100 and (work == -1 or work == (found + 1) % 2 ** 32)
