@@ -16,4 +16,7 @@ __host__ __device__ inline int drawn_work(uint32_t counted, uint32_t workgroups)
     return work < workgroups ? (int)work : -1;
 }
 
+// Whether workgroups `first` to `last` can have left the parts of an item that `wgs` share.
+__host__ __device__ inline bool parts_exist(int first, int last, int wgs) { return first >= 0 && first <= last && last < wgs; }
+
 }  // namespace kda

@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "kda_attn.h"
+#include "kda_bounds.h"
 #include "kda_launch.h"
 
 namespace kda {
@@ -1015,7 +1016,7 @@ template <class T, int D, int R, bool SPREAD> __global__ void __launch_bounds__(
     if (!row_block(p.map, p.G, R, v, b)) return;
     const int2 span = p.span[v * p.groups + hk / p.HW];
     const int parts = span.y - span.x + 1, tid = threadIdx.x, cg = tid % CG, rg = tid / CG, rows = min(b.rows - b.r0, R);
-    if (parts == 1) return;
+    if (parts == 1 || !parts_exist(span.x, span.y, p.wgs)) return;
     auto finish = [&](int row, float m, float l, const f32x4& acc) {
         const int rr = b.r0 + row;
         const size_t at = (size_t)(b.t0 + rr / p.G) * p.Hq + hk * p.G + rr % p.G;

@@ -581,7 +581,8 @@ int kda_paged_append(const void* q, const void* k, const void* v, const int32_t*
  * finite in fp32. A NaN or Inf in a row of the cache reaches no row of o that does
  * not see it. Repeated calls agree bit for bit. workspace:
  * kda_paged_attn_workspace_bytes(...) bytes, required; calls that may overlap
- * (two streams, two captured graphs) need one each. Returns KDA_OK or a negative
+ * (two streams, two captured graphs) need one each (else the results of both are
+ * undefined; nothing outside their arrays is touched). Returns KDA_OK or a negative
  * status (KDA_ENOTSUP also where the rows of all heads are more than a launch
  * takes).
  */

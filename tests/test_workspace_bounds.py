@@ -12,6 +12,7 @@ CSRC = os.path.join(ROOT, "gated_delta_rule_46_amd", "csrc")
 SOURCE = """
 #include "kda_bounds.h"
 extern "C" int drawn_work(unsigned counted, unsigned workgroups) { return kda::drawn_work(counted, workgroups); }
+extern "C" int parts_exist(int first, int last, int wgs) { return kda::parts_exist(first, last, wgs); }
 """
 
 
@@ -26,6 +27,7 @@ def lib(tmp_path_factory):
                            "-I" + os.path.join(rocm, "include"), src, "-o", out])
     lib = ctypes.CDLL(out)
     lib.drawn_work.argtypes = [ctypes.c_uint, ctypes.c_uint]
+    lib.parts_exist.argtypes = [ctypes.c_int] * 3
     return lib
 
 
@@ -55,3 +57,10 @@ def test_work_from_another_calls_words(lib):
     for found in (0, 1, 99, 100, 0x3f800000, 0x7fc00000, 0x7fffffff, 0x80000000, 0xbf800000, 0xfffffffe, 0xffffffff):
         work = lib.drawn_work(found, 100)
         assert -1 <= work < 100 and (work == -1 or work == (found + 1) % 2 ** 32)
+
+
+def test_parts_of_shared_items(lib):
+    for first, last, wgs in ((0, 0, 1), (0, 255, 256), (17, 17, 256), (511, 511, 512)):
+        assert lib.parts_exist(first, last, wgs)
+    for first, last in ((-1, 0), (0, 256), (256, 256), (5, 4), (0x3f800000, 0x3f800000), (-2 ** 31, 2 ** 31 - 1), (0, -1)):
+        assert not lib.parts_exist(first, last, 256)
