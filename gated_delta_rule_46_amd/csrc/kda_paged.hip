@@ -91,83 +91,87 @@ template <class T, int D> __global__ void __launch_bounds__(256) paged_append_ke
     __shared__ float s_cos[4][64], s_sin[4][64];
     constexpr int V = 16 / (int)sizeof(T), U = D / (2 * V);   // elements of a piece, units of two of them in a row
     const int w = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
-    const int t = blockIdx.x * 4 + w;
-    if (t >= p.rows) return;
-    int seq, i;
-    if (!token_place(p.map, t, seq, i)) return;
-    const int ctx = p.ctx[seq];
-    const long row = (long)ctx + i;
-    const int slot = ctx < 0 || row > 0x7fffffffL ? -1 : p.pages.row(seq, (int)row);
-    const int half = p.rot / 2;
-    if (lane < half) {
-        const double turns = (double)(p.pos ? p.pos[t] : row) * (double)p.freqs[lane] * 0.15915494309189535;
-        // half turns as two floats: with one, cosines and sines are off by up to 1.9 x 2^-24, with
-        // both by 1.3 (no change in time)
-        const double x = 2.0 * (turns - rint(turns));
-        const float hi = (float)x, lo = (float)(x - (double)hi) * 3.14159265f;
-        float sn, cs;
-        sincospif(hi, &sn, &cs);
-        s_cos[w][lane] = fmaf(-lo, sn, cs);
-        s_sin[w][lane] = fmaf(lo, cs, sn);
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    const int rot_units = half / V;
-    const int hq = p.q ? p.Hq : 0, heads = hq + 2 * p.Hkv;
-    for (int e = lane; e < heads * U; e += WAVE) {
-        const int h = e / U, u = e % U;
-        const T* from;
-        T* to = nullptr;
-        bool turn = true;
-        if (h < hq) {
-            const size_t at = ((size_t)t * p.Hq + h) * D;
-            from = static_cast<const T*>(p.q) + at;
-            to = static_cast<T*>(p.q_out) + at;
-        } else {
-            const bool isv = h >= hq + p.Hkv;
-            const int hk = h - hq - (isv ? p.Hkv : 0);
-            from = static_cast<const T*>(isv ? p.v : p.k) + ((size_t)t * p.Hkv + hk) * D;
-            if (slot < 0) continue;
-            to = static_cast<T*>(isv ? p.Vp : p.Kp) + ((size_t)slot * p.Hkv + hk) * D;
-            turn = !isv;
+    // (a wave goes on to further tokens only where a launch has no room for a wave each, from 2^26 on)
+    for (long at = (long)blockIdx.x * 4 + w; at < p.rows; at += 4L * gridDim.x) {
+        const int t = (int)at;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the last token's angles are done with
+        __builtin_amdgcn_wave_barrier();
+        int seq, i;
+        if (!token_place(p.map, t, seq, i)) continue;
+        const int ctx = p.ctx[seq];
+        const long row = (long)ctx + i;
+        const int slot = ctx < 0 || row > 0x7fffffffL ? -1 : p.pages.row(seq, (int)row);
+        const int half = p.rot / 2;
+        if (lane < half) {
+            const double turns = (double)(p.pos ? p.pos[t] : row) * (double)p.freqs[lane] * 0.15915494309189535;
+            // half turns as two floats: with one, cosines and sines are off by up to 1.9 x 2^-24, with
+            // both by 1.3 (no change in time)
+            const double x = 2.0 * (turns - rint(turns));
+            const float hi = (float)x, lo = (float)(x - (double)hi) * 3.14159265f;
+            float sn, cs;
+            sincospif(hi, &sn, &cs);
+            s_cos[w][lane] = fmaf(-lo, sn, cs);
+            s_sin[w][lane] = fmaf(lo, cs, sn);
         }
-        if (ctx < 0) {   // left out: only q's rows are written
-            const uint4 z = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(to + 2 * u * V) = z;
-            *reinterpret_cast<uint4*>(to + (2 * u + 1) * V) = z;
-            continue;
-        }
-        turn = turn && u < rot_units;
-        const bool halves = !neighbours && u < rot_units;
-        const int a = (halves ? u : 2 * u) * V, b = halves ? a + half : a + V;
-        uint4 x = *reinterpret_cast<const uint4*>(from + a), y = *reinterpret_cast<const uint4*>(from + b);
-        if (turn) {
-            T xs[V], ys[V];
-            __builtin_memcpy(xs, &x, 16);
-            __builtin_memcpy(ys, &y, 16);
-            if (halves) {
-#pragma unroll
-                for (int m = 0; m < V; ++m) {
-                    const float c = s_cos[w][a + m], s = s_sin[w][a + m], f = from_el(xs[m]), g = from_el(ys[m]);
-                    store1(xs + m, f * c - g * s);
-                    store1(ys + m, f * s + g * c);
-                }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const int rot_units = half / V;
+        const int hq = p.q ? p.Hq : 0, heads = hq + 2 * p.Hkv;
+        for (int e = lane; e < heads * U; e += WAVE) {
+            const int h = e / U, u = e % U;
+            const T* from;
+            T* to = nullptr;
+            bool turn = true;
+            if (h < hq) {
+                const size_t at = ((size_t)t * p.Hq + h) * D;
+                from = static_cast<const T*>(p.q) + at;
+                to = static_cast<T*>(p.q_out) + at;
             } else {
-#pragma unroll
-                for (int m = 0; m < V; m += 2) {
-                    const float c = s_cos[w][(a + m) / 2], s = s_sin[w][(a + m) / 2], f = from_el(xs[m]), g = from_el(xs[m + 1]);
-                    store1(xs + m, f * c - g * s);
-                    store1(xs + m + 1, f * s + g * c);
-                    const float c2 = s_cos[w][(b + m) / 2], s2 = s_sin[w][(b + m) / 2], f2 = from_el(ys[m]), g2 = from_el(ys[m + 1]);
-                    store1(ys + m, f2 * c2 - g2 * s2);
-                    store1(ys + m + 1, f2 * s2 + g2 * c2);
-                }
+                const bool isv = h >= hq + p.Hkv;
+                const int hk = h - hq - (isv ? p.Hkv : 0);
+                from = static_cast<const T*>(isv ? p.v : p.k) + ((size_t)t * p.Hkv + hk) * D;
+                if (slot < 0) continue;
+                to = static_cast<T*>(isv ? p.Vp : p.Kp) + ((size_t)slot * p.Hkv + hk) * D;
+                turn = !isv;
             }
-            __builtin_memcpy(&x, xs, 16);
-            __builtin_memcpy(&y, ys, 16);
+            if (ctx < 0) {   // left out: only q's rows are written
+                const uint4 z = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(to + 2 * u * V) = z;
+                *reinterpret_cast<uint4*>(to + (2 * u + 1) * V) = z;
+                continue;
+            }
+            turn = turn && u < rot_units;
+            const bool halves = !neighbours && u < rot_units;
+            const int a = (halves ? u : 2 * u) * V, b = halves ? a + half : a + V;
+            uint4 x = *reinterpret_cast<const uint4*>(from + a), y = *reinterpret_cast<const uint4*>(from + b);
+            if (turn) {
+                T xs[V], ys[V];
+                __builtin_memcpy(xs, &x, 16);
+                __builtin_memcpy(ys, &y, 16);
+                if (halves) {
+#pragma unroll
+                    for (int m = 0; m < V; ++m) {
+                        const float c = s_cos[w][a + m], s = s_sin[w][a + m], f = from_el(xs[m]), g = from_el(ys[m]);
+                        store1(xs + m, f * c - g * s);
+                        store1(ys + m, f * s + g * c);
+                    }
+                } else {
+#pragma unroll
+                    for (int m = 0; m < V; m += 2) {
+                        const float c = s_cos[w][(a + m) / 2], s = s_sin[w][(a + m) / 2], f = from_el(xs[m]), g = from_el(xs[m + 1]);
+                        store1(xs + m, f * c - g * s);
+                        store1(xs + m + 1, f * s + g * c);
+                        const float c2 = s_cos[w][(b + m) / 2], s2 = s_sin[w][(b + m) / 2], f2 = from_el(ys[m]), g2 = from_el(ys[m + 1]);
+                        store1(ys + m, f2 * c2 - g2 * s2);
+                        store1(ys + m + 1, f2 * s2 + g2 * c2);
+                    }
+                }
+                __builtin_memcpy(&x, xs, 16);
+                __builtin_memcpy(&y, ys, 16);
+            }
+            *reinterpret_cast<uint4*>(to + a) = x;
+            *reinterpret_cast<uint4*>(to + b) = y;
         }
-        *reinterpret_cast<uint4*>(to + a) = x;
-        *reinterpret_cast<uint4*>(to + b) = y;
     }
 }
 
@@ -1175,7 +1179,8 @@ template <class T, int D> hipError_t append(const PagedArgs& a) {
     p.map = SeqMap{a.cu_seqlens, a.T, a.N};
     p.rows = a.cu_seqlens ? a.T : a.N * a.T;
     p.Hq = a.Hq; p.Hkv = a.Hkv; p.rot = a.rot_dim;
-    return launch(paged_append_kernel<T, D>, (size_t)(p.rows + 3) / 4, 256, 0, a.stream, p, a.neighbours);
+    const size_t wgs = std::min(((size_t)p.rows + 3) / 4, (size_t)0xffffff);   // of 256 threads: fewer than 2^32
+    return launch(paged_append_kernel<T, D>, wgs, 256, 0, a.stream, p, a.neighbours);
 }
 
 #define KDA_PAGED_DIM(d, D, ...)                                       \
