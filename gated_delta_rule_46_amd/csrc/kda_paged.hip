@@ -368,7 +368,7 @@ template <class T> constexpr int v_stride32(int d) { return sizeof(T) == 2 ? (d 
 // for 2,048 to 8,192 tokens of one sequence, of which 2 are the plan's, 2 to 4 the loads' way
 // and 2 to 4 the join of the waves' shares. Two tiles ahead with 32 rows spill (89 us, one 49).
 template <class T, int D, int RT> struct Few {
-    // one workgroup a CU, of as many waves as registers leave room for
+    // workgroups of eight waves, two a SIMD, or of four where registers leave room for one
     static constexpr int NW = sizeof(T) == 4 && D == 128 ? 4 : 8, DEPTH = RT == 1 ? 2 : 1, R = 16 * RT;
     static constexpr size_t tiles = sizeof(T) * NW * 32 * v_stride16<T>(D), join = sizeof(float) * NW * R * (D + 4);
     static constexpr size_t lds = tiles > join ? tiles : join;
@@ -687,7 +687,10 @@ template <> struct Weights<uint16_t> {
     }
 };
 
-template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_lds<T, D, RW>() > 80 * 1024 ? 1 : 2)) paged_rows_kernel(AttnParams p) {
+// workgroups that a CU holds at once
+template <class T, int D, int RW> constexpr int rows_at_once() { return rows_lds<T, D, RW>() > 80 * 1024 ? 1 : 2; }
+
+template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_at_once<T, D, RW>())) paged_rows_kernel(AttnParams p) {
     using S = Shape<T, RW>;
     constexpr int KS = S::KS, R = S::R, KT = S::KT, KB = S::KB, NX = KT / 32, GT = 64 * RW;
     constexpr int ST = tile_stride<T>(D), SV = v_stride32<T>(D), KD = D / 16, MD = D / 32, PER = 16 / (int)sizeof(T), CPR = D / PER, NL = KT * CPR / GT;
@@ -1100,8 +1103,17 @@ int block_rows(int T, int N, int G, bool packed) {
     const long rows = packed ? ((long)T + N - 1) / N * G : (long)T * G;
     return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
-// Workgroups that share the keys: what a CU holds at once, times 256.
-int shared_wgs(int R) { return R <= 32 ? 256 : 512; }
+// Workgroups that share the keys: as many as the chip's 256 CUs hold at once of the kernel for
+// more rows, so that each is given its share in the same turn. fp32 with 64 rows at 128 channels
+// has LDS for one a CU: 8 trees of 12 tokens over 8,192, 16 and 4 heads, 130 us, with two 141; 64
+// of 16 over 100 to 4,096, 32 and 8 heads, 460 and 476. Of the kernel for few rows one a CU, also
+// where it has registers for two (bf16 at 32 channels: 64 single tokens over 100 to 4,096 49 us,
+// with two 45; 8 trees of 8 over 8,192 22 and 23).
+template <class T, int D, int R> constexpr int shared_wgs() {
+    if constexpr (R <= 32) return 256;
+    else return 256 * rows_at_once<T, D, R / 32>();
+}
+constexpr int most_shared_wgs(int R) { return R <= 32 ? 256 : 512; }   // of any type and head size
 // kv heads that the waves of a workgroup take side by side
 int heads_together(int Hkv, int waves) {
     int hw = waves;
@@ -1145,7 +1157,8 @@ template <class T, int D, int R> hipError_t attend(const PagedArgs& a, Plan pl) 
     if ((p.capacity / 32 + 1) * pl.blocks > 0x7fffffffL) pl.shared = false;   // units are counted in 31 bits
     const size_t items = (size_t)pl.blocks * p.groups;
     if (pl.shared) {
-        p.wgs = shared_wgs(R);
+        p.wgs = shared_wgs<T, D, R>();
+        static_assert(shared_wgs<T, D, R>() <= most_shared_wgs(R), "");
         char* ws = static_cast<char*>(a.workspace);
         p.span = reinterpret_cast<int2*>(ws);
         ws += al256(items * 8);
@@ -1202,7 +1215,7 @@ bool paged_attn_fits(int T, int N, int Hq, int Hkv, bool packed) {
 size_t paged_attn_workspace_bytes(int T, int N, int Hq, int Hkv, int d, bool packed) {
     const Plan pl = make_plan(T, N, Hkv, Hq / Hkv, packed);
     if (!pl.shared) return 256;
-    const size_t slots = (size_t)2 * shared_wgs(pl.R) * pl.R * (pl.R <= 32 ? heads_together(Hkv, 8) : 1);
+    const size_t slots = (size_t)2 * most_shared_wgs(pl.R) * pl.R * (pl.R <= 32 ? heads_together(Hkv, 8) : 1);
     return al256((size_t)pl.blocks * Hkv * 8) + al256(slots * 8) + slots * d * 4 + 256;
 }
 

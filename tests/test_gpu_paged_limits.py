@@ -1,8 +1,9 @@
-"""Appending to a paged cache where a launch has no room for a wave a token."""
+"""A paged cache at the limits of launches: more tokens than one has waves, and no more
+workgroups to share the keys than the chip holds at once."""
 import pytest
 import torch
 
-from test_gpu_paged import BF16, F32, kda  # noqa: F401  (kda: the fixture)
+from test_gpu_paged import BF16, F32, check, kda, make  # noqa: F401  (kda: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +47,19 @@ def test_more_tokens_than_a_launch_has_waves(kda, lens):  # noqa: F811
             want = kda.paged_append(k[:, some], v[:, some], *small, torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
                                     ctx[:1], q=q[:, some], pos=pos, freqs=freqs)
             assert torch.equal(out[:, some], want) and torch.equal(rows(pools[0], n, first, end), small[0][0])
+
+
+@pytest.mark.parametrize("dtype,d,T,wgs", [(F32, 128, 16, 256), (F32, 64, 16, 512), (BF16, 128, 16, 512), (F32, 128, 32, 512),
+                                           (F32, 128, 4, 256), (BF16, 64, 4, 256)])
+def test_keys_are_shared_by_what_the_chip_holds(kda, dtype, d, T, wgs):  # noqa: F811
+    """The first words of a workspace say for each kv head (up to 32 rows: for all that waves
+    take side by side, here both) which workgroups have left parts of it. A workgroup of fp32 rows at 128 channels in blocks of 64 takes 135 KB of a CU's 160 KB of
+    LDS: one a CU, 256 in all, where the others' are two. Results as ever."""
+    x = make([T], [16384], 8, 2, d, dtype, 16, packed=False, seed=d)
+    ws = torch.zeros(kda.paged_attn_workspace_bytes(1, T, 8, 2, d), dtype=torch.uint8, device="cuda")
+    check(kda, x, workspace=ws)
+    spans = ws[:16].view(torch.int32).tolist()
+    if T * 4 <= 32:
+        assert spans == [0, wgs - 1, 0, 0]
+    else:
+        assert spans[0] == 0 and spans[3] == wgs - 1 and all(s in (wgs // 2, wgs // 2 - 1) for s in spans[1:3])
