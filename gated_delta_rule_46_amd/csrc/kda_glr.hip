@@ -540,9 +540,7 @@ template <class TG, class TX, int V, int R> __global__ void __launch_bounds__(NT
 
 // Forward of a batch whose sequences and tiles fill the chip: a workgroup takes a tile of
 // one sequence through all its blocks, the next one's loads under way, and reads everything
-// once. Taken from 256 such pairs on, one a CU: B=32 T=1024 C=1024 bf16 39 us against the
-// single pass's 47, B=16 T=4096 C=2048 157 against 155; with 128 of them it is slower
-// (B=8 T=4096 C=2048, 99 against 86).
+// once. `stream_of` says when it is taken.
 template <class TG, class TX, int V, int R> __global__ void __launch_bounds__(NT, 2) glr_stream_kernel(GlrParams p) {
     using B = Block<TG, TX, V, R, false>;
     constexpr int TILE = B::TILE, SLOTS = B::SLOTS, ROWS = B::L::ROWS;
@@ -617,6 +615,20 @@ constexpr int pass_rows(bool wide, bool bf16) {
     return !wide ? Lay<1, pass_r<1>()>::ROWS : bf16 ? Lay<8, pass_r<8>()>::ROWS : Lay<4, pass_r<4>()>::ROWS;
 }
 constexpr int grad_rows(bool wide) { return wide ? 128 : 64; }
+// The streaming forward holds two blocks. With fp32 decays beside bf16 x eight tokens of each
+// spill (B=16 T=4096 C=2048, 4, 6 and 8 tokens: 195, 199 and 289 us).
+template <class TG, class TX, bool WIDE> constexpr int stream_r() { return WIDE && sizeof(TG) > sizeof(TX) ? 4 : glr_r<WIDE>(); }
+
+// Whether the forward streams: from 256 pairs of a sequence and a tile on, one a CU, and in fp32
+// up to 2^25 values of x. The streaming kernel's us against the single pass's:
+//   bf16 (T, 16 of C=2048)      512: 18, 27    1,024: 40, 47    2,048: 82, 85     4,096: 158, 156
+//   fp32 decays beside bf16     512: 24, 35    1,024: 47, 57    2,048: 99, 107    4,096: 195, 197
+//   fp32                        512: 36, 46    1,024: 81, 84    2,048: 169, 153   4,096: 317, 287
+// (fp32, 32 of T=2048 C=1024 and 64 of T=2048 C=509: 159, 152 and 231, 198.) With 128 pairs it is
+// slower (bf16, 8 of T=4096 C=2048: 99, 86).
+bool stream_of(const GlrArgs& a, int tiles) {
+    return !a.cu_seqlens && (long)a.N * tiles >= 256 && (a.bf16 || (long)a.N * a.T * a.C <= 1L << 25);
+}
 
 template <class F> auto with_types(bool bf16, bool gate_bf16, bool wide, F f) {
     using U = uint16_t;
@@ -661,8 +673,8 @@ hipError_t run(const GlrArgs& a, bool grad) {
             hipLaunchKernelGGL((glr_grad_kernel<TG, TX, V, R>), wgs, nt, 0, a.stream, p);
             return hipGetLastError();
         }
-        if (!packed && !p.alone && (long)a.N * p.tiles >= 256) {
-            hipLaunchKernelGGL((glr_stream_kernel<TG, TX, V, R>), dim3(a.N * p.tiles), nt, 0, a.stream, p);
+        if (!p.alone && stream_of(a, p.tiles)) {
+            hipLaunchKernelGGL((glr_stream_kernel<TG, TX, V, stream_r<TG, TX, wide.value>()>), dim3(a.N * p.tiles), nt, 0, a.stream, p);
             return hipGetLastError();
         }
         if (!p.alone) {
