@@ -19,9 +19,10 @@
 // decays and sums are fp32 throughout; results are rounded once.
 //
 // Bound by memory (2 operations an element). bf16, B=2 C=2048: forward of T=8192 45 us for
-// 213 MB at 4.8 TB/s, and 3 to 5 us for the clear before it; gradient of T=4096 20 us (sums,
-// 5.1 TB/s) and 32 us (5.2 TB/s): it reads its inputs twice, as one pass would need both
-// the states from the front and the adjoints from the back.
+// 213 MB at 4.7 TB/s, and 3 to 5 us for the clear before it; gradient of T=4096 20 us (sums,
+// 5.1 TB/s) and 32 us (5.2 TB/s): it reads all its inputs twice. (The sums need a and x alone,
+// for the states; adjoints could follow each other through one reverse pass as the forward's
+// states do, which would save reading dh once, an eighth of the bytes.)
 #include <algorithm>
 #include <type_traits>
 
@@ -455,7 +456,7 @@ __device__ __forceinline__ Run take_up(const uint64_t* w, long step, int count) 
 // the first of a sequence, which alone reads h0 (h_T may be h0), and every GROUP-th leave
 // the state behind them instead, so that no block looks back over more than GROUP words. Which
 // words a block takes up, and in which order, does not depend on when they came. GROUP: one
-// sequence of T=131072, C=256 takes 128, 81 and 71 us with states at every 8th, 16th and 32nd
+// sequence of T=131072, C=256 takes 97, 67 and 60 us with states at every 8th, 16th and 32nd
 // block. A third workgroup a CU would spill (58 us against 49 at B=2 T=8192 C=2048).
 template <class TG, class TX, int V, int R> __global__ void __launch_bounds__(NT) glr_pass_kernel(GlrParams p) {
     using B = Block<TG, TX, V, R, false>;
@@ -608,8 +609,9 @@ template <class TG, class TX, int V> __global__ void __launch_bounds__(NT) glr_d
 template <class TX, bool WIDE> constexpr int glr_v() { return WIDE ? 16 / (int)sizeof(TX) : 1; }
 template <bool WIDE> constexpr int glr_r() { return WIDE ? 8 : 16; }
 // The forward's single pass takes more: fewer blocks look back, with registers for two
-// workgroups a CU. B=2 T=8192 C=2048 bf16, 4, 8, 12 and 16 tokens: 69, 49, 48 and 52 us; B=1
-// T=4096 fp32, 8, 12 and 16: 31, 27 and 24 us; C=2049 bf16, 16, 32, 48 and 64: 38, 29, 24 and 23.
+// workgroups a CU. B=2 T=8192 C=2048 bf16, 4, 8, 12 and 16 tokens: 69, 50, 48 and 52 us; B=1
+// T=4096 C=2048 fp32, 8, 12 and 16: 30, 26 and 24 us; B=1 T=4096 C=2049 bf16, 16, 32, 48 and 64:
+// 38, 29, 24 and 23.
 template <int V> constexpr int pass_r() { return V == 8 ? 12 : V == 4 ? 16 : 64; }
 constexpr int pass_rows(bool wide, bool bf16) {
     return !wide ? Lay<1, pass_r<1>()>::ROWS : bf16 ? Lay<8, pass_r<8>()>::ROWS : Lay<4, pass_r<4>()>::ROWS;
@@ -621,10 +623,10 @@ template <class TG, class TX, bool WIDE> constexpr int stream_r() { return WIDE 
 
 // Whether the forward streams: from 256 pairs of a sequence and a tile on, one a CU, and in fp32
 // up to 2^25 values of x. The streaming kernel's us against the single pass's:
-//   bf16 (T, 16 of C=2048)      512: 18, 27    1,024: 40, 47    2,048: 82, 85     4,096: 158, 156
-//   fp32 decays beside bf16     512: 24, 35    1,024: 47, 57    2,048: 99, 107    4,096: 195, 197
-//   fp32                        512: 36, 46    1,024: 81, 84    2,048: 169, 153   4,096: 317, 287
-// (fp32, 32 of T=2048 C=1024 and 64 of T=2048 C=509: 159, 152 and 231, 198.) With 128 pairs it is
+//   bf16 (T, 16 of C=2048)      512: 17, 27    1,024: 40, 47    2,048: 81, 85     4,096: 158, 156
+//   fp32 decays beside bf16     512: 25, 35    1,024: 47, 57    2,048: 99, 107    4,096: 194, 198
+//   fp32                        512: 36, 46    1,024: 80, 84    2,048: 166, 152   4,096: 320, 287
+// (fp32, 32 of T=2048 C=1024 and 64 of T=2048 C=509: 159, 152 and 229, 199.) With 128 pairs it is
 // slower (bf16, 8 of T=4096 C=2048: 99, 86).
 bool stream_of(const GlrArgs& a, int tiles) {
     return !a.cu_seqlens && (long)a.N * tiles >= 256 && (a.bf16 || (long)a.N * a.T * a.C <= 1L << 25);

@@ -84,7 +84,7 @@ __device__ __forceinline__ bool token_place(const SeqMap& m, int t, int& seq, in
 // Angles are formed and reduced to one turn in 64 bits (position and frequency
 // are exact, their product is at positions where 32 bits have no fraction left),
 // the rest is fp32, rounded once. Bound by memory: 7,213 tokens of eight prompts,
-// 16 and 4 heads of 128 channels, bf16 16.9 us at 5.2 TB/s; 46 drafted tokens 4.2 us,
+// 16 and 4 heads of 128 channels, bf16 16.4 us at 5.4 TB/s; 46 drafted tokens 4.3 us,
 // most of it the way from the offsets over the table to the rows.
 template <class T, int D> __global__ void __launch_bounds__(256) paged_append_kernel(AppendParams p, bool neighbours) {
     lds_poison(0);
@@ -364,9 +364,11 @@ template <class T> constexpr int v_stride32(int d) { return sizeof(T) == 2 ? (d 
 // product's operand (kpos order). bf16 probabilities enter it as two bf16 numbers (3 of 40 us
 // at 8 sequences of 8,192 tokens): o is then off by no more than its own rounding.
 // Bound by memory: one token of 64 sequences of 100 to 4,096 tokens, 32 and 8 heads of 128
-// channels, bf16 115 us at 4.8 TB/s, of 4,096 tokens each 197 us at 5.5. Small calls: 13 us
+// channels, bf16 112 us at 5.0 TB/s, of 4,096 tokens each 197 us at 5.5. Small calls: 13 us
 // for 2,048 to 8,192 tokens of one sequence, of which 2 are the plan's, 2 to 4 the loads' way
-// and 2 to 4 the join of the waves' shares. Two tiles ahead with 32 rows spill (89 us, one 49).
+// and 2 to 4 the join of the waves' shares. Two tiles ahead with 32 rows spill (89 us, one 49);
+// with 16 at 128 channels bf16 three registers wait in scratch from before the loop over tiles
+// until behind it, none within.
 template <class T, int D, int RT> struct Few {
     // workgroups of eight waves, two a SIMD, or of four where registers leave room for one
     static constexpr int NW = sizeof(T) == 4 && D == 128 ? 4 : 8, DEPTH = RT == 1 ? 2 : 1, R = 16 * RT;
@@ -648,11 +650,11 @@ __global__ void __launch_bounds__((64 * Few<T, D, RT>::NW), (Few<T, D, RT>::NW /
 // put o off by 1.4 times its own rounding (2,048 tokens over 6,144 168 us, two products 206;
 // 2,048 alone 51 and 56; 8 trees of 64 90 and 100). Bound by the turns that scores,
 // exponentials and products take within two waves a SIMD: 2,048 tokens over 6,144, 16 and 4
-// heads of 128 channels, bf16 206 to 216 us (560 to 580 TFLOP/s). Without gain, tried with one
-// product: 256 rows in eight waves (3 to 6% faster from 2,048 rows and long contexts on, 3 to 5%
-// slower at 256 rows and for short ones), with its two halves of waves a phase apart as well (189
-// us against 175), two tiles of rows a wave at one wave a SIMD (213), exponentials beside the
-// next tile's scores (207), wave priorities and orders of the loads.
+// heads of 128 channels, bf16 206 to 216 us (560 to 590 TFLOP/s), matrix units busy for 40% of
+// it. Without gain, tried with one product: 256 rows in eight waves (3 to 6% faster from 2,048
+// rows and long contexts on, 3 to 5% slower at 256 rows and for short ones), with its two halves
+// of waves a phase apart as well (189 us against 175), two tiles of rows a wave at one wave a SIMD
+// (213), exponentials beside the next tile's scores (207), wave priorities and orders of the loads.
 template <class T, int RW> struct Shape {
     static constexpr int KS = 4 / RW, R = 32 * RW, KT = sizeof(T) == 2 && RW == 4 ? 64 : 32, KB = KS * KT;
 };
@@ -1014,7 +1016,7 @@ template <class T, int D, int RW> __global__ void __launch_bounds__(256, (rows_a
 // Joins the parts of a shared item's rows, four values a thread, in J workgroups: as many
 // rows at a time as a workgroup has room for, or (SPREAD) one row at a time with its parts
 // spread over the workgroup, for few rows in many parts. Parts are added in their order: the
-// same bits every time. 64 sequences 8.5 us, one of 8,191 tokens 4.8, 2,048 rows 13.7 (60 MB).
+// same bits every time. 64 sequences 8.1 us, one of 8,191 tokens 4.7, 2,048 rows 14.1 (60 MB).
 template <class T, int D, int R, bool SPREAD> __global__ void __launch_bounds__(256) paged_join_kernel(AttnParams p, int J) {
     lds_poison(0);
     constexpr int CG = D / 4, RG = 256 / CG;
@@ -1096,19 +1098,19 @@ template <class K, class... P> hipError_t launch(K kern, size_t x, int threads, 
 // Rows of a block: as many as the longest run of rows that a sequence can have
 // fills (a packed batch: its mean). Up to 32 rows go to 16x16 tiles: the other kernel is
 // quicker for 32 rows in bf16 at 128 channels (8 sequences of 8 tokens over 8,192, 16 and 4
-// heads: 41 us against 47; 64 over 4,096, 32 and 8 heads: 203 and 216) and slower elsewhere (256
-// of 5 tokens over 2,048: 414 and 380; 64 of 8 at 64 channels 126 and 120, at 32 104 and 88, in
-// fp32 846 and 482).
+// heads: 40 us against 45; 64 over 4,096, 32 and 8 heads: 205 and 215) and slower elsewhere (256
+// of 5 tokens over 2,048: 414 and 379; 64 of 8 at 64 channels 125 and 120, at 32 103 and 88, in
+// fp32 843 and 481).
 int block_rows(int T, int N, int G, bool packed) {
     const long rows = packed ? ((long)T + N - 1) / N * G : (long)T * G;
     return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
 // Workgroups that share the keys: as many as the chip's 256 CUs hold at once of the kernel for
 // more rows, so that each is given its share in the same turn. fp32 with 64 rows at 128 channels
-// has LDS for one a CU: 8 trees of 12 tokens over 8,192, 16 and 4 heads, 130 us, with two 141; 64
-// of 16 over 100 to 4,096, 32 and 8 heads, 460 and 476. Of the kernel for few rows one a CU, also
+// has LDS for one a CU: 8 trees of 12 tokens over 8,192, 16 and 4 heads, 129 us, with two 141; 64
+// of 16 over 100 to 4,096, 32 and 8 heads, 462 and 475. Of the kernel for few rows one a CU, also
 // where it has registers for two (bf16 at 32 channels: 64 single tokens over 100 to 4,096 49 us,
-// with two 45; 8 trees of 8 over 8,192 22 and 23).
+// with two 43; 8 trees of 8 over 8,192 21 and 23).
 template <class T, int D, int R> constexpr int shared_wgs() {
     if constexpr (R <= 32) return 256;
     else return 256 * rows_at_once<T, D, R / 32>();
@@ -1128,11 +1130,12 @@ struct Plan {
 };
 // Keys are shared out among workgroups, or every block of rows and head (group) is a
 // workgroup's own. bf16, 128 channels, 32 / 8 heads, shared and then not, us. Few rows:
-// 400 sequences of 100 to 4,096 tokens 586 and 816, 900 of 100 to 2,048 679 and 784:
+// 400 sequences of 100 to 4,096 tokens 591 and 821, 900 of 100 to 2,048 688 and 795:
 // shared as long as the plan can count the blocks. More rows, items of 64 sequences of
-// 100 to 8,192 tokens with 32 new ones (512 items) 312 and 387; from 1,024 items on they fill
-// the chip by themselves, and the parts' sums cost more than the evener split gives: 128 of
-// 2,048 tokens with 16 new ones 226 and 218, prompts of 16 x 512 tokens (16 / 4 heads) 77 and 54.
+// 100 to 8,192 tokens with 32 new ones (512 items) 312 and 391, of 100 sequences (800) 482 and
+// 613; from 1,024 items on they fill the chip by themselves, and the parts' sums cost more than
+// the evener split gives: 128 sequences of 2,048 tokens with 16 new ones 225 and 219, prompts of
+// 16 x 512 tokens (16 / 4 heads) 78 and 51.
 Plan make_plan(int T, int N, int Hkv, int G, bool packed) {
     Plan pl;
     pl.R = block_rows(T, N, G, packed);

@@ -2,7 +2,7 @@
 
     python -m gated_delta_rule_46_amd.profile_run [--fwd 3] [--bwd 2] [--bwd-token 0] [--decode 8]
                                                   [--copy-mib 256] [--mixers CASE,CASE|all]
-                                                  [--mixer-calls 12] [--rates]
+                                                  [--mixer-calls 12] [--rates] [--sizes GROUP,GROUP|all]
 
 Runs, on cuda:0 and with seeded synthetic inputs: --fwd forward calls on the
 workload --fwd-workload names (ckda: Complex KDA, B=2, H=16, T=8192, d=128,
@@ -17,9 +17,13 @@ WRITE_SIZE against a known byte count.
 
 --mixers runs listed cases of perf/operators.py (linear attention and window
 attention) and perf/more_operators.py (gated linear recurrence, paged cache),
---mixer-calls calls of each on three sets of inputs in turn; alone, with --fwd 0 --bwd 0 --decode 0. --rates prints what large copies and
-large matrix products reach on this card, and both one-token state updates
-(decode_step, linattn_decode_step) on one state and on three in turn.
+--mixer-calls calls of each on three sets of inputs in turn; alone, with --fwd 0
+--bwd 0 --decode 0. --rates prints what large copies and large matrix products
+reach on this card, and both one-token state updates (decode_step,
+linattn_decode_step) on one state and on three in turn. --sizes times the sizes
+at which the recurrence's and the paged cache's choices of a kernel, a block or
+a split were made (groups: see `sizes`); KDA_LIB names a build with a choice
+turned over, for the other side.
 """
 from __future__ import annotations
 
@@ -78,6 +82,51 @@ def print_rates(torch, kda):
                   % (name, n, s * 1e6, 8 * N * H * d * d / s / 1e12), flush=True)
 
 
+def sizes():
+    """{group: [case]}: cases of perf/more_operators.py by the choice that they bear on."""
+    def attn(N, T, ctx, heads, dtype="bf16", d=128, page=16, tree=False):
+        lo, hi = ctx if isinstance(ctx, tuple) else (ctx, ctx)
+        return dict(op="attn", dtype=dtype, N=N, T=T, ctx_lo=lo, ctx_hi=hi, tree=tree, Hq=heads[0], Hkv=heads[1], d=d, page=page)
+
+    def recur(B, T, C, dtype="bf16", gate=None, op="glr_fwd", packed=False):
+        batch = dict(lens=",".join([str(T)] * B)) if packed else dict(B=B, T=T)
+        return dict(op=op, dtype=dtype, gate=gate or dtype, **batch, C=C, h0=False)
+
+    wide, narrow = (32, 8), (16, 4)
+    return {
+        "share_few": [attn(400, 1, (100, 4096), wide), attn(900, 1, (100, 2048), wide)],
+        "share_rows": [attn(64, 32, (100, 8192), wide, tree=True), attn(100, 32, (100, 8192), wide, tree=True),
+                       attn(128, 16, 2048, wide, tree=True), attn(16, 512, 0, narrow)],
+        "row_blocks": [attn(8, 8, 8192, narrow, page=32, tree=True), attn(64, 8, 4096, wide, tree=True),
+                       attn(256, 5, 2048, wide, tree=True), attn(64, 8, 4096, wide, d=64, tree=True),
+                       attn(64, 8, 4096, wide, d=32, tree=True), attn(64, 8, 4096, wide, "f32", tree=True)],
+        "at_once": [attn(8, 12, 8192, narrow, "f32", tree=True), attn(1, 16, 16384, narrow, "f32", tree=True),
+                    attn(64, 16, (100, 4096), wide, "f32", tree=True)],
+        "at_once_few": [attn(64, 1, (100, 4096), wide, d=32), attn(8, 8, 8192, narrow, d=32, page=32, tree=True)],
+        "two_products": [attn(1, 2048, 6144, narrow, page=128), attn(1, 2048, 0, narrow, page=128),
+                         attn(8, 64, (2048, 16384), narrow, page=32, tree=True)],
+        "attn_f32": [attn(64, 1, (100, 4096), wide, "f32"), attn(1, 1024, 4096, narrow, "f32", page=128)],
+        "stream": [recur(16, T, 2048, *ty) for ty in (("bf16",), ("bf16", "f32"), ("f32",)) for T in (512, 1024, 2048, 4096)]
+        + [recur(32, 2048, 1024, "f32"), recur(64, 2048, 509, "f32"), recur(8, 4096, 2048)],
+        "states": [recur(1, 131072, 256)],
+        "gradients": [recur(2, 4096, 2048, *ty, op="glr_bwd") for ty in (("bf16",), ("bf16", "f32"), ("f32", "f32"))],
+        "short": [recur(256, 8, 4096, op=op, packed=p) for op in ("glr_fwd", "glr_bwd") for p in (False, True)],
+        "tokens": [recur(2, 8192, 2048), recur(1, 4096, 2048, "f32"), recur(1, 4096, 2049)],
+    }
+
+
+def print_sizes(torch, names):
+    m = operators("more_operators")
+    for group, cases in sizes().items():
+        if names != "all" and group not in names.split(","):
+            continue
+        for case in cases:
+            states = [m.prepare(case, seed) for seed in range(3)]
+            s = sorted(timed(torch, lambda i: m.run(states[i % 3]), 60) for _ in range(5))[2]
+            print("%s | %s | %.1f us" % (group, " ".join("%s=%.24s" % x for x in case.items() if x[0] != "h0"), s * 1e6), flush=True)
+            del states
+
+
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--fwd", type=int, default=3)
@@ -89,6 +138,7 @@ def main(argv=None) -> int:
     ap.add_argument("--mixers", default="")
     ap.add_argument("--mixer-calls", type=int, default=12)
     ap.add_argument("--rates", action="store_true")
+    ap.add_argument("--sizes", default="")
     args = ap.parse_args(argv)
 
     sys.path.insert(0, ROOT)
@@ -152,6 +202,8 @@ def main(argv=None) -> int:
             del states
     if args.rates:
         print_rates(torch, kda)
+    if args.sizes:
+        print_sizes(torch, args.sizes)
     if args.copy_mib > 0:
         src = torch.ones(args.copy_mib << 20, device=dev, dtype=torch.uint8)
         dst = torch.empty_like(src)

@@ -477,11 +477,15 @@ int kda_swa_cache_fill(const void* k, const void* v, void* K_cache, void* V_cach
  * wanted); cu_seqlens and N as for kda_chunk_fwd. h has the type of x (`dtype`),
  * states are fp32. gate_dtype: KDA_F32, or KDA_BF16 with bf16 x (decays near one
  * have no bf16 neighbours, so that fp32 decays go with either). Any decay is
- * allowed, zero and negative ones included, as long as the product of the
- * decays over every run of a sequence's tokens is finite in fp32: these products
- * are formed directly. h_T may be h0, h must not alias an input. Rows of h at or
- * behind cu_seqlens[N] are left as they are. A NaN or Inf at a token reaches the
- * later outputs of its sequence and channel, no others.
+ * allowed, zero and negative ones included, as long as the products of the decays
+ * over runs of a sequence's tokens, which are formed directly, stay within fp32: no
+ * run's product may overflow, nor one that falls below fp32's smallest number be
+ * brought back by decays larger than one behind it (1e-25, 1e-25, then 1e25 may pass
+ * nothing on). Decays of magnitude up to one are never in question. h_T may be h0, h
+ * must not alias an input. Rows of h at or behind cu_seqlens[N] are left as they are.
+ * A NaN or Inf at a token reaches the later outputs of its sequence and channel, no
+ * others. Tokens follow each other: of a tree of drafts (kda_paged_attn) each branch
+ * is a sequence of its own here, from the state of the tokens before it.
  *
  * C <= 2^20, and N * (T + 128) < 2^31; KDA_ENOTSUP beyond, and where blocks of
  * 128 tokens (64 where C is no multiple of 8, fp32 x: of 4) and 64 channels are
